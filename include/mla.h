@@ -439,6 +439,83 @@ mla_status mla_append_kv(const uint16_t* h, const uint16_t* w_dkr, uint16_t* cac
  * after it has finished. */
 mla_status mla_copy16(const void* src, void* dst, size_t bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The prompt side: a ragged CHUNK of new tokens. Sequence b owns rows cu[b] ..
+ * cu[b+1] - 1 of the row arrays (n_b = cu[b+1] - cu[b] >= 0 new tokens; cu
+ * [B + 1] int32, nondecreasing, cu[0] >= 0), and seq_lens[b] counts them: row j
+ * of sequence b sits at position seq_lens[b] - n_b + j. T is the number of rows
+ * of the arrays; rows at and past cu[B] belong to no sequence and their outputs
+ * are left as they were, so a captured call serves any chunk of at most T rows
+ * and B sequences. 1 <= B <= MLA_MAX_BATCH, 1 <= T <= 2^20.
+ * The cache is bf16 (fp8_scales NULL) or e4m3 codes with fp8_scales [576]
+ * float32, one scale per column (see mla_quantize_fp8). Lengths outside
+ * [n_b, max_pages_per_seq * page_size], page ids outside the pool and rows
+ * outside [0, T) are reported in err_word as MLA_ERR_BOUNDS; what they touch is
+ * clamped or skipped. Every input but the weights is read after the kernel
+ * before has finished.
+ *
+ * mla_append_chunk — the new tokens' cache rows written into their pages, the
+ * row of mla_append_kv:
+ *   row[i] = sum_k h[t][k] w_dkr[i][k], the pairs from column 512 on rotated by
+ *   pos * rope_theta^(-2i/64);  cache row = bf16(row) or e4m3(row / fp8_scales)
+ * (fp32 sums; one rounding: nearest even, saturating at +-448 for e4m3).
+ *   h [T][d_model] bf16, w_dkr [576][d_model] bf16, d_model a multiple of 64, at
+ *   most 65536; workspace >= mla_append_chunk_workspace_bytes(T, d_model) bytes,
+ *   no initial contents needed. w_dkr may be read while the kernel before is
+ *   still finishing. Sums are added in a fixed order: results are reproducible
+ *   bit for bit. Two rows that name the same cache row leave one of the two. */
+size_t mla_append_chunk_workspace_bytes(int T, int d_model);
+mla_status mla_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                            int d_model, int num_pages, int page_size, int max_pages_per_seq, float rope_theta,
+                            void* workspace, size_t workspace_bytes, int32_t* err_word, void* stream);
+
+/* mla_read_kv — cache rows read back from their pages: row cu[b] + i of `rows`
+ * is token first[b] + i of sequence b (first [B] int32, NULL = 0 for all), as it
+ * is from a bf16 cache, bf16(fp8_scales[d] * e4m3(code)) from an FP8 one, zeros
+ * for tokens at and past seq_lens[b]. rows [n_rows][576] bf16; rows at and past
+ * cu[B] are left as they were. Here seq_lens is only the bound of the context
+ * (it need not count the rows). Unused block-table entries are never read. */
+mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t* block_table,
+                       const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* rows, int B,
+                       int n_rows, int num_pages, int page_size, int max_pages_per_seq, int32_t* err_word,
+                       void* stream);
+
+/* mla_attend_chunk — attention of the chunk over the paged cache, the new tokens'
+ * own rows included (append them first):
+ *   z_s = softmax_scale * (q_nope . (c_s W^UK) + q_rope . k^R_s),  s <= L_b - n_b + j
+ *   out[t][h] = softmax(z) (c_s W^UV),  lse[t][h] = ln sum_s exp(z_s)
+ * in one of two forms of the same sums (form = MLA_CHUNK_AUTO chooses by the
+ * chunk's mean length T / B):
+ *   MLA_CHUNK_EXPANDED  keys and values of every head are expanded from the latents
+ *     first (fp16, the score and weight products on fp16 and bf16 operands, fp32
+ *     sums). For long chunks. An expanded key or value of 65520 or more is reported
+ *     as MLA_ERR_RANGE; below 2^-14 their resolution is 2^-25.
+ *   MLA_CHUNK_ABSORBED  every new token is decoded over the latents (mla_absorb_q,
+ *     mla_decode_paged, mla_combine, mla_out_proj with their roundings). For few new
+ *     tokens on a context; T <= MLA_MAX_BATCH.
+ * A cached token whose expanded values are not finite (NaN or infinite latents)
+ * gives NaN to the queries that see it and to no other.
+ *   q_nope [T][H][128] bf16, q_rope [T][H][64] bf16 (already rotated),
+ *   w_uk, w_uv as for mla_absorb_q and mla_out_proj, out [T][H][128] bf16,
+ *   lse [T][H] float or NULL (both in device memory),
+ *   max_tokens  at least the sum of the contexts of the sequences that have new
+ *               tokens (it sizes the workspace; a sequence beyond it is skipped and
+ *               reported), <= 2^30
+ *   workspace   >= mla_attend_chunk_workspace_bytes(B, T, H, max_tokens, form) bytes,
+ *               no initial contents needed. Calls sharing a workspace must not
+ *               overlap on the GPU. The size of the absorbed form depends on the
+ *               current device; 0 if an argument is invalid.
+ * w_uk and w_uv may be read while the kernel before is still finishing. */
+enum { MLA_CHUNK_AUTO = 0, MLA_CHUNK_EXPANDED = 1, MLA_CHUNK_ABSORBED = 2 };
+size_t mla_attend_chunk_workspace_bytes(int B, int T, int H, int64_t max_tokens, int form);
+mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
+                            const uint16_t* w_uv, const void* cache, const float* fp8_scales,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                            int H, int num_pages, int page_size, int max_pages_per_seq, int64_t max_tokens,
+                            float softmax_scale, int form, uint16_t* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* err_word, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

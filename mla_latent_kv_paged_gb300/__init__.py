@@ -12,6 +12,10 @@ The names follow the C ABI in ``include/mla.h``:
   decode_paged  split-KV scores and softmax-weighted latent sums over pages
   combine       log-sum-exp merge of the split partials -> u, lse
   out_proj      out = u W_UV (per head)
+and, for a ragged chunk of new tokens (the prompt side):
+  append_chunk  the chunk's cache rows written into their pages, bf16 or FP8
+  attend_chunk  attention of the chunk over the paged cache
+  read_kv       cache rows read back from their pages
 """
 from __future__ import annotations
 
@@ -48,6 +52,8 @@ EXPORTS = [
     "mla_merge_w_comb", "mla_out_comb_workspace_bytes", "mla_out_comb",
     "mla_quantize_fp8", "mla_decode_paged_fp8", "mla_decode_paged_planned_fp8",
     "mla_copy16",
+    "mla_append_chunk_workspace_bytes", "mla_append_chunk", "mla_read_kv",
+    "mla_attend_chunk_workspace_bytes", "mla_attend_chunk",
 ]
 
 
@@ -152,6 +158,18 @@ def _load(path: str):
     L.mla_decode_paged_fp8.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, f, i, vp, sz, vp, vp]
     L.mla_decode_paged_planned_fp8.restype = i
     L.mla_decode_paged_planned_fp8.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, f, i, vp, sz, vp, vp]
+    i64 = ctypes.c_int64
+    L.mla_append_chunk_workspace_bytes.restype = sz
+    L.mla_append_chunk_workspace_bytes.argtypes = [i, i]
+    L.mla_append_chunk.restype = i
+    L.mla_append_chunk.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, f, vp, sz, vp, vp]
+    L.mla_read_kv.restype = i
+    L.mla_read_kv.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
+    L.mla_attend_chunk_workspace_bytes.restype = sz
+    L.mla_attend_chunk_workspace_bytes.argtypes = [i, i, i, i64, i]
+    L.mla_attend_chunk.restype = i
+    L.mla_attend_chunk.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i64, f, i, vp, vp, vp, sz, vp,
+                                   vp]
     return L
 
 
@@ -464,6 +482,176 @@ def out_proj(u, w_uv, out=None, stream=None):
                             u.shape[-1], w_uv.shape[1], _stream(stream))
     _check(st, "mla_out_proj")
     return out
+
+
+# ---------------------------------------------------------------- chunks of new tokens
+CHUNK_FORMS = {"auto": 0, "expanded": 1, "absorbed": 2}
+
+
+def _tensor(name, t, dtypes, shape, dev):
+    """Check one argument: contiguous, one of ``dtypes``, ``shape`` (None = any extent), on ``dev``."""
+    if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
+        raise ValueError(f"{name}: dtype {t.dtype}")
+    if len(t.shape) != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the cache on {dev}")
+
+
+def _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word):
+    """Check the paged-cache arguments of the chunk calls; returns (device, B)."""
+    import torch
+    dev, B = cache.device, block_table.shape[0] if block_table.dim() == 2 else 0
+    if dev.type != "cuda":
+        raise ValueError(f"cache: on {dev}, a CUDA device is needed")
+    fp8 = cache.dtype == torch.uint8
+    if fp8 != (fp8_scales is not None):
+        raise ValueError("an FP8 cache (uint8 codes) needs its column scales fp8_scales, a bf16 cache has none")
+    _tensor("cache", cache, (torch.uint8, torch.bfloat16), (None, None, D_ROW), dev)
+    _tensor("block_table", block_table, torch.int32, (None, None), dev)
+    _tensor("seq_lens", seq_lens, torch.int32, (B,), dev)
+    _tensor("cu", cu, torch.int32, (B + 1,), dev)
+    if fp8:
+        _tensor("fp8_scales", fp8_scales, torch.float32, (D_ROW,), dev)
+    if err_word is not None and (err_word.dtype != torch.int32 or err_word.numel() < 1 or err_word.device != dev):
+        raise ValueError("err_word: an int32 tensor beside the cache")
+    return dev, B
+
+
+def _room(workspace, need, dev):
+    """The workspace given (its size is checked by the call) or a new one of ``need`` bytes."""
+    import torch
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    if not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace: a contiguous tensor beside the cache")
+    return workspace
+
+
+def append_chunk_workspace_bytes(T: int, d_model: int) -> int:
+    n = int(lib().mla_append_chunk_workspace_bytes(T, d_model))
+    if n == 0:
+        raise MlaError(1, "mla_append_chunk_workspace_bytes")
+    return n
+
+
+def append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, *, fp8_scales=None, rope_theta: float = 10000.0,
+                 workspace=None, err_word=None, stream=None):
+    """Write the cache rows of a ragged chunk of new tokens into their pages.
+
+    h [T, d_model] bf16: rows cu[b] .. cu[b+1]-1 (cu [B+1] int32) are sequence b's new
+    tokens, at the end of its context (seq_lens [B] int32 already counts them). w_dkr
+    [576, d_model] bf16 as for append_kv, cache [num_pages, page_size, 576] bf16, or
+    uint8 e4m3 codes with their column scales fp8_scales [576] float32: the rows are
+    then quantised as they are written. Rows of h at and past cu[B] are ignored. The
+    workspace (allocated when none is given) is returned for reuse.
+    """
+    import torch
+    dev, B = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    _tensor("h", h, torch.bfloat16, (None, None), dev)
+    T, d_model = h.shape
+    _tensor("w_dkr", w_dkr, torch.bfloat16, (D_ROW, d_model), dev)
+    with torch.cuda.device(dev):
+        need = append_chunk_workspace_bytes(T, d_model)
+        workspace = _room(workspace, need, dev)
+        st = lib().mla_append_chunk(_ptr(h), _ptr(w_dkr), _ptr(cache), _ptr(fp8_scales), _ptr(block_table),
+                                    _ptr(seq_lens), _ptr(cu), B, T, d_model, cache.shape[0], cache.shape[1],
+                                    block_table.shape[1], float(rope_theta), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _ptr(err_word), _stream(stream))
+    _check(st, "mla_append_chunk")
+    return workspace
+
+
+def read_kv(cache, block_table, seq_lens, cu, *, n_rows: int, first=None, fp8_scales=None, out=None, err_word=None,
+            stream=None):
+    """Cache rows read back: row cu[b] + i of the result [n_rows, 576] bf16 is token
+    first[b] + i (first [B] int32, None = 0) of sequence b, dequantised from an FP8 cache
+    (uint8 codes with fp8_scales), zeros at and past seq_lens[b]. Rows at and past cu[B]
+    are left as they were in ``out`` (undefined in a new tensor)."""
+    import torch
+    dev, B = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    if first is not None:
+        _tensor("first", first, torch.int32, (B,), dev)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((n_rows, D_ROW), dtype=torch.bfloat16, device=dev)
+        _tensor("out", out, torch.bfloat16, (n_rows, D_ROW), dev)
+        st = lib().mla_read_kv(_ptr(cache), _ptr(fp8_scales), _ptr(block_table), _ptr(seq_lens), _ptr(first), _ptr(cu),
+                               _ptr(out), B, n_rows, cache.shape[0], cache.shape[1], block_table.shape[1],
+                               _ptr(err_word), _stream(stream))
+    _check(st, "mla_read_kv")
+    return out
+
+
+def attend_chunk_workspace_bytes(B: int, T: int, H: int, max_tokens: int, form: str = "auto") -> int:
+    n = int(lib().mla_attend_chunk_workspace_bytes(B, T, H, max_tokens, CHUNK_FORMS[form]))
+    if n == 0:
+        raise MlaError(1, "mla_attend_chunk_workspace_bytes")
+    return n
+
+
+def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *, max_tokens: int | None = None,
+                 fp8_scales=None, softmax_scale: float = DEFAULT_SCALE, form: str = "auto", out=None, lse=None,
+                 workspace=None, err_word=None, stream=None):
+    """Attention of a ragged chunk of new tokens over the paged cache, their own rows
+    included (append_chunk them first). Returns out [T, H, 128] bf16.
+
+    q_nope [T, H, 128], q_rope [T, H, 64] (rotated) bf16, rows cu[b] .. cu[b+1]-1 being
+    sequence b's new tokens; row j of n sees tokens 0 .. seq_lens[b] - n + j. w_uk, w_uv
+    [H, 128, 512] bf16; cache, block_table, seq_lens, cu, fp8_scales as for append_chunk.
+    max_tokens bounds the sum of the contexts (default: the block table's capacity) and
+    sizes the workspace. form: "expanded" (keys and values of every head expanded first),
+    "absorbed" (each token decoded over the latents) or "auto" (by the mean chunk length).
+    lse [T, H] float32, when given, receives the log-sum-exp of the scores. Rows at and
+    past cu[B] of out and lse are left as they were.
+    """
+    import torch
+    dev, B = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    if form not in CHUNK_FORMS:
+        raise ValueError(f"form: {form!r}, expected one of {sorted(CHUNK_FORMS)}")
+    bf = torch.bfloat16
+    _tensor("q_nope", q_nope, bf, (None, None, D_NOPE), dev)
+    T, H = q_nope.shape[0], q_nope.shape[1]
+    _tensor("q_rope", q_rope, bf, (T, H, D_R), dev)
+    _tensor("w_uk", w_uk, bf, (H, D_NOPE, D_C), dev)
+    _tensor("w_uv", w_uv, bf, (H, D_V, D_C), dev)
+    if lse is not None:
+        _tensor("lse", lse, torch.float32, (T, H), dev)
+    if max_tokens is None:
+        max_tokens = B * block_table.shape[1] * cache.shape[1]
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((T, H, D_V), dtype=bf, device=dev)
+        _tensor("out", out, bf, (T, H, D_V), dev)
+        need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
+        workspace = _room(workspace, need, dev)
+        st = lib().mla_attend_chunk(_ptr(q_nope), _ptr(q_rope), _ptr(w_uk), _ptr(w_uv), _ptr(cache), _ptr(fp8_scales),
+                                    _ptr(block_table), _ptr(seq_lens), _ptr(cu), B, T, H, cache.shape[0],
+                                    cache.shape[1], block_table.shape[1], max_tokens, float(softmax_scale),
+                                    CHUNK_FORMS[form], _ptr(out), _ptr(lse), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _ptr(err_word), _stream(stream))
+    _check(st, "mla_attend_chunk")
+    return out
+
+
+def chunk_step(h, q_nope, q_rope, w_dkr, w_uk, w_uv, cache, block_table, seq_lens, cu, *,
+               max_tokens: int | None = None, fp8_scales=None, rope_theta: float = 10000.0,
+               softmax_scale: float = DEFAULT_SCALE, form: str = "auto", out=None, bufs: dict | None = None,
+               err_word=None, stream=None):
+    """One layer's attention step of a prompt chunk: append_chunk, then attend_chunk over
+    the cache that now holds the chunk (decode_step's counterpart for ragged chunks).
+
+    ``bufs`` may hold preallocated append_workspace and attend_workspace tensors.
+    Returns out [T, H, 128] bf16.
+    """
+    bufs = bufs or {}
+    append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, fp8_scales=fp8_scales, rope_theta=rope_theta,
+                 workspace=bufs.get("append_workspace"), err_word=err_word, stream=stream)
+    return attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, max_tokens=max_tokens,
+                        fp8_scales=fp8_scales, softmax_scale=softmax_scale, form=form, out=out,
+                        workspace=bufs.get("attend_workspace"), err_word=err_word, stream=stream)
 
 
 def decode_step(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, *, n_q: int,

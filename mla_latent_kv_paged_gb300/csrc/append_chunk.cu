@@ -1,0 +1,369 @@
+// Latent-cache rows of a ragged chunk of new tokens, written into their pages as
+// bf16 or, quantised as they are written, as e4m3 codes with one scale per column.
+//
+// What it computes (Huny's Dev Blog "MLA 아키텍처 해부" section 1.2,
+// c_t^KV = h_t W^DKV, and section 2.2, k^R_t = RoPE(h_t W^KR); section 6 item 4:
+// FP8 on the latent needs per-channel scales): for row t of sequence b at
+// position pos = L_b - n_b + (t - cu[b]),
+//   row[i] = sum_k h[t][k] w_dkr[i][k], the pairs from column 512 on rotated
+//   cache row = bf16(row[i])   or   e4m3(row[i] / scales[i]), saturating
+// The quotient is taken from the fp32 sum: a row is rounded once.
+//
+// A GEMM [T x d_model] x [d_model x 576]: weight-streaming for a few rows,
+// tensor-bound for a prompt. A CTA computes 128 rows x 192 columns (three column
+// tiles; the positional columns lie in the last) over a slice of d_model, fed
+// through a five-stage TMA ring. When the tiles alone do not fill the SMs the
+// reduction over d_model is split: each split writes fp32 partials and a second
+// kernel adds them in split order (results are bit-reproducible), rotates,
+// quantises and scatters; with one split the GEMM's own epilogue does that.
+#include <math.h>
+
+#include "chunk.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kN = 192;                 // output columns per CTA
+constexpr int kColTiles = kRow / kN;    // 3
+constexpr int kM = 128;                 // rows per CTA
+constexpr int kStages = 5;
+constexpr uint32_t kABytes = kM * 128, kBBytes = kN * 128, kStageBytes = kABytes + kBBytes;
+constexpr uint32_t kOffBar = kStages * kStageBytes;
+constexpr uint32_t kOffFreq = kOffBar + (2 * kStages + 2) * 8;  // 8-byte aligned
+constexpr uint32_t kOffSlots = kOffFreq + 32 * 8;
+constexpr uint32_t kSmem = kOffSlots + 16;
+constexpr uint32_t kTmCols = 256;
+constexpr int kThreads = 192;  // warps 0..3 epilogue, 4 producer, 5 MMA issuer
+constexpr int kCtas = 152;     // one per SM
+
+struct Shape {
+  int tiles, KB, S;
+};
+// Splits of the d_model reduction: what fills the SMs, at least two 64-wide
+// blocks each. A function of (T, d_model) only.
+inline Shape shape_of(int T, int d_model) {
+  Shape a;
+  a.tiles = (T + kM - 1) / kM;
+  a.KB = d_model / 64;
+  const int fill = kCtas / (kColTiles * a.tiles);
+  a.S = fill < a.KB / 2 ? fill : a.KB / 2;
+  if (a.S < 1) a.S = 1;
+  return a;
+}
+
+// Fraction of a turn per position of positional pair i, in units of 2^-64 turns:
+// theta^(-2i/64) / (2 pi). pos times it modulo 2^64 is the angle's fraction of a
+// turn, exact to 2^-64 pos + the double's rounding, whatever the position.
+__device__ __forceinline__ uint64_t turn_fraction(double theta, int i) {
+  return __double2ull_rn(pow(theta, -2.0 * (double)i / kDR) * 0.15915494309189535 * 18446744073709551616.0);
+}
+__device__ __forceinline__ void rotate(float& x, float& y, uint64_t per_pos, int pos) {
+  const int32_t turn = (int32_t)((per_pos * (uint64_t)(uint32_t)pos) >> 32);  // [-1/2, 1/2) in 2^-32
+  float sn, cs;
+  sincosf((float)turn * 1.4629180792671596e-9f /* 2 pi 2^-32 */, &sn, &cs);
+  const float rx = x * cs - y * sn;
+  y = x * sn + y * cs;
+  x = rx;
+}
+// two quotients -> two e4m3 codes (lo in the low byte), nearest even, saturating
+__device__ __forceinline__ uint32_t quantise2(float x, float y, float sx, float sy) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(__fdiv_rn(y, sy)), "f"(__fdiv_rn(x, sx)));
+  return r;
+}
+
+struct Target {
+  int64_t row;  // row of the pool, or -1
+  int pos;
+};
+// Where row t goes. Out-of-range lengths and page ids are reported; such a row
+// (and a row of no sequence) is not written.
+__device__ Target target_of(const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_lens,
+                            const int32_t* __restrict__ block_table, int B, int t, int num_pages, int page_size,
+                            int max_pages, bool report, int32_t* err_word) {
+  Target r = {-1, 0};
+  const int b = row_sequence(cu, B, t);
+  if (b < 0) return r;
+  const int n = cu[b + 1] - cu[b], max_tokens = max_pages * page_size, raw = seq_lens[b];
+  const int L = min(max(raw, n), max_tokens);
+  const int pos = L - n + (t - cu[b]);
+  bool bad = raw != L;
+  if (pos >= 0 && pos < max_tokens) {
+    const int page = block_table[(int64_t)b * max_pages + pos / page_size];
+    if (page >= 0 && page < num_pages)
+      r = {(int64_t)page * page_size + pos % page_size, pos};
+    else
+      bad = true;
+  } else {
+    bad = true;
+  }
+  if (bad && report) report_error(err_word, MLA_ERR_BOUNDS);
+  return r;
+}
+
+struct Args {
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu;
+  const float* scales;  // null: bf16 cache
+  void* cache;
+  float* partials;
+  int32_t* err_word;
+  double theta;
+  int B, T, KB, S, num_pages, page_size, max_pages;
+};
+
+template <bool kDirect, bool kF8>
+__global__ void __launch_bounds__(kThreads, 1)
+append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h, Args a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nt = blockIdx.x, s = blockIdx.y, tile = blockIdx.z;
+  const int kb0 = (int)((int64_t)s * a.KB / a.S), nkb = (int)((int64_t)(s + 1) * a.KB / a.S) - kb0;
+  auto full = [&](int i) { return sbase + kOffBar + 8u * i; };
+  auto empty = [&](int i) { return sbase + kOffBar + 8u * (kStages + i); };
+  const uint32_t bar_d = sbase + kOffBar + 8u * 2 * kStages;
+  uint64_t* freq = reinterpret_cast<uint64_t*>(smem + kOffFreq);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlots);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffSlots + 4);
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) report_error(a.err_word, MLA_ERR_CUDA);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 1);
+    }
+    mbar_init(bar_d, 1);
+    mbar_init(bar_d + 8, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_slot), kTmCols);
+    tmem_relinquish();
+  }
+  if (kDirect && warp == 0) freq[lane] = turn_fraction(a.theta, lane);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      prefetch_tmap(&map_w);
+      prefetch_tmap(&map_h);
+      const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
+      // the first stages' weights while the kernel before is finishing (weights
+      // are never its output); the hidden states after the wait
+      const int early = nkb < kStages ? nkb : kStages;
+      for (int k = 0; k < early; ++k) {
+        mbar_arrive_expect_tx(full(k), kStageBytes);
+        tma_load_2d(sbase + k * kStageBytes + kABytes, &map_w, full(k), (kb0 + k) * 64, nt * kN, keep);
+      }
+      grid_dependency_wait();
+      int k = 0;
+      for (; k < nkb; ++k) {
+        const int st = k % kStages;
+        if (k >= kStages) {
+          if (!wait_phase(empty(st), (uint32_t)((k / kStages - 1) & 1), abort_flag, a.err_word)) break;
+          mbar_arrive_expect_tx(full(st), kStageBytes);
+          tma_load_2d(sbase + st * kStageBytes + kABytes, &map_w, full(st), (kb0 + k) * 64, nt * kN, keep);
+        }
+        tma_load_2d(sbase + st * kStageBytes, &map_h, full(st), (kb0 + k) * 64, tile * kM, stream);
+      }
+      if (k < nkb) {  // gave up: let the copies in flight land before the CTA can exit
+        for (int i = k > kStages ? k - kStages : 0; i < k; ++i) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(full(i % kStages), (uint32_t)((i / kStages) & 1)) && clock64() - t0 < kWaitLimitCycles) {
+          }
+        }
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(kM, kN, false, false);
+      const uint64_t d0 = smem_desc(0, 16, 1024, kSwizzle128B);
+      auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
+      for (int k = 0; k < nkb; ++k) {
+        const int st = k % kStages;
+        if (!wait_phase(full(st), (uint32_t)((k / kStages) & 1), abort_flag, a.err_word)) break;
+        tc_fence_after();
+        const uint64_t ad = d0 + da(sbase + st * kStageBytes), bd = d0 + da(sbase + st * kStageBytes + kABytes);
+#pragma unroll
+        for (int k4 = 0; k4 < 4; ++k4) mma_ss(tmem, ad + 2 * k4, bd + 2 * k4, idesc, (k > 0 || k4 > 0) ? 1u : 0u);
+        mma_commit(empty(st));
+      }
+      mma_commit(bar_d);
+      mma_commit(bar_d + 8);
+      wait_mmas(bar_d + 8);
+    }
+  } else {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int row = warp * 32 + lane, t = tile * kM + row;
+    Target to = {-1, 0};
+    if (kDirect && t < a.T)
+      to = target_of(a.cu, a.seq_lens, a.block_table, a.B, t, a.num_pages, a.page_size, a.max_pages, nt == 0,
+                     a.err_word);
+    if (__all_sync(0xffffffffu, wait_phase(bar_d, 0, abort_flag, a.err_word))) {
+      tc_fence_after();
+      const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
+#pragma unroll 1
+      for (int c0 = 0; c0 < kN; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(taddr + c0, r);
+        tmem_wait_ld();
+        const int col = nt * kN + c0;
+        if (!kDirect) {
+          float4* dst = reinterpret_cast<float4*>(a.partials + (((size_t)tile * a.S + s) * kM + row) * kRow + col);
+          if (t < a.T) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              dst[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
+                                   __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+          }
+        } else if (to.row >= 0) {
+          if (col >= kDC) {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) {
+              // indexed through a switch-free rotation of the register pairs
+              float x = __uint_as_float(r[0]), y = __uint_as_float(r[1]);
+              rotate(x, y, freq[(col - kDC) / 2 + i], to.pos);
+#pragma unroll
+              for (int q = 0; q < 30; ++q) r[q] = r[q + 2];
+              r[30] = __float_as_uint(x);
+              r[31] = __float_as_uint(y);
+            }
+          }
+          if (kF8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 sc = __ldg(reinterpret_cast<const float4*>(a.scales + col) + q);
+              w[q] = quantise2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), sc.x, sc.y) |
+                     quantise2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]), sc.z, sc.w) << 16;
+            }
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.cache) + to.row * kRow + col);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.cache) + to.row * kRow + col);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = cvt_bf16x2(__uint_as_float(r[8 * q + 2 * e]), __uint_as_float(r[8 * q + 2 * e + 1]));
+              dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmCols);
+  }
+}
+
+// Row t: the split partials added in order, the positional pairs rotated, the
+// row written. Thread c handles columns 2c and 2c + 1.
+template <bool kF8>
+__global__ void __launch_bounds__(kRow / 2)
+append_chunk_finalize(Args a) {
+  const int t = blockIdx.x, c = threadIdx.x, col = 2 * c;
+  const uint64_t per_pos = col >= kDC ? turn_fraction(a.theta, (col - kDC) / 2) : 0;
+  // the GEMM before passed its own dependency wait before this kernel could
+  // start, so the lengths and tables are final; the partials are not
+  const Target to = target_of(a.cu, a.seq_lens, a.block_table, a.B, t, a.num_pages, a.page_size, a.max_pages, c == 0,
+                              a.err_word);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (to.row < 0) return;
+  const float2* p =
+      reinterpret_cast<const float2*>(a.partials + (((size_t)(t / kM) * a.S) * kM + t % kM) * kRow + col);
+  constexpr size_t kStep = (size_t)kM * kRow / 2;
+  float x = 0.f, y = 0.f;
+  constexpr int kInFlight = 16;
+  for (int s0 = 0; s0 < a.S; s0 += kInFlight) {
+    float2 v[kInFlight];
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k)
+      if (s0 + k < a.S) v[k] = __ldcg(p + (size_t)(s0 + k) * kStep);
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k)
+      if (s0 + k < a.S) {
+        x += v[k].x;
+        y += v[k].y;
+      }
+  }
+  if (col >= kDC) rotate(x, y, per_pos, to.pos);
+  if (kF8) {
+    const float2 sc = __ldg(reinterpret_cast<const float2*>(a.scales) + c);
+    reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.cache) + to.row * kRow)[c] =
+        (uint16_t)quantise2(x, y, sc.x, sc.y);
+  } else {
+    reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.cache) + to.row * kRow)[c] = cvt_bf16x2(x, y);
+  }
+}
+
+template <bool kDirect, bool kF8>
+cudaError_t launch_gemm(const CUtensorMap& mw, const CUtensorMap& mh, const Shape& sh, const Args& a, cudaStream_t s) {
+  cudaError_t e = smem_limit<append_chunk_gemm<kDirect, kF8>>(kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(append_chunk_gemm<kDirect, kF8>, dim3(kColTiles, sh.S, sh.tiles), dim3(kThreads), kSmem, s, mw, mh,
+                    a);
+}
+
+}  // namespace
+
+size_t append_chunk_workspace_bytes(int T, int d_model) {
+  const Shape sh = shape_of(T, d_model);
+  return sh.S > 1 ? (size_t)sh.tiles * sh.S * kM * kRow * 4 : 256;
+}
+
+cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
+                                const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                                int d_model, int num_pages, int page_size, int max_pages, double theta,
+                                void* workspace, int32_t* err_word, cudaStream_t s) {
+  const Shape sh = shape_of(T, d_model);
+  CUtensorMap mw, mh;
+  const uint64_t dw[2] = {(uint64_t)d_model, (uint64_t)kRow}, dh[2] = {(uint64_t)d_model, (uint64_t)T};
+  const uint64_t st[1] = {(uint64_t)d_model * 2};
+  const uint32_t bw[2] = {64, kN}, bh[2] = {64, kM};
+  if (!make_tmap(&mw, w_dkr, 2, dw, st, bw, 128) || !make_tmap(&mh, h, 2, dh, st, bh, 128))
+    return cudaErrorInvalidValue;
+  Args a = {};
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.cu = cu;
+  a.scales = fp8_scales;
+  a.cache = cache;
+  a.partials = static_cast<float*>(workspace);
+  a.err_word = err_word;
+  a.theta = theta;
+  a.B = B;
+  a.T = T;
+  a.KB = sh.KB;
+  a.S = sh.S;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  if (sh.S == 1)
+    return fp8_scales ? launch_gemm<true, true>(mw, mh, sh, a, s) : launch_gemm<true, false>(mw, mh, sh, a, s);
+  cudaError_t e = launch_gemm<false, false>(mw, mh, sh, a, s);
+  if (e != cudaSuccess) return e;
+  return fp8_scales ? launch_pdl(append_chunk_finalize<true>, dim3(T), dim3(kRow / 2), 0, s, a)
+                    : launch_pdl(append_chunk_finalize<false>, dim3(T), dim3(kRow / 2), 0, s, a);
+}
+
+}  // namespace mla

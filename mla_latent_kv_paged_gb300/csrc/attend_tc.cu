@@ -1,0 +1,362 @@
+// Attention of a ragged chunk of new tokens over expanded keys and values on the
+// 5th-generation tensor cores (tcgen05, sm_103a).
+//
+// What it computes, per head and new token t at row j of a sequence with n new
+// tokens and context L (Huny's Dev Blog "MLA 아키텍처 해부" section 2.2, the score
+// as content plus position; section 1.2, the explicit keys and values):
+//   z_s = scale (q_nope . k_s + q_rope . kr_s)     s = 0 .. L - n + j
+//   out = sum_s exp(z_s - m) v_s / sum_s exp(z_s - m)
+//
+// A CTA takes 256 query rows of one sequence and one head as two MMA tiles of
+// 128 rows and walks the keys in steps of 128, so that every key and value it
+// loads serves 256 rows. Per step and tile: S = Q K^T (three 64-wide slabs: two
+// of fp16 content, one of bf16 position, accumulated in one fp32 tile), the
+// online softmax with a thread per row, P as fp16 into the tensor memory of S,
+// O += P V. While one tile's softmax runs, the tensor cores work on the other
+// tile: P0 V, the next S0, P1 V, the next S1, ...
+//
+// Shared memory (224 KB of slabs of 16 KB): Q 6, a ring of 5 for K and one of 3
+// for V. A slab is freed by the last MMAs that read it, not a whole tile at a
+// time, so the next tile's slabs have more than 1000 cycles to arrive. Tensor
+// memory: S0, S1, O0, O1, 128 columns each.
+//
+// The running maximum is a reference that is only raised when a row exceeds it
+// by 2^8 (O is then rescaled by the thread that owns the row); P is held times
+// 2^7, so that fp16 keeps weights down to 2^-31 of the largest and never
+// overflows (2^15). Sums are fp32, of the unrounded weights.
+#include "chunk.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr uint32_t kSlab = 128 * 128;  // [128 rows][64 16-bit columns], 128B swizzle
+constexpr uint32_t kVBox = 64 * 128;   // [64 keys][64 columns]
+constexpr int kQSlabs = 6, kKStages = 5, kVStages = 3;
+constexpr uint32_t kOffK = kQSlabs * kSlab, kOffV = kOffK + kKStages * kSlab, kOffBar = kOffV + kVStages * kSlab;
+enum {
+  KF0 = 0, KE0 = KF0 + kKStages, VF0 = KE0 + kKStages, VE0 = VF0 + kVStages, QF0 = VE0 + kVStages, SF0 = QF0 + 2,
+  PF0 = SF0 + 2, OF0 = PF0 + 2, MD = OF0 + 2, kBars
+};
+constexpr uint32_t kOffSlots = kOffBar + 8 * kBars;
+constexpr uint32_t kSmem = kOffSlots + 16;
+static_assert(kSmem <= 232448, "shared memory budget");
+constexpr int kThreads = 320;  // warps 0..3 and 4..7 softmax of tile 0 and 1, 8 producer, 9 MMA issuer
+constexpr uint32_t kTmS = 0, kTmO = 256;
+constexpr float kBias = 7.0f;       // P = 2^7 exp(z - m)
+constexpr float kRescale = 8.0f;    // log2 units
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__global__ void __launch_bounds__(kThreads, 1)
+attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_kr,
+              const __grid_constant__ CUtensorMap map_v, const uint16_t* __restrict__ q_nope,
+              const uint16_t* __restrict__ q_rope, uint16_t* __restrict__ out, float* __restrict__ lse, ChunkPlan plan,
+              int H, int h0, int64_t cap, float sl2, int32_t* err_word) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hh = blockIdx.y, h = h0 + hh;
+  auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlots);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffSlots + 4);
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) report_error(err_word, MLA_ERR_CUDA);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(bar(KF0 + i), 1);
+      mbar_init(bar(KE0 + i), 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(bar(VF0 + i), 1);
+      mbar_init(bar(VE0 + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(QF0 + i), 128);
+      mbar_init(bar(SF0 + i), 1);
+      mbar_init(bar(PF0 + i), 128);
+      mbar_init(bar(OF0 + i), 1);
+    }
+    mbar_init(bar(MD), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // the work item: rows [q0, q0 + 256) of sequence b; the tiles' steps over the keys
+  int4 item = make_int4(-1, 0, 0, 0);
+  if ((int)blockIdx.x < plan.hdr[0]) item = plan.item[blockIdx.x];
+  const int b = item.x, q0 = item.y, n = item.z, c0 = item.w;
+  const int L = b >= 0 ? plan.len_eff[b] : 0;
+  const int64_t k0 = b >= 0 ? plan.pstart[b] : 0;  // first expanded row of the sequence
+  const bool two = n - q0 > 128;
+  auto steps = [&](int x) {  // of tile x: up to the last token that its last row sees
+    if (b < 0 || (x == 1 && !two)) return 0;
+    return (L - n + min(q0 + 128 * (x + 1), n) + kKvTile - 1) / kKvTile;
+  };
+  const int n0 = steps(0), n1 = steps(1), nkv = max(n0, n1);
+
+  if (warp == 8) {
+    if (lane == 0 && nkv > 0) {
+      prefetch_tmap(&map_k);
+      prefetch_tmap(&map_kr);
+      prefetch_tmap(&map_v);
+      const uint64_t keep = policy_evict_last();
+      bool ok = true;
+      int ki = 0, vi = 0;
+      for (int j = 0; j < nkv && ok; ++j) {
+        const int row = (int)(k0 + (int64_t)j * kKvTile), hrow = (int)((int64_t)hh * cap + row);
+        for (int s = 0; s < 3; ++s, ++ki) {
+          const int st = ki % kKStages;
+          if (ki >= kKStages && !wait_phase(bar(KE0 + st), (uint32_t)((ki / kKStages - 1) & 1), abort_flag, err_word)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(KF0 + st), kSlab);
+          if (s < 2)
+            tma_load_2d(sbase + kOffK + st * kSlab, &map_k, bar(KF0 + st), 64 * s, hrow, keep);
+          else
+            tma_load_2d(sbase + kOffK + st * kSlab, &map_kr, bar(KF0 + st), kDC, row, keep);
+        }
+        for (int s = 0; s < 2 && ok; ++s, ++vi) {
+          const int st = vi % kVStages;
+          if (vi >= kVStages && !wait_phase(bar(VE0 + st), (uint32_t)((vi / kVStages - 1) & 1), abort_flag, err_word)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sbase + kOffV + st * kSlab;
+          mbar_arrive_expect_tx(bar(VF0 + st), kSlab);
+          tma_load_2d(dst, &map_v, bar(VF0 + st), 0, hrow + 64 * s, keep);
+          tma_load_2d(dst + kVBox, &map_v, bar(VF0 + st), 64, hrow + 64 * s, keep);
+        }
+      }
+      if (*abort_flag) {  // let the copies in flight land before the CTA can exit
+        const long long t0 = clock64();
+        for (int i = ki > kKStages ? ki - kKStages : 0; i < ki; ++i)
+          while (!mbar_try_wait(bar(KF0 + i % kKStages), (uint32_t)((i / kKStages) & 1)) &&
+                 clock64() - t0 < kWaitLimitCycles) {
+          }
+        for (int i = vi > kVStages ? vi - kVStages : 0; i < vi; ++i)
+          while (!mbar_try_wait(bar(VF0 + i % kVStages), (uint32_t)((i / kVStages) & 1)) &&
+                 clock64() - t0 < kWaitLimitCycles) {
+          }
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0 && nkv > 0) {
+      constexpr uint32_t kIdC = idesc_f16(128, 128, false, false), kIdR = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kIdV = idesc_f16(128, 128, false, true);
+      auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
+      const uint64_t d0 = smem_desc(0, 16, 1024, kSwizzle128B);
+      const uint64_t dv = smem_desc(0, kVBox, 1024, kSwizzle128B);
+      bool ok = true;
+      // S of tile x = Q K^T of step j; `last`: no other tile reads these slabs
+      auto scores = [&](int x, int j, bool last) {
+        for (int s = 0; s < 3 && ok; ++s) {
+          const int i = 3 * j + s, st = i % kKStages;
+          ok = wait_phase(bar(KF0 + st), (uint32_t)((i / kKStages) & 1), abort_flag, err_word);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t ad = d0 + da(sbase + (3 * x + s) * kSlab), bd = d0 + da(sbase + kOffK + st * kSlab);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tmem + kTmS + 128 * x, ad + 2 * k, bd + 2 * k, s < 2 ? kIdC : kIdR, (s > 0 || k > 0) ? 1u : 0u);
+          if (last) mma_commit(bar(KE0 + st));
+        }
+        mma_commit(bar(SF0 + x));
+      };
+      auto values = [&](int x, int j, bool last) {
+        ok = wait_phase(bar(PF0 + x), (uint32_t)(j & 1), abort_flag, err_word);
+        for (int s = 0; s < 2 && ok; ++s) {
+          const int i = 2 * j + s, st = i % kVStages;
+          ok = wait_phase(bar(VF0 + st), (uint32_t)((i / kVStages) & 1), abort_flag, err_word);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t bd = dv + da(sbase + kOffV + st * kSlab);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(tmem + kTmO + 128 * x, tmem + kTmS + 128 * x + 32 * s + 8 * k, bd + (k * 2048 >> 4), kIdV,
+                   (j > 0 || s > 0 || k > 0) ? 1u : 0u);
+          if (last) mma_commit(bar(VE0 + st));
+        }
+      };
+      ok = wait_phase(bar(QF0), 0, abort_flag, err_word);
+      if (ok) scores(0, 0, !two);
+      if (ok && two) {
+        ok = wait_phase(bar(QF0 + 1), 0, abort_flag, err_word);
+        if (ok) scores(1, 0, true);
+      }
+      // tile 1, when there is one, takes at least as many steps as tile 0
+      for (int j = 0; j < nkv && ok; ++j) {
+        if (j < n0) {
+          values(0, j, !two);
+          if (ok && j + 1 < n0) scores(0, j + 1, !two);
+          if (ok && j + 1 == n0) mma_commit(bar(OF0));
+        }
+        if (ok && j < n1) {
+          values(1, j, true);
+          if (ok && j + 1 < n1) scores(1, j + 1, true);
+          if (ok && j + 1 == n1) mma_commit(bar(OF0 + 1));
+        }
+      }
+      mma_commit(bar(MD));
+      wait_mmas(bar(MD));
+    }
+  } else if (nkv > 0) {
+    const int x = warp >> 2, tid = threadIdx.x & 127, row = tid;  // row == tensor-memory lane
+    const int nx = x ? n1 : n0, r0 = q0 + 128 * x;
+    if (nx > 0) {
+      // the tile's queries: content as fp16 (exact for bf16 values of normal fp16
+      // size), position as it is, into the swizzled slabs
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int i = tid; i < 128 * 16; i += 128) {
+        const int r = i >> 4, ch = i & 15;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r0 + r < n) w = __ldg(reinterpret_cast<const uint4*>(q_nope + ((size_t)(c0 + r0 + r) * H + h) * kDNope) + ch);
+        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+        uint32_t f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          f[k] = cvt_f16x2(bf16_lo(e[k]), bf16_hi(e[k]));
+          top = max(top, max((e[k] << 16) & 0x7FFFFFFFu, e[k] & 0x7FFF0000u));
+        }
+        st_shared_v4(sbase + (3 * x + (ch >> 3)) * kSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
+      }
+      if (top >= 0x477FF000u && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
+#pragma unroll 4
+      for (int i = tid; i < 128 * 8; i += 128) {
+        const int r = i >> 3, ch = i & 7;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r0 + r < n) w = __ldg(reinterpret_cast<const uint4*>(q_rope + ((size_t)(c0 + r0 + r) * H + h) * kDR) + ch);
+        st_shared_v4(sbase + (3 * x + 2) * kSlab + r * 128 + ((ch ^ (r & 7)) << 4), w.x, w.y, w.z, w.w);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(QF0 + x));
+
+      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t tS = tmem + kTmS + 128 * x + lane_off, tO = tmem + kTmO + 128 * x + lane_off;
+      const int first_seen = L - n + r0 + 1;                       // tokens that the tile's first row sees
+      const int seen = L - n + min(r0 + row, n - 1) + 1;           // tokens that this row sees
+      float ref = -INFINITY, sum = 0.f;
+      bool ok = true;
+      for (int j = 0; j < nx; ++j) {
+        // the warp leaves together: the tensor-memory loads below need every lane
+        ok = __all_sync(0xffffffffu, wait_phase(bar(SF0 + x), (uint32_t)(j & 1), abort_flag, err_word));
+        if (!ok) break;
+        tc_fence_after();
+        float z[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(z + 32 * c));
+        tmem_wait_ld();
+        if ((j + 1) * kKvTile > first_seen) {
+          const int lim = seen - j * kKvTile;
+#pragma unroll
+          for (int c = 0; c < 128; ++c) z[c] = c < lim ? z[c] : -INFINITY;
+        }
+        float m4[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+        for (int c = 4; c < 128; ++c) m4[c & 3] = fmaxf(m4[c & 3], z[c]);
+        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // all MMAs issued before this step's scores are done, the last P V among them
+        if (__any_sync(0xffffffffu, mx * sl2 > ref * sl2 + kRescale)) {
+          const float up = fmaxf(ref, mx);
+          if (j > 0) {
+            const float f = ref == up ? 1.f : ex2((ref - up) * sl2);
+            sum *= f;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+              tmem_st32(tO + c, o);
+            }
+          }
+          ref = up;
+        }
+        const float off = kBias - (ref == -INFINITY ? 0.f : ref * sl2);
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            const float a = ex2(fmaf(z[c + 2 * q], sl2, off)), e = ex2(fmaf(z[c + 2 * q + 1], sl2, off));
+            s4[q & 1] += a;
+            s4[2 + (q & 1)] += e;
+            p[q] = cvt_f16x2(a, e);
+          }
+          tmem_st16(tS + c / 2, p);
+        }
+        sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(PF0 + x));
+      }
+      if (ok && __all_sync(0xffffffffu, wait_phase(bar(OF0 + x), 0, abort_flag, err_word))) {
+        tc_fence_after();
+        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays NaN
+        const bool live = r0 + row < n;
+        const size_t at = (size_t)(c0 + r0 + row) * H + h;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t o[32], w[16];
+          tmem_ld32(tO + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            w[q] = cvt_bf16x2(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
+          if (live) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              reinterpret_cast<uint4*>(out + at * kDV + c)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          }
+        }
+        if (lse && live) lse[at] = sum > 0.f ? (ref * sl2 - kBias + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const uint16_t* q_rope, uint16_t* out,
+                          float* lse, int B, int T, int H, int h0, int heads, int64_t cap, float scale,
+                          int32_t* err_word, cudaStream_t s) {
+  CUtensorMap mk, mr, mv;
+  const uint64_t dk[2] = {kDNope, (uint64_t)heads * cap}, sk[1] = {kDNope * 2};
+  const uint64_t dr[2] = {kRow, (uint64_t)cap}, sr[1] = {kRow * 2};
+  const uint32_t bk[2] = {64, 128}, bv[2] = {64, 64};
+  if (!make_tmap(&mk, plan.k, 2, dk, sk, bk, 128) || !make_tmap(&mr, plan.rows, 2, dr, sr, bk, 128) ||
+      !make_tmap(&mv, plan.v, 2, dk, sk, bv, 128))
+    return cudaErrorInvalidValue;
+  cudaError_t e = smem_limit<attend_kernel>(kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attend_kernel, dim3(chunk_max_items(B, T), heads), dim3(kThreads), kSmem, s, mk, mr, mv, q_nope,
+                    q_rope, out, lse, plan, H, h0, cap, scale * 1.4426950408889634f, err_word);
+}
+
+}  // namespace mla

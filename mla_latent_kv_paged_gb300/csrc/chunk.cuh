@@ -1,0 +1,134 @@
+// Declarations shared by the kernels that work on a ragged chunk of new tokens
+// (append_chunk, read_kv, attend_chunk): sequence b owns rows cu[b] .. cu[b+1]
+// of the row arrays; rows at and past cu[B] belong to no sequence.
+#pragma once
+
+#include "mla_internal.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+
+constexpr int kMaxChunkRows = 1 << 20;  // rows of one call
+constexpr int kQTile = 256;             // query rows of one attention work item (two MMA tiles of 128)
+constexpr int kKvTile = 128;            // cached tokens of one attention step; padding of the expanded rows
+
+// The sequence that owns row t, or -1. Safe for any contents of cu: the search
+// stays inside [0, B) and its result is checked against its own bounds.
+__device__ inline int row_sequence(const int32_t* __restrict__ cu, int B, int t) {
+  int lo = 0, hi = B - 1;  // largest b with cu[b] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(cu + mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1) ? lo : -1;
+}
+
+// The MMA issuer's last act: every MMA it issued is done (a wait that gave up
+// elsewhere included) before the CTA gives its tensor memory back. Bounded.
+__device__ __forceinline__ void wait_mmas(uint32_t bar) {
+  const long long t0 = clock64();
+  while (!sm100::mbar_try_wait(bar, 0) && clock64() - t0 < sm100::kWaitLimitCycles) {
+  }
+}
+
+// ---------------------------------------------------------------- workspaces
+// The arrays start at the first 256-byte boundary of the caller's workspace (the
+// sizes below include the room for it).
+inline char* workspace_base(void* p) {
+  return reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(p) + 255) & ~(uintptr_t)255);
+}
+// Expanded form. cap: rows of the expanded cache (a multiple of kKvTile).
+struct ChunkPlan {
+  int32_t* hdr;      // [64] hdr[0] = query items, hdr[1] = expanded rows in use
+  int32_t* pstart;   // [B + 1] first expanded row of each sequence, a multiple of kKvTile
+  int32_t* len_eff;  // [B] context lengths in use (clamped; 0 without new rows)
+  int4* item;        // [max_items] {sequence, first query row in it, rows of the sequence, its first row}
+  uint16_t* rows;    // [cap][576] bf16, the sequences' cache rows; zeros from a context's end to its padding
+  uint16_t* k;       // [heads][cap][128] fp16 keys without position
+  uint16_t* v;       // [heads][cap][128] fp16 values
+};
+
+inline int64_t chunk_cap(int64_t max_tokens, int B) {
+  const int64_t c = max_tokens + (int64_t)(kKvTile - 1) * B;
+  return (c + kKvTile - 1) / kKvTile * kKvTile;
+}
+inline int chunk_max_items(int B, int T) { return T / kQTile + (B < T ? B : T); }
+
+inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t cap, ChunkPlan* p) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  const size_t o_hdr = take(64 * 4), o_ps = take((size_t)(B + 1) * 4), o_le = take((size_t)B * 4);
+  const size_t o_it = take((size_t)chunk_max_items(B, T) * 16);
+  const size_t o_r = take((size_t)cap * kRow * 2);
+  const size_t o_k = take((size_t)heads * cap * kDNope * 2), o_v = take((size_t)heads * cap * kDV * 2);
+  if (base && p) {
+    char* c = workspace_base(base);
+    p->hdr = reinterpret_cast<int32_t*>(c + o_hdr);
+    p->pstart = reinterpret_cast<int32_t*>(c + o_ps);
+    p->len_eff = reinterpret_cast<int32_t*>(c + o_le);
+    p->item = reinterpret_cast<int4*>(c + o_it);
+    p->rows = reinterpret_cast<uint16_t*>(c + o_r);
+    p->k = reinterpret_cast<uint16_t*>(c + o_k);
+    p->v = reinterpret_cast<uint16_t*>(c + o_v);
+  }
+  return off + 256;
+}
+
+// Absorbed form: each new token is a decode sequence of its own.
+struct ChunkRows {
+  int32_t* hdr;      // [64] hdr[0] = rows that belong to a sequence
+  int32_t* len;      // [T] tokens the row attends (1 for rows of no sequence)
+  int32_t* seq_row;  // [T] block-table row (-1 for rows of no sequence)
+  uint16_t* q_abs;   // [T][H][576] bf16
+  uint16_t* u;       // [T][H][512] bf16
+  void* decode_ws;   // workspace of the decode over T sequences
+};
+
+inline size_t chunk_rows_layout(void* base, int T, int H, int G, ChunkRows* p) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  const size_t o_hdr = take(64 * 4), o_l = take((size_t)T * 4), o_s = take((size_t)T * 4);
+  const size_t o_q = take((size_t)T * H * kRow * 2), o_u = take((size_t)T * H * kDC * 2);
+  const size_t o_d = take(plan_layout(nullptr, T, 1, H, G, nullptr));
+  if (base && p) {
+    char* c = workspace_base(base);
+    p->hdr = reinterpret_cast<int32_t*>(c + o_hdr);
+    p->len = reinterpret_cast<int32_t*>(c + o_l);
+    p->seq_row = reinterpret_cast<int32_t*>(c + o_s);
+    p->q_abs = reinterpret_cast<uint16_t*>(c + o_q);
+    p->u = reinterpret_cast<uint16_t*>(c + o_u);
+    p->decode_ws = c + o_d;
+  }
+  return off + 256;
+}
+
+// ---------------------------------------------------------------- launchers
+cudaError_t launch_read_kv(const void* cache, const float* fp8_scales, const int32_t* block_table,
+                           const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* out, int B,
+                           int n_rows, int num_pages, int page_size, int max_pages, int32_t* err_word,
+                           cudaStream_t s);
+size_t append_chunk_workspace_bytes(int T, int d_model);
+cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
+                                const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                                int d_model, int num_pages, int page_size, int max_pages, double theta,
+                                void* workspace, int32_t* err_word, cudaStream_t s);
+cudaError_t launch_chunk_plan(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
+                              int64_t max_total, const ChunkPlan& plan, int32_t* err_word, cudaStream_t s);
+cudaError_t launch_chunk_rows(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
+                              const ChunkRows& rows, int32_t* err_word, cudaStream_t s);
+// keys and values of heads [h0, h0 + heads) of every expanded row
+cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uint16_t* w_uv, int H, int h0, int heads,
+                          int64_t cap, int32_t* err_word, cudaStream_t s);
+cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const uint16_t* q_rope, uint16_t* out,
+                          float* lse, int B, int T, int H, int h0, int heads, int64_t cap, float scale,
+                          int32_t* err_word, cudaStream_t s);
+
+}  // namespace mla

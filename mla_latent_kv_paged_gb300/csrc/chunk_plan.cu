@@ -1,0 +1,134 @@
+// Plans of a ragged chunk of new tokens over the paged cache, from seq_lens and
+// cu on the device (so a captured graph follows their contents).
+//   chunk_plan_kernel  expanded form: where each sequence's expanded rows start
+//                      (contexts padded to 128 rows) and the list of query items
+//                      (256 rows of one sequence each, the last rows of a
+//                      sequence first: they see the most tokens, so the longest
+//                      work starts first)
+//   chunk_rows_kernel  absorbed form: every new row as a decode sequence of its own
+// Integer work on a few thousand numbers, one block: bound by launch and barrier
+// latency.
+#include "chunk.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Exclusive scan over the block's threads of a 64-bit value; *total = the sum.
+__device__ int64_t block_scan(int64_t v, int64_t* total) {
+  __shared__ int64_t sums[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  __syncthreads();
+  *total = all;
+  return before + x - v;
+}
+
+// New rows [*c0, *c0 + n) and context length of sequence b, clamped to the row
+// array and the block table; anything out of range is reported.
+__device__ int sequence_of_chunk(const int32_t* seq_lens, const int32_t* cu, int b, int T, int max_tokens, int* c0,
+                                 int* len, int32_t* err_word) {
+  const int a = cu[b], e = cu[b + 1];
+  const int first = min(max(a, 0), T), end = min(max(e, first), T);
+  const int n = min(end - first, max_tokens);
+  int L = seq_lens[b];
+  if (a != first || e != first + n || ((L < n || L > max_tokens) && n > 0)) report_error(err_word, MLA_ERR_BOUNDS);
+  L = min(max(L, n), max_tokens);
+  *c0 = first;
+  *len = n > 0 ? L : 0;  // a sequence without new rows takes no part
+  return n;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+chunk_plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu, int B, int T, int max_tokens,
+                  int64_t max_total, int max_items, ChunkPlan plan, int32_t* err_word) {
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
+  const int tid = threadIdx.x;
+  int64_t row_base = 0, item_base = 0, token_base = 0;
+  for (int b0 = 0; b0 < B; b0 += kThreads) {
+    const int b = b0 + tid;
+    int c0 = 0, L = 0, n = 0;
+    if (b < B) n = sequence_of_chunk(seq_lens, cu, b, T, max_tokens, &c0, &L, err_word);
+    int64_t rows = (int64_t)(L + kKvTile - 1) / kKvTile * kKvTile;
+    int items = (n + kQTile - 1) / kQTile;
+    int64_t row_sum, item_sum, token_sum;
+    const int64_t t0 = token_base + block_scan(L, &token_sum);
+    // a sequence that passes the tokens (or, with overlapping rows, the items) the
+    // caller announced is left out: no expanded rows, no work
+    const bool fits = t0 + L <= max_total;
+    if (!fits) rows = 0;
+    const int64_t r0 = row_base + block_scan(rows, &row_sum);
+    const int64_t i0 = item_base + block_scan(items, &item_sum);
+    if (b < B) {
+      if (!fits || i0 + items > max_items) report_error(err_word, MLA_ERR_BOUNDS);
+      plan.pstart[b] = (int)r0;
+      plan.len_eff[b] = fits ? L : 0;
+      for (int k = 0; k < items; ++k)
+        if (i0 + k < max_items)
+          plan.item[i0 + k] = make_int4(fits ? b : -1, (items - 1 - k) * kQTile, n, c0);
+    }
+    row_base += row_sum;
+    token_base += token_sum;
+    item_base += item_sum;
+  }
+  if (tid == 0) {
+    plan.pstart[B] = (int)row_base;
+    plan.hdr[0] = (int)min(item_base, (int64_t)max_items);
+    plan.hdr[1] = (int)row_base;
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+chunk_rows_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu, int B, int T, int max_tokens,
+                  ChunkRows rows, int32_t* err_word) {
+  sm100::grid_dependency_wait();
+  const int t = blockIdx.x * kThreads + threadIdx.x;
+  if (t < T) {
+    const int b = row_sequence(cu, B, t);
+    int len = 1, row = -1;
+    if (b >= 0) {
+      int c0, L;
+      const int n = sequence_of_chunk(seq_lens, cu, b, T, max_tokens, &c0, &L, err_word);
+      const int j = t - c0;
+      if (j >= 0 && j < n) {
+        len = L - n + j + 1;
+        row = b;
+      }
+    }
+    rows.len[t] = len;
+    rows.seq_row[t] = row;
+  }
+  if (t == 0) rows.hdr[0] = min(max(cu[B], 0), T);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_plan(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
+                              int64_t max_total, const ChunkPlan& plan, int32_t* err_word, cudaStream_t s) {
+  return launch_pdl(chunk_plan_kernel, dim3(1), dim3(kThreads), 0, s, seq_lens, cu, B, T, max_tokens, max_total,
+                    chunk_max_items(B, T), plan, err_word);
+}
+
+cudaError_t launch_chunk_rows(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
+                              const ChunkRows& rows, int32_t* err_word, cudaStream_t s) {
+  return launch_pdl(chunk_rows_kernel, dim3((T + kThreads - 1) / kThreads), dim3(kThreads), 0, s, seq_lens, cu, B, T,
+                    max_tokens, rows, err_word);
+}
+
+}  // namespace mla

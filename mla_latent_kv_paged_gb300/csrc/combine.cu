@@ -23,7 +23,8 @@ constexpr int kCPT = kCols / 2;  // columns per thread
 constexpr int kKB = 2;         // partials whose loads are in flight together
 
 __global__ void __launch_bounds__(kThreads)
-combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __restrict__ lse_out) {
+combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __restrict__ lse_out,
+               const int32_t* __restrict__ rows_live) {
   __shared__ uint32_t tile[128][kCols / 2 + 1];  // bf16 pairs, padded row
   // The next kernel (the up-projection) may start now and load its weights
   // while the decode kernel's last CTAs and this merge run; it reads u only
@@ -98,9 +99,14 @@ combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __res
           }
         }
       }
+    } else {  // no finite partial: NaN if one of them is
+      for (int k = k0; k < k1; ++k) {
+        const float l = lse_of(k);
+        if (l != l) wsum = l;
+      }
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum > 0.f ? 1.f / wsum : (wsum == 0.f ? 0.f : wsum);  // a NaN partial stays NaN
 #pragma unroll
   for (int c = 0; c < kCPT / 2; ++c)
     tile[h][(kCPT / 2) * part + c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
@@ -115,16 +121,16 @@ combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __res
     o.w = tile[row][4 * q + 3];
     *reinterpret_cast<uint4*>(u + ((size_t)bj * H + row) * kDC + blockIdx.y * kCols + 8 * q) = o;
   }
-  if (lse_out && blockIdx.y == 0 && part == 0 && h < H)
-    lse_out[(size_t)bj * H + h] = wsum > 0.f ? m + logf(wsum) : -INFINITY;
+  if (lse_out && blockIdx.y == 0 && part == 0 && h < H && (!rows_live || bj < *rows_live))
+    lse_out[(size_t)bj * H + h] = wsum > 0.f ? m + logf(wsum) : (wsum == 0.f ? -INFINITY : wsum);
 }
 
 }  // namespace
 
 cudaError_t launch_combine(const Plan& plan, int B, int n_q, int H, uint16_t* u, float* lse,
-                           cudaStream_t s) {
+                           cudaStream_t s, const int32_t* rows_live) {
   dim3 grid(B * n_q, kDC / kCols);
-  return launch_pdl(combine_kernel, grid, dim3(kThreads), 0, s, plan, n_q, H, u, lse);
+  return launch_pdl(combine_kernel, grid, dim3(kThreads), 0, s, plan, n_q, H, u, lse, rows_live);
 }
 
 }  // namespace mla

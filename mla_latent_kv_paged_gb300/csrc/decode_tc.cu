@@ -264,17 +264,20 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
     const int tile_mask = (1 << tile_shift) - 1;
     struct Cursor {
       int it, pg, pg1, base, id_l, pg0, seq;  // pg0, seq: the piece's first tile and its sequence
-      size_t row;  // block-table row of the current range
+      int64_t row;  // block-table row of the current range (its first entry), or < 0: page 0
+    };
+    auto table_row = [&](int seq) -> int64_t {
+      return (int64_t)(plan.seq_row ? plan.seq_row[seq] : seq) * max_pages;
     };
     auto cur_load = [&](Cursor& c) {
       const int mine = c.base + lane;
-      c.id_l = mine < c.pg1 ? block_table[c.row + (mine >> tile_shift)] : 0;
+      c.id_l = mine < c.pg1 && c.row >= 0 ? block_table[c.row + (mine >> tile_shift)] : 0;
     };
     auto cur_init = [&](Cursor& c, int it) {
       c.it = it;
       if (it < it1) {
         c.seq = plan.item_seq[it];
-        c.row = (size_t)c.seq * max_pages;
+        c.row = table_row(c.seq);
         c.pg = c.base = c.pg0 = plan.item_tile0[it];
         c.pg1 = plan.item_tile1[it];
         cur_load(c);
@@ -296,7 +299,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
       ld.it = d0.x;
       if (d0.x < it1) {
         ld.seq = d0.y;
-        ld.row = (size_t)d0.y * max_pages;
+        ld.row = table_row(d0.y);
         ld.pg = ld.base = ld.pg0 = d0.z;
         ld.pg1 = d0.w;
         cur_load(ld);
@@ -918,7 +921,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             tc_fence_before();
             mbar_arrive(bar(OFREE));
             if (rank == 0 && row < H)
-              plan.lse_part[orow] = l_tot > 0.f ? (m_new + log2f(l_tot)) * kLn2 : -INFINITY;
+              // a chunk's row (seq_row) keeps a sum that is not a number, so that the
+              // merge passes it on
+              plan.lse_part[orow] =
+                  l_tot > 0.f ? (m_new + log2f(l_tot)) * kLn2 : (plan.seq_row && l_tot != l_tot ? l_tot : -INFINITY);
           }
         }
         if (ntiles >= 2) ++lg_n;

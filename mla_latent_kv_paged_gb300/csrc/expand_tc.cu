@@ -1,0 +1,230 @@
+// Keys and values of every head expanded from the cached latents, for the
+// attention of a chunk of new tokens (attend_tc.cu):
+//   k[h][s][i] = sum_c row_s[c] w_uk[h][i][c]      v[h][s][i] = sum_c row_s[c] w_uv[h][i][c]
+// (Huny's Dev Blog "MLA 아키텍처 해부" section 1.2, k^C = c W^UK, v^C = c W^UV),
+// bf16 operands, fp32 sums, rounded once to fp16: three more mantissa bits than
+// bf16 for the two products that follow, |value| < 65520 (beyond: MLA_ERR_RANGE).
+//
+// Tensor-bound: 2 x 512 x 256 flop per (token, head). A CTA keeps 128 tokens'
+// latents in shared memory (128 KB) and streams the weights of consecutive heads
+// past them (a [256 = 128 of W_UK, 128 of W_UV][32] box per ring slot, N = 256
+// MMAs), so each unit of work reads its 256 KB of weights from L2 and nothing
+// else; two accumulators in tensor memory let the write-out of one head run
+// under the MMAs of the next. The units (token tile, head) are dealt out as
+// equal contiguous runs, one run per CTA.
+//
+// A value row that is not finite is written as zeros, with a NaN in its key row:
+// the queries that see the token get NaN, those that do not are untouched (a
+// zero weight times a NaN value would reach them).
+#include "chunk.cuh"
+#include "sm100.cuh"
+
+namespace mla {
+namespace {
+
+using namespace sm100;
+
+constexpr int kStages = 6;
+constexpr int kKB = kDC / 32;                       // 16 boxes of 32 latent columns
+constexpr uint32_t kASlab = 128 * 128;              // [128 tokens][64 columns], 128B swizzle
+constexpr uint32_t kABytes = 8 * kASlab;
+constexpr uint32_t kBHalf = 128 * 64, kBBytes = 2 * kBHalf;  // [256 rows][32 columns], 64B swizzle
+constexpr uint32_t kOffB = kABytes, kOffBar = kOffB + kStages * kBBytes;
+enum { FULL0 = 0, EMPTY0 = FULL0 + kStages, AF = EMPTY0 + kStages, AE, DF0, DE0 = DF0 + 2, MD = DE0 + 2, kBars };
+constexpr uint32_t kOffSlots = kOffBar + 8 * kBars;
+constexpr uint32_t kSmem = kOffSlots + 16;
+static_assert(kSmem <= 232448, "shared memory budget");
+constexpr int kThreads = 192;  // warps 0..3 write-out, 4 producer, 5 MMA issuer
+constexpr uint32_t kF16Limit = 0x477FF000u;  // 65520.0f: from here on fp16 rounds to infinity
+
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// 128 accumulator columns of one token as fp16 to dst; the largest |value| as bits.
+__device__ __forceinline__ uint32_t write_row(uint32_t taddr, uint16_t* dst) {
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int c0 = 0; c0 < 128; c0 += 32) {
+    uint32_t r[32], w[16];
+    tmem_ld32(taddr + c0, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int q = 0; q < 32; ++q) top = max(top, r[q] & 0x7FFFFFFFu);
+#pragma unroll
+    for (int q = 0; q < 16; ++q) w[q] = cvt_f16x2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1]));
+    st_global_32(dst + c0, w);
+    st_global_32(dst + c0 + 16, w + 8);
+  }
+  return top;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constant__ CUtensorMap map_uk,
+              const __grid_constant__ CUtensorMap map_uv, ChunkPlan plan, int h0, int heads, int64_t cap,
+              int32_t* err_word) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlots);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffSlots + 4);
+  if (sbase & 1023u) {
+    if (threadIdx.x == 0) report_error(err_word, MLA_ERR_CUDA);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(FULL0 + i), 1);
+      mbar_init(bar(EMPTY0 + i), 1);
+    }
+    mbar_init(bar(AF), 1);
+    mbar_init(bar(AE), 1);
+    mbar_init(bar(MD), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(DF0 + i), 1);
+      mbar_init(bar(DE0 + i), 128);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 5) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int64_t units = (int64_t)(plan.hdr[1] / kKvTile) * heads;
+  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+
+  if (warp == 4) {
+    if (lane == 0) {
+      prefetch_tmap(&map_rows);
+      prefetch_tmap(&map_uk);
+      prefetch_tmap(&map_uv);
+      const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
+      bool ok = true;
+      int it = 0, loads = 0;
+      for (int64_t u = u0; u < u1 && ok; ++u) {
+        const int m = (int)(u / heads), h = h0 + (int)(u % heads);
+        if (u == u0 || u % heads == 0) {  // the next 128 tokens, once the MMAs on the last ones are done
+          if (loads > 0 && !wait_phase(bar(AE), (uint32_t)((loads - 1) & 1), abort_flag, err_word)) break;
+          mbar_arrive_expect_tx(bar(AF), kABytes);
+          for (int c = 0; c < 8; ++c) tma_load_2d(sbase + c * kASlab, &map_rows, bar(AF), 64 * c, m * 128, stream);
+          ++loads;
+        }
+        for (int kb = 0; kb < kKB; ++kb, ++it) {
+          const int st = it % kStages;
+          if (it >= kStages && !wait_phase(bar(EMPTY0 + st), (uint32_t)((it / kStages - 1) & 1), abort_flag, err_word)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = sbase + kOffB + st * kBBytes;
+          mbar_arrive_expect_tx(bar(FULL0 + st), kBBytes);
+          tma_load_2d(dst, &map_uk, bar(FULL0 + st), 32 * kb, h * 128, keep);
+          tma_load_2d(dst + kBHalf, &map_uv, bar(FULL0 + st), 32 * kb, h * 128, keep);
+        }
+      }
+      if (*abort_flag) {  // let the copies in flight land before the CTA can exit
+        for (int i = it > kStages ? it - kStages : 0; i < it; ++i) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(bar(FULL0 + i % kStages), (uint32_t)((i / kStages) & 1)) &&
+                 clock64() - t0 < kWaitLimitCycles) {
+          }
+        }
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16(128, 256, false, false);
+      auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
+      const uint64_t ad0 = smem_desc(0, 16, 1024, kSwizzle128B) + da(sbase);
+      const uint64_t bd0 = smem_desc(0, 16, 512, kSwizzle64B);
+      bool ok = true;
+      int it = 0, loads = 0, n = 0;
+      for (int64_t u = u0; u < u1 && ok; ++u, ++n) {
+        const int buf = n & 1;
+        if (u == u0 || u % heads == 0) {
+          if (!wait_phase(bar(AF), (uint32_t)(loads & 1), abort_flag, err_word)) break;
+          ++loads;
+        }
+        if (n >= 2 && !wait_phase(bar(DE0 + buf), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, err_word)) break;
+        for (int kb = 0; kb < kKB; ++kb, ++it) {
+          const int st = it % kStages;
+          if (!wait_phase(bar(FULL0 + st), (uint32_t)((it / kStages) & 1), abort_flag, err_word)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = ad0 + (((kb >> 1) * kASlab + (kb & 1) * 64) >> 4);
+          const uint64_t bd = bd0 + da(sbase + kOffB + st * kBBytes);
+          mma_ss(tmem + 256 * buf, ad, bd, idesc, kb > 0 ? 1u : 0u);
+          mma_ss(tmem + 256 * buf, ad + 2, bd + 2, idesc, 1u);
+          mma_commit(bar(EMPTY0 + st));
+        }
+        if (!ok) break;
+        mma_commit(bar(DF0 + buf));
+        if ((u + 1) % heads == 0 && u + 1 < u1) mma_commit(bar(AE));
+      }
+      mma_commit(bar(MD));
+      wait_mmas(bar(MD));
+    }
+  } else {
+    int n = 0;
+    for (int64_t u = u0; u < u1; ++u, ++n) {
+      const int m = (int)(u / heads), hh = (int)(u % heads), buf = n & 1;
+      if (!__all_sync(0xffffffffu, wait_phase(bar(DF0 + buf), (uint32_t)((n >> 1) & 1), abort_flag, err_word))) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + 256 * buf + ((uint32_t)(warp * 32) << 16);
+      const int64_t at = ((int64_t)hh * cap + m * 128 + warp * 32 + lane) * 128;
+      uint16_t *kd = plan.k + at, *vd = plan.v + at;
+      const uint32_t vtop = write_row(taddr + 128, vd);
+      const uint32_t ktop = write_row(taddr, kd);
+      tc_fence_before();
+      mbar_arrive(bar(DE0 + buf));
+      if (max(vtop, ktop) >= kF16Limit) {
+        if ((vtop >= kF16Limit && vtop < 0x7F800000u) || (ktop >= kF16Limit && ktop < 0x7F800000u))
+          report_error(err_word, MLA_ERR_RANGE);
+        if (vtop >= kF16Limit) {
+          for (int q = 0; q < 16; ++q) reinterpret_cast<uint4*>(vd)[q] = make_uint4(0, 0, 0, 0);
+          kd[0] = 0x7FFF;  // NaN
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uint16_t* w_uv, int H, int h0, int heads,
+                          int64_t cap, int32_t* err_word, cudaStream_t s) {
+  CUtensorMap mr, mk, mv;
+  const uint64_t dr[2] = {kRow, (uint64_t)cap}, sr[1] = {kRow * 2};
+  const uint64_t dw[2] = {kDC, (uint64_t)H * 128}, sw[1] = {kDC * 2};
+  const uint32_t br[2] = {64, 128}, bw[2] = {32, 128};
+  if (!make_tmap(&mr, plan.rows, 2, dr, sr, br, 128) || !make_tmap(&mk, w_uk, 2, dw, sw, bw, 64) ||
+      !make_tmap(&mv, w_uv, 2, dw, sw, bw, 64))
+    return cudaErrorInvalidValue;
+  cudaError_t e = smem_limit<expand_kernel>(kSmem);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int64_t units = cap / kKvTile * heads;
+  return launch_pdl(expand_kernel, dim3((unsigned)(units < sms ? units : sms)), dim3(kThreads), kSmem, s, mr, mk, mv,
+                    plan, h0, heads, cap, err_word);
+}
+
+}  // namespace mla

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "chunk.cuh"
 #include "mla_internal.cuh"
 
 using namespace mla;
@@ -327,6 +328,149 @@ mla_status mla_append_kv(const uint16_t* h, const uint16_t* w_dkr, uint16_t* cac
   return launch_status(launch_append(h, w_dkr, cache, block_table, seq_lens, B, n_q, d_model, num_pages, page_size,
                                      max_pages_per_seq, (double)rope_theta, workspace, err_word,
                                      (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------------------ chunks of new tokens
+namespace {
+bool chunk_counts_ok(int B, int T) { return B <= MLA_MAX_BATCH && T <= kMaxChunkRows; }
+// heads whose keys and values are expanded at once: all of them while those fit
+// kExpandBytes (the default workspace stays bounded on long contexts)
+constexpr int64_t kExpandBytes = (int64_t)2 << 30;
+int chunk_head_group(int H, int64_t cap) {
+  int64_t g = kExpandBytes / (cap * (kDNope + kDV) * 2);
+  if (g < 1) g = 1;
+  if (g >= H) return H;
+  const int64_t rounds = (H + g - 1) / g;
+  return (int)((H + rounds - 1) / rounds);
+}
+// Expanding costs 2 * 512 * 256 flop per (token, head) whatever the chunk;
+// absorbed attention costs 2176 flop per (query, token, head) against 640.
+constexpr int kAbsorbedRows = 128;
+int chunk_form(int form, int B, int T) {
+  if (form != MLA_CHUNK_AUTO) return form;
+  return T <= MLA_MAX_BATCH && T <= (int64_t)kAbsorbedRows * B ? MLA_CHUNK_ABSORBED : MLA_CHUNK_EXPANDED;
+}
+}  // namespace
+
+mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t* block_table,
+                       const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* rows, int B,
+                       int n_rows, int num_pages, int page_size, int max_pages_per_seq, int32_t* err_word,
+                       void* stream) {
+  if (!cache || !block_table || !seq_lens || !cu || !rows) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(cache) || !aligned16(fp8_scales) || !aligned16(block_table) || !aligned16(seq_lens) ||
+      !aligned16(first) || !aligned16(cu) || !aligned16(rows))
+    return MLA_ERR_INVALID_ARG;
+  if (B < 1 || n_rows < 1 || num_pages < 1 || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (B > MLA_MAX_BATCH || n_rows > INT32_MAX / 2 || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  return launch_status(launch_read_kv(cache, fp8_scales, block_table, seq_lens, first, cu, rows, B, n_rows, num_pages,
+                                      page_size, max_pages_per_seq, err_word, (cudaStream_t)stream));
+}
+
+size_t mla_append_chunk_workspace_bytes(int T, int d_model) {
+  if (T < 1 || T > kMaxChunkRows || d_model < 64 || d_model % 64 != 0 || d_model > 65536) return 0;
+  return append_chunk_workspace_bytes(T, d_model);
+}
+
+mla_status mla_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                            int d_model, int num_pages, int page_size, int max_pages_per_seq, float rope_theta,
+                            void* workspace, size_t workspace_bytes, int32_t* err_word, void* stream) {
+  if (!h || !w_dkr || !cache || !block_table || !seq_lens || !cu || !workspace) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(h) || !aligned16(w_dkr) || !aligned16(cache) || !aligned16(fp8_scales) || !aligned16(block_table) ||
+      !aligned16(seq_lens) || !aligned16(cu) || !aligned16(workspace))
+    return MLA_ERR_INVALID_ARG;
+  if (B < 1 || T < 1 || num_pages < 1 || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (!(rope_theta > 1.f) || rope_theta > 3.0e38f) return MLA_ERR_INVALID_ARG;
+  if (!chunk_counts_ok(B, T) || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (d_model < 64 || d_model % 64 != 0 || d_model > 65536) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (workspace_bytes < append_chunk_workspace_bytes(T, d_model)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  return launch_status(launch_append_chunk(h, w_dkr, cache, fp8_scales, block_table, seq_lens, cu, B, T, d_model,
+                                           num_pages, page_size, max_pages_per_seq, (double)rope_theta, workspace,
+                                           err_word, (cudaStream_t)stream));
+}
+
+size_t mla_attend_chunk_workspace_bytes(int B, int T, int H, int64_t max_tokens, int form) {
+  if (B < 1 || T < 1 || !chunk_counts_ok(B, T) || !heads_ok(H) || max_tokens < 1 || max_tokens > INT32_MAX / 2 ||
+      form < MLA_CHUNK_AUTO || form > MLA_CHUNK_ABSORBED)
+    return 0;
+  form = chunk_form(form, B, T);
+  if (form == MLA_CHUNK_ABSORBED) {
+    if (T > MLA_MAX_BATCH) return 0;
+    const int G = mla_decode_default_splits(1);
+    return G < 1 ? 0 : chunk_rows_layout(nullptr, T, H, G, nullptr);
+  }
+  const int64_t cap = chunk_cap(max_tokens, B);
+  return chunk_layout(nullptr, B, T, chunk_head_group(H, cap), cap, nullptr);
+}
+
+mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
+                            const uint16_t* w_uv, const void* cache, const float* fp8_scales,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                            int H, int num_pages, int page_size, int max_pages_per_seq, int64_t max_tokens,
+                            float softmax_scale, int form, uint16_t* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* err_word, void* stream) {
+  if (!q_nope || !q_rope || !w_uk || !w_uv || !cache || !block_table || !seq_lens || !cu || !out || !workspace)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_nope) || !aligned16(q_rope) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(cache) ||
+      !aligned16(fp8_scales) || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(cu) ||
+      !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) || !aligned16(workspace))
+    return MLA_ERR_INVALID_ARG;
+  if (B < 1 || T < 1 || num_pages < 1 || max_pages_per_seq < 1 || max_tokens < 1) return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || softmax_scale > 3.0e38f) return MLA_ERR_INVALID_ARG;
+  if (form < MLA_CHUNK_AUTO || form > MLA_CHUNK_ABSORBED) return MLA_ERR_INVALID_ARG;
+  if (!chunk_counts_ok(B, T) || !heads_ok(H) || !page_size_ok(page_size) || max_tokens > INT32_MAX / 2)
+    return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  const int max_tokens_seq = max_pages_per_seq * page_size;
+  cudaStream_t s = (cudaStream_t)stream;
+  form = chunk_form(form, B, T);
+  if (form == MLA_CHUNK_ABSORBED) {
+    if (T > MLA_MAX_BATCH) return MLA_ERR_UNSUPPORTED_SHAPE;
+    const int G = mla_decode_default_splits(1);
+    if (G < 1) return MLA_ERR_CUDA;
+    if (workspace_bytes < chunk_rows_layout(nullptr, T, H, G, nullptr)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+    ChunkRows r;
+    chunk_rows_layout(workspace, T, H, G, &r);
+    Plan plan;
+    plan_layout(r.decode_ws, T, 1, H, G, &plan);
+    plan.seq_row = r.seq_row;
+    mla_status st = launch_status(launch_chunk_rows(seq_lens, cu, B, T, max_tokens_seq, r, err_word, s));
+    // an ordinary launch: the plan reads the rows' lengths, which the kernel before writes
+    if (st == MLA_OK)
+      st = launch_status(launch_plan(r.len, nullptr, T, 1, max_pages_per_seq, page_size, num_pages, G, plan, err_word,
+                                     s, false));
+    if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s));
+    if (st == MLA_OK)
+      st = launch_status(fp8_scales ? launch_decode_fp8(r.q_abs, static_cast<const uint8_t*>(cache), fp8_scales,
+                                                        block_table, T, 1, H, num_pages, page_size,
+                                                        max_pages_per_seq, softmax_scale, G, plan, err_word, s)
+                                    : launch_decode(r.q_abs, static_cast<const uint16_t*>(cache), block_table, T, 1,
+                                                    H, num_pages, page_size, max_pages_per_seq, softmax_scale, G,
+                                                    plan, err_word, s));
+    if (st == MLA_OK) st = launch_status(launch_combine(plan, T, 1, H, r.u, lse, s, r.hdr));
+    if (st == MLA_OK) st = launch_status(launch_out_proj(r.u, w_uv, out, T, H, s, r.hdr));
+    return st;
+  }
+  const int64_t cap = chunk_cap(max_tokens, B);
+  const int group = chunk_head_group(H, cap);
+  if (workspace_bytes < chunk_layout(nullptr, B, T, group, cap, nullptr)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  ChunkPlan plan;
+  chunk_layout(workspace, B, T, group, cap, &plan);
+  mla_status st = launch_status(launch_chunk_plan(seq_lens, cu, B, T, max_tokens_seq, max_tokens, plan, err_word, s));
+  // the contexts' rows, each sequence from its own multiple of 128 on, zeros behind its end
+  if (st == MLA_OK)
+    st = launch_status(launch_read_kv(cache, fp8_scales, block_table, plan.len_eff, nullptr, plan.pstart, plan.rows, B,
+                                      (int)cap, num_pages, page_size, max_pages_per_seq, err_word, s));
+  for (int h0 = 0; h0 < H && st == MLA_OK; h0 += group) {
+    const int heads = H - h0 < group ? H - h0 : group;
+    st = launch_status(launch_expand(plan, w_uk, w_uv, H, h0, heads, cap, err_word, s));
+    if (st == MLA_OK)
+      st = launch_status(launch_attend(plan, q_nope, q_rope, out, lse, B, T, H, h0, heads, cap, softmax_scale,
+                                       err_word, s));
+  }
+  return st;
 }
 
 }  // extern "C"

@@ -34,6 +34,9 @@ struct Plan {
   float* lse_part;       // [I][n_q][H]
   uint16_t* o_part;      // [I][n_q][64][H][8] fp16, head-minor
   int4* range_desc;      // [G + 1] {first item, its sequence, its first tile, its end tile}
+  // block-table row of each sequence; null: sequence b uses row b. A row of -1 reads page 0
+  // (rows of a chunk that belong to no sequence: their result is not used).
+  const int32_t* seq_row = nullptr;
 };
 
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -163,12 +166,14 @@ cudaError_t launch_quantize_fp8(const uint16_t* rows, const float* scales, uint8
                                 cudaStream_t s);
 // Worker clusters (CTA pairs) of the decode kernel that fit on the device at once.
 int decode_max_workers();
+// rows_live (device, may be null): lse is written for rows < *rows_live only
 cudaError_t launch_combine(const Plan& plan, int B, int n_q, int H, uint16_t* u, float* lse,
-                           cudaStream_t s);
+                           cudaStream_t s, const int32_t* rows_live = nullptr);
 cudaError_t launch_absorb_q(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
                             uint16_t* q_abs, int T, int H, cudaStream_t s);
+// rows_live (device, may be null): only rows t < *rows_live are written
 cudaError_t launch_out_proj(const uint16_t* u, const uint16_t* w_uv, uint16_t* out, int T, int H,
-                            cudaStream_t s);
+                            cudaStream_t s, const int32_t* rows_live = nullptr);
 cudaError_t launch_merge_w_kq(const uint16_t* w_uq, const uint16_t* w_uk, uint16_t* w_kq, int d_q, int H,
                               cudaStream_t s);
 size_t out_comb_workspace_bytes(int T, int H, int d_model);

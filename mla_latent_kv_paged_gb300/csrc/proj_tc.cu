@@ -53,7 +53,7 @@ template <bool kAbsorb, int kNT>
 __global__ void __launch_bounds__(kThreads, 1)
 proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const uint16_t* __restrict__ weights, const uint16_t* __restrict__ q_rope, uint16_t* __restrict__ out,
-               int T, int H, int out_row, int32_t* err_word) {
+               int T, int H, int out_row, const int32_t* __restrict__ rows_live, int32_t* err_word) {
   using C = ProjCfg<kAbsorb, kNT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -106,6 +106,10 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   // when every kernel before this one has finished: none of them still reads
   // the workspace, so consecutive steps may share one
   if (!kAbsorb) grid_launch_dependents();
+  // rows at and past *rows_live are computed at most as part of a tile, never
+  // written; the first tile always runs, since its loads are under way
+  const int live = !kAbsorb && rows_live ? min(T, *rows_live) : T;
+  if (!kAbsorb) T = max(live, 1);
 
   const uint32_t idesc = idesc_bf16(128, C::NT, kAbsorb, false);
   auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
@@ -182,7 +186,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     __syncthreads();
     for (int i = threadIdx.x; i < C::NT * 16; i += kThreads) {
       const int row = i >> 4, part = i & 15, t = t0 + row;
-      if (t < T) {
+      if (t < live) {
         uint4 v;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -207,13 +211,13 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 
 template <bool kAbsorb, int kNT>
 cudaError_t launch_proj(const CUtensorMap& ma, const CUtensorMap& mb, const uint16_t* w, const uint16_t* q_rope,
-                        uint16_t* out, int T, int H, int out_row, cudaStream_t s) {
+                        uint16_t* out, int T, int H, int out_row, cudaStream_t s, const int32_t* rows_live = nullptr) {
   using C = ProjCfg<kAbsorb, kNT>;
   cudaError_t e = smem_limit<proj_tc_kernel<kAbsorb, kNT>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(H, kAbsorb ? kDC / 128 : 1);
   return launch_pdl(proj_tc_kernel<kAbsorb, kNT>, grid, dim3(kThreads), C::kSmem, s, ma, mb, w, q_rope, out, T,
-                    H, out_row, (int32_t*)nullptr);
+                    H, out_row, rows_live, (int32_t*)nullptr);
 }
 
 bool maps(CUtensorMap* ma, CUtensorMap* mb, const uint16_t* w, const uint16_t* act, int T, int H, int K, int nt) {
@@ -249,12 +253,12 @@ cudaError_t launch_merge_w_kq(const uint16_t* w_uq, const uint16_t* w_uk, uint16
 }
 
 cudaError_t launch_out_proj(const uint16_t* u, const uint16_t* w_uv, uint16_t* out, int T, int H,
-                            cudaStream_t s) {
+                            cudaStream_t s, const int32_t* rows_live) {
   const int nt = T <= 32 ? 32 : 64;
   CUtensorMap ma, mb;
   if (!maps(&ma, &mb, w_uv, u, T, H, kDC, nt)) return cudaErrorInvalidValue;
-  if (nt == 32) return launch_proj<false, 32>(ma, mb, w_uv, nullptr, out, T, H, kDV, s);
-  return launch_proj<false, 64>(ma, mb, w_uv, nullptr, out, T, H, kDV, s);
+  if (nt == 32) return launch_proj<false, 32>(ma, mb, w_uv, nullptr, out, T, H, kDV, s, rows_live);
+  return launch_proj<false, 64>(ma, mb, w_uv, nullptr, out, T, H, kDV, s, rows_live);
 }
 
 }  // namespace mla
