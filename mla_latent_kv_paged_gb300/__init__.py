@@ -19,6 +19,7 @@ and, for a ragged chunk of new tokens (the prompt side):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -488,46 +489,74 @@ def out_proj(u, w_uv, out=None, stream=None):
 CHUNK_FORMS = {"auto": 0, "expanded": 1, "absorbed": 2}
 
 
-def _tensor(name, t, dtypes, shape, dev):
-    """Check one argument: contiguous, one of ``dtypes``, ``shape`` (None = any extent), on ``dev``."""
-    if t.dtype not in (dtypes if isinstance(dtypes, tuple) else (dtypes,)):
-        raise ValueError(f"{name}: dtype {t.dtype}")
-    if len(t.shape) != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+def _tensor(name, t, dtype, shape, dev):
+    """Check one argument: ``dtype``, ``shape`` (a tuple), contiguous, on CUDA device number ``dev``."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, the cache on {dev}")
+    raise ValueError(f"{name}: on {t.device}, the cache on cuda:{dev}")
+
+
+def _dims(name, t, n):
+    if t.dim() != n:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {n} dimensions")
+    return t.shape
 
 
 def _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word):
-    """Check the paged-cache arguments of the chunk calls; returns (device, B)."""
+    """Check the paged-cache arguments of the chunk calls; returns (device number, B)."""
     import torch
-    dev, B = cache.device, block_table.shape[0] if block_table.dim() == 2 else 0
-    if dev.type != "cuda":
-        raise ValueError(f"cache: on {dev}, a CUDA device is needed")
-    fp8 = cache.dtype == torch.uint8
+    dev = cache.get_device()
+    if dev < 0:
+        raise ValueError(f"cache: on {cache.device}, a CUDA device is needed")
+    fp8 = cache.dtype is torch.uint8
     if fp8 != (fp8_scales is not None):
         raise ValueError("an FP8 cache (uint8 codes) needs its column scales fp8_scales, a bf16 cache has none")
-    _tensor("cache", cache, (torch.uint8, torch.bfloat16), (None, None, D_ROW), dev)
-    _tensor("block_table", block_table, torch.int32, (None, None), dev)
-    _tensor("seq_lens", seq_lens, torch.int32, (B,), dev)
-    _tensor("cu", cu, torch.int32, (B + 1,), dev)
+    num_pages, page_size, _ = _dims("cache", cache, 3)
+    _tensor("cache", cache, torch.uint8 if fp8 else torch.bfloat16, (num_pages, page_size, D_ROW), dev)
+    B, max_pages = _dims("block_table", block_table, 2)
+    i32 = torch.int32
+    _tensor("block_table", block_table, i32, (B, max_pages), dev)
+    _tensor("seq_lens", seq_lens, i32, (B,), dev)
+    _tensor("cu", cu, i32, (B + 1,), dev)
     if fp8:
         _tensor("fp8_scales", fp8_scales, torch.float32, (D_ROW,), dev)
-    if err_word is not None and (err_word.dtype != torch.int32 or err_word.numel() < 1 or err_word.device != dev):
+    if err_word is not None and (err_word.dtype is not i32 or err_word.numel() < 1 or err_word.get_device() != dev):
         raise ValueError("err_word: an int32 tensor beside the cache")
     return dev, B
 
 
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _current(dev):
+    """A context in which device ``dev`` is the current one (nothing to do where it is already)."""
+    import torch
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with device ``dev`` current (a kernel launches on the current device)."""
+    import torch
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    with _current(dev):
+        return fn(*args, s.cuda_stream)
+
+
 def _room(workspace, need, dev):
-    """The workspace given (its size is checked by the call) or a new one of ``need`` bytes."""
+    """(workspace, its bytes): the one given (its size is checked by the call), or a new one."""
     import torch
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    if not workspace.is_contiguous() or workspace.device != dev:
+        return torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}"), need
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace: a contiguous tensor beside the cache")
-    return workspace
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def append_chunk_workspace_bytes(T: int, d_model: int) -> int:
@@ -550,16 +579,14 @@ def append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, *, fp8_scales=None,
     """
     import torch
     dev, B = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
-    _tensor("h", h, torch.bfloat16, (None, None), dev)
-    T, d_model = h.shape
+    T, d_model = _dims("h", h, 2)
+    _tensor("h", h, torch.bfloat16, (T, d_model), dev)
     _tensor("w_dkr", w_dkr, torch.bfloat16, (D_ROW, d_model), dev)
-    with torch.cuda.device(dev):
-        need = append_chunk_workspace_bytes(T, d_model)
-        workspace = _room(workspace, need, dev)
-        st = lib().mla_append_chunk(_ptr(h), _ptr(w_dkr), _ptr(cache), _ptr(fp8_scales), _ptr(block_table),
-                                    _ptr(seq_lens), _ptr(cu), B, T, d_model, cache.shape[0], cache.shape[1],
-                                    block_table.shape[1], float(rope_theta), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _ptr(err_word), _stream(stream))
+    workspace, room = _room(workspace, append_chunk_workspace_bytes(T, d_model), dev)
+    num_pages, page_size, _ = cache.shape
+    st = _call(lib().mla_append_chunk, dev, stream, h.data_ptr(), w_dkr.data_ptr(), cache.data_ptr(),
+               _address(fp8_scales), block_table.data_ptr(), seq_lens.data_ptr(), cu.data_ptr(), B, T, d_model,
+               num_pages, page_size, block_table.shape[1], rope_theta, workspace.data_ptr(), room, _address(err_word))
     _check(st, "mla_append_chunk")
     return workspace
 
@@ -574,13 +601,13 @@ def read_kv(cache, block_table, seq_lens, cu, *, n_rows: int, first=None, fp8_sc
     dev, B = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
     if first is not None:
         _tensor("first", first, torch.int32, (B,), dev)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((n_rows, D_ROW), dtype=torch.bfloat16, device=dev)
-        _tensor("out", out, torch.bfloat16, (n_rows, D_ROW), dev)
-        st = lib().mla_read_kv(_ptr(cache), _ptr(fp8_scales), _ptr(block_table), _ptr(seq_lens), _ptr(first), _ptr(cu),
-                               _ptr(out), B, n_rows, cache.shape[0], cache.shape[1], block_table.shape[1],
-                               _ptr(err_word), _stream(stream))
+    if out is None:
+        out = torch.empty((n_rows, D_ROW), dtype=torch.bfloat16, device=cache.device)
+    _tensor("out", out, torch.bfloat16, (n_rows, D_ROW), dev)
+    num_pages, page_size, _ = cache.shape
+    st = _call(lib().mla_read_kv, dev, stream, cache.data_ptr(), _address(fp8_scales), block_table.data_ptr(),
+               seq_lens.data_ptr(), _address(first), cu.data_ptr(), out.data_ptr(), B, n_rows, num_pages, page_size,
+               block_table.shape[1], _address(err_word))
     _check(st, "mla_read_kv")
     return out
 
@@ -612,26 +639,27 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
     if form not in CHUNK_FORMS:
         raise ValueError(f"form: {form!r}, expected one of {sorted(CHUNK_FORMS)}")
     bf = torch.bfloat16
-    _tensor("q_nope", q_nope, bf, (None, None, D_NOPE), dev)
-    T, H = q_nope.shape[0], q_nope.shape[1]
+    T, H, _ = _dims("q_nope", q_nope, 3)
+    _tensor("q_nope", q_nope, bf, (T, H, D_NOPE), dev)
     _tensor("q_rope", q_rope, bf, (T, H, D_R), dev)
     _tensor("w_uk", w_uk, bf, (H, D_NOPE, D_C), dev)
     _tensor("w_uv", w_uv, bf, (H, D_V, D_C), dev)
     if lse is not None:
         _tensor("lse", lse, torch.float32, (T, H), dev)
+    num_pages, page_size, _ = cache.shape
+    max_pages = block_table.shape[1]
     if max_tokens is None:
-        max_tokens = B * block_table.shape[1] * cache.shape[1]
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((T, H, D_V), dtype=bf, device=dev)
-        _tensor("out", out, bf, (T, H, D_V), dev)
+        max_tokens = B * max_pages * page_size
+    if out is None:
+        out = torch.empty((T, H, D_V), dtype=bf, device=cache.device)
+    _tensor("out", out, bf, (T, H, D_V), dev)
+    with _current(dev):
         need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
-        workspace = _room(workspace, need, dev)
-        st = lib().mla_attend_chunk(_ptr(q_nope), _ptr(q_rope), _ptr(w_uk), _ptr(w_uv), _ptr(cache), _ptr(fp8_scales),
-                                    _ptr(block_table), _ptr(seq_lens), _ptr(cu), B, T, H, cache.shape[0],
-                                    cache.shape[1], block_table.shape[1], max_tokens, float(softmax_scale),
-                                    CHUNK_FORMS[form], _ptr(out), _ptr(lse), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _ptr(err_word), _stream(stream))
+    workspace, room = _room(workspace, need, dev)
+    st = _call(lib().mla_attend_chunk, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(), w_uk.data_ptr(),
+               w_uv.data_ptr(), cache.data_ptr(), _address(fp8_scales), block_table.data_ptr(), seq_lens.data_ptr(),
+               cu.data_ptr(), B, T, H, num_pages, page_size, max_pages, max_tokens, softmax_scale, CHUNK_FORMS[form],
+               out.data_ptr(), _address(lse), workspace.data_ptr(), room, _address(err_word))
     _check(st, "mla_attend_chunk")
     return out
 

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h, Args a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const int nt = blockIdx.x, s = blockIdx.y, tile = blockIdx.z;
   const int kb0 = (int)((int64_t)s * a.KB / a.S), nkb = (int)((int64_t)(s + 1) * a.KB / a.S) - kb0;
   auto full = [&](int i) { return sbase + kOffBar + 8u * i; };
@@ -155,7 +155,7 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 4) {
-    if (lane == 0) {
+    if (elect()) {
       prefetch_tmap(&map_w);
       prefetch_tmap(&map_h);
       const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
@@ -186,7 +186,7 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
       }
     }
   } else if (warp == 5) {
-    if (lane == 0) {
+    if (elect()) {
       const uint32_t idesc = idesc_bf16(kM, kN, false, false);
       const uint64_t d0 = smem_desc(0, 16, 1024, kSwizzle128B);
       auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };

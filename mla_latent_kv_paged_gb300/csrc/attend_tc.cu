@@ -40,10 +40,11 @@ enum {
   KF0 = 0, KE0 = KF0 + kKStages, VF0 = KE0 + kKStages, VE0 = VF0 + kVStages, QF0 = VE0 + kVStages, SF0 = QF0 + 2,
   PF0 = SF0 + 2, OF0 = PF0 + 2, MD = OF0 + 2, kBars
 };
-constexpr uint32_t kOffSlots = kOffBar + 8 * kBars;
+constexpr uint32_t kOffX = kOffBar + 8 * kBars;  // [2 tiles][2 halves][128] half-row maxima, then sums
+constexpr uint32_t kOffSlots = kOffX + 4 * 128 * 4;
 constexpr uint32_t kSmem = kOffSlots + 16;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr int kThreads = 320;  // warps 0..3 and 4..7 softmax of tile 0 and 1, 8 producer, 9 MMA issuer
+constexpr int kThreads = 576;  // warps 0..15 softmax, 16 producer, 17 MMA issuer
 constexpr uint32_t kTmS = 0, kTmO = 256;
 constexpr float kBias = 7.0f;       // P = 2^7 exp(z - m)
 constexpr float kRescale = 8.0f;    // log2 units
@@ -52,6 +53,31 @@ constexpr float kLn2 = 0.69314718055994530942f;
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+// pairs of fp32 values
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_kr,
               const __grid_constant__ CUtensorMap map_v, const uint16_t* __restrict__ q_nope,
@@ -59,7 +85,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
               int H, int h0, int64_t cap, float sl2, int32_t* err_word) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index();
   const int hh = blockIdx.y, h = h0 + hh;
   auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlots);
@@ -78,16 +104,16 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       mbar_init(bar(VE0 + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(QF0 + i), 128);
+      mbar_init(bar(QF0 + i), 256);
       mbar_init(bar(SF0 + i), 1);
-      mbar_init(bar(PF0 + i), 128);
+      mbar_init(bar(PF0 + i), 256);
       mbar_init(bar(OF0 + i), 1);
     }
     mbar_init(bar(MD), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 17) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -111,8 +137,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
   };
   const int n0 = steps(0), n1 = steps(1), nkv = max(n0, n1);
 
-  if (warp == 8) {
-    if (lane == 0 && nkv > 0) {
+  if (warp == 16) {
+    if (nkv > 0 && elect()) {
       prefetch_tmap(&map_k);
       prefetch_tmap(&map_kr);
       prefetch_tmap(&map_v);
@@ -157,8 +183,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
           }
       }
     }
-  } else if (warp == 9) {
-    if (lane == 0 && nkv > 0) {
+  } else if (warp == 17) {
+    if (nkv > 0 && elect()) {
       constexpr uint32_t kIdC = idesc_f16(128, 128, false, false), kIdR = idesc_bf16(128, 128, false, false);
       constexpr uint32_t kIdV = idesc_f16(128, 128, false, true);
       auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
@@ -218,14 +244,15 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       wait_mmas(bar(MD));
     }
   } else if (nkv > 0) {
-    const int x = warp >> 2, tid = threadIdx.x & 127, row = tid;  // row == tensor-memory lane
+    // tile x, column half y; the row is the tensor-memory lane of this thread
+    const int x = (warp >> 2) & 1, y = warp >> 3, row = threadIdx.x & 127, tid = row + 128 * y;
     const int nx = x ? n1 : n0, r0 = q0 + 128 * x;
     if (nx > 0) {
       // the tile's queries: content as fp16 (exact for bf16 values of normal fp16
       // size), position as it is, into the swizzled slabs
       uint32_t top = 0;
 #pragma unroll 4
-      for (int i = tid; i < 128 * 16; i += 128) {
+      for (int i = tid; i < 128 * 16; i += 256) {
         const int r = i >> 4, ch = i & 15;
         uint4 w = make_uint4(0, 0, 0, 0);
         if (r0 + r < n) w = __ldg(reinterpret_cast<const uint4*>(q_nope + ((size_t)(c0 + r0 + r) * H + h) * kDNope) + ch);
@@ -240,7 +267,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       }
       if (top >= 0x477FF000u && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
 #pragma unroll 4
-      for (int i = tid; i < 128 * 8; i += 128) {
+      for (int i = tid; i < 128 * 8; i += 256) {
         const int r = i >> 3, ch = i & 7;
         uint4 w = make_uint4(0, 0, 0, 0);
         if (r0 + r < n) w = __ldg(reinterpret_cast<const uint4*>(q_rope + ((size_t)(c0 + r0 + r) * H + h) * kDR) + ch);
@@ -250,73 +277,104 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       mbar_arrive(bar(QF0 + x));
 
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t tS = tmem + kTmS + 128 * x + lane_off, tO = tmem + kTmO + 128 * x + lane_off;
+      const uint32_t tS = tmem + kTmS + 128 * x + lane_off, tO = tmem + kTmO + 128 * x + 64 * y + lane_off;
       const int first_seen = L - n + r0 + 1;                       // tokens that the tile's first row sees
       const int seen = L - n + min(r0 + row, n - 1) + 1;           // tokens that this row sees
-      float ref = -INFINITY, sum = 0.f;
+      volatile float* mine = reinterpret_cast<float*>(smem + kOffX) + (2 * x + y) * 128 + row;
+      volatile float* theirs = reinterpret_cast<float*>(smem + kOffX) + (2 * x + (y ^ 1)) * 128 + row;
+      auto meet = [&] { asm volatile("bar.sync %0, 256;" ::"r"(1 + x) : "memory"); };  // the tile's 256 threads
+      float ref = -INFINITY;
+      uint64_t sum2[2] = {0, 0};
       bool ok = true;
-      for (int j = 0; j < nx; ++j) {
+      int j = 0;
+      for (; j < nx; ++j) {
         // the warp leaves together: the tensor-memory loads below need every lane
         ok = __all_sync(0xffffffffu, wait_phase(bar(SF0 + x), (uint32_t)(j & 1), abort_flag, err_word));
-        if (!ok) break;
         tc_fence_after();
-        float z[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(z + 32 * c));
+        uint32_t z[64];
+        tmem_ld32(tS + 64 * y, *reinterpret_cast<uint32_t(*)[32]>(z));
+        tmem_ld32(tS + 64 * y + 32, *reinterpret_cast<uint32_t(*)[32]>(z + 32));
         tmem_wait_ld();
         if ((j + 1) * kKvTile > first_seen) {
-          const int lim = seen - j * kKvTile;
+          const int lim = seen - j * kKvTile - 64 * y;
 #pragma unroll
-          for (int c = 0; c < 128; ++c) z[c] = c < lim ? z[c] : -INFINITY;
+          for (int c = 0; c < 64; ++c) z[c] = c < lim ? z[c] : 0xFF800000u;
         }
-        float m4[4] = {z[0], z[1], z[2], z[3]};
+        float m4[4];
 #pragma unroll
-        for (int c = 4; c < 128; ++c) m4[c & 3] = fmaxf(m4[c & 3], z[c]);
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        for (int c = 0; c < 4; ++c) m4[c] = __uint_as_float(z[c]);
+#pragma unroll
+        for (int c = 4; c < 60; c += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            m4[q] = fmaxf(m4[q], fmaxf(__uint_as_float(z[c + 2 * q]), __uint_as_float(z[c + 2 * q + 1])));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) m4[c] = fmaxf(m4[c], __uint_as_float(z[60 + c]));
+        float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        *mine = mx;
+        meet();  // also: both halves of S are in registers, P may overwrite them
+        // (the next step's maxima follow its scores, which follow every thread's P)
+        mx = fmaxf(mx, *theirs);
         // all MMAs issued before this step's scores are done, the last P V among them
         if (__any_sync(0xffffffffu, mx * sl2 > ref * sl2 + kRescale)) {
           const float up = fmaxf(ref, mx);
           if (j > 0) {
             const float f = ref == up ? 1.f : ex2((ref - up) * sl2);
-            sum *= f;
+            const uint64_t f2 = pack2(f, f);
+            sum2[0] = mul2(sum2[0], f2);
+            sum2[1] = mul2(sum2[1], f2);
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + c, o);
+            for (int c = 0; c < 64; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
-              tmem_st32(tO + c, o);
+              for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * f);
+              tmem_st16(tO + c, o);
             }
           }
           ref = up;
         }
         const float off = kBias - (ref == -INFINITY ? 0.f : ref * sl2);
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t off2 = pack2(off, off), sl22 = pack2(sl2, sl2);
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
           uint32_t p[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
-            const float a = ex2(fmaf(z[c + 2 * q], sl2, off)), e = ex2(fmaf(z[c + 2 * q + 1], sl2, off));
-            s4[q & 1] += a;
-            s4[2 + (q & 1)] += e;
+            const uint64_t t = fma2(pack2(__uint_as_float(z[c + 2 * q]), __uint_as_float(z[c + 2 * q + 1])), sl22, off2);
+            float a, e;
+            unpack2(t, a, e);
+            a = ex2(a);
+            e = ex2(e);
+            sum2[q & 1] = add2(sum2[q & 1], pack2(a, e));
             p[q] = cvt_f16x2(a, e);
           }
-          tmem_st16(tS + c / 2, p);
+          tmem_st16(tS + 32 * y + c / 2, p);
         }
-        sum += (s4[0] + s4[1]) + (s4[2] + s4[3]);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(PF0 + x));
+        if (!ok) break;
       }
+      // the two halves' sums
+      float s0, s1, sum;
+      unpack2(add2(sum2[0], sum2[1]), s0, s1);
+      sum = s0 + s1;
+      if (!ok) {  // gave up: the barriers of this tile stay matched, nothing is written
+        for (++j; j < nx; ++j) meet();
+      }
+      meet();  // the last maxima are read
+      *mine = sum;
+      meet();
+      sum += *theirs;  // the same in both halves
       if (ok && __all_sync(0xffffffffu, wait_phase(bar(OF0 + x), 0, abort_flag, err_word))) {
         tc_fence_after();
         const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays NaN
         const bool live = r0 + row < n;
         const size_t at = (size_t)(c0 + r0 + row) * H + h;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
           uint32_t o[32], w[16];
           tmem_ld32(tO + c, o);
           tmem_wait_ld();
@@ -326,16 +384,18 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
           if (live) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              reinterpret_cast<uint4*>(out + at * kDV + c)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+              reinterpret_cast<uint4*>(out + at * kDV + 64 * y + c)[q] =
+                  make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
           }
         }
-        if (lse && live) lse[at] = sum > 0.f ? (ref * sl2 - kBias + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
+        if (lse && live && y == 0)
+          lse[at] = sum > 0.f ? (ref * sl2 - kBias + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -22,6 +22,8 @@ constexpr int kCols = 64;      // latent columns per block
 constexpr int kCPT = kCols / 2;  // columns per thread
 constexpr int kKB = 2;         // partials whose loads are in flight together
 
+// kRows: the rows of a chunk, of which only those below *rows_live write their lse
+template <bool kRows>
 __global__ void __launch_bounds__(kThreads)
 combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __restrict__ lse_out,
                const int32_t* __restrict__ rows_live) {
@@ -99,14 +101,14 @@ combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __res
           }
         }
       }
-    } else {  // no finite partial: NaN if one of them is
+    } else if (kRows) {  // no finite partial: NaN if one of them is
       for (int k = k0; k < k1; ++k) {
         const float l = lse_of(k);
         if (l != l) wsum = l;
       }
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : (wsum == 0.f ? 0.f : wsum);  // a NaN partial stays NaN
+  const float inv = wsum > 0.f ? 1.f / wsum : (!kRows || wsum == 0.f ? 0.f : wsum);  // a NaN partial stays NaN
 #pragma unroll
   for (int c = 0; c < kCPT / 2; ++c)
     tile[h][(kCPT / 2) * part + c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
@@ -121,8 +123,8 @@ combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __res
     o.w = tile[row][4 * q + 3];
     *reinterpret_cast<uint4*>(u + ((size_t)bj * H + row) * kDC + blockIdx.y * kCols + 8 * q) = o;
   }
-  if (lse_out && blockIdx.y == 0 && part == 0 && h < H && (!rows_live || bj < *rows_live))
-    lse_out[(size_t)bj * H + h] = wsum > 0.f ? m + logf(wsum) : (wsum == 0.f ? -INFINITY : wsum);
+  if (lse_out && blockIdx.y == 0 && part == 0 && h < H && (!kRows || bj < *rows_live))
+    lse_out[(size_t)bj * H + h] = wsum > 0.f ? m + logf(wsum) : (!kRows || wsum == 0.f ? -INFINITY : wsum);
 }
 
 }  // namespace
@@ -130,7 +132,8 @@ combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __res
 cudaError_t launch_combine(const Plan& plan, int B, int n_q, int H, uint16_t* u, float* lse,
                            cudaStream_t s, const int32_t* rows_live) {
   dim3 grid(B * n_q, kDC / kCols);
-  return launch_pdl(combine_kernel, grid, dim3(kThreads), 0, s, plan, n_q, H, u, lse, rows_live);
+  return rows_live ? launch_pdl(combine_kernel<true>, grid, dim3(kThreads), 0, s, plan, n_q, H, u, lse, rows_live)
+                   : launch_pdl(combine_kernel<false>, grid, dim3(kThreads), 0, s, plan, n_q, H, u, lse, rows_live);
 }
 
 }  // namespace mla

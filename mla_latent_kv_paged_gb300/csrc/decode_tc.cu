@@ -169,12 +169,17 @@ __device__ __forceinline__ uint32_t scale_bf16x2_to_f16x2(uint32_t w, float s0, 
   return cvt_f16x2(bf16_lo(w) * s0, bf16_hi(w) * s1);
 }
 
-template <bool kF8>
+// kRows: the sequences are rows of a chunk (chunk.cuh): seq_row[b] is the block-table
+// row of sequence b, -1 for a row of no sequence (it reads page 0 and its result
+// is not used). A template parameter, because any change to the plain kernel's
+// code costs it a few per cent (decode call 38.8 -> 39.5 us with a run-time test).
+template <bool kF8, bool kRows>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_kr,
                  const __grid_constant__ CUtensorMap map_qkr, const __grid_constant__ CUtensorMap map_q,
                  const int32_t* __restrict__ block_table, int n_q, int H, int max_pages, int num_pages,
-                 int tile_shift, float sl2, Plan plan, const float* __restrict__ fp8_scales, int32_t* err_word) {
+                 int tile_shift, float sl2, Plan plan, const float* __restrict__ fp8_scales, int32_t* err_word,
+                 const int32_t* __restrict__ seq_row) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
@@ -267,11 +272,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
       int64_t row;  // block-table row of the current range (its first entry), or < 0: page 0
     };
     auto table_row = [&](int seq) -> int64_t {
-      return (int64_t)(plan.seq_row ? plan.seq_row[seq] : seq) * max_pages;
+      return (int64_t)(kRows ? seq_row[seq] : seq) * max_pages;
     };
     auto cur_load = [&](Cursor& c) {
       const int mine = c.base + lane;
-      c.id_l = mine < c.pg1 && c.row >= 0 ? block_table[c.row + (mine >> tile_shift)] : 0;
+      c.id_l = mine < c.pg1 && (!kRows || c.row >= 0) ? block_table[c.row + (mine >> tile_shift)] : 0;
     };
     auto cur_init = [&](Cursor& c, int it) {
       c.it = it;
@@ -921,10 +926,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             tc_fence_before();
             mbar_arrive(bar(OFREE));
             if (rank == 0 && row < H)
-              // a chunk's row (seq_row) keeps a sum that is not a number, so that the
-              // merge passes it on
+              // a chunk's row keeps a sum that is not a number, so that the merge passes it on
               plan.lse_part[orow] =
-                  l_tot > 0.f ? (m_new + log2f(l_tot)) * kLn2 : (plan.seq_row && l_tot != l_tot ? l_tot : -INFINITY);
+                  l_tot > 0.f ? (m_new + log2f(l_tot)) * kLn2 : (kRows && l_tot != l_tot ? l_tot : -INFINITY);
           }
         }
         if (ntiles >= 2) ++lg_n;
@@ -952,7 +956,21 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
 
 // ---------------------------------------------------------------- host side
 int decode_max_workers() {
-  if (smem_limit<decode_tc_kernel<false>>(kSmemBytes) != cudaSuccess) {
+  // a property of the kernel and the device: asked once per device (the query
+  // takes tens of microseconds of host time)
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  const bool cached = dev >= 0 && dev < kMaxDevices;
+  if (cached) {
+    const int n = known[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+  }
+  if (smem_limit<decode_tc_kernel<false, false>>(kSmemBytes) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
@@ -968,18 +986,19 @@ int decode_max_workers() {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, decode_tc_kernel<false>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, decode_tc_kernel<false, false>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
+  if (cached && n > 0) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
 namespace {
 // The query maps and the launch, shared by the bf16 and FP8 caches (the page
 // maps differ: 16-bit swizzled boxes, or unswizzled 8-bit rows).
-template <bool kF8>
-cudaError_t launch_decode_impl(const CUtensorMap& map_c, const CUtensorMap& map_kr, const uint16_t* q_abs,
+template <bool kF8, bool kRows>
+cudaError_t launch_decode_as(const CUtensorMap& map_c, const CUtensorMap& map_kr, const uint16_t* q_abs,
                                const float* fp8_scales, const int32_t* block_table, int B, int n_q, int H,
                                int num_pages, int page_size, int max_pages, float scale, int G, const Plan& plan,
                                int32_t* err_word,
@@ -991,13 +1010,17 @@ cudaError_t launch_decode_impl(const CUtensorMap& map_c, const CUtensorMap& map_
   if (!make_tmap(&map_qkr, q_abs, 2, q_dims, row_stride, box_qkr, 64) ||
       !make_tmap(&map_q, q_abs, 2, q_dims, row_stride, box_q, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = smem_limit<decode_tc_kernel<kF8>>(kSmemBytes);
+  cudaError_t e = smem_limit<decode_tc_kernel<kF8, kRows>>(kSmemBytes);
   if (e != cudaSuccess) return e;
   const float sl2 = scale * 1.4426950408889634f;
   dim3 grid(2 * G, n_q, 1);
-  return launch_pdl(decode_tc_kernel<kF8>, grid, dim3(kThreads), kSmemBytes, s, map_c, map_kr, map_qkr, map_q,
+  return launch_pdl(decode_tc_kernel<kF8, kRows>, grid, dim3(kThreads), kSmemBytes, s, map_c, map_kr, map_qkr, map_q,
                     block_table, n_q, H, max_pages, num_pages, page_size == 2 * kTile ? 1 : 0, sl2, plan,
-                    fp8_scales, err_word);
+                    fp8_scales, err_word, plan.seq_row);
+}
+template <bool kF8, typename... Args>
+cudaError_t launch_decode_impl(const Plan& plan, const Args&... args) {
+  return plan.seq_row ? launch_decode_as<kF8, true>(args...) : launch_decode_as<kF8, false>(args...);
 }
 }  // namespace
 
@@ -1011,7 +1034,7 @@ cudaError_t launch_decode(const uint16_t* q_abs, const uint16_t* cache, const in
   if (!make_tmap(&map_c, cache, 2, cache_dims, row_stride, box_c, 128) ||
       !make_tmap(&map_kr, cache, 2, cache_dims, row_stride, box_kr, 64))
     return cudaErrorInvalidValue;
-  return launch_decode_impl<false>(map_c, map_kr, q_abs, nullptr, block_table, B, n_q, H, num_pages, page_size,
+  return launch_decode_impl<false>(plan, map_c, map_kr, q_abs, nullptr, block_table, B, n_q, H, num_pages, page_size,
                                    max_pages, scale, G, plan, err_word, s);
 }
 
@@ -1026,7 +1049,7 @@ cudaError_t launch_decode_fp8(const uint16_t* q_abs, const uint8_t* cache8, cons
   if (!make_tmap(&map_c, cache8, 2, cache_dims, row_stride, box_c, 0, true) ||
       !make_tmap(&map_kr, cache8, 2, cache_dims, row_stride, box_kr, 0, true))
     return cudaErrorInvalidValue;
-  return launch_decode_impl<true>(map_c, map_kr, q_abs, fp8_scales, block_table, B, n_q, H, num_pages, page_size,
+  return launch_decode_impl<true>(plan, map_c, map_kr, q_abs, fp8_scales, block_table, B, n_q, H, num_pages, page_size,
                                   max_pages, scale, G, plan, err_word, s);
 }
 

@@ -67,7 +67,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
               int32_t* err_word) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffSlots + 4);
@@ -104,7 +104,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
 
   if (warp == 4) {
-    if (lane == 0) {
+    if (elect()) {
       prefetch_tmap(&map_rows);
       prefetch_tmap(&map_uk);
       prefetch_tmap(&map_uv);
@@ -141,7 +141,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
       }
     }
   } else if (warp == 5) {
-    if (lane == 0) {
+    if (elect()) {
       const uint32_t idesc = idesc_bf16(128, 256, false, false);
       auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
       const uint64_t ad0 = smem_desc(0, 16, 1024, kSwizzle128B) + da(sbase);

@@ -49,7 +49,8 @@ struct ProjCfg {
   static constexpr uint32_t kTmCols = NT < 32 ? 32 : NT;
 };
 
-template <bool kAbsorb, int kNT>
+// kRows (out_proj): rows of a chunk, of which only those below *rows_live are written
+template <bool kAbsorb, int kNT, bool kRows>
 __global__ void __launch_bounds__(kThreads, 1)
 proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const uint16_t* __restrict__ weights, const uint16_t* __restrict__ q_rope, uint16_t* __restrict__ out,
@@ -108,8 +109,8 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   if (!kAbsorb) grid_launch_dependents();
   // rows at and past *rows_live are computed at most as part of a tile, never
   // written; the first tile always runs, since its loads are under way
-  const int live = !kAbsorb && rows_live ? min(T, *rows_live) : T;
-  if (!kAbsorb) T = max(live, 1);
+  const int live = kRows ? min(T, *rows_live) : T;
+  if (kRows) T = max(live, 1);
 
   const uint32_t idesc = idesc_bf16(128, C::NT, kAbsorb, false);
   auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
@@ -209,14 +210,14 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   }
 }
 
-template <bool kAbsorb, int kNT>
+template <bool kAbsorb, int kNT, bool kRows = false>
 cudaError_t launch_proj(const CUtensorMap& ma, const CUtensorMap& mb, const uint16_t* w, const uint16_t* q_rope,
                         uint16_t* out, int T, int H, int out_row, cudaStream_t s, const int32_t* rows_live = nullptr) {
   using C = ProjCfg<kAbsorb, kNT>;
-  cudaError_t e = smem_limit<proj_tc_kernel<kAbsorb, kNT>>(C::kSmem);
+  cudaError_t e = smem_limit<proj_tc_kernel<kAbsorb, kNT, kRows>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(H, kAbsorb ? kDC / 128 : 1);
-  return launch_pdl(proj_tc_kernel<kAbsorb, kNT>, grid, dim3(kThreads), C::kSmem, s, ma, mb, w, q_rope, out, T,
+  return launch_pdl(proj_tc_kernel<kAbsorb, kNT, kRows>, grid, dim3(kThreads), C::kSmem, s, ma, mb, w, q_rope, out, T,
                     H, out_row, rows_live, (int32_t*)nullptr);
 }
 
@@ -257,8 +258,11 @@ cudaError_t launch_out_proj(const uint16_t* u, const uint16_t* w_uv, uint16_t* o
   const int nt = T <= 32 ? 32 : 64;
   CUtensorMap ma, mb;
   if (!maps(&ma, &mb, w_uv, u, T, H, kDC, nt)) return cudaErrorInvalidValue;
-  if (nt == 32) return launch_proj<false, 32>(ma, mb, w_uv, nullptr, out, T, H, kDV, s, rows_live);
-  return launch_proj<false, 64>(ma, mb, w_uv, nullptr, out, T, H, kDV, s, rows_live);
+  if (rows_live)
+    return nt == 32 ? launch_proj<false, 32, true>(ma, mb, w_uv, nullptr, out, T, H, kDV, s, rows_live)
+                    : launch_proj<false, 64, true>(ma, mb, w_uv, nullptr, out, T, H, kDV, s, rows_live);
+  if (nt == 32) return launch_proj<false, 32>(ma, mb, w_uv, nullptr, out, T, H, kDV, s);
+  return launch_proj<false, 64>(ma, mb, w_uv, nullptr, out, T, H, kDV, s);
 }
 
 }  // namespace mla

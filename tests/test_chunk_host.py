@@ -97,14 +97,14 @@ def test_python_refusals():
     with pytest.raises(ValueError, match="CUDA device"):
         mla.attend_chunk(t(4, 2, 128), t(4, 2, 64), t(2, 128, 512), t(2, 128, 512), t(8, 64, 576), i(2, 4), i(2), i(3),
                          max_tokens=9)
-    dev = torch.device("cpu")
     with pytest.raises(ValueError, match="dtype"):
-        mla._tensor("x", t(2, 3), torch.int32, (2, 3), dev)
+        mla._tensor("x", t(2, 3), torch.int32, (2, 3), -1)
     with pytest.raises(ValueError, match="shape"):
-        mla._tensor("x", t(2, 3), torch.bfloat16, (2, 4), dev)
+        mla._tensor("x", t(2, 3), torch.bfloat16, (2, 4), -1)
     with pytest.raises(ValueError, match="shape"):
-        mla._tensor("x", t(2, 3), torch.bfloat16, (2, 3, 1), dev)
+        mla._tensor("x", t(2, 3), torch.bfloat16, (2, 3, 1), -1)
     with pytest.raises(ValueError, match="contiguous"):
-        mla._tensor("x", t(3, 2).t(), torch.bfloat16, (2, 3), dev)
+        mla._tensor("x", t(3, 2).t(), torch.bfloat16, (2, 3), -1)
     with pytest.raises(ValueError, match="on cpu"):
-        mla._tensor("x", t(2, 3), torch.bfloat16, (2, 3), torch.device("cuda"))
+        mla._tensor("x", t(2, 3), torch.bfloat16, (2, 3), 0)
+    mla._tensor("x", t(2, 3), torch.bfloat16, (2, 3), -1)
