@@ -124,16 +124,20 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // the work item: rows [q0, q0 + 256) of sequence b; the tiles' steps over the keys
-  int4 item = make_int4(-1, 0, 0, 0);
-  if ((int)blockIdx.x < plan.hdr[0]) item = plan.item[blockIdx.x];
+  // the piece: rows [q0, q0 + 256) of sequence b, steps [j0, j1) over the keys
+  int4 item = make_int4(-1, 0, 0, 0), part = make_int4(0, 0, -1, 0);
+  if ((int)blockIdx.x < plan.hdr[0]) {
+    item = plan.piece[2 * blockIdx.x];
+    part = plan.piece[2 * blockIdx.x + 1];
+  }
   const int b = item.x, q0 = item.y, n = item.z, c0 = item.w;
+  const int j0 = part.x, slot = part.z;
   const int L = b >= 0 ? plan.len_eff[b] : 0;
-  const int64_t k0 = b >= 0 ? plan.pstart[b] : 0;  // first expanded row of the sequence
+  const int64_t k0 = b >= 0 ? plan.pstart[b] + (int64_t)j0 * kKvTile : 0;  // first expanded row of the piece
   const bool two = n - q0 > 128;
-  auto steps = [&](int x) {  // of tile x: up to the last token that its last row sees
+  auto steps = [&](int x) {  // of tile x in this piece: up to the last token that its last row sees
     if (b < 0 || (x == 1 && !two)) return 0;
-    return (L - n + min(q0 + 128 * (x + 1), n) + kKvTile - 1) / kKvTile;
+    return min((L - n + min(q0 + 128 * (x + 1), n) + kKvTile - 1) / kKvTile, part.y) - j0;
   };
   const int n0 = steps(0), n1 = steps(1), nkv = max(n0, n1);
 
@@ -295,8 +299,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
         tmem_ld32(tS + 64 * y, *reinterpret_cast<uint32_t(*)[32]>(z));
         tmem_ld32(tS + 64 * y + 32, *reinterpret_cast<uint32_t(*)[32]>(z + 32));
         tmem_wait_ld();
-        if ((j + 1) * kKvTile > first_seen) {
-          const int lim = seen - j * kKvTile - 64 * y;
+        if ((j0 + j + 1) * kKvTile > first_seen) {
+          const int lim = seen - (j0 + j) * kKvTile - 64 * y;
 #pragma unroll
           for (int c = 0; c < 64; ++c) z[c] = c < lim ? z[c] : 0xFF800000u;
         }
@@ -370,14 +374,24 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
       sum += *theirs;  // the same in both halves
       if (ok && __all_sync(0xffffffffu, wait_phase(bar(OF0 + x), 0, abort_flag, err_word))) {
         tc_fence_after();
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays NaN
         const bool live = r0 + row < n;
         const size_t at = (size_t)(c0 + r0 + row) * H + h;
+        // a whole item: the output row; a piece of one: its sums and reference, as they are
+        const float inv = slot >= 0 ? 1.f : sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays NaN
+        const size_t pr = slot >= 0 ? ((size_t)slot * gridDim.y + hh) * kQTile + 128 * x + row : 0;
+        if (slot >= 0 && y == 0) plan.ml_part[pr] = make_float2(ref == -INFINITY ? ref : ref * sl2, sum);
 #pragma unroll 1
         for (int c = 0; c < 64; c += 32) {
           uint32_t o[32], w[16];
           tmem_ld32(tO + c, o);
           tmem_wait_ld();
+          if (slot >= 0) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              reinterpret_cast<uint4*>(plan.o_part + pr * kDV + 64 * y + c)[q] =
+                  make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            continue;
+          }
 #pragma unroll
           for (int q = 0; q < 16; ++q)
             w[q] = cvt_bf16x2(__uint_as_float(o[2 * q]) * inv, __uint_as_float(o[2 * q + 1]) * inv);
@@ -388,7 +402,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
                   make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
           }
         }
-        if (lse && live && y == 0)
+        if (lse && live && y == 0 && slot < 0)
           lse[at] = sum > 0.f ? (ref * sl2 - kBias + log2f(sum)) * kLn2 : (sum == 0.f ? -INFINITY : sum);
       }
     }
@@ -401,11 +415,45 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
   }
 }
 
+// Items that were cut over the keys: out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k,
+// added in the order of the pieces. A warp per row, 16 bytes a lane; the partials of
+// a row are read once (HBM or L2-bound, 512 bytes a piece).
+__global__ void __launch_bounds__(256)
+join_kernel(ChunkPlan plan, uint16_t* __restrict__ out, float* __restrict__ lse, int H, int h0) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if ((int)blockIdx.x >= plan.hdr[2]) return;
+  const int4 jn = plan.join[blockIdx.x];  // {first slot, pieces, first row, rows}
+  const int hh = blockIdx.y, heads = gridDim.y, lane = threadIdx.x & 31;
+  for (int r = blockIdx.z * 8 + (threadIdx.x >> 5); r < jn.w; r += 8 * gridDim.z) {
+    auto at = [&](int k) { return ((size_t)(jn.x + k) * heads + hh) * kQTile + r; };
+    float m = -INFINITY;
+    for (int k = 0; k < jn.y; ++k) m = fmaxf(m, __ldcg(&plan.ml_part[at(k)].x));
+    float l = 0.f, a0 = 0.f, a1 = 0.f, a2 = 0.f, a3 = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < jn.y; ++k) {
+      const float2 ml = __ldcg(&plan.ml_part[at(k)]);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(plan.o_part + at(k) * kDV) + lane);
+      const float w = ml.x == m ? 1.f : ex2(ml.x - m);
+      l = fmaf(w, ml.y, l);
+      a0 = fmaf(w, o.x, a0);
+      a1 = fmaf(w, o.y, a1);
+      a2 = fmaf(w, o.z, a2);
+      a3 = fmaf(w, o.w, a3);
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const size_t row = (size_t)(jn.z + r) * H + h0 + hh;
+    reinterpret_cast<uint2*>(out + row * kDV)[lane] =
+        make_uint2(cvt_bf16x2(a0 * inv, a1 * inv), cvt_bf16x2(a2 * inv, a3 * inv));
+    if (lse && lane == 0) lse[row] = l > 0.f ? (m - kBias + log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const uint16_t* q_rope, uint16_t* out,
-                          float* lse, int B, int T, int H, int h0, int heads, int64_t cap, float scale,
-                          int32_t* err_word, cudaStream_t s) {
+                          float* lse, int B, int T, int H, int h0, int heads, int64_t cap, int slots,
+                          float scale, int32_t* err_word, cudaStream_t s) {
   CUtensorMap mk, mr, mv;
   const uint64_t dk[2] = {kDNope, (uint64_t)heads * cap}, sk[1] = {kDNope * 2};
   const uint64_t dr[2] = {kRow, (uint64_t)cap}, sr[1] = {kRow * 2};
@@ -415,8 +463,11 @@ cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const u
     return cudaErrorInvalidValue;
   cudaError_t e = smem_limit<attend_kernel>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attend_kernel, dim3(chunk_max_items(B, T), heads), dim3(kThreads), kSmem, s, mk, mr, mv, q_nope,
-                    q_rope, out, lse, plan, H, h0, cap, scale * 1.4426950408889634f, err_word);
+  e = launch_pdl(attend_kernel, dim3(chunk_max_items(B, T) + slots, heads), dim3(kThreads), kSmem, s, mk, mr, mv,
+                 q_nope, q_rope, out, lse, plan, H, h0, cap, scale * 1.4426950408889634f, err_word);
+  if (e != cudaSuccess || slots == 0) return e;
+  const int joins = chunk_max_items(B, T) < slots / 2 ? chunk_max_items(B, T) : slots / 2;  // two pieces at least
+  return launch_pdl(join_kernel, dim3(joins, heads, 8), dim3(256), 0, s, plan, out, lse, H, h0);
 }
 
 }  // namespace mla

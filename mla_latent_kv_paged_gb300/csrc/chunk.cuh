@@ -39,10 +39,15 @@ inline char* workspace_base(void* p) {
 }
 // Expanded form. cap: rows of the expanded cache (a multiple of kKvTile).
 struct ChunkPlan {
-  int32_t* hdr;      // [64] hdr[0] = query items, hdr[1] = expanded rows in use
+  int32_t* hdr;      // [64] hdr[0] = pieces, hdr[1] = expanded rows in use, hdr[2] = items in several pieces
   int32_t* pstart;   // [B + 1] first expanded row of each sequence, a multiple of kKvTile
   int32_t* len_eff;  // [B] context lengths in use (clamped; 0 without new rows)
   int4* item;        // [max_items] {sequence, first query row in it, rows of the sequence, its first row}
+  int4* piece;       // [max_items + slots][2] the item's four numbers; {first step over the keys, end step,
+                     // slot of the partial result or -1, 0}
+  int4* join;        // [slots] {first slot, pieces, first row of the item, its rows}
+  float* o_part;     // [slots * heads][256][128] sums of weighted values of a piece
+  float2* ml_part;   // [slots * heads][256] {reference maximum in log2 units, sum of weights}
   uint16_t* rows;    // [cap][576] bf16, the sequences' cache rows; zeros from a context's end to its padding
   uint16_t* k;       // [heads][cap][128] fp16 keys without position
   uint16_t* v;       // [heads][cap][128] fp16 values
@@ -54,7 +59,23 @@ inline int64_t chunk_cap(int64_t max_tokens, int B) {
 }
 inline int chunk_max_items(int B, int T) { return T / kQTile + (B < T ? B : T); }
 
-inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t cap, ChunkPlan* p) {
+// Work items are split over the keys only while they number fewer than four per
+// SM (the imbalance of the last of more waves is small), and into at most as many
+// pieces; a piece has at least kMinPiece steps.
+constexpr int kSplitCtas = 4 * 152;
+constexpr int kMinPiece = 4;
+// Room for partial results, in pieces; 0: no item is split.
+inline int chunk_slots(int B, int T, int heads, int64_t max_tokens) {
+  if ((int64_t)(T / kQTile) * heads >= kSplitCtas) return 0;
+  const int64_t by_steps = (int64_t)chunk_max_items(B, T) * ((max_tokens + kKvTile - 1) / kKvTile / kMinPiece);
+  const int64_t by_ctas = kSplitCtas / heads;
+  const int64_t n = by_steps < by_ctas ? by_steps : by_ctas;
+  return n < 2 ? 0 : (int)n;
+}
+
+inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_tokens, ChunkPlan* p) {
+  const int64_t cap = chunk_cap(max_tokens, B);
+  const int slots = chunk_slots(B, T, heads, max_tokens);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t o = off;
@@ -63,6 +84,8 @@ inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t cap, Chu
   };
   const size_t o_hdr = take(64 * 4), o_ps = take((size_t)(B + 1) * 4), o_le = take((size_t)B * 4);
   const size_t o_it = take((size_t)chunk_max_items(B, T) * 16);
+  const size_t o_pc = take(((size_t)chunk_max_items(B, T) + slots) * 32), o_j = take((size_t)slots * 16);
+  const size_t o_o = take((size_t)slots * heads * kQTile * kDV * 4), o_m = take((size_t)slots * heads * kQTile * 8);
   const size_t o_r = take((size_t)cap * kRow * 2);
   const size_t o_k = take((size_t)heads * cap * kDNope * 2), o_v = take((size_t)heads * cap * kDV * 2);
   if (base && p) {
@@ -71,6 +94,10 @@ inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t cap, Chu
     p->pstart = reinterpret_cast<int32_t*>(c + o_ps);
     p->len_eff = reinterpret_cast<int32_t*>(c + o_le);
     p->item = reinterpret_cast<int4*>(c + o_it);
+    p->piece = reinterpret_cast<int4*>(c + o_pc);
+    p->join = reinterpret_cast<int4*>(c + o_j);
+    p->o_part = reinterpret_cast<float*>(c + o_o);
+    p->ml_part = reinterpret_cast<float2*>(c + o_m);
     p->rows = reinterpret_cast<uint16_t*>(c + o_r);
     p->k = reinterpret_cast<uint16_t*>(c + o_k);
     p->v = reinterpret_cast<uint16_t*>(c + o_v);
@@ -121,14 +148,15 @@ cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* 
                                 int d_model, int num_pages, int page_size, int max_pages, double theta,
                                 void* workspace, int32_t* err_word, cudaStream_t s);
 cudaError_t launch_chunk_plan(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
-                              int64_t max_total, const ChunkPlan& plan, int32_t* err_word, cudaStream_t s);
+                              int64_t max_total, int heads, const ChunkPlan& plan, int32_t* err_word,
+                              cudaStream_t s);
 cudaError_t launch_chunk_rows(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
                               const ChunkRows& rows, int32_t* err_word, cudaStream_t s);
 // keys and values of heads [h0, h0 + heads) of every expanded row
 cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uint16_t* w_uv, int H, int h0, int heads,
                           int64_t cap, int32_t* err_word, cudaStream_t s);
 cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const uint16_t* q_rope, uint16_t* out,
-                          float* lse, int B, int T, int H, int h0, int heads, int64_t cap, float scale,
-                          int32_t* err_word, cudaStream_t s);
+                          float* lse, int B, int T, int H, int h0, int heads, int64_t cap, int slots,
+                          float scale, int32_t* err_word, cudaStream_t s);
 
 }  // namespace mla

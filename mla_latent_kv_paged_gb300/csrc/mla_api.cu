@@ -402,7 +402,7 @@ size_t mla_attend_chunk_workspace_bytes(int B, int T, int H, int64_t max_tokens,
     return G < 1 ? 0 : chunk_rows_layout(nullptr, T, H, G, nullptr);
   }
   const int64_t cap = chunk_cap(max_tokens, B);
-  return chunk_layout(nullptr, B, T, chunk_head_group(H, cap), cap, nullptr);
+  return chunk_layout(nullptr, B, T, chunk_head_group(H, cap), max_tokens, nullptr);
 }
 
 mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
@@ -454,11 +454,11 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
     return st;
   }
   const int64_t cap = chunk_cap(max_tokens, B);
-  const int group = chunk_head_group(H, cap);
-  if (workspace_bytes < chunk_layout(nullptr, B, T, group, cap, nullptr)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const int group = chunk_head_group(H, cap), slots = chunk_slots(B, T, group, max_tokens);
+  if (workspace_bytes < chunk_layout(nullptr, B, T, group, max_tokens, nullptr)) return MLA_ERR_WORKSPACE_TOO_SMALL;
   ChunkPlan plan;
-  chunk_layout(workspace, B, T, group, cap, &plan);
-  mla_status st = launch_status(launch_chunk_plan(seq_lens, cu, B, T, max_tokens_seq, max_tokens, plan, err_word, s));
+  chunk_layout(workspace, B, T, group, max_tokens, &plan);
+  mla_status st = launch_status(launch_chunk_plan(seq_lens, cu, B, T, max_tokens_seq, max_tokens, group, plan, err_word, s));
   // the contexts' rows, each sequence from its own multiple of 128 on, zeros behind its end
   if (st == MLA_OK)
     st = launch_status(launch_read_kv(cache, fp8_scales, block_table, plan.len_eff, nullptr, plan.pstart, plan.rows, B,
@@ -467,7 +467,7 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
     const int heads = H - h0 < group ? H - h0 : group;
     st = launch_status(launch_expand(plan, w_uk, w_uv, H, h0, heads, cap, err_word, s));
     if (st == MLA_OK)
-      st = launch_status(launch_attend(plan, q_nope, q_rope, out, lse, B, T, H, h0, heads, cap, softmax_scale,
+      st = launch_status(launch_attend(plan, q_nope, q_rope, out, lse, B, T, H, h0, heads, cap, slots, softmax_scale,
                                        err_word, s));
   }
   return st;

@@ -461,3 +461,36 @@ def test_back_to_back_calls_share_a_workspace(mla):
     for f, c, g in got:
         want, _, bound = ref.attend(c)
         check(g, want, bound[f], f)
+
+
+@pytest.mark.parametrize("new,lens,H", [([5], [4000], 1), ([200, 3, 300], [3000, 2500, 300], 2),
+                                        ([300], [20000], 3), ([1, 1], [128, 129], 1), ([513], [1300], 5)])
+def test_attend_cut_over_the_keys(mla, err, new, lens, H):
+    """Few heads and rows on long contexts: the items are cut over the keys and joined."""
+    import torch
+    c = ref.Chunk(new, lens, H=H, seed=50, pad_rows=3)
+    want, lse_want, bound = ref.attend(c)
+    out = torch.full((c.T, H, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.T, H), 5.0, device="cuda")
+    kw = dict(max_tokens=sum(lens), form="expanded", lse=lse, err_word=err)
+    mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), out=out, **kw)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(out[:c.total], want, bound["expanded"], "cut")
+    assert (lse[:c.total].double() - lse_want).abs().max().item() <= 0.02
+    assert (out[c.total:] == 3.0).all() and (lse[c.total:] == 5.0).all()
+    again = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), **kw)
+    assert torch.equal(again[:c.total], out[:c.total])
+
+
+def test_attend_cut_rising_scores(mla, err):
+    """Pieces whose references lie far apart."""
+    import torch
+    c = ref.Chunk([40], [6000], H=1, seed=51)
+    s = torch.arange(6000, device="cuda", dtype=torch.float32)
+    c.cache.view(-1, 576)[c.rows(0), 512] = (s * (64.0 / 6000)).to(torch.bfloat16)
+    c.q_rope[::2, :, 0], c.q_rope[1::2, :, 0] = 32.0, -32.0
+    want, _, bound = ref.attend(c)
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=6000, form="expanded",
+                           err_word=err)
+    check(got, want, bound["expanded"], "rising")
