@@ -5,13 +5,15 @@
 // bf16 operands, fp32 sums, rounded once to fp16: three more mantissa bits than
 // bf16 for the two products that follow, |value| < 65520 (beyond: MLA_ERR_RANGE).
 //
-// Tensor-bound: 2 x 512 x 256 flop per (token, head). A CTA keeps 128 tokens'
-// latents in shared memory (128 KB) and streams the weights of consecutive heads
-// past them (a [256 = 128 of W_UK, 128 of W_UV][32] box per ring slot, N = 256
-// MMAs), so each unit of work reads its 256 KB of weights from L2 and nothing
-// else; two accumulators in tensor memory let the write-out of one head run
-// under the MMAs of the next. The units (token tile, head) are dealt out as
-// equal contiguous runs, one run per CTA.
+// Tensor-bound: 2 x 512 x 256 flop per (token, head). A pair of CTAs (one
+// M = 256, N = 256 MMA over two SMs) keeps 2 x 128 tokens' latents in shared
+// memory (128 KB each) and streams the weights of consecutive heads past them:
+// the even CTA holds the W_UK half of each ring slot, the odd one the W_UV half
+// ([128 rows][64 columns]), so a CTA reads 128 KB of weights from L2 per 256
+// tokens and head (one CTA on its own, 256 KB per 128 tokens, was bound by that
+// stream: 500 us for 128 heads of 16384 tokens). Two accumulators in tensor
+// memory let the write-out of one head run under the MMAs of the next. The units
+// (pair of token tiles, head) are dealt out as equal contiguous runs.
 //
 // A value row that is not finite is written as zeros, with a NaN in its key row:
 // the queries that see the token get NaN, those that do not are untouched (a
@@ -25,10 +27,10 @@ namespace {
 using namespace sm100;
 
 constexpr int kStages = 6;
-constexpr int kKB = kDC / 32;                       // 16 boxes of 32 latent columns
+constexpr int kKB = kDC / 64;                       // 8 boxes of 64 latent columns
 constexpr uint32_t kASlab = 128 * 128;              // [128 tokens][64 columns], 128B swizzle
 constexpr uint32_t kABytes = 8 * kASlab;
-constexpr uint32_t kBHalf = 128 * 64, kBBytes = 2 * kBHalf;  // [256 rows][32 columns], 64B swizzle
+constexpr uint32_t kBBytes = 128 * 128;             // this CTA's half of B: [128 rows][64 columns], 128B swizzle
 constexpr uint32_t kOffB = kABytes, kOffBar = kOffB + kStages * kBBytes;
 enum { FULL0 = 0, EMPTY0 = FULL0 + kStages, AF = EMPTY0 + kStages, AE, DF0, DE0 = DF0 + 2, MD = DE0 + 2, kBars };
 constexpr uint32_t kOffSlots = kOffBar + 8 * kBars;
@@ -61,13 +63,14 @@ __device__ __forceinline__ uint32_t write_row(uint32_t taddr, uint16_t* dst) {
   return top;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constant__ CUtensorMap map_uk,
               const __grid_constant__ CUtensorMap map_uv, ChunkPlan plan, int h0, int heads, int64_t cap,
               int32_t* err_word) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = warp_index(), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
   auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffSlots + 4);
@@ -85,38 +88,45 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
     mbar_init(bar(MD), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(DF0 + i), 1);
-      mbar_init(bar(DE0 + i), 128);
+      mbar_init(bar(DE0 + i), 8);  // the write-out warps of both CTAs
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 5) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any copy or arrive across the pair
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t units = (int64_t)(plan.hdr[1] / kKvTile) * heads;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  // token tiles in pairs; CTA `rank` has tile 2m + rank (past the last one: computed, not written)
+  const int tiles = plan.hdr[1] / kKvTile;
+  const int64_t units = (int64_t)((tiles + 1) / 2) * heads;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int64_t u0 = units * pair / pairs, u1 = units * (pair + 1) / pairs;
 
   if (warp == 4) {
     if (elect()) {
       prefetch_tmap(&map_rows);
-      prefetch_tmap(&map_uk);
-      prefetch_tmap(&map_uv);
+      const CUtensorMap* map_w = rank == 0 ? &map_uk : &map_uv;
+      prefetch_tmap(map_w);
       const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
+      // the pair's copies complete on the even CTA's barriers, which it arms for both
+      const uint32_t af = mapa(bar(AF), 0);
       bool ok = true;
       int it = 0, loads = 0;
       for (int64_t u = u0; u < u1 && ok; ++u) {
         const int m = (int)(u / heads), h = h0 + (int)(u % heads);
-        if (u == u0 || u % heads == 0) {  // the next 128 tokens, once the MMAs on the last ones are done
+        if (u == u0 || u % heads == 0) {  // the next tokens, once the MMAs on the last ones are done
           if (loads > 0 && !wait_phase(bar(AE), (uint32_t)((loads - 1) & 1), abort_flag, err_word)) break;
-          mbar_arrive_expect_tx(bar(AF), kABytes);
-          for (int c = 0; c < 8; ++c) tma_load_2d(sbase + c * kASlab, &map_rows, bar(AF), 64 * c, m * 128, stream);
+          if (rank == 0) mbar_arrive_expect_tx(bar(AF), 2 * kABytes);
+          for (int c = 0; c < 8; ++c)
+            tma_load_2d_pair(sbase + c * kASlab, &map_rows, af, 64 * c, (2 * m + (int)rank) * 128, stream);
           ++loads;
         }
         for (int kb = 0; kb < kKB; ++kb, ++it) {
@@ -125,27 +135,26 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
             ok = false;
             break;
           }
-          const uint32_t dst = sbase + kOffB + st * kBBytes;
-          mbar_arrive_expect_tx(bar(FULL0 + st), kBBytes);
-          tma_load_2d(dst, &map_uk, bar(FULL0 + st), 32 * kb, h * 128, keep);
-          tma_load_2d(dst + kBHalf, &map_uv, bar(FULL0 + st), 32 * kb, h * 128, keep);
+          if (rank == 0) mbar_arrive_expect_tx(bar(FULL0 + st), 2 * kBBytes);
+          tma_load_2d_pair(sbase + kOffB + st * kBBytes, map_w, mapa(bar(FULL0 + st), 0), 64 * kb, h * 128, keep);
         }
       }
-      if (*abort_flag) {  // let the copies in flight land before the CTA can exit
-        for (int i = it > kStages ? it - kStages : 0; i < it; ++i) {
-          const long long t0 = clock64();
+      if (rank == 0 && *abort_flag) {
+        // let the pair's copies in flight land before the pair can exit (the odd CTA
+        // waits for this one below; where it issued fewer, the limit ends the wait)
+        const long long t0 = clock64();
+        for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
           while (!mbar_try_wait(bar(FULL0 + i % kStages), (uint32_t)((i / kStages) & 1)) &&
                  clock64() - t0 < kWaitLimitCycles) {
           }
-        }
       }
     }
   } else if (warp == 5) {
-    if (elect()) {
-      const uint32_t idesc = idesc_bf16(128, 256, false, false);
+    if (rank == 0 && elect()) {
+      const uint32_t idesc = idesc_bf16(256, 256, false, false);
       auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
       const uint64_t ad0 = smem_desc(0, 16, 1024, kSwizzle128B) + da(sbase);
-      const uint64_t bd0 = smem_desc(0, 16, 512, kSwizzle64B);
+      const uint64_t bd0 = smem_desc(0, 16, 1024, kSwizzle128B);
       bool ok = true;
       int it = 0, loads = 0, n = 0;
       for (int64_t u = u0; u < u1 && ok; ++u, ++n) {
@@ -154,7 +163,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
           if (!wait_phase(bar(AF), (uint32_t)(loads & 1), abort_flag, err_word)) break;
           ++loads;
         }
-        if (n >= 2 && !wait_phase(bar(DE0 + buf), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, err_word)) break;
+        if (n >= 2 && !wait_phase(bar(DE0 + buf), (uint32_t)(((n >> 1) - 1) & 1), abort_flag, err_word, true)) break;
         for (int kb = 0; kb < kKB; ++kb, ++it) {
           const int st = it % kStages;
           if (!wait_phase(bar(FULL0 + st), (uint32_t)((it / kStages) & 1), abort_flag, err_word)) {
@@ -162,17 +171,16 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
             break;
           }
           tc_fence_after();
-          const uint64_t ad = ad0 + (((kb >> 1) * kASlab + (kb & 1) * 64) >> 4);
-          const uint64_t bd = bd0 + da(sbase + kOffB + st * kBBytes);
-          mma_ss(tmem + 256 * buf, ad, bd, idesc, kb > 0 ? 1u : 0u);
-          mma_ss(tmem + 256 * buf, ad + 2, bd + 2, idesc, 1u);
-          mma_commit(bar(EMPTY0 + st));
+          const uint64_t ad = ad0 + (kb * kASlab >> 4), bd = bd0 + da(sbase + kOffB + st * kBBytes);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_ss_pair(tmem + 256 * buf, ad + 2 * k, bd + 2 * k, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+          mma_commit_pair(bar(EMPTY0 + st), 3);
         }
         if (!ok) break;
-        mma_commit(bar(DF0 + buf));
-        if ((u + 1) % heads == 0 && u + 1 < u1) mma_commit(bar(AE));
+        mma_commit_pair(bar(DF0 + buf), 3);
+        if ((u + 1) % heads == 0 && u + 1 < u1) mma_commit_pair(bar(AE), 3);
       }
-      mma_commit(bar(MD));
+      mma_commit_pair(bar(MD), 1);
       wait_mmas(bar(MD));
     }
   } else {
@@ -182,12 +190,17 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
       if (!__all_sync(0xffffffffu, wait_phase(bar(DF0 + buf), (uint32_t)((n >> 1) & 1), abort_flag, err_word))) break;
       tc_fence_after();
       const uint32_t taddr = tmem + 256 * buf + ((uint32_t)(warp * 32) << 16);
-      const int64_t at = ((int64_t)hh * cap + m * 128 + warp * 32 + lane) * 128;
+      const int tile = 2 * m + (int)rank;
+      const int64_t at = ((int64_t)hh * cap + (int64_t)tile * 128 + warp * 32 + lane) * 128;
       uint16_t *kd = plan.k + at, *vd = plan.v + at;
-      const uint32_t vtop = write_row(taddr + 128, vd);
-      const uint32_t ktop = write_row(taddr, kd);
+      uint32_t vtop = 0, ktop = 0;
+      if (tile < tiles) {
+        vtop = write_row(taddr + 128, vd);
+        ktop = write_row(taddr, kd);
+      }
       tc_fence_before();
-      mbar_arrive(bar(DE0 + buf));
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(mapa(bar(DE0 + buf), 0));
       if (max(vtop, ktop) >= kF16Limit) {
         if ((vtop >= kF16Limit && vtop < 0x7F800000u) || (ktop >= kF16Limit && ktop < 0x7F800000u))
           report_error(err_word, MLA_ERR_RANGE);
@@ -200,9 +213,10 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // nothing of the pair is under way: MMAs, copies, arrives
   if (warp == 5) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -213,17 +227,18 @@ cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uin
   CUtensorMap mr, mk, mv;
   const uint64_t dr[2] = {kRow, (uint64_t)cap}, sr[1] = {kRow * 2};
   const uint64_t dw[2] = {kDC, (uint64_t)H * 128}, sw[1] = {kDC * 2};
-  const uint32_t br[2] = {64, 128}, bw[2] = {32, 128};
-  if (!make_tmap(&mr, plan.rows, 2, dr, sr, br, 128) || !make_tmap(&mk, w_uk, 2, dw, sw, bw, 64) ||
-      !make_tmap(&mv, w_uv, 2, dw, sw, bw, 64))
+  const uint32_t br[2] = {64, 128};
+  if (!make_tmap(&mr, plan.rows, 2, dr, sr, br, 128) || !make_tmap(&mk, w_uk, 2, dw, sw, br, 128) ||
+      !make_tmap(&mv, w_uv, 2, dw, sw, br, 128))
     return cudaErrorInvalidValue;
   cudaError_t e = smem_limit<expand_kernel>(kSmem);
   int dev = 0, sms = 0;
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int64_t units = cap / kKvTile * heads;
-  return launch_pdl(expand_kernel, dim3((unsigned)(units < sms ? units : sms)), dim3(kThreads), kSmem, s, mr, mk, mv,
+  const int64_t units = (cap / kKvTile + 1) / 2 * heads;
+  const int pairs = sms / 2;
+  return launch_pdl(expand_kernel, dim3(2 * (unsigned)(units < pairs ? units : pairs)), dim3(kThreads), kSmem, s, mr, mk, mv,
                     plan, h0, heads, cap, err_word);
 }
 
