@@ -15,7 +15,7 @@
 // memory let the write-out of one head run under the MMAs of the next. The units
 // (pair of token tiles, head) are dealt out as equal contiguous runs.
 //
-// A value row that is not finite is written as zeros, with a NaN in its key row:
+// Half a value row that is not finite is written as zeros, with a NaN in its key row:
 // the queries that see the token get NaN, those that do not are untouched (a
 // zero weight times a NaN value would reach them).
 #include "chunk.cuh"
@@ -36,7 +36,7 @@ enum { FULL0 = 0, EMPTY0 = FULL0 + kStages, AF = EMPTY0 + kStages, AE, DF0, DE0 
 constexpr uint32_t kOffSlots = kOffBar + 8 * kBars;
 constexpr uint32_t kSmem = kOffSlots + 16;
 static_assert(kSmem <= 232448, "shared memory budget");
-constexpr int kThreads = 192;  // warps 0..3 write-out, 4 producer, 5 MMA issuer
+constexpr int kThreads = 320;  // warps 0..7 write-out, 8 producer, 9 MMA issuer
 constexpr uint32_t kF16Limit = 0x477FF000u;  // 65520.0f: from here on fp16 rounds to infinity
 
 __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
@@ -45,20 +45,18 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
                : "memory");
 }
 
-// 128 accumulator columns of one token as fp16 to dst; the largest |value| as bits.
-__device__ __forceinline__ uint32_t write_row(uint32_t taddr, uint16_t* dst) {
+// 64 values of one token as fp16 to dst; the largest |value| as bits.
+__device__ __forceinline__ uint32_t write_row(const uint32_t (&r)[64], uint16_t* dst) {
   uint32_t top = 0;
-#pragma unroll 1
-  for (int c0 = 0; c0 < 128; c0 += 32) {
-    uint32_t r[32], w[16];
-    tmem_ld32(taddr + c0, r);
-    tmem_wait_ld();
 #pragma unroll
-    for (int q = 0; q < 32; ++q) top = max(top, r[q] & 0x7FFFFFFFu);
+  for (int c = 0; c < 64; c += 16) {
+    uint32_t w[8];
 #pragma unroll
-    for (int q = 0; q < 16; ++q) w[q] = cvt_f16x2(__uint_as_float(r[2 * q]), __uint_as_float(r[2 * q + 1]));
-    st_global_32(dst + c0, w);
-    st_global_32(dst + c0 + 16, w + 8);
+    for (int q = 0; q < 8; ++q) {
+      top = max(top, max(r[c + 2 * q] & 0x7FFFFFFFu, r[c + 2 * q + 1] & 0x7FFFFFFFu));
+      w[q] = cvt_f16x2(__uint_as_float(r[c + 2 * q]), __uint_as_float(r[c + 2 * q + 1]));
+    }
+    st_global_32(dst + c, w);
   }
   return top;
 }
@@ -88,12 +86,12 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
     mbar_init(bar(MD), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(DF0 + i), 1);
-      mbar_init(bar(DE0 + i), 8);  // the write-out warps of both CTAs
+      mbar_init(bar(DE0 + i), 16);  // the write-out warps of both CTAs
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
     tmem_relinquish_pair();
   }
@@ -110,7 +108,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int64_t u0 = units * pair / pairs, u1 = units * (pair + 1) / pairs;
 
-  if (warp == 4) {
+  if (warp == 8) {
     if (elect()) {
       prefetch_tmap(&map_rows);
       const CUtensorMap* map_w = rank == 0 ? &map_uk : &map_uv;
@@ -149,7 +147,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
           }
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     if (rank == 0 && elect()) {
       const uint32_t idesc = idesc_bf16(256, 256, false, false);
       auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
@@ -189,23 +187,30 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
       const int m = (int)(u / heads), hh = (int)(u % heads), buf = n & 1;
       if (!__all_sync(0xffffffffu, wait_phase(bar(DF0 + buf), (uint32_t)((n >> 1) & 1), abort_flag, err_word))) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + 256 * buf + ((uint32_t)(warp * 32) << 16);
-      const int tile = 2 * m + (int)rank;
-      const int64_t at = ((int64_t)hh * cap + (int64_t)tile * 128 + warp * 32 + lane) * 128;
+      // a warp per 32 tokens and half of the columns of keys and values; the
+      // accumulator is given back before anything is stored (the remote arrive
+      // releases, so it would wait for the stores)
+      const int quad = warp & 3, half = warp >> 2, tile = 2 * m + (int)rank;
+      const uint32_t taddr = tmem + 256 * buf + 64 * half + ((uint32_t)(quad * 32) << 16);
+      const int64_t at = ((int64_t)hh * cap + (int64_t)tile * 128 + quad * 32 + lane) * 128 + 64 * half;
       uint16_t *kd = plan.k + at, *vd = plan.v + at;
-      uint32_t vtop = 0, ktop = 0;
-      if (tile < tiles) {
-        vtop = write_row(taddr + 128, vd);
-        ktop = write_row(taddr, kd);
+      uint32_t kr[64], vr[64];
+#pragma unroll
+      for (int c = 0; c < 64; c += 32) {
+        tmem_ld32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(kr + c));
+        tmem_ld32(taddr + 128 + c, *reinterpret_cast<uint32_t(*)[32]>(vr + c));
       }
+      tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_remote(mapa(bar(DE0 + buf), 0));
+      if (tile >= tiles) continue;
+      const uint32_t vtop = write_row(vr, vd), ktop = write_row(kr, kd);
       if (max(vtop, ktop) >= kF16Limit) {
         if ((vtop >= kF16Limit && vtop < 0x7F800000u) || (ktop >= kF16Limit && ktop < 0x7F800000u))
           report_error(err_word, MLA_ERR_RANGE);
         if (vtop >= kF16Limit) {
-          for (int q = 0; q < 16; ++q) reinterpret_cast<uint4*>(vd)[q] = make_uint4(0, 0, 0, 0);
+          for (int q = 0; q < 8; ++q) reinterpret_cast<uint4*>(vd)[q] = make_uint4(0, 0, 0, 0);
           kd[0] = 0x7FFF;  // NaN
         }
       }
@@ -214,7 +219,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // nothing of the pair is under way: MMAs, copies, arrives
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
