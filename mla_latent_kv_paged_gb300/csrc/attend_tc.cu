@@ -124,20 +124,16 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // the piece: rows [q0, q0 + 256) of sequence b, steps [j0, j1) over the keys
-  int4 item = make_int4(-1, 0, 0, 0), part = make_int4(0, 0, -1, 0);
-  if ((int)blockIdx.x < plan.hdr[0]) {
-    item = plan.piece[2 * blockIdx.x];
-    part = plan.piece[2 * blockIdx.x + 1];
-  }
-  const int b = item.x, q0 = item.y, n = item.z, c0 = item.w;
-  const int j0 = part.x, slot = part.z;
-  const int L = b >= 0 ? plan.len_eff[b] : 0;
-  const int64_t k0 = b >= 0 ? plan.pstart[b] + (int64_t)j0 * kKvTile : 0;  // first expanded row of the piece
+  // the piece: query rows [q0, q0 + 256) of n, steps [j0, j1) over the keys (read
+  // beside the number of pieces; what lies past it is not used)
+  const int4 qp = plan.piece[2 * blockIdx.x], kp = plan.piece[2 * blockIdx.x + 1];
+  const bool work = (int)blockIdx.x < plan.hdr[0];
+  const int q0 = qp.x, n = qp.y, c0 = qp.z, L = qp.w, j0 = kp.x, slot = kp.z;
+  const int64_t k0 = kp.w + (int64_t)j0 * kKvTile;  // first expanded row of the piece
   const bool two = n - q0 > 128;
   auto steps = [&](int x) {  // of tile x in this piece: up to the last token that its last row sees
-    if (b < 0 || (x == 1 && !two)) return 0;
-    return min((L - n + min(q0 + 128 * (x + 1), n) + kKvTile - 1) / kKvTile, part.y) - j0;
+    if (!work || (x == 1 && !two)) return 0;
+    return min((L - n + min(q0 + 128 * (x + 1), n) + kKvTile - 1) / kKvTile, kp.y) - j0;
   };
   const int n0 = steps(0), n1 = steps(1), nkv = max(n0, n1);
 
@@ -254,28 +250,38 @@ attend_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__
     if (nx > 0) {
       // the tile's queries: content as fp16 (exact for bf16 values of normal fp16
       // size), position as it is, into the swizzled slabs
+      // (all twelve loads of a thread in flight together)
+      uint4 wn[8], wr[4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = tid + 256 * k, r = i >> 4, ch = i & 15;
+        wn[k] = make_uint4(0, 0, 0, 0);
+        if (r0 + r < n) wn[k] = __ldg(reinterpret_cast<const uint4*>(q_nope + ((size_t)(c0 + r0 + r) * H + h) * kDNope) + ch);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = tid + 256 * k, r = i >> 3, ch = i & 7;
+        wr[k] = make_uint4(0, 0, 0, 0);
+        if (r0 + r < n) wr[k] = __ldg(reinterpret_cast<const uint4*>(q_rope + ((size_t)(c0 + r0 + r) * H + h) * kDR) + ch);
+      }
       uint32_t top = 0;
-#pragma unroll 4
-      for (int i = tid; i < 128 * 16; i += 256) {
-        const int r = i >> 4, ch = i & 15;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r0 + r < n) w = __ldg(reinterpret_cast<const uint4*>(q_nope + ((size_t)(c0 + r0 + r) * H + h) * kDNope) + ch);
-        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int i = tid + 256 * k, r = i >> 4, ch = i & 15;
+        const uint32_t e[4] = {wn[k].x, wn[k].y, wn[k].z, wn[k].w};
         uint32_t f[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          f[k] = cvt_f16x2(bf16_lo(e[k]), bf16_hi(e[k]));
-          top = max(top, max((e[k] << 16) & 0x7FFFFFFFu, e[k] & 0x7FFF0000u));
+        for (int q = 0; q < 4; ++q) {
+          f[q] = cvt_f16x2(bf16_lo(e[q]), bf16_hi(e[q]));
+          top = max(top, max((e[q] << 16) & 0x7FFFFFFFu, e[q] & 0x7FFF0000u));
         }
         st_shared_v4(sbase + (3 * x + (ch >> 3)) * kSlab + r * 128 + (((ch & 7) ^ (r & 7)) << 4), f[0], f[1], f[2], f[3]);
       }
       if (top >= 0x477FF000u && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
-#pragma unroll 4
-      for (int i = tid; i < 128 * 8; i += 256) {
-        const int r = i >> 3, ch = i & 7;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r0 + r < n) w = __ldg(reinterpret_cast<const uint4*>(q_rope + ((size_t)(c0 + r0 + r) * H + h) * kDR) + ch);
-        st_shared_v4(sbase + (3 * x + 2) * kSlab + r * 128 + ((ch ^ (r & 7)) << 4), w.x, w.y, w.z, w.w);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = tid + 256 * k, r = i >> 3, ch = i & 7;
+        st_shared_v4(sbase + (3 * x + 2) * kSlab + r * 128 + ((ch ^ (r & 7)) << 4), wr[k].x, wr[k].y, wr[k].z, wr[k].w);
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(QF0 + x));

@@ -43,8 +43,9 @@ struct ChunkPlan {
   int32_t* pstart;   // [B + 1] first expanded row of each sequence, a multiple of kKvTile
   int32_t* len_eff;  // [B] context lengths in use (clamped; 0 without new rows)
   int4* item;        // [max_items] {sequence, first query row in it, rows of the sequence, its first row}
-  int4* piece;       // [max_items + slots][2] the item's four numbers; {first step over the keys, end step,
-                     // slot of the partial result or -1, 0}
+  int4* piece;       // [max_items + slots][2] {first query row, rows of the sequence, its first row, its context};
+                     // {first step over the keys, end step, slot of the partial result or -1, first expanded
+                     // row of the sequence}: all that a work item needs, in one read
   int4* join;        // [slots] {first slot, pieces, first row of the item, its rows}
   float* o_part;     // [slots * heads][256][128] sums of weighted values of a piece
   float2* ml_part;   // [slots * heads][256] {reference maximum in log2 units, sum of weights}

@@ -145,9 +145,9 @@ chunk_plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restric
     if (q > 0) {
       const int4 it = plan.item[i];
       for (int k = 0; k < q; ++k) {
-        plan.piece[2 * (k0 + k)] = it;
+        plan.piece[2 * (k0 + k)] = make_int4(it.y, it.z, it.w, plan.len_eff[it.x]);
         plan.piece[2 * (k0 + k) + 1] = make_int4((int)((int64_t)k * st / q), (int)((int64_t)(k + 1) * st / q),
-                                                 q > 1 ? (int)s0 + k : -1, 0);
+                                                 q > 1 ? (int)s0 + k : -1, plan.pstart[it.x]);
       }
       if (q > 1) plan.join[n0] = make_int4((int)s0, q, it.w + it.y, min(kQTile, it.z - it.y));
     }
