@@ -40,6 +40,7 @@ inline char* workspace_base(void* p) {
 // Expanded form. cap: rows of the expanded cache (a multiple of kKvTile).
 struct ChunkPlan {
   int32_t* hdr;      // [64] hdr[0] = pieces, hdr[1] = expanded rows in use, hdr[2] = items in several pieces
+  int32_t* counter;  // [kMaxHeads] the next item of each round of heads, beyond one per CTA
   int32_t* pstart;   // [B + 1] first expanded row of each sequence, a multiple of kKvTile
   int32_t* len_eff;  // [B] context lengths in use (clamped; 0 without new rows)
   int4* item;        // [max_items] {sequence, first query row in it, rows of the sequence, its first row}
@@ -83,7 +84,7 @@ inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_toke
     off = align256(off + bytes);
     return o;
   };
-  const size_t o_hdr = take(64 * 4), o_ps = take((size_t)(B + 1) * 4), o_le = take((size_t)B * 4);
+  const size_t o_hdr = take(64 * 4), o_cn = take(kMaxHeads * 4), o_ps = take((size_t)(B + 1) * 4), o_le = take((size_t)B * 4);
   const size_t o_it = take((size_t)chunk_max_items(B, T) * 16);
   const size_t o_pc = take(((size_t)chunk_max_items(B, T) + slots) * 32), o_j = take((size_t)slots * 16);
   const size_t o_o = take((size_t)slots * heads * kQTile * kDV * 4), o_m = take((size_t)slots * heads * kQTile * 8);
@@ -92,6 +93,7 @@ inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_toke
   if (base && p) {
     char* c = workspace_base(base);
     p->hdr = reinterpret_cast<int32_t*>(c + o_hdr);
+    p->counter = reinterpret_cast<int32_t*>(c + o_cn);
     p->pstart = reinterpret_cast<int32_t*>(c + o_ps);
     p->len_eff = reinterpret_cast<int32_t*>(c + o_le);
     p->item = reinterpret_cast<int4*>(c + o_it);
@@ -157,7 +159,7 @@ cudaError_t launch_chunk_rows(const int32_t* seq_lens, const int32_t* cu, int B,
 cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uint16_t* w_uv, int H, int h0, int heads,
                           int64_t cap, int32_t* err_word, cudaStream_t s);
 cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const uint16_t* q_rope, uint16_t* out,
-                          float* lse, int B, int T, int H, int h0, int heads, int64_t cap, int slots,
+                          float* lse, int B, int T, int H, int h0, int heads, int64_t cap, int slots, int round,
                           float scale, int32_t* err_word, cudaStream_t s);
 
 }  // namespace mla

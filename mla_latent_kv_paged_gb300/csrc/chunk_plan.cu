@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kFixed = 3;  // a piece's start and end, in steps (about 1.6 us each)
+constexpr int kRanked = 512;
 constexpr int kJoin = 4;   // the launch that joins the pieces, in steps
 
 // Exclusive scan over the block's threads of a 64-bit value; *total = the sum.
@@ -63,6 +64,7 @@ chunk_plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restric
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
   const int tid = threadIdx.x;
+  if (tid < kMaxHeads) plan.counter[tid] = 0;
   int64_t row_base = 0, item_base = 0, token_base = 0;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
     const int b = b0 + tid;
@@ -134,14 +136,30 @@ chunk_plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restric
   const int parts = best == ~0ull ? 1 : (int)(best & 255) + 1;
   const int p = parts == 1 ? INT32_MAX / 2 : (longest + parts - 1) / parts;
   int64_t piece_base = 0, slot_base = 0, join_base = 0;
+  // listed longest first where they are few enough to be ranked by comparison (the
+  // items of a sequence come that way already)
+  const bool ranked = items <= kRanked;
+  if (ranked) {
+    for (int i = tid; i < items; i += kThreads) steps_s[i] = steps_of(i);
+    __syncthreads();
+  }
   for (int i0 = 0; i0 < items; i0 += kThreads) {
     const int i = i0 + tid;
     const int st = i < items ? steps_of(i) : 0;
     const int q = st > 0 ? (st + p - 1) / p : 0;
     int64_t piece_sum, slot_sum, join_sum;
-    const int64_t k0 = piece_base + block_scan(q, &piece_sum);
+    int64_t k0 = piece_base + block_scan(q, &piece_sum);
     const int64_t s0 = slot_base + block_scan(q > 1 ? q : 0, &slot_sum);
     const int64_t n0 = join_base + block_scan(q > 1 ? 1 : 0, &join_sum);
+    if (ranked && q > 0) {  // the pieces of every item whose pieces are longer, then of those before it
+      k0 = 0;
+      for (int o = 0; o < items; ++o) {
+        const int so = steps_s[o], qo = (so + p - 1) / p;
+        // so / qo > st / q, in integers
+        const int64_t d = (int64_t)so * q - (int64_t)st * qo;
+        if (qo > 0 && (d > 0 || (d == 0 && o < i))) k0 += qo;
+      }
+    }
     if (q > 0) {
       const int4 it = plan.item[i];
       for (int k = 0; k < q; ++k) {

@@ -467,8 +467,8 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
     const int heads = H - h0 < group ? H - h0 : group;
     st = launch_status(launch_expand(plan, w_uk, w_uv, H, h0, heads, cap, err_word, s));
     if (st == MLA_OK)
-      st = launch_status(launch_attend(plan, q_nope, q_rope, out, lse, B, T, H, h0, heads, cap, slots, softmax_scale,
-                                       err_word, s));
+      st = launch_status(launch_attend(plan, q_nope, q_rope, out, lse, B, T, H, h0, heads, cap, slots, h0 / group,
+                                       softmax_scale, err_word, s));
   }
   return st;
 }
