@@ -488,9 +488,10 @@ mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t
  * in one of two forms of the same sums (form = MLA_CHUNK_AUTO chooses by the
  * chunk's mean length T / B):
  *   MLA_CHUNK_EXPANDED  keys and values of every head are expanded from the latents
- *     first (fp16, the score and weight products on fp16 and bf16 operands, fp32
- *     sums). For long chunks. An expanded key or value of 65520 or more is reported
- *     as MLA_ERR_RANGE; below 2^-14 their resolution is 2^-25.
+ *     first, and rounded to fp16 (so are content queries, the rows of an FP8 cache
+ *     and, with one, the weights; fp32 sums everywhere). For long chunks. Any of
+ *     these of 65520 or more is reported as MLA_ERR_RANGE; below 2^-14 their
+ *     resolution is 2^-25.
  *   MLA_CHUNK_ABSORBED  every new token is decoded over the latents (mla_absorb_q,
  *     mla_decode_paged, mla_combine, mla_out_proj with their roundings). For few new
  *     tokens on a context; T <= MLA_MAX_BATCH.

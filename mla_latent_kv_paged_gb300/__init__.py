@@ -19,7 +19,6 @@ and, for a ragged chunk of new tokens (the prompt side):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -535,17 +534,13 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _current(dev):
-    """A context in which device ``dev`` is the current one (nothing to do where it is already)."""
-    import torch
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev else torch.cuda.device(dev)
-
-
 def _call(fn, dev, stream, *args):
     """fn(*args, stream) with device ``dev`` current (a kernel launches on the current device)."""
     import torch
     s = torch.cuda.current_stream(dev) if stream is None else stream
-    with _current(dev):
+    if torch.cuda.current_device() == dev:
+        return fn(*args, s.cuda_stream)
+    with torch.cuda.device(dev):
         return fn(*args, s.cuda_stream)
 
 
@@ -653,8 +648,11 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
     if out is None:
         out = torch.empty((T, H, D_V), dtype=bf, device=cache.device)
     _tensor("out", out, bf, (T, H, D_V), dev)
-    with _current(dev):
-        need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
+    else:
+        need = 0
     workspace, room = _room(workspace, need, dev)
     st = _call(lib().mla_attend_chunk, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(), w_uk.data_ptr(),
                w_uv.data_ptr(), cache.data_ptr(), _address(fp8_scales), block_table.data_ptr(), seq_lens.data_ptr(),

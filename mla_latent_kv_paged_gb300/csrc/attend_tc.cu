@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_qr,
               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_kr,
               const __grid_constant__ CUtensorMap map_v, uint16_t* __restrict__ out, float* __restrict__ lse,
-              ChunkPlan plan, int32_t* counter, int H, int h0, int heads, int64_t cap, float sl2, int32_t* err_word) {
+              ChunkPlan plan, int32_t* counter, int H, int h0, int heads, int64_t cap, float sl2, bool rope_f16,
+              int32_t* err_word) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = warp_index();
@@ -293,7 +294,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     // arrives in its place.
     const int x = warp - 17;
     if (elect()) {
-      constexpr uint32_t kIdC = idesc_f16(128, 128, false, false), kIdR = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kIdC = idesc_f16(128, 128, false, false);
+      const uint32_t id_r = rope_f16 ? kIdC : idesc_bf16(128, 128, false, false);
       constexpr uint32_t kIdV = idesc_f16(128, 128, false, true);
       auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
       const uint64_t dq = smem_desc(0, 16, 1024, kSwizzle128B) + da(sbase + 3 * x * kSlab);
@@ -310,7 +312,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           tc_fence_after();
           const uint64_t ad = dq + (s * kSlab >> 4), bd = dk + ((uint64_t)ks * kSlab >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ss(tS, ad + 2 * k, bd + 2 * k, s < 2 ? kIdC : kIdR, (s > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < 4; ++k) mma_ss(tS, ad + 2 * k, bd + 2 * k, s < 2 ? kIdC : id_r, (s > 0 || k > 0) ? 1u : 0u);
           mma_commit(bar(KE0 + ks));
         } else {
           mbar_arrive(bar(KE0 + ks));
@@ -438,7 +440,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       if (lane == 0) mbar_arrive(bar(IE0 + it % kItems));
     };
     // the tile's queries, in place: content from bf16 to fp16 (exact for values of
-    // normal fp16 size), position as it is
+    // normal fp16 size), position as the cache's (fp16 for an FP8 cache, else as it is)
     auto convert = [&](int it, uint32_t uses) {
       const Item t = item_of(it);
       if (!t.live) return false;
@@ -446,9 +448,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       if (!wait(QL0 + x, uses)) return false;
       const int rows = t.n - t.q0 - 128 * x;
       uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int i = tid + 256 * k;  // 16 bytes of the two content slabs
+#pragma unroll 4
+      for (int k = 0; k < (rope_f16 ? 12 : 8); ++k) {
+        const int i = tid + 256 * k;  // 16 bytes of the two content slabs, then of the positional one
         const uint32_t at = sbase + 3 * x * kSlab + 16 * i;
         uint32_t e[4];
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3]) : "r"(at));
@@ -647,7 +649,7 @@ join_kernel(ChunkPlan plan, uint16_t* __restrict__ out, float* __restrict__ lse,
 
 cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const uint16_t* q_rope, uint16_t* out,
                           float* lse, int B, int T, int H, int h0, int heads, int64_t cap, int slots, int round,
-                          float scale, int32_t* err_word, cudaStream_t s) {
+                          float scale, bool f16, int32_t* err_word, cudaStream_t s) {
   CUtensorMap mq, mqr, mk, mr, mv;
   const uint64_t dq[3] = {kDNope, (uint64_t)H, (uint64_t)T}, sq[2] = {kDNope * 2, (uint64_t)H * kDNope * 2};
   const uint64_t dqr[3] = {kDR, (uint64_t)H, (uint64_t)T}, sqr[2] = {kDR * 2, (uint64_t)H * kDR * 2};
@@ -665,7 +667,8 @@ cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const u
   if (e != cudaSuccess) return e;
   const int64_t most = ((int64_t)chunk_max_items(B, T) + slots) * heads;
   e = launch_pdl(attend_kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), kSmem, s, mq, mqr, mk, mr,
-                 mv, out, lse, plan, plan.counter + round, H, h0, heads, cap, scale * 1.4426950408889634f, err_word);
+                 mv, out, lse, plan, plan.counter + round, H, h0, heads, cap, scale * 1.4426950408889634f, f16,
+                 err_word);
   if (e != cudaSuccess || slots == 0) return e;
   const int joins = chunk_max_items(B, T) < slots / 2 ? chunk_max_items(B, T) : slots / 2;  // two pieces at least
   return launch_pdl(join_kernel, dim3(joins, heads, 8), dim3(256), 0, s, plan, out, lse, H, h0);

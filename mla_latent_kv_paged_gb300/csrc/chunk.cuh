@@ -23,6 +23,21 @@ __device__ inline int row_sequence(const int32_t* __restrict__ cu, int B, int t)
   return __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1) ? lo : -1;
 }
 
+// New rows [*c0, *c0 + n) and context length of sequence b, clamped to the row
+// array and the block table; anything out of range is reported.
+__device__ inline int sequence_of_chunk(const int32_t* seq_lens, const int32_t* cu, int b, int T, int max_tokens, int* c0,
+                                 int* len, int32_t* err_word) {
+  const int a = cu[b], e = cu[b + 1];
+  const int first = min(max(a, 0), T), end = min(max(e, first), T);
+  const int n = min(end - first, max_tokens);
+  int L = seq_lens[b];
+  if (a != first || e != first + n || ((L < n || L > max_tokens) && n > 0)) report_error(err_word, MLA_ERR_BOUNDS);
+  L = min(max(L, n), max_tokens);
+  *c0 = first;
+  *len = n > 0 ? L : 0;  // a sequence without new rows takes no part
+  return n;
+}
+
 // The MMA issuer's last act: every MMA it issued is done (a wait that gave up
 // elsewhere included) before the CTA gives its tensor memory back. Bounded.
 __device__ __forceinline__ void wait_mmas(uint32_t bar) {
@@ -50,7 +65,9 @@ struct ChunkPlan {
   int4* join;        // [slots] {first slot, pieces, first row of the item, its rows}
   float* o_part;     // [slots * heads][256][128] sums of weighted values of a piece
   float2* ml_part;   // [slots * heads][256] {reference maximum in log2 units, sum of weights}
-  uint16_t* rows;    // [cap][576] bf16, the sequences' cache rows; zeros from a context's end to its padding
+  uint16_t* rows;    // [cap][576] the sequences' cache rows, bf16 (of an FP8 cache: fp16, see launch_rows_f16);
+                     // zeros from a context's end to its padding
+  uint16_t* w16;     // [2][H][128][512] fp16 copies of w_uk and w_uv (FP8 cache only)
   uint16_t* k;       // [heads][cap][128] fp16 keys without position
   uint16_t* v;       // [heads][cap][128] fp16 values
 };
@@ -75,7 +92,8 @@ inline int chunk_slots(int B, int T, int heads, int64_t max_tokens) {
   return n < 2 ? 0 : (int)n;
 }
 
-inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_tokens, ChunkPlan* p) {
+// w_heads: heads of the weight copies (0: none)
+inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_tokens, int w_heads, ChunkPlan* p) {
   const int64_t cap = chunk_cap(max_tokens, B);
   const int slots = chunk_slots(B, T, heads, max_tokens);
   size_t off = 0;
@@ -89,6 +107,7 @@ inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_toke
   const size_t o_pc = take(((size_t)chunk_max_items(B, T) + slots) * 32), o_j = take((size_t)slots * 16);
   const size_t o_o = take((size_t)slots * heads * kQTile * kDV * 4), o_m = take((size_t)slots * heads * kQTile * 8);
   const size_t o_r = take((size_t)cap * kRow * 2);
+  const size_t o_w = take((size_t)w_heads * (kDNope + kDV) * kDC * 2);
   const size_t o_k = take((size_t)heads * cap * kDNope * 2), o_v = take((size_t)heads * cap * kDV * 2);
   if (base && p) {
     char* c = workspace_base(base);
@@ -102,6 +121,7 @@ inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_toke
     p->o_part = reinterpret_cast<float*>(c + o_o);
     p->ml_part = reinterpret_cast<float2*>(c + o_m);
     p->rows = reinterpret_cast<uint16_t*>(c + o_r);
+    p->w16 = reinterpret_cast<uint16_t*>(c + o_w);
     p->k = reinterpret_cast<uint16_t*>(c + o_k);
     p->v = reinterpret_cast<uint16_t*>(c + o_v);
   }
@@ -111,7 +131,6 @@ inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_toke
 // Absorbed form: each new token is a decode sequence of its own.
 struct ChunkRows {
   int32_t* hdr;      // [64] hdr[0] = rows that belong to a sequence
-  int32_t* len;      // [T] tokens the row attends (1 for rows of no sequence)
   int32_t* seq_row;  // [T] block-table row (-1 for rows of no sequence)
   uint16_t* q_abs;   // [T][H][576] bf16
   uint16_t* u;       // [T][H][512] bf16
@@ -125,13 +144,12 @@ inline size_t chunk_rows_layout(void* base, int T, int H, int G, ChunkRows* p) {
     off = align256(off + bytes);
     return o;
   };
-  const size_t o_hdr = take(64 * 4), o_l = take((size_t)T * 4), o_s = take((size_t)T * 4);
+  const size_t o_hdr = take(64 * 4), o_s = take((size_t)T * 4);
   const size_t o_q = take((size_t)T * H * kRow * 2), o_u = take((size_t)T * H * kDC * 2);
   const size_t o_d = take(plan_layout(nullptr, T, 1, H, G, nullptr));
   if (base && p) {
     char* c = workspace_base(base);
     p->hdr = reinterpret_cast<int32_t*>(c + o_hdr);
-    p->len = reinterpret_cast<int32_t*>(c + o_l);
     p->seq_row = reinterpret_cast<int32_t*>(c + o_s);
     p->q_abs = reinterpret_cast<uint16_t*>(c + o_q);
     p->u = reinterpret_cast<uint16_t*>(c + o_u);
@@ -145,6 +163,16 @@ cudaError_t launch_read_kv(const void* cache, const float* fp8_scales, const int
                            const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* out, int B,
                            int n_rows, int num_pages, int page_size, int max_pages, int32_t* err_word,
                            cudaStream_t s);
+// The same into an fp16 workspace, of an FP8 cache: scale * e4m3 rounded to fp16 (2^-11
+// relative; to bf16 it would be 2^-8, as much as the output's own rounding).
+// |value| >= 65520 is reported.
+cudaError_t launch_rows_f16(const void* cache8, const float* fp8_scales, const int32_t* block_table,
+                            const int32_t* seq_lens, const int32_t* cu, uint16_t* out, int B, int n_rows,
+                            int num_pages, int page_size, int max_pages, int32_t* err_word, cudaStream_t s);
+// ... and the weights that multiply them (MMA operands have one type): exact for bf16
+// values of normal fp16 size, |value| >= 65520 is reported. out [2][H][128][512].
+cudaError_t launch_weights_f16(const uint16_t* w_uk, const uint16_t* w_uv, uint16_t* out, int H, int32_t* err_word,
+                               cudaStream_t s);
 size_t append_chunk_workspace_bytes(int T, int d_model);
 cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
                                 const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
@@ -153,13 +181,15 @@ cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* 
 cudaError_t launch_chunk_plan(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
                               int64_t max_total, int heads, const ChunkPlan& plan, int32_t* err_word,
                               cudaStream_t s);
-cudaError_t launch_chunk_rows(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
-                              const ChunkRows& rows, int32_t* err_word, cudaStream_t s);
-// keys and values of heads [h0, h0 + heads) of every expanded row
+// the decode plan of a chunk's T rows, each a sequence of its own (plan.cu)
+cudaError_t launch_rows_plan(const int32_t* seq_lens, const int32_t* cu, int sequences, int T, int max_pages,
+                             int page_size, int num_pages, int G, const Plan& plan, int32_t* seq_row, int32_t* live,
+                             int32_t* err_word, cudaStream_t s);
+// keys and values of heads [h0, h0 + heads) of every expanded row; f16: rows and weights are fp16, not bf16
 cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uint16_t* w_uv, int H, int h0, int heads,
-                          int64_t cap, int32_t* err_word, cudaStream_t s);
+                          int64_t cap, bool f16, int32_t* err_word, cudaStream_t s);
 cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const uint16_t* q_rope, uint16_t* out,
                           float* lse, int B, int T, int H, int h0, int heads, int64_t cap, int slots, int round,
-                          float scale, int32_t* err_word, cudaStream_t s);
+                          float scale, bool f16, int32_t* err_word, cudaStream_t s);
 
 }  // namespace mla

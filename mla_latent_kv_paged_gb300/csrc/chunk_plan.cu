@@ -1,12 +1,8 @@
-// Plans of a ragged chunk of new tokens over the paged cache, from seq_lens and
-// cu on the device (so a captured graph follows their contents).
-//   chunk_plan_kernel  expanded form: where each sequence's expanded rows start
-//                      (contexts padded to 128 rows) and the list of query items
-//                      (256 rows of one sequence each, the last rows of a
-//                      sequence first: they see the most tokens, so the longest
-//                      work starts first), cut over the keys into pieces when the
-//                      items alone would leave SMs idle
-//   chunk_rows_kernel  absorbed form: every new row as a decode sequence of its own
+// Plan of the expanded attention of a ragged chunk of new tokens, from seq_lens and
+// cu on the device (so a captured graph follows their contents): where each
+// sequence's expanded rows start (contexts padded to 128 rows) and the list of query
+// items (256 rows of one sequence each, the longest work first), cut over the keys
+// into pieces when the items alone would leave SMs idle.
 // Integer work on a few thousand numbers, one block: bound by launch and barrier
 // latency.
 #include "chunk.cuh"
@@ -41,21 +37,6 @@ __device__ int64_t block_scan(int64_t v, int64_t* total) {
   __syncthreads();
   *total = all;
   return before + x - v;
-}
-
-// New rows [*c0, *c0 + n) and context length of sequence b, clamped to the row
-// array and the block table; anything out of range is reported.
-__device__ int sequence_of_chunk(const int32_t* seq_lens, const int32_t* cu, int b, int T, int max_tokens, int* c0,
-                                 int* len, int32_t* err_word) {
-  const int a = cu[b], e = cu[b + 1];
-  const int first = min(max(a, 0), T), end = min(max(e, first), T);
-  const int n = min(end - first, max_tokens);
-  int L = seq_lens[b];
-  if (a != first || e != first + n || ((L < n || L > max_tokens) && n > 0)) report_error(err_word, MLA_ERR_BOUNDS);
-  L = min(max(L, n), max_tokens);
-  *c0 = first;
-  *len = n > 0 ? L : 0;  // a sequence without new rows takes no part
-  return n;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -179,29 +160,6 @@ chunk_plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restric
   }
 }
 
-__global__ void __launch_bounds__(kThreads)
-chunk_rows_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu, int B, int T, int max_tokens,
-                  ChunkRows rows, int32_t* err_word) {
-  sm100::grid_dependency_wait();
-  const int t = blockIdx.x * kThreads + threadIdx.x;
-  if (t < T) {
-    const int b = row_sequence(cu, B, t);
-    int len = 1, row = -1;
-    if (b >= 0) {
-      int c0, L;
-      const int n = sequence_of_chunk(seq_lens, cu, b, T, max_tokens, &c0, &L, err_word);
-      const int j = t - c0;
-      if (j >= 0 && j < n) {
-        len = L - n + j + 1;
-        row = b;
-      }
-    }
-    rows.len[t] = len;
-    rows.seq_row[t] = row;
-  }
-  if (t == 0) rows.hdr[0] = min(max(cu[B], 0), T);
-}
-
 }  // namespace
 
 cudaError_t launch_chunk_plan(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
@@ -209,12 +167,6 @@ cudaError_t launch_chunk_plan(const int32_t* seq_lens, const int32_t* cu, int B,
                               cudaStream_t s) {
   return launch_pdl(chunk_plan_kernel, dim3(1), dim3(kThreads), 0, s, seq_lens, cu, B, T, max_tokens, max_total,
                     chunk_max_items(B, T), heads, chunk_slots(B, T, heads, max_total), plan, err_word);
-}
-
-cudaError_t launch_chunk_rows(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
-                              const ChunkRows& rows, int32_t* err_word, cudaStream_t s) {
-  return launch_pdl(chunk_rows_kernel, dim3((T + kThreads - 1) / kThreads), dim3(kThreads), 0, s, seq_lens, cu, B, T,
-                    max_tokens, rows, err_word);
 }
 
 }  // namespace mla

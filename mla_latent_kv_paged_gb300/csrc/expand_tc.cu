@@ -2,7 +2,7 @@
 // attention of a chunk of new tokens (attend_tc.cu):
 //   k[h][s][i] = sum_c row_s[c] w_uk[h][i][c]      v[h][s][i] = sum_c row_s[c] w_uv[h][i][c]
 // (Huny's Dev Blog "MLA 아키텍처 해부" section 1.2, k^C = c W^UK, v^C = c W^UV),
-// bf16 operands, fp32 sums, rounded once to fp16: three more mantissa bits than
+// bf16 operands (fp16 for an FP8 cache), fp32 sums, rounded once to fp16: three more mantissa bits than
 // bf16 for the two products that follow, |value| < 65520 (beyond: MLA_ERR_RANGE).
 //
 // Tensor-bound: 2 x 512 x 256 flop per (token, head). A pair of CTAs (one
@@ -64,7 +64,7 @@ __device__ __forceinline__ uint32_t write_row(const uint32_t (&r)[64], uint16_t*
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constant__ CUtensorMap map_uk,
               const __grid_constant__ CUtensorMap map_uv, ChunkPlan plan, int h0, int heads, int64_t cap,
-              int32_t* err_word) {
+              uint32_t idesc, int32_t* err_word) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = warp_index(), lane = threadIdx.x & 31;
@@ -149,7 +149,6 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
     }
   } else if (warp == 9) {
     if (rank == 0 && elect()) {
-      const uint32_t idesc = idesc_bf16(256, 256, false, false);
       auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
       const uint64_t ad0 = smem_desc(0, 16, 1024, kSwizzle128B) + da(sbase);
       const uint64_t bd0 = smem_desc(0, 16, 1024, kSwizzle128B);
@@ -228,7 +227,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
 }  // namespace
 
 cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uint16_t* w_uv, int H, int h0, int heads,
-                          int64_t cap, int32_t* err_word, cudaStream_t s) {
+                          int64_t cap, bool f16, int32_t* err_word, cudaStream_t s) {
   CUtensorMap mr, mk, mv;
   const uint64_t dr[2] = {kRow, (uint64_t)cap}, sr[1] = {kRow * 2};
   const uint64_t dw[2] = {kDC, (uint64_t)H * 128}, sw[1] = {kDC * 2};
@@ -244,7 +243,8 @@ cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uin
   const int64_t units = (cap / kKvTile + 1) / 2 * heads;
   const int pairs = sms / 2;
   return launch_pdl(expand_kernel, dim3(2 * (unsigned)(units < pairs ? units : pairs)), dim3(kThreads), kSmem, s, mr, mk, mv,
-                    plan, h0, heads, cap, err_word);
+                    plan, h0, heads, cap, f16 ? idesc_f16(256, 256, false, false) : idesc_bf16(256, 256, false, false),
+                    err_word);
 }
 
 }  // namespace mla

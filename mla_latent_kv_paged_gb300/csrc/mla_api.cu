@@ -402,7 +402,8 @@ size_t mla_attend_chunk_workspace_bytes(int B, int T, int H, int64_t max_tokens,
     return G < 1 ? 0 : chunk_rows_layout(nullptr, T, H, G, nullptr);
   }
   const int64_t cap = chunk_cap(max_tokens, B);
-  return chunk_layout(nullptr, B, T, chunk_head_group(H, cap), max_tokens, nullptr);
+  // (with the weight copies that an FP8 cache needs)
+  return chunk_layout(nullptr, B, T, chunk_head_group(H, cap), max_tokens, H, nullptr);
 }
 
 mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
@@ -436,11 +437,8 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
     Plan plan;
     plan_layout(r.decode_ws, T, 1, H, G, &plan);
     plan.seq_row = r.seq_row;
-    mla_status st = launch_status(launch_chunk_rows(seq_lens, cu, B, T, max_tokens_seq, r, err_word, s));
-    // an ordinary launch: the plan reads the rows' lengths, which the kernel before writes
-    if (st == MLA_OK)
-      st = launch_status(launch_plan(r.len, nullptr, T, 1, max_pages_per_seq, page_size, num_pages, G, plan, err_word,
-                                     s, false));
+    mla_status st = launch_status(launch_rows_plan(seq_lens, cu, B, T, max_pages_per_seq, page_size, num_pages, G,
+                                                   plan, r.seq_row, r.hdr, err_word, s));
     if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s));
     if (st == MLA_OK)
       st = launch_status(fp8_scales ? launch_decode_fp8(r.q_abs, static_cast<const uint8_t*>(cache), fp8_scales,
@@ -455,20 +453,30 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
   }
   const int64_t cap = chunk_cap(max_tokens, B);
   const int group = chunk_head_group(H, cap), slots = chunk_slots(B, T, group, max_tokens);
-  if (workspace_bytes < chunk_layout(nullptr, B, T, group, max_tokens, nullptr)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const int w_heads = H;
+  if (workspace_bytes < chunk_layout(nullptr, B, T, group, max_tokens, H, nullptr)) return MLA_ERR_WORKSPACE_TOO_SMALL;
   ChunkPlan plan;
-  chunk_layout(workspace, B, T, group, max_tokens, &plan);
+  chunk_layout(workspace, B, T, group, max_tokens, H, &plan);
   mla_status st = launch_status(launch_chunk_plan(seq_lens, cu, B, T, max_tokens_seq, max_tokens, group, plan, err_word, s));
   // the contexts' rows, each sequence from its own multiple of 128 on, zeros behind its end
-  if (st == MLA_OK)
-    st = launch_status(launch_read_kv(cache, fp8_scales, block_table, plan.len_eff, nullptr, plan.pstart, plan.rows, B,
+  const bool f16 = fp8_scales != nullptr;
+  if (f16) {
+    if (st == MLA_OK)
+      st = launch_status(launch_rows_f16(cache, fp8_scales, block_table, plan.len_eff, plan.pstart, plan.rows, B,
+                                         (int)cap, num_pages, page_size, max_pages_per_seq, err_word, s));
+    if (st == MLA_OK) st = launch_status(launch_weights_f16(w_uk, w_uv, plan.w16, H, err_word, s));
+    w_uk = plan.w16;
+    w_uv = plan.w16 + (size_t)H * kDNope * kDC;
+  } else if (st == MLA_OK) {
+    st = launch_status(launch_read_kv(cache, nullptr, block_table, plan.len_eff, nullptr, plan.pstart, plan.rows, B,
                                       (int)cap, num_pages, page_size, max_pages_per_seq, err_word, s));
+  }
   for (int h0 = 0; h0 < H && st == MLA_OK; h0 += group) {
     const int heads = H - h0 < group ? H - h0 : group;
-    st = launch_status(launch_expand(plan, w_uk, w_uv, H, h0, heads, cap, err_word, s));
+    st = launch_status(launch_expand(plan, w_uk, w_uv, H, h0, heads, cap, f16, err_word, s));
     if (st == MLA_OK)
       st = launch_status(launch_attend(plan, q_nope, q_rope, out, lse, B, T, H, h0, heads, cap, slots, h0 / group,
-                                       softmax_scale, err_word, s));
+                                       softmax_scale, f16, err_word, s));
   }
   return st;
 }

@@ -13,6 +13,7 @@
 // One block of 256 threads. Integer work only; the output is a pure function
 // of (seq_lens, n_q, max_pages * page_size, G), so repeated calls give
 // identical plans.
+#include "chunk.cuh"
 #include "mla_internal.cuh"
 #include "sm100.cuh"
 
@@ -70,9 +71,37 @@ __device__ inline int64_t div_nn(int64_t a, int64_t b) {
 }
 __device__ inline int64_t ceil_div64(int64_t a, int64_t b) { return div_nn(a + b - 1, b); }
 
+// kRows: the B sequences of the plan are the rows of a chunk (n_q = 1): row t sees
+// the tokens up to its own; a row of no sequence sees one token (of page 0, see
+// Plan::seq_row). The chunk's inputs may come from the kernel before, so they are
+// read after it has finished.
+struct RowArgs {
+  const int32_t* cu;   // [sequences + 1]
+  int sequences;
+  int32_t* seq_row;    // [B] out
+  int32_t* live;       // out: rows that belong to a sequence
+};
+__device__ __forceinline__ int row_length(const int32_t* seq_lens, const RowArgs& rows, int t, int B, int max_tokens,
+                                          int32_t* err_word) {
+  const int b = row_sequence(rows.cu, rows.sequences, t);
+  int len = 1, row = -1;
+  if (b >= 0) {
+    int c0, L;
+    const int n = sequence_of_chunk(seq_lens, rows.cu, b, B, max_tokens, &c0, &L, err_word);
+    if (t - c0 < n) {
+      len = L - n + (t - c0) + 1;
+      row = b;
+    }
+  }
+  rows.seq_row[t] = row;
+  if (t == 0) *rows.live = min(max(rows.cu[rows.sequences], 0), B);
+  return len;
+}
+
+template <bool kRows>
 __global__ void __launch_bounds__(kPlanThreads, 1)
 plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table, int B,
-            int n_q, int max_tokens, int num_pages, int G, Plan plan, int32_t* err_word) {
+            int n_q, int max_tokens, int num_pages, int G, Plan plan, RowArgs rows, int32_t* err_word) {
   extern __shared__ int smem_i[];
   int* s_pstart = smem_i;            // [B+1] exclusive page prefix
   int* s_istart = smem_i + (B + 1);  // [B+1] exclusive piece prefix
@@ -83,9 +112,11 @@ plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bl
   // grid dependency wait, which covers this kernel's completion
   sm100::grid_launch_dependents();
 
+  if (kRows) sm100::grid_dependency_wait();
+
   // 1. clamp context lengths (to the block table's max_pages * page_size tokens), count tiles
   for (int b = tid; b < B; b += kPlanThreads) {
-    int L = seq_lens[b];
+    int L = kRows ? row_length(seq_lens, rows, b, B, max_tokens, err_word) : seq_lens[b];
     if (L < n_q) {
       report_error(err_word, MLA_ERR_BOUNDS);
       L = n_q;
@@ -216,15 +247,17 @@ __device__ __forceinline__ int warp_exclusive_scan(int v, int lane, int* total) 
   return x - v;
 }
 
+template <bool kRows>
 __global__ void __launch_bounds__(32, 1)
 plan_small_kernel(const int32_t* __restrict__ seq_lens, int B, int n_q, int max_tokens, int G, Plan plan,
-                  int32_t* err_word) {
+                  RowArgs rows, int32_t* err_word) {
   const int lane = threadIdx.x;
   sm100::grid_launch_dependents();
+  if (kRows) sm100::grid_dependency_wait();
   const bool live = lane < B;
   int n_b = 0;  // tiles of sequence `lane`
   if (live) {
-    int L = seq_lens[lane];
+    int L = kRows ? row_length(seq_lens, rows, lane, B, max_tokens, err_word) : seq_lens[lane];
     if (L < n_q) {
       report_error(err_word, MLA_ERR_BOUNDS);
       L = n_q;
@@ -297,22 +330,37 @@ cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* block_table, int
   const int max_tokens = max_pages * page_size;
   if (B <= 32) {
     if (overlap)
-      return launch_pdl(plan_small_kernel, dim3(1), dim3(32), 0, s, seq_lens, B, n_q, max_tokens, G, plan, err_word);
-    plan_small_kernel<<<1, 32, 0, s>>>(seq_lens, B, n_q, max_tokens, G, plan, err_word);
+      return launch_pdl(plan_small_kernel<false>, dim3(1), dim3(32), 0, s, seq_lens, B, n_q, max_tokens, G, plan,
+                        RowArgs{}, err_word);
+    plan_small_kernel<false><<<1, 32, 0, s>>>(seq_lens, B, n_q, max_tokens, G, plan, RowArgs{}, err_word);
     return cudaGetLastError();
   }
   const size_t smem = (size_t)2 * (B + 1) * sizeof(int);
   if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
     if (e != cudaSuccess) return e;
   }
   if (overlap)
-    return launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), smem, s, seq_lens, block_table, B, n_q, max_tokens,
-                      num_pages, G, plan, err_word);
+    return launch_pdl(plan_kernel<false>, dim3(1), dim3(kPlanThreads), smem, s, seq_lens, block_table, B, n_q,
+                      max_tokens, num_pages, G, plan, RowArgs{}, err_word);
   // after the previous kernel has finished (its grid dependency wait then returns at once)
-  plan_kernel<<<1, kPlanThreads, smem, s>>>(seq_lens, block_table, B, n_q, max_tokens, num_pages, G, plan, err_word);
+  plan_kernel<false><<<1, kPlanThreads, smem, s>>>(seq_lens, block_table, B, n_q, max_tokens, num_pages, G, plan,
+                                                   RowArgs{}, err_word);
   return cudaGetLastError();
+}
+
+cudaError_t launch_rows_plan(const int32_t* seq_lens, const int32_t* cu, int sequences, int T, int max_pages,
+                             int page_size, int num_pages, int G, const Plan& plan, int32_t* seq_row, int32_t* live,
+                             int32_t* err_word, cudaStream_t s) {
+  const int max_tokens = max_pages * page_size;
+  const RowArgs rows = {cu, sequences, seq_row, live};
+  if (T <= 32)
+    return launch_pdl(plan_small_kernel<true>, dim3(1), dim3(32), 0, s, seq_lens, T, 1, max_tokens, G, plan, rows,
+                      err_word);
+  const size_t smem = (size_t)2 * (T + 1) * sizeof(int);  // T <= MLA_MAX_BATCH: 32 KB
+  return launch_pdl(plan_kernel<true>, dim3(1), dim3(kPlanThreads), smem, s, seq_lens, (const int32_t*)nullptr, T, 1,
+                    max_tokens, num_pages, G, plan, rows, err_word);
 }
 
 }  // namespace mla

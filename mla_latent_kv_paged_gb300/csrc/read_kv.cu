@@ -19,7 +19,8 @@ constexpr int kRowsAtOnce = 4;
 constexpr int kThreads = kGroups * kRowsAtOnce;  // 288
 constexpr int kInFlight = 8;
 
-template <bool kF8, int kRows>
+// kF16: fp16 rows instead of bf16 (the workspace of attend_chunk)
+template <bool kF8, bool kF16, int kRows>
 __global__ void __launch_bounds__(kThreads)
 read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales, const int32_t* __restrict__ block_table,
                const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ first, const int32_t* __restrict__ cu,
@@ -56,6 +57,7 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
     for (int i = 0; i < 8; ++i) sc[i] = __ldg(scales + 8 * g + i);
   }
   __syncthreads();
+  float top = 0.f;
   constexpr int kPer = kRows / kRowsAtOnce;
   constexpr int kStep = kPer < kInFlight ? kPer : kInFlight;
 #pragma unroll 1
@@ -93,7 +95,9 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float2 x = sm100::f16x2_to_f32(f[q]);
-          p[q] = sm100::cvt_bf16x2(x.x * sc[2 * q], x.y * sc[2 * q + 1]);
+          const float a = x.x * sc[2 * q], b = x.y * sc[2 * q + 1];
+          p[q] = kF16 ? sm100::cvt_f16x2(a, b) : sm100::cvt_bf16x2(a, b);
+          if (kF16 && src[i] >= 0) top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
         }
         o = make_uint4(p[0], p[1], p[2], p[3]);
         if (src[i] == -1) o = make_uint4(0, 0, 0, 0);  // 0 x scale, whatever the scale
@@ -101,13 +105,34 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
       out[(int64_t)(t0 + i) * kGroups + g] = o;
     }
   }
+  if (kF16 && top >= 65520.f && top < INFINITY) report_error(err_word, MLA_ERR_RANGE);
 }
 
-template <bool kF8, int kRows>
+constexpr int kWThreads = 256;
+__global__ void __launch_bounds__(kWThreads)
+weights_f16_kernel(const uint4* __restrict__ w_uk, const uint4* __restrict__ w_uv, uint4* __restrict__ out, int n8,
+                   int32_t* err_word) {
+  sm100::grid_launch_dependents();  // the next kernel reads the copies after its own dependency wait
+  sm100::grid_dependency_wait();    // the workspace may still be in use
+  const int i = blockIdx.x * kWThreads + threadIdx.x;
+  if (i >= 2 * n8) return;
+  const uint4 w = i < n8 ? __ldg(w_uk + i) : __ldg(w_uv + (i - n8));
+  const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+  uint32_t f[4], top = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[k] = sm100::cvt_f16x2(bf16_lo(e[k]), bf16_hi(e[k]));
+    top = max(top, max((e[k] << 16) & 0x7FFFFFFFu, e[k] & 0x7FFF0000u));
+  }
+  out[i] = make_uint4(f[0], f[1], f[2], f[3]);
+  if (top >= 0x477FF000u && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
+}
+
+template <bool kF8, bool kF16, int kRows>
 cudaError_t launch(const void* cache, const float* scales, const int32_t* block_table, const int32_t* seq_lens,
                    const int32_t* first, const int32_t* cu, uint16_t* out, int B, int n_rows, int num_pages,
                    int page_size, int max_pages, int32_t* err_word, cudaStream_t s) {
-  return launch_pdl(read_kv_kernel<kF8, kRows>, dim3((n_rows + kRows - 1) / kRows), dim3(kThreads), 0, s, cache,
+  return launch_pdl(read_kv_kernel<kF8, kF16, kRows>, dim3((n_rows + kRows - 1) / kRows), dim3(kThreads), 0, s, cache,
                     scales, block_table, seq_lens, first, cu, reinterpret_cast<uint4*>(out), B, n_rows, num_pages,
                     page_size, max_pages, err_word);
 }
@@ -118,10 +143,25 @@ cudaError_t launch_read_kv(const void* cache, const float* fp8_scales, const int
                            const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* out, int B,
                            int n_rows, int num_pages, int page_size, int max_pages, int32_t* err_word,
                            cudaStream_t s) {
-  return fp8_scales ? launch<true, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows, num_pages,
+  return fp8_scales ? launch<true, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows, num_pages,
                                        page_size, max_pages, err_word, s)
-                    : launch<false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows,
+                    : launch<false, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows,
                                         num_pages, page_size, max_pages, err_word, s);
+}
+
+cudaError_t launch_rows_f16(const void* cache8, const float* fp8_scales, const int32_t* block_table,
+                            const int32_t* seq_lens, const int32_t* cu, uint16_t* out, int B, int n_rows,
+                            int num_pages, int page_size, int max_pages, int32_t* err_word, cudaStream_t s) {
+  return launch<true, true, 32>(cache8, fp8_scales, block_table, seq_lens, nullptr, cu, out, B, n_rows, num_pages,
+                                page_size, max_pages, err_word, s);
+}
+
+cudaError_t launch_weights_f16(const uint16_t* w_uk, const uint16_t* w_uv, uint16_t* out, int H, int32_t* err_word,
+                               cudaStream_t s) {
+  const int n8 = H * kDNope * kDC / 8;  // each of the two
+  return launch_pdl(weights_f16_kernel, dim3((2 * n8 + kWThreads - 1) / kWThreads), dim3(kWThreads), 0, s,
+                    reinterpret_cast<const uint4*>(w_uk), reinterpret_cast<const uint4*>(w_uv),
+                    reinterpret_cast<uint4*>(out), n8, err_word);
 }
 
 }  // namespace mla

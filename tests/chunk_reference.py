@@ -77,7 +77,7 @@ def attend(c: Chunk, scale=SCALE):
     times the absolute products), which moves a weight by a factor exp(+-2 dz); a weight
     is rounded once more before the value product, a value once:
       expanded  keys, values and weights in fp16 (u = 2^-11); rows of an FP8 cache are
-                first rounded to bf16 (2^-8)
+                first rounded to fp16 as well
       absorbed  absorbed query, weights and u in bf16 (2^-8), partials in fp16
     plus the output's own rounding to bf16 and fp32 sums (2^-24 per term, at most a
     few thousand terms: below 2^-11, counted as one more fp16 unit)."""
@@ -100,7 +100,7 @@ def attend(c: Chunk, scale=SCALE):
             p = torch.softmax(z, -1)
             o[:, h] = p @ v
             z_all[:, h] = torch.logsumexp(z, -1)
-            rows_u = U_BF16 if c.fp8 else 0.0
+            rows_u = U_F16 if c.fp8 else 0.0
             kabs, vabs = lat.abs() @ uk.abs().t(), lat.abs() @ uv.abs().t()
             # expanded
             dz = scale * ((qn.abs() @ k.abs().t()) * 2 * U_F16 + rows_u * (qn.abs() @ kabs.t() + qr.abs() @ kr.abs().t()))
