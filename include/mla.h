@@ -485,8 +485,8 @@ mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t
  * own rows included (append them first):
  *   z_s = softmax_scale * (q_nope . (c_s W^UK) + q_rope . k^R_s),  s <= L_b - n_b + j
  *   out[t][h] = softmax(z) (c_s W^UV),  lse[t][h] = ln sum_s exp(z_s)
- * in one of two forms of the same sums (form = MLA_CHUNK_AUTO chooses by the
- * chunk's mean length T / B):
+ * in one of two forms of the same sums (form = MLA_CHUNK_AUTO chooses by T / B,
+ * H, max_tokens / B and the kind of cache, nothing on the device):
  *   MLA_CHUNK_EXPANDED  keys and values of every head are expanded from the latents
  *     first, and rounded to fp16 (so are content queries, the rows of an FP8 cache
  *     and, with one, the weights; fp32 sums everywhere). For long chunks. Any of

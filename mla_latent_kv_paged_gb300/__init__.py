@@ -625,7 +625,8 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
     [H, 128, 512] bf16; cache, block_table, seq_lens, cu, fp8_scales as for append_chunk.
     max_tokens bounds the sum of the contexts (default: the block table's capacity) and
     sizes the workspace. form: "expanded" (keys and values of every head expanded first),
-    "absorbed" (each token decoded over the latents) or "auto" (by the mean chunk length).
+    "absorbed" (each token decoded over the latents) or "auto" (by T / B, H and max_tokens / B:
+    few new tokens on a context are absorbed).
     lse [T, H] float32, when given, receives the log-sum-exp of the scores. Rows at and
     past cu[B] of out and lse are left as they were.
     """

@@ -343,12 +343,28 @@ int chunk_head_group(int H, int64_t cap) {
   const int64_t rounds = (H + g - 1) / g;
   return (int)((H + rounds - 1) / rounds);
 }
-// Expanding costs 2 * 512 * 256 flop per (token, head) whatever the chunk;
-// absorbed attention costs 2176 flop per (query, token, head) against 640.
-constexpr int kAbsorbedRows = 128;
-int chunk_form(int form, int B, int T) {
+// The form of MLA_CHUNK_AUTO, for n = T / B new tokens on contexts of L = max_tokens / B.
+// Measured, in us: absorbed n (2.1e-4 L + 0.2) whatever H (its MMAs take 128 head rows
+// always), expanded 2.9e-4 H L (n hardly counts), beside about 25 for either; an FP8
+// cache costs the absorbed form 1.4 times as much. So absorbed up to
+// n = c H L / (L + 950), c = 1.37 (bf16) or 1.0 (FP8). Both sides at H = 128, bf16
+// (absorbed / expanded): L = 512: n = 32 35/44, 64 48/44; L = 4096: n = 128 162/184,
+// 160 203/191; L = 16384: n = 160 603/655, 192 714/659; FP8, L = 4096: n = 96 172/195,
+// 128 216/197; H = 16, L = 16384: n = 16 84/111, 32 139/112.
+int chunk_form(int form, int B, int T, int H, int64_t max_tokens, bool fp8) {
   if (form != MLA_CHUNK_AUTO) return form;
-  return T <= MLA_MAX_BATCH && T <= (int64_t)kAbsorbedRows * B ? MLA_CHUNK_ABSORBED : MLA_CHUNK_EXPANDED;
+  const double L = (double)max_tokens / B, n = (double)T / B;
+  return T <= MLA_MAX_BATCH && n * (L + 950.0) <= (fp8 ? 1.0 : 1.37) * H * L ? MLA_CHUNK_ABSORBED
+                                                                           : MLA_CHUNK_EXPANDED;
+}
+// bytes of workspace of a form that is not AUTO; 0 without a device
+size_t chunk_form_bytes(int form, int B, int T, int H, int64_t max_tokens) {
+  if (form == MLA_CHUNK_ABSORBED) {
+    const int G = T > MLA_MAX_BATCH ? -1 : mla_decode_default_splits(1);
+    return G < 1 ? 0 : chunk_rows_layout(nullptr, T, H, G, nullptr);
+  }
+  // (with the weight copies that an FP8 cache needs)
+  return chunk_layout(nullptr, B, T, chunk_head_group(H, chunk_cap(max_tokens, B)), max_tokens, H, nullptr);
 }
 }  // namespace
 
@@ -395,15 +411,10 @@ size_t mla_attend_chunk_workspace_bytes(int B, int T, int H, int64_t max_tokens,
   if (B < 1 || T < 1 || !chunk_counts_ok(B, T) || !heads_ok(H) || max_tokens < 1 || max_tokens > INT32_MAX / 2 ||
       form < MLA_CHUNK_AUTO || form > MLA_CHUNK_ABSORBED)
     return 0;
-  form = chunk_form(form, B, T);
-  if (form == MLA_CHUNK_ABSORBED) {
-    if (T > MLA_MAX_BATCH) return 0;
-    const int G = mla_decode_default_splits(1);
-    return G < 1 ? 0 : chunk_rows_layout(nullptr, T, H, G, nullptr);
-  }
-  const int64_t cap = chunk_cap(max_tokens, B);
-  // (with the weight copies that an FP8 cache needs)
-  return chunk_layout(nullptr, B, T, chunk_head_group(H, cap), max_tokens, H, nullptr);
+  // the larger of what the two kinds of cache need
+  const size_t a = chunk_form_bytes(chunk_form(form, B, T, H, max_tokens, false), B, T, H, max_tokens);
+  const size_t b = chunk_form_bytes(chunk_form(form, B, T, H, max_tokens, true), B, T, H, max_tokens);
+  return a == 0 || b == 0 ? 0 : a > b ? a : b;
 }
 
 mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
@@ -426,7 +437,7 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
   if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
   const int max_tokens_seq = max_pages_per_seq * page_size;
   cudaStream_t s = (cudaStream_t)stream;
-  form = chunk_form(form, B, T);
+  form = chunk_form(form, B, T, H, max_tokens, fp8_scales != nullptr);
   if (form == MLA_CHUNK_ABSORBED) {
     if (T > MLA_MAX_BATCH) return MLA_ERR_UNSUPPORTED_SHAPE;
     const int G = mla_decode_default_splits(1);

@@ -202,7 +202,7 @@ def test_attend(mla, err, fp8, form, new, lens, H, page, pad):
 def test_attend_auto_equals_the_form_it_chooses(mla):
     import torch
     for new, form in (([4, 4], "absorbed"), ([600], "expanded")):
-        c = ref.Chunk(new, [700] * len(new), H=2, seed=11)
+        c = ref.Chunk(new, [700] * len(new), H=16, seed=11)
         a = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=sum(c.lens))
         b = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=sum(c.lens), form=form)
         assert torch.equal(a, b)
