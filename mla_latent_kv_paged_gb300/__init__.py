@@ -80,9 +80,10 @@ def build(force: bool = False, debug: bool = False) -> str:
 def lib():
     """The loaded C library (ctypes). Raises if it has not been built."""
     global _lib
-    with _lock:
-        if _lib is None:
-            _lib = _load(LIB_PATH)
+    if _lib is None:
+        with _lock:
+            if _lib is None:
+                _lib = _load(LIB_PATH)
     return _lib
 
 
@@ -537,11 +538,14 @@ def _address(t):
 def _call(fn, dev, stream, *args):
     """fn(*args, stream) with device ``dev`` current (a kernel launches on the current device)."""
     import torch
-    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if stream is not None:
+        handle = stream.cuda_stream
+    else:  # the number alone: a Stream object takes a microsecond
+        handle = torch._C._cuda_getCurrentRawStream(dev)
     if torch.cuda.current_device() == dev:
-        return fn(*args, s.cuda_stream)
+        return fn(*args, handle)
     with torch.cuda.device(dev):
-        return fn(*args, s.cuda_stream)
+        return fn(*args, handle)
 
 
 def _room(workspace, need, dev):

@@ -10,12 +10,16 @@
 // The quotient is taken from the fp32 sum: a row is rounded once.
 //
 // A GEMM [T x d_model] x [d_model x 576]: weight-streaming for a few rows,
-// tensor-bound for a prompt. A CTA computes 128 rows x 192 columns (three column
-// tiles; the positional columns lie in the last) over a slice of d_model, fed
-// through a five-stage TMA ring. When the tiles alone do not fill the SMs the
-// reduction over d_model is split: each split writes fp32 partials and a second
-// kernel adds them in split order (results are bit-reproducible), rotates,
-// quantises and scatters; with one split the GEMM's own epilogue does that.
+// tensor-bound for a prompt. A pair of CTAs (M = 256 MMAs over two SMs) computes 256
+// rows x 288 columns (two column tiles; the positional columns lie in the second)
+// over a slice of d_model, each CTA loading its 128 rows of h and half of the
+// tile's weights through a six-stage TMA ring: 34 KB per 64-wide block and CTA
+// (one CTA on its own with 128 x 192 took 40 KB per third of that work and was
+// bound by what L2 delivers, 11.6 TB/s: 88 us for 9700 rows of 7168). When the
+// tiles alone do not fill the SMs the reduction over d_model is split: each split
+// writes fp32 partials and a second kernel adds them in split order (results are
+// bit-reproducible), rotates, quantises and scatters; with one split the GEMM's own
+// epilogue does that.
 #include <math.h>
 
 #include "chunk.cuh"
@@ -26,31 +30,45 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kN = 192;                 // output columns per CTA
-constexpr int kColTiles = kRow / kN;    // 3
-constexpr int kM = 128;                 // rows per CTA
-constexpr int kStages = 5;
-constexpr uint32_t kABytes = kM * 128, kBBytes = kN * 128, kStageBytes = kABytes + kBBytes;
+constexpr int kN = 288;               // output columns of a pair, as two MMAs of 144
+constexpr int kHalfN = kN / 2;
+constexpr int kColTiles = kRow / kN;  // 2
+constexpr int kM = 128;               // rows per CTA, 256 per pair
+constexpr int kStages = 6;
+constexpr uint32_t kABytes = kM * 128;
+constexpr uint32_t kBBox = kHalfN / 2 * 128;  // this CTA's 72 of an MMA's 144 columns
+constexpr uint32_t kStageBytes = kABytes + 2 * kBBox;
 constexpr uint32_t kOffBar = kStages * kStageBytes;
 constexpr uint32_t kOffFreq = kOffBar + (2 * kStages + 2) * 8;  // 8-byte aligned
 constexpr uint32_t kOffSlots = kOffFreq + 32 * 8;
 constexpr uint32_t kSmem = kOffSlots + 16;
-constexpr uint32_t kTmCols = 256;
+static_assert(kStageBytes % 1024 == 0 && kSmem <= 232448, "shared memory");
+constexpr uint32_t kTmCols = 512;
 constexpr int kThreads = 192;  // warps 0..3 epilogue, 4 producer, 5 MMA issuer
-constexpr int kCtas = 152;     // one per SM
+constexpr int kPairs = 76;     // one pair per two SMs
 
 struct Shape {
   int tiles, KB, S;
 };
-// Splits of the d_model reduction: what fills the SMs, at least two 64-wide
-// blocks each. A function of (T, d_model) only.
+// Splits of the d_model reduction: the cheapest by a count of waves, in units of one
+// 64-wide block of a pair (about 0.35 us): a wave's blocks and a start of eight, and
+// the partial sums' way out and back at 5 TB/s and the second launch. A function of
+// (T, d_model) only.
 inline Shape shape_of(int T, int d_model) {
   Shape a;
-  a.tiles = (T + kM - 1) / kM;
+  a.tiles = (T + 2 * kM - 1) / (2 * kM);
   a.KB = d_model / 64;
-  const int fill = kCtas / (kColTiles * a.tiles);
-  a.S = fill < a.KB / 2 ? fill : a.KB / 2;
-  if (a.S < 1) a.S = 1;
+  double best = 0.;
+  a.S = 1;
+  for (int S = 1; S <= kPairs / kColTiles && 2 * S <= (a.KB > 1 ? a.KB : 2); ++S) {
+    const int64_t waves = ((int64_t)a.tiles * kColTiles * S + kPairs - 1) / kPairs;
+    const double cost = (double)waves * ((a.KB + S - 1) / S + 8) +
+                        (S > 1 ? 8. + (double)S * T * kRow * 8. / 1.75e6 : 0.);
+    if (S == 1 || cost < best) {
+      best = cost;
+      a.S = S;
+    }
+  }
   return a;
 }
 
@@ -117,12 +135,14 @@ struct Args {
 };
 
 template <bool kDirect, bool kF8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h, Args a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  const int nt = blockIdx.x, s = blockIdx.y, tile = blockIdx.z;
+  const uint32_t rank = cluster_ctarank();
+  const int nt = blockIdx.x >> 1, s = blockIdx.y, tile = blockIdx.z;
+  const int t0 = (2 * tile + (int)rank) * kM;  // this CTA's first row
   const int kb0 = (int)((int64_t)s * a.KB / a.S), nkb = (int)((int64_t)(s + 1) * a.KB / a.S) - kb0;
   auto full = [&](int i) { return sbase + kOffBar + 8u * i; };
   auto empty = [&](int i) { return sbase + kOffBar + 8u * (kStages + i); };
@@ -145,12 +165,13 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     fence_mbar_init();
   }
   if (warp == 5) {
-    tmem_alloc(smem_u32(tmem_slot), kTmCols);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(tmem_slot), kTmCols);
+    tmem_relinquish_pair();
   }
   if (kDirect && warp == 0) freq[lane] = turn_fraction(a.theta, lane);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any copy or arrive across the pair
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
@@ -159,35 +180,40 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
       prefetch_tmap(&map_w);
       prefetch_tmap(&map_h);
       const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
+      // the pair's copies complete on the even CTA's barriers, which it arms for both
+      auto weights = [&](int st, int k) {
+        if (rank == 0) mbar_arrive_expect_tx(full(st), 2 * kStageBytes);
+        for (int m = 0; m < 2; ++m)
+          tma_load_2d_pair(sbase + st * kStageBytes + kABytes + m * kBBox, &map_w, mapa(full(st), 0), (kb0 + k) * 64,
+                           nt * kN + m * kHalfN + (int)rank * (kHalfN / 2), keep);
+      };
       // the first stages' weights while the kernel before is finishing (weights
       // are never its output); the hidden states after the wait
       const int early = nkb < kStages ? nkb : kStages;
-      for (int k = 0; k < early; ++k) {
-        mbar_arrive_expect_tx(full(k), kStageBytes);
-        tma_load_2d(sbase + k * kStageBytes + kABytes, &map_w, full(k), (kb0 + k) * 64, nt * kN, keep);
-      }
+      for (int k = 0; k < early; ++k) weights(k, k);
       grid_dependency_wait();
       int k = 0;
       for (; k < nkb; ++k) {
         const int st = k % kStages;
         if (k >= kStages) {
           if (!wait_phase(empty(st), (uint32_t)((k / kStages - 1) & 1), abort_flag, a.err_word)) break;
-          mbar_arrive_expect_tx(full(st), kStageBytes);
-          tma_load_2d(sbase + st * kStageBytes + kABytes, &map_w, full(st), (kb0 + k) * 64, nt * kN, keep);
+          weights(st, k);
         }
-        tma_load_2d(sbase + st * kStageBytes, &map_h, full(st), (kb0 + k) * 64, tile * kM, stream);
+        tma_load_2d_pair(sbase + st * kStageBytes, &map_h, mapa(full(st), 0), (kb0 + k) * 64, t0, stream);
       }
-      if (k < nkb) {  // gave up: let the copies in flight land before the CTA can exit
-        for (int i = k > kStages ? k - kStages : 0; i < k; ++i) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(full(i % kStages), (uint32_t)((i / kStages) & 1)) && clock64() - t0 < kWaitLimitCycles) {
+      if (rank == 0 && *abort_flag) {
+        // let the pair's copies in flight land before the pair can exit (the odd CTA
+        // waits for this one below; where it issued fewer, the limit ends the wait)
+        const long long start = clock64();
+        for (int i = k > kStages ? k - kStages : 0; i < k; ++i)
+          while (!mbar_try_wait(full(i % kStages), (uint32_t)((i / kStages) & 1)) &&
+                 clock64() - start < kWaitLimitCycles) {
           }
-        }
       }
     }
   } else if (warp == 5) {
-    if (elect()) {
-      const uint32_t idesc = idesc_bf16(kM, kN, false, false);
+    if (rank == 0 && elect()) {
+      const uint32_t idesc = idesc_bf16(2 * kM, kHalfN, false, false);
       const uint64_t d0 = smem_desc(0, 16, 1024, kSwizzle128B);
       auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
       for (int k = 0; k < nkb; ++k) {
@@ -196,17 +222,20 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         tc_fence_after();
         const uint64_t ad = d0 + da(sbase + st * kStageBytes), bd = d0 + da(sbase + st * kStageBytes + kABytes);
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) mma_ss(tmem, ad + 2 * k4, bd + 2 * k4, idesc, (k > 0 || k4 > 0) ? 1u : 0u);
-        mma_commit(empty(st));
+        for (int k4 = 0; k4 < 4; ++k4)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            mma_ss_pair(tmem + m * 256, ad + 2 * k4, bd + (m * kBBox >> 4) + 2 * k4, idesc, (k > 0 || k4 > 0) ? 1u : 0u);
+        mma_commit_pair(empty(st), 3);
       }
-      mma_commit(bar_d);
-      mma_commit(bar_d + 8);
+      mma_commit_pair(bar_d, 3);
+      mma_commit_pair(bar_d + 8, 1);
       wait_mmas(bar_d + 8);
     }
   } else {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int row = warp * 32 + lane, t = tile * kM + row;
+    const int row = warp * 32 + lane, t = t0 + row;
     Target to = {-1, 0};
     if (kDirect && t < a.T)
       to = target_of(a.cu, a.seq_lens, a.block_table, a.B, t, a.num_pages, a.page_size, a.max_pages, nt == 0,
@@ -215,47 +244,43 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
 #pragma unroll 1
-      for (int c0 = 0; c0 < kN; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(taddr + c0, r);
+      for (int c0 = 0; c0 < kN; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld16(taddr + (c0 < kHalfN ? c0 : 256 + c0 - kHalfN), r);
         tmem_wait_ld();
         const int col = nt * kN + c0;
         if (!kDirect) {
-          float4* dst = reinterpret_cast<float4*>(a.partials + (((size_t)tile * a.S + s) * kM + row) * kRow + col);
-          if (t < a.T) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              dst[q] = make_float4(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]),
-                                   __uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+          float* dst = a.partials + (((size_t)(2 * tile + (int)rank) * a.S + s) * kM + row) * kRow + col;
+          if (t < a.T) {  // whole 32-byte sectors
+            st_global_32(dst, r);
+            st_global_32(dst + 8, r + 8);
           }
         } else if (to.row >= 0) {
           if (col >= kDC) {
 #pragma unroll 1
-            for (int i = 0; i < 16; ++i) {
-              // indexed through a switch-free rotation of the register pairs
+            for (int i = 0; i < 8; ++i) {  // the pairs pass through the first two registers
               float x = __uint_as_float(r[0]), y = __uint_as_float(r[1]);
               rotate(x, y, freq[(col - kDC) / 2 + i], to.pos);
 #pragma unroll
-              for (int q = 0; q < 30; ++q) r[q] = r[q + 2];
-              r[30] = __float_as_uint(x);
-              r[31] = __float_as_uint(y);
+              for (int q = 0; q < 14; ++q) r[q] = r[q + 2];
+              r[14] = __float_as_uint(x);
+              r[15] = __float_as_uint(y);
             }
           }
           if (kF8) {
-            uint32_t w[8];
+            uint32_t w[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
               const float4 sc = __ldg(reinterpret_cast<const float4*>(a.scales + col) + q);
               w[q] = quantise2(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]), sc.x, sc.y) |
                      quantise2(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]), sc.z, sc.w) << 16;
             }
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.cache) + to.row * kRow + col);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.cache) + to.row * kRow + col) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           } else {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.cache) + to.row * kRow + col);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
@@ -269,9 +294,10 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // nothing of the pair is under way: MMAs, copies, arrives
   if (warp == 5) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmCols);
+    tmem_dealloc_pair(tmem, kTmCols);
   }
 }
 
@@ -320,7 +346,7 @@ template <bool kDirect, bool kF8>
 cudaError_t launch_gemm(const CUtensorMap& mw, const CUtensorMap& mh, const Shape& sh, const Args& a, cudaStream_t s) {
   cudaError_t e = smem_limit<append_chunk_gemm<kDirect, kF8>>(kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(append_chunk_gemm<kDirect, kF8>, dim3(kColTiles, sh.S, sh.tiles), dim3(kThreads), kSmem, s, mw, mh,
+  return launch_pdl(append_chunk_gemm<kDirect, kF8>, dim3(2 * kColTiles, sh.S, sh.tiles), dim3(kThreads), kSmem, s, mw, mh,
                     a);
 }
 
@@ -328,7 +354,7 @@ cudaError_t launch_gemm(const CUtensorMap& mw, const CUtensorMap& mh, const Shap
 
 size_t append_chunk_workspace_bytes(int T, int d_model) {
   const Shape sh = shape_of(T, d_model);
-  return sh.S > 1 ? (size_t)sh.tiles * sh.S * kM * kRow * 4 : 256;
+  return 256 + (sh.S > 1 ? (size_t)sh.tiles * 2 * sh.S * kM * kRow * 4 : 0);
 }
 
 cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
@@ -339,7 +365,7 @@ cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* 
   CUtensorMap mw, mh;
   const uint64_t dw[2] = {(uint64_t)d_model, (uint64_t)kRow}, dh[2] = {(uint64_t)d_model, (uint64_t)T};
   const uint64_t st[1] = {(uint64_t)d_model * 2};
-  const uint32_t bw[2] = {64, kN}, bh[2] = {64, kM};
+  const uint32_t bw[2] = {64, kHalfN / 2}, bh[2] = {64, kM};
   if (!make_tmap(&mw, w_dkr, 2, dw, st, bw, 128) || !make_tmap(&mh, h, 2, dh, st, bh, 128))
     return cudaErrorInvalidValue;
   Args a = {};
@@ -348,7 +374,7 @@ cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* 
   a.cu = cu;
   a.scales = fp8_scales;
   a.cache = cache;
-  a.partials = static_cast<float*>(workspace);
+  a.partials = reinterpret_cast<float*>(workspace_base(workspace));
   a.err_word = err_word;
   a.theta = theta;
   a.B = B;

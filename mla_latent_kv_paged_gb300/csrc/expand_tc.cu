@@ -39,12 +39,6 @@ static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kThreads = 320;  // warps 0..7 write-out, 8 producer, 9 MMA issuer
 constexpr uint32_t kF16Limit = 0x477FF000u;  // 65520.0f: from here on fp16 rounds to infinity
 
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // 64 values of one token as fp16 to dst; the largest |value| as bits.
 __device__ __forceinline__ uint32_t write_row(const uint32_t (&r)[64], uint16_t* dst) {
   uint32_t top = 0;

@@ -373,6 +373,13 @@ __device__ __forceinline__ void grid_launch_dependents() {
 
 namespace mla {
 namespace sm100 {
+// A whole 32-byte sector of global memory (32-byte aligned).
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // ---------------------------------------------------------------- CTA pairs (cta_group::2)
 // Two CTAs of a cluster (ranks 2i and 2i + 1) work on one M = 256 MMA: each holds
 // its 128 rows of A and of D and one half of B's rows, at the same shared-memory
