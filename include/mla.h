@@ -442,7 +442,7 @@ mla_status mla_copy16(const void* src, void* dst, size_t bytes, void* stream);
 /* ------------------------------------------------------------------------
  * The prompt side: a ragged CHUNK of new tokens. Sequence b owns rows cu[b] ..
  * cu[b+1] - 1 of the row arrays (n_b = cu[b+1] - cu[b] >= 0 new tokens; cu
- * [B + 1] int32, nondecreasing, cu[0] >= 0), and seq_lens[b] counts them: row j
+ * [B + 1] int32, nondecreasing from cu[0] = 0), and seq_lens[b] counts them: row j
  * of sequence b sits at position seq_lens[b] - n_b + j. T is the number of rows
  * of the arrays; rows at and past cu[B] belong to no sequence and their outputs
  * are left as they were, so a captured call serves any chunk of at most T rows
@@ -452,7 +452,9 @@ mla_status mla_copy16(const void* src, void* dst, size_t bytes, void* stream);
  * [n_b, max_pages_per_seq * page_size], page ids outside the pool and rows
  * outside [0, T) are reported in err_word as MLA_ERR_BOUNDS; what they touch is
  * clamped or skipped. Every input but the weights is read after the kernel
- * before has finished.
+ * before has finished. Outputs and workspaces overlap no input. A workspace of
+ * these calls is not one of mla_decode_plan's or mla_decode_paged's, whose plan is
+ * written while the kernel before may still be running.
  *
  * mla_append_chunk — the new tokens' cache rows written into their pages, the
  * row of mla_append_kv:

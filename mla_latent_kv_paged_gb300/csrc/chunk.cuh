@@ -31,7 +31,7 @@ __device__ inline int sequence_of_chunk(const int32_t* seq_lens, const int32_t* 
   const int first = min(max(a, 0), T), end = min(max(e, first), T);
   const int n = min(end - first, max_tokens);
   int L = seq_lens[b];
-  if (a != first || e != first + n || ((L < n || L > max_tokens) && n > 0)) report_error(err_word, MLA_ERR_BOUNDS);
+  if (a != first || (b == 0 && a != 0) || e != first + n || ((L < n || L > max_tokens) && n > 0)) report_error(err_word, MLA_ERR_BOUNDS);
   L = min(max(L, n), max_tokens);
   *c0 = first;
   *len = n > 0 ? L : 0;  // a sequence without new rows takes no part

@@ -170,8 +170,8 @@ __device__ __forceinline__ uint32_t scale_bf16x2_to_f16x2(uint32_t w, float s0, 
 }
 
 // kRows: the sequences are rows of a chunk (chunk.cuh): seq_row[b] is the block-table
-// row of sequence b, -1 for a row of no sequence (it reads page 0 and its result
-// is not used). A template parameter, because any change to the plain kernel's
+// row of sequence b, -1 for a row of no sequence (it reads zeros and its result is
+// not used). A template parameter, because any change to the plain kernel's
 // code costs it a few per cent (decode call 38.8 -> 39.5 us with a run-time test).
 template <bool kF8, bool kRows>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -269,14 +269,18 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
     const int tile_mask = (1 << tile_shift) - 1;
     struct Cursor {
       int it, pg, pg1, base, id_l, pg0, seq;  // pg0, seq: the piece's first tile and its sequence
-      int64_t row;  // block-table row of the current range (its first entry), or < 0: page 0
+      int64_t row;  // block-table row of the current range (its first entry), or < 0: none
     };
     auto table_row = [&](int seq) -> int64_t {
       return (int64_t)(kRows ? seq_row[seq] : seq) * max_pages;
     };
     auto cur_load = [&](Cursor& c) {
       const int mine = c.base + lane;
-      c.id_l = mine < c.pg1 && (!kRows || c.row >= 0) ? block_table[c.row + (mine >> tile_shift)] : 0;
+      // (a row of no sequence reads past the pool: zeros)
+      if (kRows && c.row < 0)
+        c.id_l = num_pages;
+      else
+        c.id_l = mine < c.pg1 ? block_table[c.row + (mine >> tile_shift)] : 0;
     };
     auto cur_init = [&](Cursor& c, int it) {
       c.it = it;
@@ -337,9 +341,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
         if (!ok) break;
       }
       const int sub = ld.pg & tile_mask;  // the tile's place in its page
+      const bool none = kRows && ld.row < 0;
       const int pid = cur_next(ld);
       // an id outside the pool loads zeros (TMA bounds) and is reported
-      if (lane == 0 && (pid < 0 || pid >= num_pages)) report_error(err_word, MLA_ERR_BOUNDS);
+      if (lane == 0 && !none && (pid < 0 || pid >= num_pages)) report_error(err_word, MLA_ERR_BOUNDS);
       if (!wait_phase(bar(EMPTY0 + stage), ph ^ 1u, abort_flag, err_word)) { ok = false; break; }
       if (lane == 0 && MLA_SMEM_OK(sbase + kOffStage + stage * kStageBytes, kStageBytes)) {
         const uint32_t fb = bar(FULL0 + stage);

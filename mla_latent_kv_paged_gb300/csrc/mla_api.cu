@@ -430,7 +430,7 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
       !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u) || !aligned16(workspace))
     return MLA_ERR_INVALID_ARG;
   if (B < 1 || T < 1 || num_pages < 1 || max_pages_per_seq < 1 || max_tokens < 1) return MLA_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.f) || softmax_scale > 3.0e38f) return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f) || softmax_scale > 1.0e38f) return MLA_ERR_INVALID_ARG;
   if (form < MLA_CHUNK_AUTO || form > MLA_CHUNK_ABSORBED) return MLA_ERR_INVALID_ARG;
   if (!chunk_counts_ok(B, T) || !heads_ok(H) || !page_size_ok(page_size) || max_tokens > INT32_MAX / 2)
     return MLA_ERR_UNSUPPORTED_SHAPE;

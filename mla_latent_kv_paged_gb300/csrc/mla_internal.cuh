@@ -34,7 +34,7 @@ struct Plan {
   float* lse_part;       // [I][n_q][H]
   uint16_t* o_part;      // [I][n_q][64][H][8] fp16, head-minor
   int4* range_desc;      // [G + 1] {first item, its sequence, its first tile, its end tile}
-  // block-table row of each sequence; null: sequence b uses row b. A row of -1 reads page 0
+  // block-table row of each sequence; null: sequence b uses row b. A row of -1 reads zeros
   // (rows of a chunk that belong to no sequence: their result is not used).
   const int32_t* seq_row = nullptr;
 };

@@ -72,7 +72,7 @@ __device__ inline int64_t div_nn(int64_t a, int64_t b) {
 __device__ inline int64_t ceil_div64(int64_t a, int64_t b) { return div_nn(a + b - 1, b); }
 
 // kRows: the B sequences of the plan are the rows of a chunk (n_q = 1): row t sees
-// the tokens up to its own; a row of no sequence sees one token (of page 0, see
+// the tokens up to its own; a row of no sequence sees one token of zeros (see
 // Plan::seq_row). The chunk's inputs may come from the kernel before, so they are
 // read after it has finished.
 struct RowArgs {

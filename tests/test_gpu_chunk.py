@@ -494,3 +494,103 @@ def test_attend_cut_rising_scores(mla, err):
     got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=6000, form="expanded",
                            err_word=err)
     check(got, want, bound["expanded"], "rising")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("form", ["expanded", "absorbed"])
+def test_rows_of_no_sequence_report_nothing(mla, err, form, fp8):
+    """Padding rows with any bits in their queries, and a pool whose first page holds any
+    bits: nothing of it reaches the outputs or the error word."""
+    import torch
+    c = ref.Chunk([3, 2], [100, 66], H=2, fp8=fp8, seed=60, pad_rows=150)
+    used = torch.unique(c.table[c.table >= 0])
+    free = [p for p in range(c.num_pages) if p not in used.tolist()]
+    assert free
+    # the free page first in the pool: swap it with page 0 in place
+    order = torch.arange(c.num_pages, device="cuda")
+    order[0], order[free[0]] = free[0], 0
+    c.cache = c.cache[order].contiguous()
+    c.table = torch.where(c.table < 0, c.table, torch.argsort(order).to(torch.int32)[c.table.clamp(min=0).long()])
+    c.host_table = c.table.cpu().tolist()
+    c.cache[0] = 0x7E if fp8 else 3e38
+    c.q_nope[c.total:] = 1e38
+    c.q_rope[c.total:] = float("nan")
+    want, _, bound = ref.attend(c)
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=166, fp8_scales=c.scales,
+                           form=form, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(got[:c.total], want, bound[form], form)
+
+
+def test_first_row_offset_is_reported(mla, err):
+    import torch
+    c = ref.Chunk([3, 2], [100, 66], H=2, seed=61, pad_rows=4)
+    c.cu += 1
+    for form in ("expanded", "absorbed"):
+        err.zero_()
+        mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=166, form=form, err_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == BOUNDS
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pool_beyond_32_bit_offsets(mla, err, fp8):
+    """Rows in pages whose element offsets (and, bf16, byte offsets / 2) pass 2^32."""
+    import torch
+    pages = 120000  # x 64 x 576 = 4.4e9 elements
+    c = ref.Chunk([70, 3], [300, 130], H=2, fp8=fp8, seed=62)
+    pool = torch.zeros(pages, 64, 576, dtype=c.cache.dtype, device="cuda")
+    shift = pages - c.num_pages
+    pool[shift:] = c.cache
+    c.cache, c.num_pages = pool, pages
+    c.table = torch.where(c.table < 0, c.table, c.table + shift)
+    c.host_table = c.table.cpu().tolist()
+    h, w = hidden(c.T, 128, 63)
+    rows, want_rows, slack = ref.append(c, h, w)
+    mla.append_chunk(h, w, *c.paged(), fp8_scales=c.scales, err_word=err)
+    got = c.cache.view(-1, 576)[rows]
+    got = got.view(torch.float8_e4m3fn).double() * c.scales.double() if fp8 else got.double()
+    tol = (2.0 ** -4 if fp8 else ref.U_BF16) * want_rows.abs() + 1.1 * slack
+    if fp8:
+        tol += 2.0 ** -10 * c.scales.double()
+    inside = (want_rows / c.scales.double()).abs() <= 440 if fp8 else torch.ones_like(tol, dtype=torch.bool)
+    assert ((got - want_rows).abs() <= tol)[inside].all()
+    back = mla.read_kv(*c.paged(), n_rows=73, first=torch.tensor([230, 127], dtype=torch.int32, device="cuda"),
+                       fp8_scales=c.scales, err_word=err)
+    assert ((back.double() - got).abs() <= ref.U_BF16 * got.abs()).all()
+    want, _, bound = ref.attend(c)
+    for form in ("expanded", "absorbed"):
+        o = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=430, fp8_scales=c.scales,
+                             form=form, err_word=err)
+        check(o, want, bound[form], form)
+    assert int(err.item()) == 0
+
+
+def test_many_sequences_and_the_largest_batch(mla, err):
+    """4096 sequences, most of one token; the batch limit of every call."""
+    import torch
+    B = 4096
+    new = [1] * B
+    new[7], new[4000] = 0, 30
+    lens = [1 + (b % 3) for b in range(B)]
+    lens[4000], lens[100] = 700, 130
+    c = ref.Chunk(new, lens, H=1, seed=64)
+    back = mla.read_kv(c.cache, c.table, c.seq_lens, c.cu, n_rows=c.total, err_word=err)
+    assert torch.equal(back[1], c.cache.view(-1, 576)[c.rows(1, 0, 1)][0])
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=sum(lens), form="expanded",
+                           err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    pick = [0, 1, 99, 100, 3999, 4000, 4095]
+    d = ref.Chunk([new[b] for b in pick], [lens[b] for b in pick], H=1, seed=65)
+    d.w_uk, d.w_uv = c.w_uk, c.w_uv
+    rows = []
+    for i, b in enumerate(pick):
+        d.cache.view(-1, 576)[d.rows(i)] = c.cache.view(-1, 576)[c.rows(b)]
+        rows += list(range(int(c.cu[b]), int(c.cu[b + 1])))
+    d.q_nope, d.q_rope = c.q_nope[rows].contiguous(), c.q_rope[rows].contiguous()
+    want, _, bound = ref.attend(d)
+    check(got[rows], want, bound["expanded"], "many sequences")
+    with pytest.raises(mla.MlaError):
+        mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=sum(lens), form="absorbed")
