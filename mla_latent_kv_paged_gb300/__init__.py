@@ -489,9 +489,14 @@ def out_proj(u, w_uv, out=None, stream=None):
 CHUNK_FORMS = {"auto": 0, "expanded": 1, "absorbed": 2}
 
 
+def _fits(t, dtype, shape, dev):
+    """Whether ``t`` has this dtype and shape (a tuple), is contiguous and on CUDA device number ``dev``."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
 def _tensor(name, t, dtype, shape, dev):
-    """Check one argument: ``dtype``, ``shape`` (a tuple), contiguous, on CUDA device number ``dev``."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+    """Check one argument, and say what is wrong with it."""
+    if _fits(t, dtype, shape, dev):
         return
     if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -509,7 +514,8 @@ def _dims(name, t, n):
 
 
 def _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word):
-    """Check the paged-cache arguments of the chunk calls; returns (device number, B)."""
+    """Check the paged-cache arguments of the chunk calls; returns (device number, B, pages,
+    page size, pages per sequence)."""
     import torch
     dev = cache.get_device()
     if dev < 0:
@@ -518,42 +524,47 @@ def _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word):
     if fp8 != (fp8_scales is not None):
         raise ValueError("an FP8 cache (uint8 codes) needs its column scales fp8_scales, a bf16 cache has none")
     num_pages, page_size, _ = _dims("cache", cache, 3)
-    _tensor("cache", cache, torch.uint8 if fp8 else torch.bfloat16, (num_pages, page_size, D_ROW), dev)
     B, max_pages = _dims("block_table", block_table, 2)
     i32 = torch.int32
-    _tensor("block_table", block_table, i32, (B, max_pages), dev)
-    _tensor("seq_lens", seq_lens, i32, (B,), dev)
-    _tensor("cu", cu, i32, (B + 1,), dev)
+    if not (_fits(cache, torch.uint8 if fp8 else torch.bfloat16, (num_pages, page_size, D_ROW), dev)
+            and _fits(block_table, i32, (B, max_pages), dev) and _fits(seq_lens, i32, (B,), dev)
+            and _fits(cu, i32, (B + 1,), dev)):
+        _tensor("cache", cache, torch.uint8 if fp8 else torch.bfloat16, (num_pages, page_size, D_ROW), dev)
+        _tensor("block_table", block_table, i32, (B, max_pages), dev)
+        _tensor("seq_lens", seq_lens, i32, (B,), dev)
+        _tensor("cu", cu, i32, (B + 1,), dev)
     if fp8:
         _tensor("fp8_scales", fp8_scales, torch.float32, (D_ROW,), dev)
     if err_word is not None and (err_word.dtype is not i32 or err_word.numel() < 1 or err_word.get_device() != dev):
         raise ValueError("err_word: an int32 tensor beside the cache")
-    return dev, B
+    return dev, B, num_pages, page_size, max_pages
 
 
 def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _call(fn, dev, stream, *args):
+def _call(name, fn, dev, stream, *args):
     """fn(*args, stream) with device ``dev`` current (a kernel launches on the current device)."""
     import torch
-    if stream is not None:
-        handle = stream.cuda_stream
-    else:  # the number alone: a Stream object takes a microsecond
-        handle = torch._C._cuda_getCurrentRawStream(dev)
+    # the stream's number alone: a Stream object takes a microsecond
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        return fn(*args, handle)
-    with torch.cuda.device(dev):
-        return fn(*args, handle)
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, handle)
+    if status != 0:
+        raise MlaError(status, name)
 
 
-def _room(workspace, need, dev):
-    """(workspace, its bytes): the one given (its size is checked by the call), or a new one."""
+def _room(workspace, need, like):
+    """(workspace, its bytes): the one given (its size is checked by the call), or a new one
+    of ``need`` bytes beside the tensor ``like``."""
     import torch
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}"), need
-    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        return torch.empty(need, dtype=torch.uint8, device=like.device), need
+    if not workspace.is_contiguous() or workspace.get_device() != like.get_device():
         raise ValueError("workspace: a contiguous tensor beside the cache")
     return workspace, workspace.numel() * workspace.element_size()
 
@@ -577,16 +588,14 @@ def append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, *, fp8_scales=None,
     workspace (allocated when none is given) is returned for reuse.
     """
     import torch
-    dev, B = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    dev, B, num_pages, page_size, max_pages = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
     T, d_model = _dims("h", h, 2)
     _tensor("h", h, torch.bfloat16, (T, d_model), dev)
     _tensor("w_dkr", w_dkr, torch.bfloat16, (D_ROW, d_model), dev)
-    workspace, room = _room(workspace, append_chunk_workspace_bytes(T, d_model), dev)
-    num_pages, page_size, _ = cache.shape
-    st = _call(lib().mla_append_chunk, dev, stream, h.data_ptr(), w_dkr.data_ptr(), cache.data_ptr(),
-               _address(fp8_scales), block_table.data_ptr(), seq_lens.data_ptr(), cu.data_ptr(), B, T, d_model,
-               num_pages, page_size, block_table.shape[1], rope_theta, workspace.data_ptr(), room, _address(err_word))
-    _check(st, "mla_append_chunk")
+    workspace, room = _room(workspace, append_chunk_workspace_bytes(T, d_model), cache)
+    _call("mla_append_chunk", lib().mla_append_chunk, dev, stream, h.data_ptr(), w_dkr.data_ptr(), cache.data_ptr(),
+          _address(fp8_scales), block_table.data_ptr(), seq_lens.data_ptr(), cu.data_ptr(), B, T, d_model, num_pages,
+          page_size, max_pages, rope_theta, workspace.data_ptr(), room, _address(err_word))
     return workspace
 
 
@@ -597,17 +606,16 @@ def read_kv(cache, block_table, seq_lens, cu, *, n_rows: int, first=None, fp8_sc
     (uint8 codes with fp8_scales), zeros at and past seq_lens[b]. Rows at and past cu[B]
     are left as they were in ``out`` (undefined in a new tensor)."""
     import torch
-    dev, B = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    dev, B, num_pages, page_size, max_pages = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
     if first is not None:
         _tensor("first", first, torch.int32, (B,), dev)
     if out is None:
         out = torch.empty((n_rows, D_ROW), dtype=torch.bfloat16, device=cache.device)
-    _tensor("out", out, torch.bfloat16, (n_rows, D_ROW), dev)
-    num_pages, page_size, _ = cache.shape
-    st = _call(lib().mla_read_kv, dev, stream, cache.data_ptr(), _address(fp8_scales), block_table.data_ptr(),
-               seq_lens.data_ptr(), _address(first), cu.data_ptr(), out.data_ptr(), B, n_rows, num_pages, page_size,
-               block_table.shape[1], _address(err_word))
-    _check(st, "mla_read_kv")
+    else:
+        _tensor("out", out, torch.bfloat16, (n_rows, D_ROW), dev)
+    _call("mla_read_kv", lib().mla_read_kv, dev, stream, cache.data_ptr(), _address(fp8_scales),
+          block_table.data_ptr(), seq_lens.data_ptr(), _address(first), cu.data_ptr(), out.data_ptr(), B, n_rows,
+          num_pages, page_size, max_pages, _address(err_word))
     return out
 
 
@@ -635,7 +643,7 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
     past cu[B] of out and lse are left as they were.
     """
     import torch
-    dev, B = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    dev, B, num_pages, page_size, max_pages = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
     if form not in CHUNK_FORMS:
         raise ValueError(f"form: {form!r}, expected one of {sorted(CHUNK_FORMS)}")
     bf = torch.bfloat16
@@ -646,24 +654,24 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
     _tensor("w_uv", w_uv, bf, (H, D_V, D_C), dev)
     if lse is not None:
         _tensor("lse", lse, torch.float32, (T, H), dev)
-    num_pages, page_size, _ = cache.shape
-    max_pages = block_table.shape[1]
     if max_tokens is None:
         max_tokens = B * max_pages * page_size
     if out is None:
         out = torch.empty((T, H, D_V), dtype=bf, device=cache.device)
-    _tensor("out", out, bf, (T, H, D_V), dev)
-    if workspace is None:
-        with torch.cuda.device(dev):
-            need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
     else:
-        need = 0
-    workspace, room = _room(workspace, need, dev)
-    st = _call(lib().mla_attend_chunk, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(), w_uk.data_ptr(),
-               w_uv.data_ptr(), cache.data_ptr(), _address(fp8_scales), block_table.data_ptr(), seq_lens.data_ptr(),
-               cu.data_ptr(), B, T, H, num_pages, page_size, max_pages, max_tokens, softmax_scale, CHUNK_FORMS[form],
-               out.data_ptr(), _address(lse), workspace.data_ptr(), room, _address(err_word))
-    _check(st, "mla_attend_chunk")
+        _tensor("out", out, bf, (T, H, D_V), dev)
+    need = 0
+    if workspace is None:  # (the absorbed form's size depends on the device)
+        if torch.cuda.current_device() == dev:
+            need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
+        else:
+            with torch.cuda.device(dev):
+                need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
+    workspace, room = _room(workspace, need, cache)
+    _call("mla_attend_chunk", lib().mla_attend_chunk, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(),
+          w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), _address(fp8_scales), block_table.data_ptr(),
+          seq_lens.data_ptr(), cu.data_ptr(), B, T, H, num_pages, page_size, max_pages, max_tokens, softmax_scale,
+          CHUNK_FORMS[form], out.data_ptr(), _address(lse), workspace.data_ptr(), room, _address(err_word))
     return out
 
 
