@@ -44,7 +44,7 @@ constexpr uint32_t kOffSlots = kOffFreq + 32 * 8;
 constexpr uint32_t kSmem = kOffSlots + 16;
 static_assert(kStageBytes % 1024 == 0 && kSmem <= 232448, "shared memory");
 constexpr uint32_t kTmCols = 512;
-constexpr int kThreads = 192;  // warps 0..3 epilogue, 4 producer, 5 MMA issuer
+constexpr int kThreads = 320;  // warps 0..7 epilogue, 8 producer, 9 MMA issuer
 constexpr int kPairs = 76;     // one pair per two SMs
 
 struct Shape {
@@ -80,16 +80,19 @@ __device__ __forceinline__ uint64_t turn_fraction(double theta, int i) {
 }
 __device__ __forceinline__ void rotate(float& x, float& y, uint64_t per_pos, int pos) {
   const int32_t turn = (int32_t)((per_pos * (uint64_t)(uint32_t)pos) >> 32);  // [-1/2, 1/2) in 2^-32
+  // absolute errors below 2^-21 on [-pi, pi]; the results are rounded to 2^-8 relative or coarser
   float sn, cs;
-  sincosf((float)turn * 1.4629180792671596e-9f /* 2 pi 2^-32 */, &sn, &cs);
+  __sincosf((float)turn * 1.4629180792671596e-9f /* 2 pi 2^-32 */, &sn, &cs);
   const float rx = x * cs - y * sn;
   y = x * sn + y * cs;
   x = rx;
 }
-// two quotients -> two e4m3 codes (lo in the low byte), nearest even, saturating
+// two quotients -> two e4m3 codes (lo in the low byte), nearest even, saturating. The
+// quotient is fp32's within two units (a division's last bit is nothing beside 3
+// mantissa bits, and 288 of them a thread took as long as the row's write-out).
 __device__ __forceinline__ uint32_t quantise2(float x, float y, float sx, float sy) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(__fdiv_rn(y, sy)), "f"(__fdiv_rn(x, sx)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(__fdividef(y, sy)), "f"(__fdividef(x, sx)));
   return r;
 }
 
@@ -164,7 +167,7 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc_pair(smem_u32(tmem_slot), kTmCols);
     tmem_relinquish_pair();
   }
@@ -175,7 +178,7 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 4) {
+  if (warp == 8) {
     if (elect()) {
       prefetch_tmap(&map_w);
       prefetch_tmap(&map_h);
@@ -211,7 +214,7 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
           }
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     if (rank == 0 && elect()) {
       const uint32_t idesc = idesc_bf16(2 * kM, kHalfN, false, false);
       const uint64_t d0 = smem_desc(0, 16, 1024, kSwizzle128B);
@@ -235,16 +238,17 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
   } else {
     grid_dependency_wait();
     grid_launch_dependents();
-    const int row = warp * 32 + lane, t = t0 + row;
+    // a warp per 32 rows and every other 16 columns
+    const int row = (warp & 3) * 32 + lane, t = t0 + row;
     Target to = {-1, 0};
     if (kDirect && t < a.T)
       to = target_of(a.cu, a.seq_lens, a.block_table, a.B, t, a.num_pages, a.page_size, a.max_pages, nt == 0,
                      a.err_word);
     if (__all_sync(0xffffffffu, wait_phase(bar_d, 0, abort_flag, a.err_word))) {
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
+      const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
 #pragma unroll 1
-      for (int c0 = 0; c0 < kN; c0 += 16) {
+      for (int c0 = 16 * (warp >> 2); c0 < kN; c0 += 32) {
         uint32_t r[16];
         tmem_ld16(taddr + (c0 < kHalfN ? c0 : 256 + c0 - kHalfN), r);
         tmem_wait_ld();
@@ -295,7 +299,7 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // nothing of the pair is under way: MMAs, copies, arrives
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmCols);
   }
