@@ -558,12 +558,21 @@ def _call(name, fn, dev, stream, *args):
         raise MlaError(status, name)
 
 
-def _room(workspace, need, like):
+def _new(shape, dtype, like, stream):
+    """A new tensor beside ``like``, from the memory of the stream that will use it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _room(workspace, need, like, stream):
     """(workspace, its bytes): the one given (its size is checked by the call), or a new one
     of ``need`` bytes beside the tensor ``like``."""
     import torch
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device), need
+        return _new(need, torch.uint8, like, stream), need
     if not workspace.is_contiguous() or workspace.get_device() != like.get_device():
         raise ValueError("workspace: a contiguous tensor beside the cache")
     return workspace, workspace.numel() * workspace.element_size()
@@ -592,10 +601,10 @@ def append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, *, fp8_scales=None,
     T, d_model = _dims("h", h, 2)
     _tensor("h", h, torch.bfloat16, (T, d_model), dev)
     _tensor("w_dkr", w_dkr, torch.bfloat16, (D_ROW, d_model), dev)
-    workspace, room = _room(workspace, append_chunk_workspace_bytes(T, d_model), cache)
+    workspace, room = _room(workspace, append_chunk_workspace_bytes(T, d_model), cache, stream)
     _call("mla_append_chunk", lib().mla_append_chunk, dev, stream, h.data_ptr(), w_dkr.data_ptr(), cache.data_ptr(),
           _address(fp8_scales), block_table.data_ptr(), seq_lens.data_ptr(), cu.data_ptr(), B, T, d_model, num_pages,
-          page_size, max_pages, rope_theta, workspace.data_ptr(), room, _address(err_word))
+          page_size, max_pages, float(rope_theta), workspace.data_ptr(), room, _address(err_word))
     return workspace
 
 
@@ -610,7 +619,7 @@ def read_kv(cache, block_table, seq_lens, cu, *, n_rows: int, first=None, fp8_sc
     if first is not None:
         _tensor("first", first, torch.int32, (B,), dev)
     if out is None:
-        out = torch.empty((n_rows, D_ROW), dtype=torch.bfloat16, device=cache.device)
+        out = _new((n_rows, D_ROW), torch.bfloat16, cache, stream)
     else:
         _tensor("out", out, torch.bfloat16, (n_rows, D_ROW), dev)
     _call("mla_read_kv", lib().mla_read_kv, dev, stream, cache.data_ptr(), _address(fp8_scales),
@@ -654,10 +663,9 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
     _tensor("w_uv", w_uv, bf, (H, D_V, D_C), dev)
     if lse is not None:
         _tensor("lse", lse, torch.float32, (T, H), dev)
-    if max_tokens is None:
-        max_tokens = B * max_pages * page_size
+    max_tokens = B * max_pages * page_size if max_tokens is None else int(max_tokens)
     if out is None:
-        out = torch.empty((T, H, D_V), dtype=bf, device=cache.device)
+        out = _new((T, H, D_V), bf, cache, stream)
     else:
         _tensor("out", out, bf, (T, H, D_V), dev)
     need = 0
@@ -667,11 +675,11 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
         else:
             with torch.cuda.device(dev):
                 need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
-    workspace, room = _room(workspace, need, cache)
+    workspace, room = _room(workspace, need, cache, stream)
     _call("mla_attend_chunk", lib().mla_attend_chunk, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(),
           w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), _address(fp8_scales), block_table.data_ptr(),
-          seq_lens.data_ptr(), cu.data_ptr(), B, T, H, num_pages, page_size, max_pages, max_tokens, softmax_scale,
-          CHUNK_FORMS[form], out.data_ptr(), _address(lse), workspace.data_ptr(), room, _address(err_word))
+          seq_lens.data_ptr(), cu.data_ptr(), B, T, H, num_pages, page_size, max_pages, max_tokens,
+          float(softmax_scale), CHUNK_FORMS[form], out.data_ptr(), _address(lse), workspace.data_ptr(), room, _address(err_word))
     return out
 
 

@@ -448,6 +448,31 @@ def test_calls_on_another_stream(mla):
         check(g, want, bound[f], f)
 
 
+def test_memory_of_a_call_on_another_stream_is_that_streams(mla, monkeypatch):
+    """What a call allocates for itself must not be handed out again on the current stream
+    while the other stream's kernels use it."""
+    import torch
+    c = ref.Chunk([140, 3], [200, 90], H=2, seed=25)
+    h, w = hidden(c.T, 512, 26)
+    seen = []
+    real = mla._call
+    monkeypatch.setattr(mla, "_call", lambda name, fn, dev, stream, *a: (seen.append(a), real(name, fn, dev, stream, *a)))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    need = mla.attend_chunk_workspace_bytes(2, c.T, 2, 290, "expanded")
+    mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=290, form="expanded", stream=s)
+    mla.append_chunk(h, w, *c.paged(), stream=s)
+    mla.read_kv(*c.paged(), n_rows=50, stream=s)
+    again = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in
+             (need, mla.append_chunk_workspace_bytes(c.T, 512), 50 * 576 * 2, c.T * 2 * 128 * 2)]
+    s.synchronize()
+    for t in again:
+        lo, hi = t.data_ptr(), t.data_ptr() + t.numel()
+        inputs = {x.data_ptr() for x in (c.cache, c.table, c.seq_lens, c.cu, c.q_nope, c.q_rope, c.w_uk, c.w_uv, h, w)}
+        assert not any(lo <= v < hi for a in seen for v in a if isinstance(v, int) and v > 1 << 32 and v not in inputs)
+
+
 def test_back_to_back_calls_share_a_workspace(mla):
     import torch
     cs = [ref.Chunk(n, L, H=3, seed=40 + i) for i, (n, L) in
