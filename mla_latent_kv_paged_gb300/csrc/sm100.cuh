@@ -380,6 +380,28 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
                : "memory");
 }
 
+// Four blocks of 8 registers per lane, transposed among the four lanes of a quad:
+// afterwards block k of lane i is block i of the quad's lane k. A thread that holds
+// 128 bytes of a row of its own then stores 32 bytes of each of its quad's four rows,
+// so that a store of the warp covers eight whole lines instead of a piece of 32.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[32]) {
+#pragma unroll
+  for (int s = 1; s <= 2; s <<= 1) {
+    const bool hi = (threadIdx.x & s) != 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      if (b & s) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t& lo_r = w[8 * b + i];
+        uint32_t& hi_r = w[8 * (b + s) + i];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? lo_r : hi_r, s);
+        if (hi) lo_r = got; else hi_r = got;
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- CTA pairs (cta_group::2)
 // Two CTAs of a cluster (ranks 2i and 2i + 1) work on one M = 256 MMA: each holds
 // its 128 rows of A and of D and one half of B's rows, at the same shared-memory
