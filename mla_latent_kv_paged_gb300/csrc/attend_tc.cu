@@ -26,9 +26,9 @@
 // and end stood beside 16 us of steps for a prompt of 2048: 249 -> 229 us a call).
 //
 // Bound by power where it runs long: at 2048 rows on 16384 tokens x 128 heads the
-// card sits at its limit (1365 W, the SM clock down to 1.84 GHz) and the call does
-// 1470 TFLOP/s, 86% of what cuBLAS sustains under the same cap. On short contexts it
-// is bound by the chain S -> softmax -> P V -> next S of each tile.
+// card sits at its limit (1350 W, the SM clock down to 1.70 GHz) and the call does
+// 1500 TFLOP/s, 87% of what cuBLAS sustains under the same cap (this kernel 1640 us).
+// On short contexts it is bound by the chain S -> softmax -> P V -> next S of each tile.
 //
 // The running maximum is a reference that is only raised when a row exceeds it
 // by 2^8 (O is then rescaled by the thread that owns the row); P is held times

@@ -619,3 +619,27 @@ def test_many_sequences_and_the_largest_batch(mla, err):
     check(got[rows], want, bound["expanded"], "many sequences")
     with pytest.raises(mla.MlaError):
         mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=sum(lens), form="absorbed")
+
+
+def test_two_calls_at_once_on_two_streams(mla):
+    """Calls that overlap on the GPU, each with its own workspace and outputs."""
+    import torch
+    cs = [ref.Chunk([300, 40], [900, 500], H=4, seed=70), ref.Chunk([130], [2000], H=3, seed=71)]
+    hw = [hidden(c.T, 512, 72) for c in cs]
+    wants = []
+    for c, (h, w) in zip(cs, hw):
+        rows, _, _ = ref.append(c, h, w)
+        mla.append_chunk(h, w, *c.paged())
+        wants.append(ref.attend(c))
+    streams = [torch.cuda.Stream() for _ in cs]
+    outs = [[] for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for i, (c, (h, w), s) in enumerate(zip(cs, hw, streams)):
+            for form in ("expanded", "absorbed"):
+                outs[i].append((form, mla.chunk_step(h, c.q_nope, c.q_rope, w, c.w_uk, c.w_uv, *c.paged(), form=form,
+                                                     max_tokens=sum(c.lens), stream=s)))
+    torch.cuda.synchronize()
+    for (want, _, bound), got in zip(wants, outs):
+        for form, g in got:
+            check(g, want, bound[form], form)
