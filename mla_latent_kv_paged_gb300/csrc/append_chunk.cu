@@ -50,10 +50,13 @@ constexpr int kPairs = 76;     // one pair per two SMs
 struct Shape {
   int tiles, KB, S;
 };
-// Splits of the d_model reduction: the cheapest by a count of waves, in units of one
-// 64-wide block of a pair (about 0.35 us): a wave's blocks and a start of eight, and
-// the partial sums' way out and back at 5 TB/s and the second launch. A function of
-// (T, d_model) only.
+// Splits of the d_model reduction: the cheapest by a count fitted to measured times, in
+// 64-wide blocks of a pair (0.31 us): a wave's blocks, 16 for a further wave, and beside
+// them 21 for one split, else 16 for the two launches, the partial sums' way out and
+// back, 0.0187 a row and 0.0013 a row and split, and 0.12 a split. A function of
+// (T, d_model) only. In us on the GPU, d_model 7168 (splits: time): 32 rows 1: 37.2,
+// 8: 9.6, 24: 7.0, 38: 7.9; 512 rows 1: 40.4, 4: 17.1, 12: 12.2, 19: 14.9; 2048 rows
+// 1: 40.9, 2: 36.4, 4: 29.8, 5 (a second wave): 42.8; 4096 rows 1: 41.2, 2: 50.4.
 inline Shape shape_of(int T, int d_model) {
   Shape a;
   a.tiles = (T + 2 * kM - 1) / (2 * kM);
@@ -62,8 +65,8 @@ inline Shape shape_of(int T, int d_model) {
   a.S = 1;
   for (int S = 1; S <= kPairs / kColTiles && 2 * S <= (a.KB > 1 ? a.KB : 2); ++S) {
     const int64_t waves = ((int64_t)a.tiles * kColTiles * S + kPairs - 1) / kPairs;
-    const double cost = (double)waves * ((a.KB + S - 1) / S + 8) +
-                        (S > 1 ? 8. + (double)S * T * kRow * 8. / 1.75e6 : 0.);
+    const double cost = (double)waves * ((a.KB + S - 1) / S) + 16. * (double)(waves - 1) +
+                        (S > 1 ? 16. + 0.0187 * T + 0.0013 * T * S + 0.12 * S : 21.);
     if (S == 1 || cost < best) {
       best = cost;
       a.S = S;
