@@ -250,19 +250,32 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     if (__all_sync(0xffffffffu, wait_phase(bar_d, 0, abort_flag, a.err_word))) {
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      auto tcol = [&](int c) { return taddr + (c < kHalfN ? c : 256 + c - kHalfN); };
+      if (!kDirect) {
+        // fp32 partials, 128 bytes of a row at a time, transposed in quads so that a
+        // store covers whole lines
+        float* part = a.partials + ((size_t)(2 * tile + (int)rank) * a.S + s) * kM * kRow + nt * kN + 8 * (lane & 3);
 #pragma unroll 1
-      for (int c0 = 16 * (warp >> 2); c0 < kN; c0 += 32) {
+        for (int c0 = 32 * (warp >> 2); c0 < kN; c0 += 64) {
+          uint32_t r[32];
+          tmem_ld16(tcol(c0), *reinterpret_cast<uint32_t(*)[16]>(r));
+          tmem_ld16(tcol(c0 + 16), *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+          tmem_wait_ld();
+          quad_transpose(r);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rk = (row & ~3) + k;
+            if (t0 + rk < a.T) st_global_32(part + (size_t)rk * kRow + c0, r + 8 * k);
+          }
+        }
+      }
+#pragma unroll 1
+      for (int c0 = 16 * (warp >> 2); kDirect && c0 < kN; c0 += 32) {
         uint32_t r[16];
-        tmem_ld16(taddr + (c0 < kHalfN ? c0 : 256 + c0 - kHalfN), r);
+        tmem_ld16(tcol(c0), r);
         tmem_wait_ld();
         const int col = nt * kN + c0;
-        if (!kDirect) {
-          float* dst = a.partials + (((size_t)(2 * tile + (int)rank) * a.S + s) * kM + row) * kRow + col;
-          if (t < a.T) {  // whole 32-byte sectors
-            st_global_32(dst, r);
-            st_global_32(dst + 8, r + 8);
-          }
-        } else if (to.row >= 0) {
+        if (to.row >= 0) {
           if (col >= kDC) {
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {  // the pairs pass through the first two registers
