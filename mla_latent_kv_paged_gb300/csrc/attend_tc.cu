@@ -27,7 +27,7 @@
 //
 // Bound by power where it runs long: at 2048 rows on 16384 tokens x 128 heads the
 // card sits at its limit (1350 W, the SM clock down to 1.70 GHz) and the call does
-// 1500 TFLOP/s, 87% of what cuBLAS sustains under the same cap (this kernel 1640 us).
+// 1460 TFLOP/s, 85% of what cuBLAS sustains under the same cap (this kernel 1640 us).
 // On short contexts it is bound by the chain S -> softmax -> P V -> next S of each tile.
 //
 // The running maximum is a reference that is only raised when a row exceeds it
@@ -461,7 +461,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         }
         st_shared_v4(at, e[0], e[1], e[2], e[3]);
       }
-      if (top >= 0x477FF000u && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
+      if (top >= kF16Limit && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
       fence_proxy_async_smem();
       mbar_arrive(bar(QF0 + x));
       return true;

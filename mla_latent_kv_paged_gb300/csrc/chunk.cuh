@@ -38,6 +38,20 @@ __device__ inline int sequence_of_chunk(const int32_t* seq_lens, const int32_t* 
   return n;
 }
 
+// Eight bf16 values as fp16 (exact for values of normal fp16 size); *top: the largest
+// |value| so far, as bits.
+__device__ __forceinline__ uint4 bf16x8_to_f16(uint4 w, uint32_t* top) {
+  const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+  uint32_t f[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[k] = sm100::cvt_f16x2(bf16_lo(e[k]), bf16_hi(e[k]));
+    *top = max(*top, max((e[k] << 16) & 0x7FFFFFFFu, e[k] & 0x7FFF0000u));
+  }
+  return make_uint4(f[0], f[1], f[2], f[3]);
+}
+constexpr uint32_t kF16Limit = 0x477FF000u;  // 65520.0f: from here on fp16 rounds to infinity
+
 // The MMA issuer's last act: every MMA it issued is done (a wait that gave up
 // elsewhere included) before the CTA gives its tensor memory back. Bounded.
 __device__ __forceinline__ void wait_mmas(uint32_t bar) {
@@ -132,8 +146,9 @@ inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_toke
 struct ChunkRows {
   int32_t* hdr;      // [64] hdr[0] = rows that belong to a sequence
   int32_t* seq_row;  // [T] block-table row (-1 for rows of no sequence)
-  uint16_t* q_abs;   // [T][H][576] bf16
-  uint16_t* u;       // [T][H][512] bf16
+  uint16_t* q_abs;   // [T][H][576] bf16 (fp16 on an FP8 cache)
+  uint16_t* u;       // [T][H][512] fp16
+  uint16_t* w16;     // [H][128][512] fp16 copy of w_uv
   void* decode_ws;   // workspace of the decode over T sequences
 };
 
@@ -146,6 +161,7 @@ inline size_t chunk_rows_layout(void* base, int T, int H, int G, ChunkRows* p) {
   };
   const size_t o_hdr = take(64 * 4), o_s = take((size_t)T * 4);
   const size_t o_q = take((size_t)T * H * kRow * 2), o_u = take((size_t)T * H * kDC * 2);
+  const size_t o_w = take((size_t)H * kDV * kDC * 2);
   const size_t o_d = take(plan_layout(nullptr, T, 1, H, G, nullptr));
   if (base && p) {
     char* c = workspace_base(base);
@@ -153,6 +169,7 @@ inline size_t chunk_rows_layout(void* base, int T, int H, int G, ChunkRows* p) {
     p->seq_row = reinterpret_cast<int32_t*>(c + o_s);
     p->q_abs = reinterpret_cast<uint16_t*>(c + o_q);
     p->u = reinterpret_cast<uint16_t*>(c + o_u);
+    p->w16 = reinterpret_cast<uint16_t*>(c + o_w);
     p->decode_ws = c + o_d;
   }
   return off + 256;
@@ -181,10 +198,11 @@ cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* 
 cudaError_t launch_chunk_plan(const int32_t* seq_lens, const int32_t* cu, int B, int T, int max_tokens,
                               int64_t max_total, int heads, const ChunkPlan& plan, int32_t* err_word,
                               cudaStream_t s);
-// the decode plan of a chunk's T rows, each a sequence of its own (plan.cu)
-cudaError_t launch_rows_plan(const int32_t* seq_lens, const int32_t* cu, int sequences, int T, int max_pages,
-                             int page_size, int num_pages, int G, const Plan& plan, int32_t* seq_row, int32_t* live,
-                             int32_t* err_word, cudaStream_t s);
+// the decode plan of a chunk's T rows, each a sequence of its own, and beside it the
+// fp16 copy of w_uv that out_proj takes (plan.cu)
+cudaError_t launch_rows_plan(const int32_t* seq_lens, const int32_t* cu, int sequences, int T, int H, int max_pages,
+                             int page_size, int num_pages, int G, const Plan& plan, const ChunkRows& rows,
+                             const uint16_t* w_uv, int32_t* err_word, cudaStream_t s);
 // keys and values of heads [h0, h0 + heads) of every expanded row; f16: rows and weights are fp16, not bf16
 cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uint16_t* w_uv, int H, int h0, int heads,
                           int64_t cap, bool f16, int32_t* err_word, cudaStream_t s);

@@ -22,7 +22,8 @@ constexpr int kCols = 64;      // latent columns per block
 constexpr int kCPT = kCols / 2;  // columns per thread
 constexpr int kKB = 2;         // partials whose loads are in flight together
 
-// kRows: the rows of a chunk, of which only those below *rows_live write their lse
+// kRows: the rows of a chunk, of which only those below *rows_live write their lse; u
+// is fp16 then (the partials are fp16 already: bf16 would add a rounding of 2^-8)
 template <bool kRows>
 __global__ void __launch_bounds__(kThreads)
 combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __restrict__ lse_out,
@@ -111,7 +112,8 @@ combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __res
   const float inv = wsum > 0.f ? 1.f / wsum : (!kRows || wsum == 0.f ? 0.f : wsum);  // a NaN partial stays NaN
 #pragma unroll
   for (int c = 0; c < kCPT / 2; ++c)
-    tile[h][(kCPT / 2) * part + c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+    tile[h][(kCPT / 2) * part + c] = kRows ? sm100::cvt_f16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv)
+                                           : pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
   __syncthreads();
   // row h of the slice is 128 contiguous bytes of u: 8 threads per row, 16 bytes each
   for (int i = threadIdx.x; i < H * 8; i += kThreads) {

@@ -41,7 +41,6 @@ constexpr uint32_t kOffSlots = kOffBar + 8 * kBars;
 constexpr uint32_t kSmem = kOffSlots + 16;
 static_assert(kSmem <= 232448, "shared memory budget");
 constexpr int kThreads = 320;  // warps 0..7 write-out, 8 producer, 9 MMA issuer
-constexpr uint32_t kF16Limit = 0x477FF000u;  // 65520.0f: from here on fp16 rounds to infinity
 
 // 64 values of each lane's token as fp16 to a [32 tokens][128] tile at dst; the largest
 // |value| of the lane's token as bits.

@@ -448,9 +448,9 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
     Plan plan;
     plan_layout(r.decode_ws, T, 1, H, G, &plan);
     plan.seq_row = r.seq_row;
-    mla_status st = launch_status(launch_rows_plan(seq_lens, cu, B, T, max_pages_per_seq, page_size, num_pages, G,
-                                                   plan, r.seq_row, r.hdr, err_word, s));
-    if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s));
+    mla_status st = launch_status(launch_rows_plan(seq_lens, cu, B, T, H, max_pages_per_seq, page_size, num_pages,
+                                                   G, plan, r, w_uv, err_word, s));
+    if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s, fp8_scales != nullptr));
     if (st == MLA_OK)
       st = launch_status(fp8_scales ? launch_decode_fp8(r.q_abs, static_cast<const uint8_t*>(cache), fp8_scales,
                                                         block_table, T, 1, H, num_pages, page_size,
@@ -459,12 +459,11 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
                                                     H, num_pages, page_size, max_pages_per_seq, softmax_scale, G,
                                                     plan, err_word, s));
     if (st == MLA_OK) st = launch_status(launch_combine(plan, T, 1, H, r.u, lse, s, r.hdr));
-    if (st == MLA_OK) st = launch_status(launch_out_proj(r.u, w_uv, out, T, H, s, r.hdr));
+    if (st == MLA_OK) st = launch_status(launch_out_proj(r.u, r.w16, out, T, H, s, r.hdr));
     return st;
   }
   const int64_t cap = chunk_cap(max_tokens, B);
   const int group = chunk_head_group(H, cap), slots = chunk_slots(B, T, group, max_tokens);
-  const int w_heads = H;
   if (workspace_bytes < chunk_layout(nullptr, B, T, group, max_tokens, H, nullptr)) return MLA_ERR_WORKSPACE_TOO_SMALL;
   ChunkPlan plan;
   chunk_layout(workspace, B, T, group, max_tokens, H, &plan);

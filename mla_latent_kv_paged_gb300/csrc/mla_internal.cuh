@@ -166,12 +166,15 @@ cudaError_t launch_quantize_fp8(const uint16_t* rows, const float* scales, uint8
                                 cudaStream_t s);
 // Worker clusters (CTA pairs) of the decode kernel that fit on the device at once.
 int decode_max_workers();
-// rows_live (device, may be null): lse is written for rows < *rows_live only
+// rows_live (device, may be null): a chunk's rows; lse is written for rows < *rows_live
+// only, and u is fp16
 cudaError_t launch_combine(const Plan& plan, int B, int n_q, int H, uint16_t* u, float* lse,
                            cudaStream_t s, const int32_t* rows_live = nullptr);
+// f16: q_abs in fp16 (a chunk's rows on an FP8 cache)
 cudaError_t launch_absorb_q(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
-                            uint16_t* q_abs, int T, int H, cudaStream_t s);
-// rows_live (device, may be null): only rows t < *rows_live are written
+                            uint16_t* q_abs, int T, int H, cudaStream_t s, bool f16 = false);
+// rows_live (device, may be null): a chunk's rows; only rows t < *rows_live are written,
+// and u and w_uv are fp16
 cudaError_t launch_out_proj(const uint16_t* u, const uint16_t* w_uv, uint16_t* out, int T, int H,
                             cudaStream_t s, const int32_t* rows_live = nullptr);
 cudaError_t launch_merge_w_kq(const uint16_t* w_uq, const uint16_t* w_uk, uint16_t* w_kq, int d_q, int H,

@@ -75,12 +75,22 @@ __device__ inline int64_t ceil_div64(int64_t a, int64_t b) { return div_nn(a + b
 // the tokens up to its own; a row of no sequence sees one token of zeros (see
 // Plan::seq_row). The chunk's inputs may come from the kernel before, so they are
 // read after it has finished.
+// Beside the planning threads (the first block, or its first warp) the rest of the
+// grid copies w_uv to fp16, in the time that the plan's chain of latencies takes.
 struct RowArgs {
   const int32_t* cu;   // [sequences + 1]
   int sequences;
   int32_t* seq_row;    // [B] out
   int32_t* live;       // out: rows that belong to a sequence
+  const uint4* w;      // w_uv, n8 groups of 8 values
+  uint4* w16;          // out
+  int n8;
 };
+__device__ __forceinline__ void copy_weights(const RowArgs& rows, int thread, int threads, int32_t* err_word) {
+  uint32_t top = 0;
+  for (int i = thread; i < rows.n8; i += threads) rows.w16[i] = bf16x8_to_f16(__ldg(rows.w + i), &top);
+  if (top >= kF16Limit && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
+}
 __device__ __forceinline__ int row_length(const int32_t* seq_lens, const RowArgs& rows, int t, int B, int max_tokens,
                                           int32_t* err_word) {
   const int b = row_sequence(rows.cu, rows.sequences, t);
@@ -112,7 +122,13 @@ plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bl
   // grid dependency wait, which covers this kernel's completion
   sm100::grid_launch_dependents();
 
-  if (kRows) sm100::grid_dependency_wait();
+  if (kRows) {
+    sm100::grid_dependency_wait();
+    if (blockIdx.x > 0) {
+      copy_weights(rows, (blockIdx.x - 1) * kPlanThreads + tid, (gridDim.x - 1) * kPlanThreads, err_word);
+      return;
+    }
+  }
 
   // 1. clamp context lengths (to the block table's max_pages * page_size tokens), count tiles
   for (int b = tid; b < B; b += kPlanThreads) {
@@ -248,12 +264,19 @@ __device__ __forceinline__ int warp_exclusive_scan(int v, int lane, int* total) 
 }
 
 template <bool kRows>
-__global__ void __launch_bounds__(32, 1)
+__global__ void __launch_bounds__(kRows ? kPlanThreads : 32, 1)
 plan_small_kernel(const int32_t* __restrict__ seq_lens, int B, int n_q, int max_tokens, int G, Plan plan,
                   RowArgs rows, int32_t* err_word) {
   const int lane = threadIdx.x;
   sm100::grid_launch_dependents();
-  if (kRows) sm100::grid_dependency_wait();
+  if (kRows) {
+    sm100::grid_dependency_wait();
+    const int thread = blockIdx.x * kPlanThreads + lane - 32;
+    if (thread >= 0) {
+      copy_weights(rows, thread, gridDim.x * kPlanThreads - 32, err_word);
+      return;
+    }
+  }
   const bool live = lane < B;
   int n_b = 0;  // tiles of sequence `lane`
   if (live) {
@@ -350,17 +373,26 @@ cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* block_table, int
   return cudaGetLastError();
 }
 
-cudaError_t launch_rows_plan(const int32_t* seq_lens, const int32_t* cu, int sequences, int T, int max_pages,
-                             int page_size, int num_pages, int G, const Plan& plan, int32_t* seq_row, int32_t* live,
-                             int32_t* err_word, cudaStream_t s) {
+cudaError_t launch_rows_plan(const int32_t* seq_lens, const int32_t* cu, int sequences, int T, int H, int max_pages,
+                             int page_size, int num_pages, int G, const Plan& plan, const ChunkRows& chunk,
+                             const uint16_t* w_uv, int32_t* err_word, cudaStream_t s) {
   const int max_tokens = max_pages * page_size;
-  const RowArgs rows = {cu, sequences, seq_row, live};
+  RowArgs rows = {};
+  rows.cu = cu;
+  rows.sequences = sequences;
+  rows.seq_row = chunk.seq_row;
+  rows.live = chunk.hdr;
+  rows.w = reinterpret_cast<const uint4*>(w_uv);
+  rows.w16 = reinterpret_cast<uint4*>(chunk.w16);
+  rows.n8 = H * kDV * kDC / 8;
+  // four groups a thread, up to two blocks per SM
+  const int want = (rows.n8 + 4 * kPlanThreads - 1) / (4 * kPlanThreads), blocks = 1 + (want < 304 ? want : 304);
   if (T <= 32)
-    return launch_pdl(plan_small_kernel<true>, dim3(1), dim3(32), 0, s, seq_lens, T, 1, max_tokens, G, plan, rows,
-                      err_word);
+    return launch_pdl(plan_small_kernel<true>, dim3(blocks), dim3(kPlanThreads), 0, s, seq_lens, T, 1, max_tokens, G,
+                      plan, rows, err_word);
   const size_t smem = (size_t)2 * (T + 1) * sizeof(int);  // T <= MLA_MAX_BATCH: 32 KB
-  return launch_pdl(plan_kernel<true>, dim3(1), dim3(kPlanThreads), smem, s, seq_lens, (const int32_t*)nullptr, T, 1,
-                    max_tokens, num_pages, G, plan, rows, err_word);
+  return launch_pdl(plan_kernel<true>, dim3(blocks), dim3(kPlanThreads), smem, s, seq_lens, (const int32_t*)nullptr, T,
+                    1, max_tokens, num_pages, G, plan, rows, err_word);
 }
 
 }  // namespace mla

@@ -49,7 +49,9 @@ struct ProjCfg {
   static constexpr uint32_t kTmCols = NT < 32 ? 32 : NT;
 };
 
-// kRows (out_proj): rows of a chunk, of which only those below *rows_live are written
+// kRows: rows of a chunk. absorb_q writes fp16 (for the decode on an FP8 cache, which
+// scales the query into fp16); out_proj takes fp16 u and weights, and writes only the
+// rows below *rows_live.
 template <bool kAbsorb, int kNT, bool kRows>
 __global__ void __launch_bounds__(kThreads, 1)
 proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -109,10 +111,11 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   if (!kAbsorb) grid_launch_dependents();
   // rows at and past *rows_live are computed at most as part of a tile, never
   // written; the first tile always runs, since its loads are under way
-  const int live = kRows ? min(T, *rows_live) : T;
-  if (kRows) T = max(live, 1);
+  const int live = kRows && !kAbsorb ? min(T, *rows_live) : T;
+  if (kRows && !kAbsorb) T = max(live, 1);
 
-  const uint32_t idesc = idesc_bf16(128, C::NT, kAbsorb, false);
+  const uint32_t idesc =
+      kRows && !kAbsorb ? idesc_f16(128, C::NT, kAbsorb, false) : idesc_bf16(128, C::NT, kAbsorb, false);
   auto da = [](uint32_t addr) -> uint64_t { return (uint64_t)((addr >> 4) & 0x3FFFu); };
   const uint64_t bdesc = smem_desc(0, 16, 1024, kSwizzle128B) + da(sbase + C::kOffB);
   uint32_t phase = 0;
@@ -158,7 +161,10 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     if (kAbsorb && q_rope && cblk == 0 && t0 == 0 && warp > 0) {
       for (int i = threadIdx.x - 32; i < T * (kDR / 8); i += kThreads - 32) {
         const int t = i / (kDR / 8), v = i % (kDR / 8);
-        const uint4 w = reinterpret_cast<const uint4*>(q_rope + ((size_t)t * H + h) * kDR)[v];
+        uint4 w = reinterpret_cast<const uint4*>(q_rope + ((size_t)t * H + h) * kDR)[v];
+        if (kRows)
+          w = make_uint4(cvt_f16x2(bf16_lo(w.x), bf16_hi(w.x)), cvt_f16x2(bf16_lo(w.y), bf16_hi(w.y)),
+                         cvt_f16x2(bf16_lo(w.z), bf16_hi(w.z)), cvt_f16x2(bf16_lo(w.w), bf16_hi(w.w)));
         reinterpret_cast<uint4*>(out + ((size_t)t * H + h) * out_row + kDC)[v] = w;
       }
     }
@@ -181,7 +187,8 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 #pragma unroll
       for (int v = 0; v < 32; ++v)
         asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + (uint32_t)(c0 + v) * 256u + 2u * col),
-                     "h"(float_to_bf16(__uint_as_float(r[v])))
+                     "h"(kRows && kAbsorb ? (uint16_t)cvt_f16x2(__uint_as_float(r[v]), 0.f)
+                                          : float_to_bf16(__uint_as_float(r[v])))
                      : "memory");
     }
     __syncthreads();
@@ -232,25 +239,27 @@ bool maps(CUtensorMap* ma, CUtensorMap* mb, const uint16_t* w, const uint16_t* a
 }  // namespace
 
 namespace {
+template <bool kRows>
 cudaError_t absorb_rows(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk, uint16_t* out, int T,
                         int H, int out_row, cudaStream_t s) {
   const int nt = T <= 32 ? 32 : T <= 64 ? 64 : 128;
   CUtensorMap ma, mb;
   if (!maps(&ma, &mb, w_uk, q_nope, T, H, kDNope, nt)) return cudaErrorInvalidValue;
-  if (nt == 32) return launch_proj<true, 32>(ma, mb, w_uk, q_rope, out, T, H, out_row, s);
-  if (nt == 64) return launch_proj<true, 64>(ma, mb, w_uk, q_rope, out, T, H, out_row, s);
-  return launch_proj<true, 128>(ma, mb, w_uk, q_rope, out, T, H, out_row, s);
+  if (nt == 32) return launch_proj<true, 32, kRows>(ma, mb, w_uk, q_rope, out, T, H, out_row, s);
+  if (nt == 64) return launch_proj<true, 64, kRows>(ma, mb, w_uk, q_rope, out, T, H, out_row, s);
+  return launch_proj<true, 128, kRows>(ma, mb, w_uk, q_rope, out, T, H, out_row, s);
 }
 }  // namespace
 
 cudaError_t launch_absorb_q(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
-                            uint16_t* q_abs, int T, int H, cudaStream_t s) {
-  return absorb_rows(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s);
+                            uint16_t* q_abs, int T, int H, cudaStream_t s, bool f16) {
+  return f16 ? absorb_rows<true>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s)
+             : absorb_rows<false>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s);
 }
 
 cudaError_t launch_merge_w_kq(const uint16_t* w_uq, const uint16_t* w_uk, uint16_t* w_kq, int d_q, int H,
                               cudaStream_t s) {
-  return absorb_rows(w_uq, nullptr, w_uk, w_kq, d_q, H, kDC, s);
+  return absorb_rows<false>(w_uq, nullptr, w_uk, w_kq, d_q, H, kDC, s);
 }
 
 cudaError_t launch_out_proj(const uint16_t* u, const uint16_t* w_uv, uint16_t* out, int T, int H,

@@ -119,15 +119,9 @@ weights_f16_kernel(const uint4* __restrict__ w_uk, const uint4* __restrict__ w_u
   const int i = blockIdx.x * kWThreads + threadIdx.x;
   if (i >= 2 * n8) return;
   const uint4 w = i < n8 ? __ldg(w_uk + i) : __ldg(w_uv + (i - n8));
-  const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-  uint32_t f[4], top = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    f[k] = sm100::cvt_f16x2(bf16_lo(e[k]), bf16_hi(e[k]));
-    top = max(top, max((e[k] << 16) & 0x7FFFFFFFu, e[k] & 0x7FFF0000u));
-  }
-  out[i] = make_uint4(f[0], f[1], f[2], f[3]);
-  if (top >= 0x477FF000u && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
+  uint32_t top = 0;
+  out[i] = bf16x8_to_f16(w, &top);
+  if (top >= kF16Limit && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
 }
 
 template <bool kF8, bool kF16, int kRows>

@@ -78,7 +78,8 @@ def attend(c: Chunk, scale=SCALE):
     is rounded once more before the value product, a value once:
       expanded  keys, values and weights in fp16 (u = 2^-11); rows of an FP8 cache are
                 first rounded to fp16 as well
-      absorbed  absorbed query, weights and u in bf16 (2^-8), partials in fp16
+      absorbed  absorbed query and weights in bf16 (2^-8; in fp16 on an FP8 cache, the
+                query once more after its scaling), partials, u and W^UV in fp16
     plus the output's own rounding to bf16 and fp32 sums (2^-24 per term, at most a
     few thousand terms: below 2^-11, counted as one more fp16 unit)."""
     outs, lses, be, ba = [], [], [], []
@@ -108,10 +109,11 @@ def attend(c: Chunk, scale=SCALE):
             e1[:, h] = U_BF16 * o[:, h].abs() + (p @ v.abs()) * (3 * U_F16 + torch.expm1(2 * dz)) + rows_u * (p @ vabs)
             # absorbed
             qa = qn @ uk
-            dz = scale * U_BF16 * 1.25 * (qa.abs() @ lat.abs().t() + qr.abs() @ kr.abs().t())
+            unit = 2 * U_F16 if c.fp8 else U_BF16
+            dz = scale * unit * 1.25 * (qa.abs() @ lat.abs().t() + qr.abs() @ kr.abs().t())
             dz = dz.masked_fill(hidden, 0).amax(-1, keepdim=True)
             u = p @ lat
-            du = U_BF16 * u.abs() + (p @ lat.abs()) * (U_BF16 + 3 * U_F16 + torch.expm1(2 * dz))
+            du = U_F16 * u.abs() + (p @ lat.abs()) * (unit + 3 * U_F16 + torch.expm1(2 * dz))
             e2[:, h] = 1.01 * U_BF16 * o[:, h].abs() + du @ uv.abs().t() + U_F16 * (u.abs() @ uv.abs().t())
         outs.append(o), lses.append(z_all), be.append(e1), ba.append(e2)
     return torch.cat(outs), torch.cat(lses), {"expanded": torch.cat(be), "absorbed": torch.cat(ba)}

@@ -150,20 +150,22 @@ def test_append_reports_and_skips_bad_targets(mla, err):
 
 
 # ------------------------------------------------------------------ attend_chunk
-# The roundings of a form are independent, so over many outputs they add in squares: at
-# most four of half a bf16 step each (absorbed: query, weights, u, output; expanded on an
-# FP8 cache: rows in keys and in values, output), 2 x 2^-8 of the norm.
-REL = 2 * ref.U_BF16
+# The roundings of a form are independent, so over many outputs they add in squares. Half
+# a bf16 step (2^-8) each: absorbed on a bf16 cache the query, the weights and the output,
+# sqrt(3) 2^-8 < 1.75 x 2^-8 of the norm; else the output alone, beside at most eight in
+# fp16 (2^-11): sqrt(1 + 8 / 64) 2^-8 < 1.1 x 2^-8.
+REL = 1.75 * ref.U_BF16
+REL_F16 = 1.1 * ref.U_BF16
 
 
-def check(got, want, bound, what):
+def check(got, want, bound, what, rel_max=REL):
     import torch
     assert torch.isfinite(got).all(), what
     off = (got.double() - want).abs()
     worst = (off / bound).max().item()
     assert worst <= 1.0, f"{what}: {worst:.3f} of the bound, max |diff| {off.max().item():.3e}"
     rel = (off.norm() / want.norm()).item()
-    assert rel <= REL, f"{what}: {rel:.2e} of the norm"
+    assert rel <= rel_max, f"{what}: {rel:.2e} of the norm"
 
 
 SHAPES = [
@@ -193,9 +195,9 @@ def test_attend(mla, err, fp8, form, new, lens, H, page, pad):
                            form=form, out=out, lse=lse, err_word=err)
     torch.cuda.synchronize()
     assert int(err.item()) == 0
-    check(got[:c.total], want, bound[form], form)
+    check(got[:c.total], want, bound[form], form, REL_F16 if fp8 or form == "expanded" else REL)
     # an lse moves by at most the largest score error of its row
-    assert (lse[:c.total].double() - lse_want).abs().max().item() <= (0.02 if form == "expanded" and not fp8 else 0.12)
+    assert (lse[:c.total].double() - lse_want).abs().max().item() <= (0.12 if form == "absorbed" and not fp8 else 0.02)
     assert (out[c.total:] == 3.0).all() and (lse[c.total:] == 5.0).all()
 
 
