@@ -8,6 +8,7 @@ import torch
 D_C, D_R, D_ROW = 512, 64, 576
 SCALE = 1.0 / math.sqrt(192.0)
 U_BF16, U_F16, U_F32 = 2.0 ** -8, 2.0 ** -11, 2.0 ** -24  # half a step, relative
+TINY_F16 = 2.0 ** -25  # half a step of fp16 below its normal range (2^-14)
 NAN_CODE = 0x7F  # e4m3 NaN
 
 
@@ -80,8 +81,11 @@ def attend(c: Chunk, scale=SCALE):
                 first rounded to fp16 as well
       absorbed  absorbed query and weights in bf16 (2^-8; in fp16 on an FP8 cache, the
                 query once more after its scaling), partials, u and W^UV in fp16
-    plus the output's own rounding to bf16 and fp32 sums (2^-24 per term, at most a
-    few thousand terms: below 2^-11, counted as one more fp16 unit)."""
+    plus the output's own rounding to bf16 and the fp32 sums. Those are off by 2^-24 of
+    the absolute products per term, whatever the products cancel to: 512 terms for a key
+    or a value (2^-15 of |c| |W|), 192 for a score, 128 for an absorbed query. The sums
+    over the keys have at most a few thousand terms: below 2^-11 of sum p |v|, counted as
+    one more fp16 unit. Below 2^-14 fp16 rounds by 2^-25 whatever the value is."""
     outs, lses, be, ba = [], [], [], []
     for b, (n, L) in enumerate(zip(c.new, c.lens)):
         if n == 0:
@@ -104,13 +108,18 @@ def attend(c: Chunk, scale=SCALE):
             rows_u = U_F16 if c.fp8 else 0.0
             kabs, vabs = lat.abs() @ uk.abs().t(), lat.abs() @ uv.abs().t()
             # expanded
-            dz = scale * ((qn.abs() @ k.abs().t()) * 2 * U_F16 + rows_u * (qn.abs() @ kabs.t() + qr.abs() @ kr.abs().t()))
+            rope_abs = qr.abs() @ kr.abs().t()
+            tiny = TINY_F16 * (qn.abs().sum(-1, keepdim=True) + k.abs().sum(-1)[None])
+            dz = scale * ((qn.abs() @ k.abs().t()) * 2 * U_F16 + tiny + (rows_u + 512 * U_F32) * (qn.abs() @ kabs.t())
+                          + (rows_u + 192 * U_F32) * rope_abs)
             dz = dz.masked_fill(hidden, 0).amax(-1, keepdim=True)
-            e1[:, h] = U_BF16 * o[:, h].abs() + (p @ v.abs()) * (3 * U_F16 + torch.expm1(2 * dz)) + rows_u * (p @ vabs)
+            e1[:, h] = U_BF16 * o[:, h].abs() + (p @ v.abs()) * (3 * U_F16 + torch.expm1(2 * dz))
+            e1[:, h] += TINY_F16 + (rows_u + 512 * U_F32) * (p @ vabs)
             # absorbed
             qa = qn @ uk
             unit = 2 * U_F16 if c.fp8 else U_BF16
-            dz = scale * unit * 1.25 * (qa.abs() @ lat.abs().t() + qr.abs() @ kr.abs().t())
+            dz = scale * unit * 1.25 * (qa.abs() @ lat.abs().t() + rope_abs)
+            dz += scale * 128 * U_F32 * ((qn.abs() @ uk.abs()) @ lat.abs().t())
             dz = dz.masked_fill(hidden, 0).amax(-1, keepdim=True)
             u = p @ lat
             du = U_F16 * u.abs() + (p @ lat.abs()) * (unit + 3 * U_F16 + torch.expm1(2 * dz))

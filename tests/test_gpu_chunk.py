@@ -201,6 +201,21 @@ def test_attend(mla, err, fp8, form, new, lens, H, page, pad):
     assert (out[c.total:] == 3.0).all() and (lse[c.total:] == 5.0).all()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("form", ["expanded", "absorbed"])
+def test_attend_values_whose_products_cancel(mla, err, form, fp8):
+    """A row that sees one key answers with that key's value. Among 128 x 128 values a few
+    are 1e-5 of the products they sum: off by the fp32 sum's 2^-24 of the absolute products
+    per term (measured: about 1 x 2^-24 of a sum of 14), not by a fraction of themselves."""
+    c = ref.Chunk([1, 2, 1, 1], [1, 2, 1, 1], H=128, fp8=fp8, seed=0)
+    want, _, bound = ref.attend(c)
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=5, fp8_scales=c.scales,
+                           form=form, err_word=err)
+    assert int(err.item()) == 0
+    assert want.abs().min().item() < 2.0 ** -14
+    check(got, want, bound[form], form, REL_F16 if fp8 or form == "expanded" else REL)
+
+
 def test_attend_auto_equals_the_form_it_chooses(mla):
     import torch
     for new, form in (([4, 4], "absorbed"), ([600], "expanded")):
