@@ -491,13 +491,14 @@ mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t
  * H, max_tokens / B and the kind of cache, nothing on the device):
  *   MLA_CHUNK_EXPANDED  keys and values of every head are expanded from the latents
  *     first, and rounded to fp16 (so are content queries, the rows of an FP8 cache
- *     and, with one, the weights; fp32 sums everywhere). For long chunks. Any of
- *     these of 65520 or more is reported as MLA_ERR_RANGE; below 2^-14 their
- *     resolution is 2^-25.
+ *     and, with one, the weights; fp32 sums everywhere). For long chunks.
  *   MLA_CHUNK_ABSORBED  every new token is decoded over the latents (the kernels of
  *     mla_absorb_q, mla_decode_paged, mla_combine and mla_out_proj; absorbed query and
  *     weights rounded to bf16 as there, u and W^UV to fp16, and on an FP8 cache all of
- *     them to fp16). For few new tokens on a context; T <= MLA_MAX_BATCH.
+ *     them to fp16, the query times the scales). For few new tokens on a context;
+ *     T <= MLA_MAX_BATCH.
+ * Any of the values that a form rounds to fp16, if it is finite and 65520 or more, is
+ * reported as MLA_ERR_RANGE; below 2^-14 their resolution is 2^-25.
  * A cached token whose expanded values are not finite (NaN or infinite latents)
  * gives NaN to the queries that see it and to no other.
  *   q_nope [T][H][128] bf16, q_rope [T][H][64] bf16 (already rotated),

@@ -146,7 +146,7 @@ inline size_t chunk_layout(void* base, int B, int T, int heads, int64_t max_toke
 struct ChunkRows {
   int32_t* hdr;      // [64] hdr[0] = rows that belong to a sequence
   int32_t* seq_row;  // [T] block-table row (-1 for rows of no sequence)
-  uint16_t* q_abs;   // [T][H][576] bf16 (fp16 on an FP8 cache)
+  uint16_t* q_abs;   // [T][H][576] bf16 (on an FP8 cache fp16, scaled by its columns)
   uint16_t* u;       // [T][H][512] fp16
   uint16_t* w16;     // [H][128][512] fp16 copy of w_uv
   void* decode_ws;   // workspace of the decode over T sequences

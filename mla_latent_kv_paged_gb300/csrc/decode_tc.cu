@@ -164,20 +164,16 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
-// bf16 pair (fp16 for a chunk's rows) times two scales, as an fp16 pair
-template <bool kRows>
-__device__ __forceinline__ uint32_t scale_pair_to_f16x2(uint32_t w, float s0, float s1) {
-  if (kRows) {
-    const float2 f = f16x2_to_f32(w);
-    return cvt_f16x2(f.x * s0, f.y * s1);
-  }
+// bf16 pair times two scales, as an fp16 pair
+__device__ __forceinline__ uint32_t scale_bf16x2_to_f16x2(uint32_t w, float s0, float s1) {
   return cvt_f16x2(bf16_lo(w) * s0, bf16_hi(w) * s1);
 }
 
 // kRows: the sequences are rows of a chunk (chunk.cuh): seq_row[b] is the block-table
 // row of sequence b, -1 for a row of no sequence (it reads zeros and its result is
-// not used); on an FP8 cache the absorbed query is fp16. A template parameter, because any change to the plain kernel's
-// code costs it a few per cent (decode call 38.8 -> 39.5 us with a run-time test).
+// not used); on an FP8 cache the absorbed query comes in fp16 and scaled. A template
+// parameter, because any change to the plain kernel's code costs it a few per cent
+// (decode call 38.8 -> 39.5 us with a run-time test).
 template <bool kF8, bool kRows>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_kr,
@@ -587,10 +583,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(r[4 * c]), "=r"(r[4 * c + 1]), "=r"(r[4 * c + 2]), "=r"(r[4 * c + 3])
                            : "r"(sq + m * kQBoxBytes + ((c ^ (row & 7)) * 16)));
-            if (kF8) {  // the FP8 cache's column scales fold into the query (fp16)
+            if (kF8 && !kRows) {  // the FP8 cache's column scales fold into the query (fp16)
               const float* sc = fp8_scales + 256 * rank + 128 * q + 64 * m;
 #pragma unroll
-              for (int k = 0; k < 32; ++k) r[k] = scale_pair_to_f16x2<kRows>(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
+              for (int k = 0; k < 32; ++k) r[k] = scale_bf16x2_to_f16x2(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
             }
             tmem_st32(tQ + 64 * q + 32 * m, r);
           }
@@ -603,10 +599,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(r[4 * c]), "=r"(r[4 * c + 1]), "=r"(r[4 * c + 2]), "=r"(r[4 * c + 3])
                            : "r"(sr + rl * 64 + ((c ^ ((rl >> 1) & 3)) * 16)));
-            if (kF8) {
+            if (kF8 && !kRows) {
               const float* sc = fp8_scales + kDC + 32 * rank;
 #pragma unroll
-              for (int k = 0; k < 16; ++k) r[k] = scale_pair_to_f16x2<kRows>(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
+              for (int k = 0; k < 16; ++k) r[k] = scale_bf16x2_to_f16x2(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
             }
             tmem_st16(tmem + lane_off + kTmQr, r);
           }

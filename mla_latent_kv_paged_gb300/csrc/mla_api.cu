@@ -450,7 +450,7 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
     plan.seq_row = r.seq_row;
     mla_status st = launch_status(launch_rows_plan(seq_lens, cu, B, T, H, max_pages_per_seq, page_size, num_pages,
                                                    G, plan, r, w_uv, err_word, s));
-    if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s, fp8_scales != nullptr));
+    if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s, r.hdr, fp8_scales, err_word));
     if (st == MLA_OK)
       st = launch_status(fp8_scales ? launch_decode_fp8(r.q_abs, static_cast<const uint8_t*>(cache), fp8_scales,
                                                         block_table, T, 1, H, num_pages, page_size,

@@ -23,6 +23,7 @@
 // the [rows][128 columns] tile through shared memory and writes each output
 // row as 16-byte stores. N (rows per tile) is 32, 64 or 128, the smallest
 // that holds the batch's rows.
+#include "chunk.cuh"
 #include "mla_internal.cuh"
 #include "sm100.cuh"
 
@@ -49,14 +50,17 @@ struct ProjCfg {
   static constexpr uint32_t kTmCols = NT < 32 ? 32 : NT;
 };
 
-// kRows: rows of a chunk. absorb_q writes fp16 (for the decode on an FP8 cache, which
-// scales the query into fp16); out_proj takes fp16 u and weights, and writes only the
+// kRows: rows of a chunk. absorb_q (for the decode on an FP8 cache) scales the query by
+// the cache's column scales and writes fp16, so that it is rounded once and its range is
+// that of the product that the decode takes; of the rows below *rows_live it reports
+// values that fp16 does not hold. out_proj takes fp16 u and weights, and writes only the
 // rows below *rows_live.
 template <bool kAbsorb, int kNT, bool kRows>
 __global__ void __launch_bounds__(kThreads, 1)
 proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const uint16_t* __restrict__ weights, const uint16_t* __restrict__ q_rope, uint16_t* __restrict__ out,
-               int T, int H, int out_row, const int32_t* __restrict__ rows_live, int32_t* err_word) {
+               int T, int H, int out_row, const int32_t* __restrict__ rows_live,
+               const float* __restrict__ col_scales, int32_t* err_word) {
   using C = ProjCfg<kAbsorb, kNT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -111,8 +115,16 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   if (!kAbsorb) grid_launch_dependents();
   // rows at and past *rows_live are computed at most as part of a tile, never
   // written; the first tile always runs, since its loads are under way
-  const int live = kRows && !kAbsorb ? min(T, *rows_live) : T;
+  const int live = kRows ? min(T, *rows_live) : T;
   if (kRows && !kAbsorb) T = max(live, 1);
+  constexpr bool kScaled = kRows && kAbsorb;
+  bool beyond = false;  // a scaled query outside fp16
+  auto scaled = [&](float x, float scale, int t) {
+    const float y = x * scale;
+    const uint32_t top = __float_as_uint(y) & 0x7FFFFFFFu;
+    beyond |= top >= kF16Limit && top < 0x7F800000u && t < live;
+    return y;
+  };
 
   const uint32_t idesc =
       kRows && !kAbsorb ? idesc_f16(128, C::NT, kAbsorb, false) : idesc_bf16(128, C::NT, kAbsorb, false);
@@ -156,15 +168,20 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
       }
       mma_commit(bar_d);  // arrives once the MMAs (if any) finished
     }
-    // rotated positional query, copied unchanged next to the absorbed one, by
+    // rotated positional query, copied (on an FP8 cache scaled) next to the absorbed one, by
     // warps 1..3 while thread 0 waits for the tiles
     if (kAbsorb && q_rope && cblk == 0 && t0 == 0 && warp > 0) {
       for (int i = threadIdx.x - 32; i < T * (kDR / 8); i += kThreads - 32) {
         const int t = i / (kDR / 8), v = i % (kDR / 8);
         uint4 w = reinterpret_cast<const uint4*>(q_rope + ((size_t)t * H + h) * kDR)[v];
-        if (kRows)
-          w = make_uint4(cvt_f16x2(bf16_lo(w.x), bf16_hi(w.x)), cvt_f16x2(bf16_lo(w.y), bf16_hi(w.y)),
-                         cvt_f16x2(bf16_lo(w.z), bf16_hi(w.z)), cvt_f16x2(bf16_lo(w.w), bf16_hi(w.w)));
+        if (kScaled) {
+          const float* sc = col_scales + kDC + 8 * v;
+          uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            e[k] = cvt_f16x2(scaled(bf16_lo(e[k]), sc[2 * k], t), scaled(bf16_hi(e[k]), sc[2 * k + 1], t));
+          w = make_uint4(e[0], e[1], e[2], e[3]);
+        }
         reinterpret_cast<uint4*>(out + ((size_t)t * H + h) * out_row + kDC)[v] = w;
       }
     }
@@ -179,6 +196,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int col = warp * 32 + lane;
     const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t tile = sbase + C::kOffB;
+    const float col_scale = kScaled ? col_scales[cblk * 128 + col] : 1.f;
 #pragma unroll 1
     for (int c0 = 0; c0 < C::NT; c0 += 32) {
       uint32_t r[32];
@@ -187,14 +205,14 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 #pragma unroll
       for (int v = 0; v < 32; ++v)
         asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + (uint32_t)(c0 + v) * 256u + 2u * col),
-                     "h"(kRows && kAbsorb ? (uint16_t)cvt_f16x2(__uint_as_float(r[v]), 0.f)
-                                          : float_to_bf16(__uint_as_float(r[v])))
+                     "h"(kScaled ? (uint16_t)cvt_f16x2(scaled(__uint_as_float(r[v]), col_scale, t0 + c0 + v), 0.f)
+                                 : float_to_bf16(__uint_as_float(r[v])))
                      : "memory");
     }
     __syncthreads();
     for (int i = threadIdx.x; i < C::NT * 16; i += kThreads) {
       const int row = i >> 4, part = i & 15, t = t0 + row;
-      if (t < live) {
+      if (t < (kAbsorb ? T : live)) {
         uint4 v;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
@@ -209,6 +227,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     __syncthreads();  // D and the B tile are free for the next rows
     tc_fence_after();
   }
+  if (kScaled && beyond) report_error(err_word, MLA_ERR_RANGE);
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -219,13 +238,14 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 
 template <bool kAbsorb, int kNT, bool kRows = false>
 cudaError_t launch_proj(const CUtensorMap& ma, const CUtensorMap& mb, const uint16_t* w, const uint16_t* q_rope,
-                        uint16_t* out, int T, int H, int out_row, cudaStream_t s, const int32_t* rows_live = nullptr) {
+                        uint16_t* out, int T, int H, int out_row, cudaStream_t s, const int32_t* rows_live = nullptr,
+                        const float* col_scales = nullptr, int32_t* err_word = nullptr) {
   using C = ProjCfg<kAbsorb, kNT>;
   cudaError_t e = smem_limit<proj_tc_kernel<kAbsorb, kNT, kRows>>(C::kSmem);
   if (e != cudaSuccess) return e;
   const dim3 grid(H, kAbsorb ? kDC / 128 : 1);
   return launch_pdl(proj_tc_kernel<kAbsorb, kNT, kRows>, grid, dim3(kThreads), C::kSmem, s, ma, mb, w, q_rope, out, T,
-                    H, out_row, rows_live, (int32_t*)nullptr);
+                    H, out_row, rows_live, col_scales, err_word);
 }
 
 bool maps(CUtensorMap* ma, CUtensorMap* mb, const uint16_t* w, const uint16_t* act, int T, int H, int K, int nt) {
@@ -241,20 +261,23 @@ bool maps(CUtensorMap* ma, CUtensorMap* mb, const uint16_t* w, const uint16_t* a
 namespace {
 template <bool kRows>
 cudaError_t absorb_rows(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk, uint16_t* out, int T,
-                        int H, int out_row, cudaStream_t s) {
+                        int H, int out_row, cudaStream_t s, const int32_t* rows_live = nullptr,
+                        const float* col_scales = nullptr, int32_t* err_word = nullptr) {
   const int nt = T <= 32 ? 32 : T <= 64 ? 64 : 128;
   CUtensorMap ma, mb;
   if (!maps(&ma, &mb, w_uk, q_nope, T, H, kDNope, nt)) return cudaErrorInvalidValue;
-  if (nt == 32) return launch_proj<true, 32, kRows>(ma, mb, w_uk, q_rope, out, T, H, out_row, s);
-  if (nt == 64) return launch_proj<true, 64, kRows>(ma, mb, w_uk, q_rope, out, T, H, out_row, s);
-  return launch_proj<true, 128, kRows>(ma, mb, w_uk, q_rope, out, T, H, out_row, s);
+  const auto launch = nt == 32   ? launch_proj<true, 32, kRows>
+                      : nt == 64 ? launch_proj<true, 64, kRows>
+                                 : launch_proj<true, 128, kRows>;
+  return launch(ma, mb, w_uk, q_rope, out, T, H, out_row, s, rows_live, col_scales, err_word);
 }
 }  // namespace
 
 cudaError_t launch_absorb_q(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
-                            uint16_t* q_abs, int T, int H, cudaStream_t s, bool f16) {
-  return f16 ? absorb_rows<true>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s)
-             : absorb_rows<false>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s);
+                            uint16_t* q_abs, int T, int H, cudaStream_t s, const int32_t* rows_live,
+                            const float* col_scales, int32_t* err_word) {
+  return col_scales ? absorb_rows<true>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s, rows_live, col_scales, err_word)
+                    : absorb_rows<false>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s);
 }
 
 cudaError_t launch_merge_w_kq(const uint16_t* w_uq, const uint16_t* w_uk, uint16_t* w_kq, int d_q, int H,

@@ -79,8 +79,8 @@ def attend(c: Chunk, scale=SCALE):
     is rounded once more before the value product, a value once:
       expanded  keys, values and weights in fp16 (u = 2^-11); rows of an FP8 cache are
                 first rounded to fp16 as well
-      absorbed  absorbed query and weights in bf16 (2^-8; in fp16 on an FP8 cache, the
-                query once more after its scaling), partials, u and W^UV in fp16
+      absorbed  absorbed query and weights in bf16 (2^-8; on an FP8 cache in fp16, the
+                query times the scales), partials, u and W^UV in fp16
     plus the output's own rounding to bf16 and the fp32 sums. Those are off by 2^-24 of
     the absolute products per term, whatever the products cancel to: 512 terms for a key
     or a value (2^-15 of |c| |W|), 192 for a score, 128 for an absorbed query. The sums
@@ -117,9 +117,11 @@ def attend(c: Chunk, scale=SCALE):
             e1[:, h] += TINY_F16 + (rows_u + 512 * U_F32) * (p @ vabs)
             # absorbed
             qa = qn @ uk
-            unit = 2 * U_F16 if c.fp8 else U_BF16
+            unit = U_F16 if c.fp8 else U_BF16
             dz = scale * unit * 1.25 * (qa.abs() @ lat.abs().t() + rope_abs)
             dz += scale * 128 * U_F32 * ((qn.abs() @ uk.abs()) @ lat.abs().t())
+            if c.fp8:
+                dz += scale * TINY_F16 * (x / c.scales.double()).abs().sum(-1)
             dz = dz.masked_fill(hidden, 0).amax(-1, keepdim=True)
             u = p @ lat
             du = U_F16 * u.abs() + (p @ lat.abs()) * (unit + 3 * U_F16 + torch.expm1(2 * dz))

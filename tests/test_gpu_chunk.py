@@ -283,6 +283,34 @@ def test_attend_reports_expanded_values_outside_fp16(mla, err):
     assert torch.isfinite(got[:50]).all()
 
 
+def test_attend_large_queries_on_small_scales(mla, err):
+    """Queries beyond fp16 on an FP8 cache of small values, absorbed: the query is scaled
+    by the cache's columns before it is rounded."""
+    c = ref.Chunk([3, 2], [200, 66], H=3, fp8=True, seed=19)
+    c.scales *= 2.0 ** -7
+    c.q_nope *= 2.0 ** 17
+    c.q_rope *= 2.0 ** 17
+    want, _, bound = ref.attend(c, ref.SCALE * 2.0 ** -10)
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=266, fp8_scales=c.scales,
+                           softmax_scale=ref.SCALE * 2.0 ** -10, form="absorbed", err_word=err)
+    assert int(err.item()) == 0
+    check(got, want, bound["absorbed"], "large queries", REL_F16)
+
+
+@pytest.mark.parametrize("form,part", [(f, p) for f in ("expanded", "absorbed") for p in ("nope", "rope")])
+def test_attend_reports_queries_outside_fp16(mla, err, form, part):
+    import torch
+    c = ref.Chunk([5, 2], [200, 66], H=3, fp8=True, seed=20, pad_rows=2)
+    want, _, bound = ref.attend(c)
+    (c.q_nope if part == "nope" else c.q_rope)[4, 1] = 1e9
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=266, fp8_scales=c.scales,
+                           form=form, err_word=err)
+    assert int(err.item()) == RANGE
+    keep = torch.ones(7, 3, dtype=torch.bool, device="cuda")
+    keep[4, 1] = False
+    check(got[:7][keep], want[keep], bound[form][keep], form, REL_F16)
+
+
 @pytest.mark.parametrize("form", ["expanded", "absorbed"])
 def test_attend_reports_bad_lengths_pages_and_rows(mla, err, form):
     import torch
