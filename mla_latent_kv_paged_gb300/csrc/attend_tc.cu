@@ -447,21 +447,23 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       if ((x ? t.n1 : t.n0) == 0) return true;
       if (!wait(QL0 + x, uses)) return false;
       const int rows = t.n - t.q0 - 128 * x;
-      uint32_t top = 0;
+      bool beyond = false;  // of each row by itself: a NaN in one hides nothing in another
 #pragma unroll 4
       for (int k = 0; k < (rope_f16 ? 12 : 8); ++k) {
         const int i = tid + 256 * k;  // 16 bytes of the two content slabs, then of the positional one
         const uint32_t at = sbase + 3 * x * kSlab + 16 * i;
         uint32_t e[4];
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(e[0]), "=r"(e[1]), "=r"(e[2]), "=r"(e[3]) : "r"(at));
+        uint32_t top = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if (((i >> 3) & 127) < rows) top = max(top, max((e[q] << 16) & 0x7FFFFFFFu, e[q] & 0x7FFF0000u));
+          top = max(top, max((e[q] << 16) & 0x7FFFFFFFu, e[q] & 0x7FFF0000u));
           e[q] = cvt_f16x2(bf16_lo(e[q]), bf16_hi(e[q]));
         }
         st_shared_v4(at, e[0], e[1], e[2], e[3]);
+        beyond |= top >= kF16Limit && top < 0x7F800000u && ((i >> 3) & 127) < rows;
       }
-      if (top >= kF16Limit && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
+      if (beyond) report_error(err_word, MLA_ERR_RANGE);
       fence_proxy_async_smem();
       mbar_arrive(bar(QF0 + x));
       return true;

@@ -87,9 +87,13 @@ struct RowArgs {
   int n8;
 };
 __device__ __forceinline__ void copy_weights(const RowArgs& rows, int thread, int threads, int32_t* err_word) {
-  uint32_t top = 0;
-  for (int i = thread; i < rows.n8; i += threads) rows.w16[i] = bf16x8_to_f16(__ldg(rows.w + i), &top);
-  if (top >= kF16Limit && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
+  bool beyond = false;  // of each group by itself: a NaN in one hides nothing in another
+  for (int i = thread; i < rows.n8; i += threads) {
+    uint32_t top = 0;
+    rows.w16[i] = bf16x8_to_f16(__ldg(rows.w + i), &top);
+    beyond |= top >= kF16Limit && top < 0x7F800000u;
+  }
+  if (beyond) report_error(err_word, MLA_ERR_RANGE);
 }
 __device__ __forceinline__ int row_length(const int32_t* seq_lens, const RowArgs& rows, int t, int B, int max_tokens,
                                           int32_t* err_word) {

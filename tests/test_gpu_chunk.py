@@ -311,6 +311,34 @@ def test_attend_reports_queries_outside_fp16(mla, err, form, part):
     check(got[:7][keep], want[keep], bound[form][keep], form, REL_F16)
 
 
+def test_attend_reports_a_query_outside_fp16_beside_a_nan(mla, err):
+    import torch
+    c = ref.Chunk([100], [100], H=1, seed=21)
+    want, _, bound = ref.attend(c)
+    c.q_nope[3] = float("nan")
+    c.q_nope[35] = 1e9  # rows 32 apart are one thread's
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=100, form="expanded",
+                           err_word=err)
+    assert int(err.item()) == RANGE
+    keep = torch.ones(100, dtype=torch.bool, device="cuda")
+    keep[[3, 35]] = False
+    check(got[keep], want[keep], bound["expanded"][keep], "expanded", REL_F16)
+
+
+@pytest.mark.parametrize("form,fp8", [("expanded", True), ("absorbed", False), ("absorbed", True)])
+def test_attend_reports_weights_outside_fp16_beside_nans(mla, err, form, fp8):
+    import torch
+    c = ref.Chunk([2], [70], H=3, fp8=fp8, seed=22)
+    want, _, bound = ref.attend(c)
+    c.w_uv[0] = float("nan")
+    c.w_uv[2] = 1e6
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=70, fp8_scales=c.scales,
+                           form=form, err_word=err)
+    assert int(err.item()) == RANGE
+    assert torch.isnan(got[:, 0]).all()
+    check(got[:, 1], want[:, 1], bound[form][:, 1], form)
+
+
 @pytest.mark.parametrize("form", ["expanded", "absorbed"])
 def test_attend_reports_bad_lengths_pages_and_rows(mla, err, form):
     import torch
