@@ -103,26 +103,26 @@ struct Target {
   int64_t row;  // row of the pool, or -1
   int pos;
 };
-// Where row t goes. Out-of-range lengths and page ids are reported; such a row
-// (and a row of no sequence) is not written.
+// Where row t goes. A row whose sequence's length does not hold the new rows or passes
+// the block table, or whose page id is out of range, is reported and not written (a
+// clamped length would put it over another token's row); a row of no sequence is not
+// written.
 __device__ Target target_of(const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_lens,
                             const int32_t* __restrict__ block_table, int B, int t, int num_pages, int page_size,
                             int max_pages, bool report, int32_t* err_word) {
   Target r = {-1, 0};
   const int b = row_sequence(cu, B, t);
   if (b < 0) return r;
-  const int n = cu[b + 1] - cu[b], max_tokens = max_pages * page_size, raw = seq_lens[b];
-  const int L = min(max(raw, n), max_tokens);
-  const int pos = L - n + (t - cu[b]);
-  bool bad = raw != L;
-  if (pos >= 0 && pos < max_tokens) {
+  const int64_t n = (int64_t)cu[b + 1] - cu[b];
+  const int L = seq_lens[b];
+  bool bad = L < n || L > max_pages * page_size;
+  if (!bad) {
+    const int pos = (int)(L - n + ((int64_t)t - cu[b]));
     const int page = block_table[(int64_t)b * max_pages + pos / page_size];
     if (page >= 0 && page < num_pages)
       r = {(int64_t)page * page_size + pos % page_size, pos};
     else
       bad = true;
-  } else {
-    bad = true;
   }
   if (bad && report) report_error(err_word, MLA_ERR_BOUNDS);
   return r;

@@ -1,0 +1,71 @@
+"""The chunk operators where their inputs leave the ordinary: bad lengths and row ranges,
+quotients next to a tie, angles next to a quarter turn, two rows for one cache row, values
+below fp16's normal range, scores far beyond fp32's integers. On the GPU, against 64 bits."""
+import pytest
+
+from tests import chunk_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+OK, BOUNDS, RANGE = 0, 6, 7
+
+
+@pytest.fixture(scope="module")
+def mla():
+    import mla_latent_kv_paged_gb300 as m
+    m.build()
+    return m
+
+
+@pytest.fixture()
+def err():
+    import torch
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def hidden(T, d_model, seed):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    h = torch.randn(T, d_model, generator=g, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(576, d_model, generator=g, device="cuda") * d_model ** -0.5).to(torch.bfloat16)
+    return h, w
+
+
+def bits(t):
+    import torch
+    return t.view(torch.uint8) if t.dtype == torch.uint8 else t.view(torch.int16)
+
+
+# ------------------------------------------------------------------ append_chunk: what is written
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d_model", [64, 1024])  # one split, many
+@pytest.mark.parametrize("bad", ["short", "zero", "negative", "beyond the table", "huge"])
+def test_append_writes_no_row_of_a_bad_length(mla, err, bad, d_model, fp8):
+    """A length that does not hold the new rows, or passes the block table: none of the
+    sequence's rows goes anywhere (its cached rows are not replaced by rows rotated for
+    another position), the others are written."""
+    import torch
+    c = ref.Chunk([4, 3, 2], [70, 100, 20], H=1, fp8=fp8, seed=80)
+    h, w = hidden(c.T, d_model, 81)
+    rows, want, slack = ref.append(c, h, w)
+    table = c.table.clone()
+    table[1, 2:] = table[1, 1]  # every entry of the row is a page of its own
+    c.table = table
+    c.seq_lens[1] = {"short": 2, "zero": 0, "negative": -7, "beyond the table": c.max_pages * c.page + 1,
+                     "huge": 2 ** 31 - 1}[bad]
+    before = c.cache.clone()
+    mla.append_chunk(h, w, *c.paged(), fp8_scales=c.scales, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == BOUNDS
+    kept = torch.ones(c.num_pages * c.page, dtype=torch.bool, device="cuda")
+    kept[rows[:4]] = kept[rows[7:]] = False
+    assert torch.equal(bits(c.cache).view(-1, 576)[kept], bits(before).view(-1, 576)[kept])
+    for part in (slice(0, 4), slice(7, 9)):
+        got, y, s = c.cache.view(-1, 576)[rows[part]], want[part], slack[part]
+        if fp8:
+            got, y, s = got.view(torch.float8_e4m3fn), y / c.scales.double(), s / c.scales.double()
+            tol = 2.0 ** -4 * y.abs() + 2.0 ** -10 + 1.1 * s
+            y = y.clamp(-448, 448)
+        else:
+            tol = ref.U_BF16 * y.abs() + 1.1 * s
+        assert ((got.double() - y).abs() <= tol).all()
