@@ -451,8 +451,8 @@ mla_status mla_copy16(const void* src, void* dst, size_t bytes, void* stream);
  * float32, one scale per column (see mla_quantize_fp8). Lengths outside
  * [n_b, max_pages_per_seq * page_size], page ids outside the pool and rows
  * outside [0, T) are reported in err_word as MLA_ERR_BOUNDS; what they touch is
- * clamped or skipped (mla_append_chunk writes no row of a sequence whose length is
- * out of range, and no row whose page is). Every input but the weights is read after the kernel
+ * clamped or skipped (mla_append_chunk writes no row of a sequence whose length or
+ * rows are out of range, and no row whose page is). Every input but the weights is read after the kernel
  * before has finished. Outputs and workspaces overlap no input. A workspace of
  * these calls is not one of mla_decode_plan's or mla_decode_paged's, whose plan is
  * written while the kernel before may still be running.

@@ -104,20 +104,19 @@ struct Target {
   int pos;
 };
 // Where row t goes. A row whose sequence's length does not hold the new rows or passes
-// the block table, or whose page id is out of range, is reported and not written (a
-// clamped length would put it over another token's row); a row of no sequence is not
-// written.
+// the block table, whose sequence has rows outside the array, or whose page id is out of
+// range, is reported and not written (a clamped length would put it over another token's
+// row); a row of no sequence is not written.
 __device__ Target target_of(const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_lens,
-                            const int32_t* __restrict__ block_table, int B, int t, int num_pages, int page_size,
-                            int max_pages, bool report, int32_t* err_word) {
+                            const int32_t* __restrict__ block_table, int B, int T, int t, int num_pages,
+                            int page_size, int max_pages, bool report, int32_t* err_word) {
   Target r = {-1, 0};
   const int b = row_sequence(cu, B, t);
   if (b < 0) return r;
-  const int64_t n = (int64_t)cu[b + 1] - cu[b];
-  const int L = seq_lens[b];
-  bool bad = L < n || L > max_pages * page_size;
+  const int first = cu[b], end = cu[b + 1], L = seq_lens[b];
+  bool bad = first < 0 || end > T || L < end - first || L > max_pages * page_size;
   if (!bad) {
-    const int pos = (int)(L - n + ((int64_t)t - cu[b]));
+    const int pos = L - (end - t);
     const int page = block_table[(int64_t)b * max_pages + pos / page_size];
     if (page >= 0 && page < num_pages)
       r = {(int64_t)page * page_size + pos % page_size, pos};
@@ -241,12 +240,13 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
   } else {
     grid_dependency_wait();
     grid_launch_dependents();
+    if (blockIdx.x == 0 && s == 0 && tile == 0) report_rows(a.cu, a.B, a.T, threadIdx.x, 256, a.err_word);
     // a warp per 32 rows and every other 16 columns
     const int row = (warp & 3) * 32 + lane, t = t0 + row;
     Target to = {-1, 0};
     if (kDirect && t < a.T)
-      to = target_of(a.cu, a.seq_lens, a.block_table, a.B, t, a.num_pages, a.page_size, a.max_pages, nt == 0,
-                     a.err_word);
+      to = target_of(a.cu, a.seq_lens, a.block_table, a.B, a.T, t, a.num_pages, a.page_size, a.max_pages,
+                     nt == 0, a.err_word);
     if (__all_sync(0xffffffffu, wait_phase(bar_d, 0, abort_flag, a.err_word))) {
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -330,8 +330,8 @@ append_chunk_finalize(Args a) {
   const uint64_t per_pos = col >= kDC ? turn_fraction(a.theta, (col - kDC) / 2) : 0;
   // the GEMM before passed its own dependency wait before this kernel could
   // start, so the lengths and tables are final; the partials are not
-  const Target to = target_of(a.cu, a.seq_lens, a.block_table, a.B, t, a.num_pages, a.page_size, a.max_pages, c == 0,
-                              a.err_word);
+  const Target to = target_of(a.cu, a.seq_lens, a.block_table, a.B, a.T, t, a.num_pages, a.page_size, a.max_pages,
+                              c == 0, a.err_word);
   grid_dependency_wait();
   grid_launch_dependents();
   if (to.row < 0) return;

@@ -23,6 +23,19 @@ __device__ inline int row_sequence(const int32_t* __restrict__ cu, int B, int t)
   return __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1) ? lo : -1;
 }
 
+// Reports a cu that does not start at 0, decreases or passes the T rows of the array:
+// rows that no thread of one of their own would meet. Every `threads`-th sequence from
+// `thread` on; for one block of the grid.
+__device__ inline void report_rows(const int32_t* __restrict__ cu, int B, int T, int thread, int threads,
+                                   int32_t* err_word) {
+  bool bad = false;
+  for (int b = thread; b < B; b += threads) {
+    const int a = __ldg(cu + b), e = __ldg(cu + b + 1);
+    bad |= (b == 0 && a != 0) || e < a || e > T;
+  }
+  if (bad) report_error(err_word, MLA_ERR_BOUNDS);
+}
+
 // New rows [*c0, *c0 + n) and context length of sequence b, clamped to the row
 // array and the block table; anything out of range is reported.
 __device__ inline int sequence_of_chunk(const int32_t* seq_lens, const int32_t* cu, int b, int T, int max_tokens, int* c0,

@@ -36,6 +36,11 @@ def bits(t):
     return t.view(torch.uint8) if t.dtype == torch.uint8 else t.view(torch.int16)
 
 
+def ints(v):
+    import torch
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
 # ------------------------------------------------------------------ append_chunk: what is written
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("d_model", [64, 1024])  # one split, many
@@ -69,3 +74,52 @@ def test_append_writes_no_row_of_a_bad_length(mla, err, bad, d_model, fp8):
         else:
             tol = ref.U_BF16 * y.abs() + 1.1 * s
         assert ((got.double() - y).abs() <= tol).all()
+
+
+CUTS = [[1, 5, 9], [0, 4, 12], [0, 6, 4], [-2, 4, 9], [0, 20, 9]]  # of 9 rows
+
+
+@pytest.mark.parametrize("d_model", [64, 1024])
+@pytest.mark.parametrize("cu", CUTS)
+def test_append_reports_rows_outside_the_array(mla, err, cu, d_model):
+    import torch
+    c = ref.Chunk([4, 5], [70, 100], H=1, seed=82)
+    h, w = hidden(c.T, d_model, 83)
+    c.cu = ints(cu)
+    allowed = torch.cat([c.rows(0), c.rows(1)])
+    before = c.cache.clone()
+    mla.append_chunk(h, w, *c.paged(), err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == BOUNDS
+    other = torch.ones(c.num_pages * c.page, dtype=torch.bool, device="cuda")
+    other[allowed] = False
+    assert torch.equal(bits(c.cache).view(-1, 576)[other], bits(before).view(-1, 576)[other])
+
+
+def test_append_writes_no_row_of_a_sequence_cut_short(mla, err):
+    """Rows cu[1] .. cu[2]-1 of which the array holds the first only: attention would place
+    that one last, its own count places it first, so it is not written at all."""
+    import torch
+    for d_model in (64, 1024):
+        c = ref.Chunk([4, 5], [70, 100], H=1, seed=84)
+        h, w = hidden(5, d_model, 85)
+        rows = c.rows(0, 66, 70)
+        before = c.cache.clone()
+        err.zero_()
+        mla.append_chunk(h, w, *c.paged(), err_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == BOUNDS
+        kept = torch.ones(c.num_pages * c.page, dtype=torch.bool, device="cuda")
+        kept[rows] = False
+        assert torch.equal(bits(c.cache).view(-1, 576)[kept], bits(before).view(-1, 576)[kept])
+        assert not torch.equal(bits(c.cache).view(-1, 576)[rows], bits(before).view(-1, 576)[rows])
+
+
+def test_append_with_room_behind_the_last_row_reports_nothing(mla, err):
+    import torch
+    for d_model in (64, 1024):
+        c = ref.Chunk([0, 4, 0, 5, 0], [0, 70, 3, 100, 0], H=1, seed=86, pad_rows=300)
+        h, w = hidden(c.T, d_model, 87)
+        mla.append_chunk(h, w, *c.paged(), err_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == OK
