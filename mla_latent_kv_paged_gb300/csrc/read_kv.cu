@@ -52,6 +52,7 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
     }
     src[i] = r;
   }
+  if (blockIdx.x == 0) report_rows(cu, B, n_rows, threadIdx.x, kThreads, err_word);
   const int g = threadIdx.x % kGroups, r0 = threadIdx.x / kGroups;
   float sc[8];
   if (kF8) {

@@ -123,3 +123,21 @@ def test_append_with_room_behind_the_last_row_reports_nothing(mla, err):
         mla.append_chunk(h, w, *c.paged(), err_word=err)
         torch.cuda.synchronize()
         assert int(err.item()) == OK
+
+
+# ------------------------------------------------------------------ read_kv
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("cu", CUTS)
+def test_read_reports_rows_outside_the_array(mla, err, cu, fp8):
+    import torch
+    c = ref.Chunk([4, 5], [70, 100], H=1, fp8=fp8, seed=96)
+    c.cu = ints(cu)
+    room = torch.full((9 + 20, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    mla.read_kv(*c.paged(), n_rows=9, fp8_scales=c.scales, out=room[:9], err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == BOUNDS
+    assert (room[9:] == 7.0).all()
+    if cu == [0, 4, 12]:  # the rows that are there are right
+        for b, lo, n in ((0, 0, 4), (1, 4, 5)):
+            x = c.values(b, 0, n)
+            assert ((room[lo:lo + n].double() - x).abs() <= ref.U_BF16 * x.abs()).all()
