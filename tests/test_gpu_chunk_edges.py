@@ -125,6 +125,37 @@ def test_append_with_room_behind_the_last_row_reports_nothing(mla, err):
         assert int(err.item()) == OK
 
 
+# ------------------------------------------------------------------ append_chunk: the values
+@pytest.mark.parametrize("d_model", [64, 1024])
+@pytest.mark.parametrize("seed", [90, 91, 92])
+def test_append_quotients_next_to_ties(mla, err, seed, d_model):
+    """The codes are those of the fp32 quotient, as mla_quantize_fp8's: columns whose
+    quotient lies on or beside the middle of two codes, scales from 2^-110 to 2^127."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c = ref.Chunk([1] * 8, [1] * 8, H=1, fp8=True, seed=seed)  # position 0: nothing is rotated
+    h = torch.zeros(8, d_model, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(576, d_model, dtype=torch.bfloat16, device="cuda")
+    h[:, 0] = 2.0 ** -torch.arange(8, device="cuda")
+    w[:, 0] = torch.randn(576, generator=g, device="cuda").to(torch.bfloat16)
+    low = torch.arange(1, 126, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    high = torch.arange(2, 127, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    pick = ((low + high) / 2)[torch.randint(0, 125, (576,), generator=g, device="cuda")]
+    c.scales = (w[:, 0].float().abs() / pick).clamp(min=2.0 ** -100)  # row 0 on the ties, half of it in row 1, ...
+    wide = torch.arange(0, 576, 9, device="cuda")
+    e = torch.linspace(-110, 127, len(wide), device="cuda").round()
+    c.scales[wide] = 2.0 ** e
+    w[wide, 0] = (1.5 * 2.0 ** e.clamp(max=126)).to(torch.bfloat16)
+    x = h[:, :1] * w[:, 0]  # exact: by powers of two; every other product is zero
+    mla.append_chunk(h, w, *c.paged(), fp8_scales=c.scales, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == OK
+    rows = torch.cat([c.rows(b) for b in range(8)])
+    got = c.cache.view(-1, 576)[rows]
+    assert torch.equal(got, (x.float() / c.scales).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    assert torch.equal(got, mla.quantize_fp8(x.contiguous(), c.scales))
+
+
 # ------------------------------------------------------------------ read_kv
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("cu", CUTS)
