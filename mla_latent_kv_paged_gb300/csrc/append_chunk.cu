@@ -81,11 +81,25 @@ inline Shape shape_of(int T, int d_model) {
 __device__ __forceinline__ uint64_t turn_fraction(double theta, int i) {
   return __double2ull_rn(pow(theta, -2.0 * (double)i / kDR) * 0.15915494309189535 * 18446744073709551616.0);
 }
-__device__ __forceinline__ void rotate(float& x, float& y, uint64_t per_pos, int pos) {
-  const int32_t turn = (int32_t)((per_pos * (uint64_t)(uint32_t)pos) >> 32);  // [-1/2, 1/2) in 2^-32
-  // absolute errors below 2^-21 on [-pi, pi]; the results are rounded to 2^-8 relative or coarser
-  float sn, cs;
-  __sincosf((float)turn * 1.4629180792671596e-9f /* 2 pi 2^-32 */, &sn, &cs);
+// The turn is taken apart into the nearest quarter and the rest, so that a sine or cosine
+// that is small keeps fp32's relative precision: within 2^-22 of itself, and 2^-32 of a
+// turn in the angle. (With __sincosf, 2^-21 whatever the size, small ones were off by
+// more than their bf16 rounding; it is no faster here.)
+__device__ __forceinline__ void turn_of(uint64_t per_pos, int pos, float& sn, float& cs) {
+  const uint32_t turn = (uint32_t)((per_pos * (uint64_t)(uint32_t)pos + 0x80000000u) >> 32);
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;
+  sincospif((float)(int32_t)(turn - (quarter << 30)) * 0x1p-31f, &sn, &cs);
+  if (quarter & 1u) {
+    const float t = sn;
+    sn = cs;
+    cs = -t;
+  }
+  if (quarter & 2u) {
+    sn = -sn;
+    cs = -cs;
+  }
+}
+__device__ __forceinline__ void rotate(float& x, float& y, float sn, float cs) {
   const float rx = x * cs - y * sn;
   y = x * sn + y * cs;
   x = rx;
@@ -316,7 +330,9 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {  // the pairs pass through the first two registers
               float x = __uint_as_float(r[0]), y = __uint_as_float(r[1]);
-              rotate(x, y, freq[(col - kDC) / 2 + i], to.pos);
+              float sn, cs;
+              turn_of(freq[(col - kDC) / 2 + i], to.pos, sn, cs);
+              rotate(x, y, sn, cs);
 #pragma unroll
               for (int q = 0; q < 14; ++q) r[q] = r[q + 2];
               r[14] = __float_as_uint(x);
@@ -361,6 +377,8 @@ append_chunk_finalize(Args a) {
   // start, so the lengths and tables are final; the partials are not
   const Target to = target_of(a.cu, a.seq_lens, a.block_table, a.B, a.T, t, a.num_pages, a.page_size, a.max_pages,
                               c == 0, a.err_word);
+  float sn = 0.f, cs = 1.f;
+  if (col >= kDC) turn_of(per_pos, to.pos, sn, cs);
   grid_dependency_wait();
   grid_launch_dependents();
   if (to.row < 0) return;
@@ -381,7 +399,7 @@ append_chunk_finalize(Args a) {
         y += v[k].y;
       }
   }
-  if (col >= kDC) rotate(x, y, per_pos, to.pos);
+  if (col >= kDC) rotate(x, y, sn, cs);
   if (kF8) {
     const float2 sc = __ldg(reinterpret_cast<const float2*>(a.scales) + c);
     reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(a.cache) + to.row * kRow)[c] =

@@ -156,6 +156,31 @@ def test_append_quotients_next_to_ties(mla, err, seed, d_model):
     assert torch.equal(got, mla.quantize_fp8(x.contiguous(), c.scales))
 
 
+@pytest.mark.parametrize("d_model", [64, 1024])
+@pytest.mark.parametrize("last", [2000, 130000])
+def test_append_rotation_keeps_small_sines(mla, err, last, d_model):
+    """Rows whose pairs are (1, 0) before the rotation: the cosine and the sine themselves.
+    A value is rounded to bf16 (2^-8 of it), after an angle within 2^-32 of a turn
+    (below 2^-29) and a sine or cosine within 2^-22 of itself."""
+    import torch
+    n = 2000
+    c = ref.Chunk([n], [last], H=1, seed=93)
+    h = torch.zeros(n, d_model, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(576, d_model, dtype=torch.bfloat16, device="cuda")
+    h[:, 0] = 1.0
+    w[512::2, 0] = 1.0
+    mla.append_chunk(h, w, *c.paged(), err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == OK
+    got = c.cache.view(-1, 576)[c.rows(0, last - n, last), 512:].double()
+    pos = torch.arange(last - n, last, dtype=torch.float64, device="cuda")
+    ang = pos[:, None] * torch.tensor([10000.0 ** (-i / 32) for i in range(32)], dtype=torch.float64, device="cuda")
+    want = torch.stack([ang.cos(), ang.sin()], -1).reshape(n, 64)
+    assert (want.abs() < 1e-3).sum() > 20
+    off = (got - want).abs()
+    assert (off <= (ref.U_BF16 + 2.0 ** -21) * want.abs() + 2.0 ** -29).all(), (off / want.abs()).max().item()
+
+
 # ------------------------------------------------------------------ read_kv
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("cu", CUTS)
