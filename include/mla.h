@@ -477,7 +477,7 @@ mla_status mla_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cach
  * is token first[b] + i of sequence b (first [B] int32, NULL = 0 for all), as it
  * is from a bf16 cache, bf16(fp8_scales[d] * e4m3(code)) from an FP8 one, zeros
  * for tokens at and past seq_lens[b]. rows [n_rows][576] bf16; rows at and past
- * cu[B] are left as they were; 1 <= n_rows < 2^30 takes T's place. Here seq_lens is
+ * cu[B] are left as they were; 1 <= n_rows <= 2^30 takes T's place. Here seq_lens is
  * only the bound of the context (it need not count the rows). Unused block-table
  * entries are never read. */
 mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t* block_table,

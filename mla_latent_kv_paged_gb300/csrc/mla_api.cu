@@ -377,7 +377,7 @@ mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t
       !aligned16(first) || !aligned16(cu) || !aligned16(rows))
     return MLA_ERR_INVALID_ARG;
   if (B < 1 || n_rows < 1 || num_pages < 1 || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
-  if (B > MLA_MAX_BATCH || n_rows > INT32_MAX / 2 || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (B > MLA_MAX_BATCH || n_rows > kMaxTokens || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
   if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
   return launch_status(launch_read_kv(cache, fp8_scales, block_table, seq_lens, first, cu, rows, B, n_rows, num_pages,
                                       page_size, max_pages_per_seq, err_word, (cudaStream_t)stream));
@@ -408,7 +408,7 @@ mla_status mla_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cach
 }
 
 size_t mla_attend_chunk_workspace_bytes(int B, int T, int H, int64_t max_tokens, int form) {
-  if (B < 1 || T < 1 || !chunk_counts_ok(B, T) || !heads_ok(H) || max_tokens < 1 || max_tokens > INT32_MAX / 2 ||
+  if (B < 1 || T < 1 || !chunk_counts_ok(B, T) || !heads_ok(H) || max_tokens < 1 || max_tokens > kMaxTokens ||
       form < MLA_CHUNK_AUTO || form > MLA_CHUNK_ABSORBED)
     return 0;
   // the larger of what the two kinds of cache need
@@ -432,7 +432,7 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
   if (B < 1 || T < 1 || num_pages < 1 || max_pages_per_seq < 1 || max_tokens < 1) return MLA_ERR_INVALID_ARG;
   if (!(softmax_scale > 0.f) || softmax_scale > 1.0e38f) return MLA_ERR_INVALID_ARG;
   if (form < MLA_CHUNK_AUTO || form > MLA_CHUNK_ABSORBED) return MLA_ERR_INVALID_ARG;
-  if (!chunk_counts_ok(B, T) || !heads_ok(H) || !page_size_ok(page_size) || max_tokens > INT32_MAX / 2)
+  if (!chunk_counts_ok(B, T) || !heads_ok(H) || !page_size_ok(page_size) || max_tokens > kMaxTokens)
     return MLA_ERR_UNSUPPORTED_SHAPE;
   if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
   const int max_tokens_seq = max_pages_per_seq * page_size;

@@ -146,8 +146,9 @@ cudaError_t smem_limit(size_t bytes) {
 // page_size: 64 or 128 tokens (1 or 2 tiles per block-table entry)
 inline bool page_size_ok(int page_size) { return page_size == kTile || page_size == 2 * kTile; }
 // sizes in tokens that stay in int32 (positions, and rows of the cache)
+constexpr int kMaxTokens = 1 << 30;  // of one context, of one call's contexts, of one call's rows
 inline bool token_counts_ok(int num_pages, int page_size, int max_pages) {
-  return (int64_t)max_pages * page_size <= INT32_MAX / 2 && (int64_t)num_pages * page_size <= INT32_MAX;
+  return (int64_t)max_pages * page_size <= kMaxTokens && (int64_t)num_pages * page_size <= INT32_MAX;
 }
 cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* block_table, int B, int n_q,
                         int max_pages, int page_size, int num_pages, int G, const Plan& plan, int32_t* err_word,
