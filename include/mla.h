@@ -498,7 +498,7 @@ mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t
  *     mla_absorb_q, mla_decode_paged, mla_combine and mla_out_proj; absorbed query and
  *     weights rounded to bf16 as there, u and W^UV to fp16, and on an FP8 cache all of
  *     them to fp16, the query times the scales). For few new tokens on a context;
- *     T <= MLA_MAX_BATCH.
+ *     T <= MLA_MAX_BATCH, T * max_pages_per_seq * page_size < 2^37.
  * Any of the values that a form rounds to fp16, if it is finite and 65520 or more, is
  * reported as MLA_ERR_RANGE; below 2^-14 their resolution is 2^-25.
  * A cached token whose expanded values are not finite (NaN or infinite latents)

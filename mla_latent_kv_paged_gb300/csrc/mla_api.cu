@@ -440,6 +440,8 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
   form = chunk_form(form, B, T, H, max_tokens, fp8_scales != nullptr);
   if (form == MLA_CHUNK_ABSORBED) {
     if (T > MLA_MAX_BATCH) return MLA_ERR_UNSUPPORTED_SHAPE;
+    // the plan counts the tiles of all rows' contexts, each row's by itself, in 32 bits
+    if ((int64_t)T * ((max_tokens_seq + kTile - 1) / kTile) > INT32_MAX) return MLA_ERR_UNSUPPORTED_SHAPE;
     const int G = mla_decode_default_splits(1);
     if (G < 1) return MLA_ERR_CUDA;
     if (workspace_bytes < chunk_rows_layout(nullptr, T, H, G, nullptr)) return MLA_ERR_WORKSPACE_TOO_SMALL;

@@ -39,3 +39,11 @@ def test_contexts_and_rows_of_up_to_2_to_the_30(lib):
     assert need > (1 << 30) * 1152
     assert attend(lib, need - 1, max_tokens=1 << 30) == SMALL
     assert attend(lib, need - 1, max_tokens=(1 << 30) + 1) == SHAPE
+
+
+def test_absorbed_rows_whose_tiles_pass_32_bits_are_refused(lib):
+    """4096 rows that may each see 2^25 tokens are 2^31 tiles of 64 for the decode plan."""
+    for page, most in ((64, (1 << 19) - 1), (128, (1 << 18) - 1)):
+        assert attend(lib, 1, T=4096, page=page, maxp=most, form=2) != SHAPE
+        assert attend(lib, 1, T=4096, page=page, maxp=most + 1, form=2) == SHAPE
+        assert attend(lib, 1, T=4095, page=page, maxp=most + 1, form=2) != SHAPE
