@@ -72,6 +72,7 @@ constexpr int kEarly = 3;  // steps before an item's end at which the next one i
 constexpr int64_t kTailBytes = 64 << 20;  // half of L2
 constexpr float kBias = 7.0f;       // P = 2^7 exp(z - m)
 constexpr float kRescale = 8.0f;    // log2 units
+constexpr float kExactOff = 4096.f;  // log2 units
 constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -510,7 +511,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         meet();
         mx = fmaxf(mx, get());
         // all MMAs issued before this step's scores are done, the last P V among them
-        if (__any_sync(0xffffffffu, mx * sl2 > ref * sl2 + kRescale)) {
+        // (the difference first: it is exact where the products would round it away)
+        if (__any_sync(0xffffffffu, (mx - ref) * sl2 > kRescale)) {
           const float up = fmaxf(ref, mx);
           if (j > 0) {
             const float f = ref == up ? 1.f : ex2((ref - up) * sl2);
@@ -529,7 +531,15 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           }
           ref = up;
         }
-        const float off = kBias - (ref == -INFINITY ? 0.f : ref * sl2);
+        const float base = ref == -INFINITY ? 0.f : ref;
+        float off = kBias - base * sl2;
+        // A product beyond 2^12 would bring its rounding (2^-13 and more) into the weights,
+        // beyond 2^28 overflow or lose them all: the reference is taken off first there.
+        if (__any_sync(0xffffffffu, fabsf(base) * sl2 > kExactOff)) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c) z[c] = __float_as_uint(__uint_as_float(z[c]) - base);
+          off = kBias;
+        }
         const uint64_t off2 = pack2(off, off), sl22 = pack2(sl2, sl2);
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
@@ -572,7 +582,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const bool part = t.slot >= 0;
         const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);  // NaN stays NaN
         const size_t pr = part ? ((size_t)t.slot * heads + t.hh) * kQTile + 128 * x + row : 0;
-        if (part && y == 0) plan.ml_part[pr] = make_float2(ref == -INFINITY ? ref : ref * sl2, sum);
+        if (part && y == 0) plan.ml_part[pr] = make_float2(ref, sum);
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           uint32_t o[32];
@@ -613,11 +623,12 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   }
 }
 
-// Items that were cut over the keys: out = sum_k 2^(m_k - m) O_k / sum_k 2^(m_k - m) l_k,
+// Items that were cut over the keys:
+//   out = sum_k 2^((m_k - m) sl2) O_k / sum_k 2^((m_k - m) sl2) l_k,
 // added in the order of the pieces. A warp per row, 16 bytes a lane; the partials of
 // a row are read once (HBM or L2-bound, 512 bytes a piece).
 __global__ void __launch_bounds__(256)
-join_kernel(ChunkPlan plan, uint16_t* __restrict__ out, float* __restrict__ lse, int H, int h0) {
+join_kernel(ChunkPlan plan, uint16_t* __restrict__ out, float* __restrict__ lse, int H, int h0, float sl2) {
   grid_dependency_wait();
   grid_launch_dependents();
   if ((int)blockIdx.x >= plan.hdr[2]) return;
@@ -632,7 +643,7 @@ join_kernel(ChunkPlan plan, uint16_t* __restrict__ out, float* __restrict__ lse,
     for (int k = 0; k < jn.y; ++k) {
       const float2 ml = __ldcg(&plan.ml_part[at(k)]);
       const float4 o = __ldcg(reinterpret_cast<const float4*>(plan.o_part + at(k) * kDV) + lane);
-      const float w = ml.x == m ? 1.f : ex2(ml.x - m);
+      const float w = ml.x == m ? 1.f : ex2((ml.x - m) * sl2);
       l = fmaf(w, ml.y, l);
       a0 = fmaf(w, o.x, a0);
       a1 = fmaf(w, o.y, a1);
@@ -643,7 +654,7 @@ join_kernel(ChunkPlan plan, uint16_t* __restrict__ out, float* __restrict__ lse,
     const size_t row = (size_t)(jn.z + r) * H + h0 + hh;
     reinterpret_cast<uint2*>(out + row * kDV)[lane] =
         make_uint2(cvt_bf16x2(a0 * inv, a1 * inv), cvt_bf16x2(a2 * inv, a3 * inv));
-    if (lse && lane == 0) lse[row] = l > 0.f ? (m - kBias + log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+    if (lse && lane == 0) lse[row] = l > 0.f ? (m * sl2 - kBias + log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
   }
 }
 
@@ -667,13 +678,14 @@ cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const u
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
+  const float sl2 = scale * 1.4426950408889634f;
   const int64_t most = ((int64_t)chunk_max_items(B, T) + slots) * heads;
   e = launch_pdl(attend_kernel, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), kSmem, s, mq, mqr, mk, mr,
-                 mv, out, lse, plan, plan.counter + round, H, h0, heads, cap, scale * 1.4426950408889634f, f16,
+                 mv, out, lse, plan, plan.counter + round, H, h0, heads, cap, sl2, f16,
                  err_word);
   if (e != cudaSuccess || slots == 0) return e;
   const int joins = chunk_max_items(B, T) < slots / 2 ? chunk_max_items(B, T) : slots / 2;  // two pieces at least
-  return launch_pdl(join_kernel, dim3(joins, heads, 8), dim3(256), 0, s, plan, out, lse, H, h0);
+  return launch_pdl(join_kernel, dim3(joins, heads, 8), dim3(256), 0, s, plan, out, lse, H, h0, sl2);
 }
 
 }  // namespace mla

@@ -91,7 +91,7 @@ struct ChunkPlan {
                      // row of the sequence}: all that a work item needs, in one read
   int4* join;        // [slots] {first slot, pieces, first row of the item, its rows}
   float* o_part;     // [slots * heads][256][128] sums of weighted values of a piece
-  float2* ml_part;   // [slots * heads][256] {reference maximum in log2 units, sum of weights}
+  float2* ml_part;   // [slots * heads][256] {reference maximum of the scores, sum of weights}
   uint16_t* rows;    // [cap][576] the sequences' cache rows, bf16 (of an FP8 cache: fp16, see launch_rows_f16);
                      // zeros from a context's end to its padding
   uint16_t* w16;     // [2][H][128][512] fp16 copies of w_uk and w_uv (FP8 cache only)

@@ -197,3 +197,69 @@ def test_read_reports_rows_outside_the_array(mla, err, cu, fp8):
         for b, lo, n in ((0, 0, 4), (1, 4, 5)):
             x = c.values(b, 0, n)
             assert ((room[lo:lo + n].double() - x).abs() <= ref.U_BF16 * x.abs()).all()
+
+
+# ------------------------------------------------------------------ attend_chunk
+def scored(c, q, kr):
+    """Scores of position alone, on the first positional column: exact products."""
+    c.q_nope.zero_()
+    c.q_rope.zero_()
+    c.q_rope[:c.total, :, 0] = q
+    pool = c.cache.view(-1, 576)
+    for b in range(len(c.lens)):
+        pool[c.rows(b), 512] = kr[b]
+
+
+@pytest.mark.parametrize("size", [10, 20, 28, 30, 60, 100])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attend_scores_of_any_size(mla, err, sign, size):
+    """Scores of up to 2^103: the tokens of the largest share the weight equally, whatever
+    fp32 cannot tell of the scores themselves. (Score differences are 2^10 / 14 at least:
+    every other weight is below 2^-100.)"""
+    import torch
+    c = ref.Chunk([300, 3], [900, 5000], H=2, seed=97)
+    kr = [torch.arange(L, device="cuda") % 7 + 1 for L in c.lens]
+    scored(c, sign * 2.0 ** size, [k.to(torch.bfloat16) for k in kr])
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=5900, form="expanded",
+                           err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == OK
+    at = 0
+    for b, (n, L) in enumerate(zip(c.new, c.lens)):
+        lat = c.values(b)[:, :512]
+        seen = torch.arange(L, device="cuda")[None] <= torch.arange(L - n, L, device="cuda")[:, None]
+        k = (sign * kr[b]).double()[None].masked_fill(~seen, float("-inf"))
+        p = (k == k.amax(-1, keepdim=True)).double()
+        p /= p.sum(-1, keepdim=True)
+        for h in range(2):
+            uv = c.w_uv[h].double()
+            v, vabs = lat @ uv.t(), lat.abs() @ uv.abs().t()
+            want = p @ v
+            tol = ref.U_BF16 * want.abs() + 4 * ref.U_F16 * (p @ v.abs()) + ref.TINY_F16 + 512 * ref.U_F32 * (p @ vabs)
+            assert ((got[at:at + n, h].double() - want).abs() <= tol).all(), (b, h)
+        at += n
+
+
+def test_attend_scores_a_rounding_apart(mla, err):
+    """Two scores that differ by two units in fp32's last place, which at this size are 296
+    (2^12 / sqrt(192)): all the weight is the larger one's, also between pieces cut over
+    the keys."""
+    import torch
+    c = ref.Chunk([2], [6000], H=1, seed=98)
+    kr = torch.full((6000,), -1.0, device="cuda")
+    scored(c, 2.0 ** 34, [kr.to(torch.bfloat16)])
+    pool = c.cache.view(-1, 576)
+    first, second = c.rows(0, 10, 11), c.rows(0, 5500, 5501)
+    pool[first, 512], pool[second, 512] = 1.0, 1.0
+    c.q_rope[:, :, 1] = 2.0 ** 12  # 2^34 + 2^12 against 2^34
+    pool[c.rows(0), 513] = 0.0
+    for high, low in ((second, first), (first, second)):
+        pool[high, 513], pool[low, 513] = 1.0, 0.0
+        got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=6000, form="expanded",
+                               err_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == OK
+        lat = pool[high, :512].double()
+        v, vabs = lat @ c.w_uv[0].double().t(), lat.abs() @ c.w_uv[0].double().abs().t()
+        tol = (ref.U_BF16 + 4 * ref.U_F16) * v.abs() + ref.TINY_F16 + 512 * ref.U_F32 * vabs
+        assert ((got[:, 0].double() - v).abs() <= tol).all()
