@@ -500,7 +500,9 @@ mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t
  *     them to fp16, the query times the scales). For few new tokens on a context;
  *     T <= MLA_MAX_BATCH, T * max_pages_per_seq * page_size < 2^37.
  * Any of the values that a form rounds to fp16, if it is finite and 65520 or more, is
- * reported as MLA_ERR_RANGE; below 2^-14 their resolution is 2^-25.
+ * reported as MLA_ERR_RANGE; below 2^-14 their resolution is 2^-25. (The absorbed form's
+ * partial scores are among them, as offsets in log2 units from the middle of each 32
+ * tokens': scores that lie 131000 and more apart.)
  * A cached token whose expanded values are not finite (NaN or infinite latents)
  * gives NaN to the queries that see it and to no other.
  *   q_nope [T][H][128] bf16, q_rope [T][H][64] bf16 (already rotated),

@@ -656,6 +656,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
               }
           }
           const float mid = lo <= hi ? 0.5f * lo + 0.5f * hi : 0.f;
+          // offsets that fp16 does not hold (the difference of halves: both ends may be large)
+          if (kRows && row < H && 0.5f * hi - 0.5f * lo >= 65520.f && hi < INFINITY && lo > -INFINITY)
+            report_error(err_word, MLA_ERR_RANGE);
           const uint32_t xoff = (uint32_t)(g & 1) * kXBytes;
           const uint32_t xa = r_x + xoff + (uint32_t)row * 16;
           const uint32_t xf = r_xf + 8u * (uint32_t)(g & 1);

@@ -263,3 +263,25 @@ def test_attend_scores_a_rounding_apart(mla, err):
         v, vabs = lat @ c.w_uv[0].double().t(), lat.abs() @ c.w_uv[0].double().abs().t()
         tol = (ref.U_BF16 + 4 * ref.U_F16) * v.abs() + ref.TINY_F16 + 512 * ref.U_F32 * vabs
         assert ((got[:, 0].double() - v).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_absorbed_reports_scores_too_far_apart(mla, err, fp8):
+    """The absorbed form exchanges partial scores as fp16 offsets: beyond them, a report."""
+    import torch
+    c = ref.Chunk([3, 2], [200, 66], H=3, fp8=fp8, seed=99)
+    c.q_nope.zero_()
+    c.q_rope.zero_()
+    c.q_rope[:, :, 0] = 2.0 ** 14
+
+    def run(scale):
+        err.zero_()
+        out = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=266, fp8_scales=c.scales,
+                               softmax_scale=scale, form="absorbed", err_word=err)
+        torch.cuda.synchronize()
+        return out, int(err.item())
+
+    out, e = run(2.0 ** -2)   # scores of about +-2^13
+    assert e == OK and torch.isfinite(out).all()
+    out, e = run(2.0 ** 6)    # ... of +-2^21
+    assert e == RANGE
