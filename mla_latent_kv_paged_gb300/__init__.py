@@ -65,7 +65,7 @@ class MlaError(RuntimeError):
 
 DEBUG_LIB_PATH = os.path.join(_HERE, "libmla_gb300_debug.so")
 DEBUG_EXPORTS = ["mla_debug_read_counters", "mla_debug_reset", "mla_debug_set_wait_limit",
-                 "mla_debug_set_skip_producer"]
+                 "mla_debug_set_skip_producer", "mla_debug_set_skip_loads"]
 
 _lock = threading.Lock()
 _lib = None
@@ -102,6 +102,8 @@ def debug_lib():
             L.mla_debug_set_wait_limit.argtypes = [ctypes.c_longlong]
             L.mla_debug_set_skip_producer.restype = ctypes.c_int
             L.mla_debug_set_skip_producer.argtypes = [ctypes.c_int]
+            L.mla_debug_set_skip_loads.restype = ctypes.c_int
+            L.mla_debug_set_skip_loads.argtypes = [ctypes.c_int, ctypes.c_int]
             _debug_lib = L
     return _debug_lib
 

@@ -244,11 +244,12 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
       };
       // the first stages' weights while the kernel before is finishing (weights
       // are never its output); the hidden states after the wait
-      const int early = nkb < kStages ? nkb : kStages;
+      const int skip = skip_loads(), loads = skip == 1 || (skip == 2 && rank == 1) ? 0 : nkb;
+      const int early = loads < kStages ? loads : kStages;
       for (int k = 0; k < early; ++k) weights(k, k);
       grid_dependency_wait();
       int k = 0;
-      for (; k < nkb; ++k) {
+      for (; k < loads; ++k) {
         const int st = k % kStages;
         if (k >= kStages) {
           if (!wait_phase(empty(st), (uint32_t)((k / kStages - 1) & 1), abort_flag, a.err_word)) break;
@@ -256,13 +257,14 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         }
         tma_load_2d_pair(sbase + st * kStageBytes, &map_h, mapa(full(st), 0), (kb0 + k) * 64, t0, stream);
       }
-      if (rank == 0 && *abort_flag) {
-        // let the pair's copies in flight land before the pair can exit (the odd CTA
-        // waits for this one below; where it issued fewer, the limit ends the wait)
+      if (rank == 0) {
+        // let the pair's copies in flight land before the pair can exit, whoever gives up
+        // and whenever (the odd CTA waits for this one below; where it issued fewer, the
+        // limit ends the wait)
         const long long start = clock64();
         for (int i = k > kStages ? k - kStages : 0; i < k; ++i)
           while (!mbar_try_wait(full(i % kStages), (uint32_t)((i / kStages) & 1)) &&
-                 clock64() - start < kWaitLimitCycles) {
+                 clock64() - start < wait_limit()) {
           }
       }
     }
@@ -458,5 +460,9 @@ cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* 
   return fp8_scales ? launch_pdl(append_chunk_finalize<true>, dim3(T), dim3(kRow / 2), 0, s, a)
                     : launch_pdl(append_chunk_finalize<false>, dim3(T), dim3(kRow / 2), 0, s, a);
 }
+
+#if MLA_DEBUG_CHECKS
+cudaError_t debug_append_chunk(const long long* limit, const int* skip) { return sm100::debug_set(limit, skip); }
+#endif
 
 }  // namespace mla

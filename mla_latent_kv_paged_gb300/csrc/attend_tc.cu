@@ -177,7 +177,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                                              (long long)(kTailBytes / head_bytes))
                                   : 0;
       const int64_t bulk = (int64_t)(heads - tail) * pieces;
-      bool ok = true;
+      const int skip = skip_loads();
+      bool ok = skip != 3;
       int ki = 0, vi = 0;
       int64_t idx = blockIdx.x;
       // item `it` into its slot: {q0, n, c0, L, j0, j1, slot, first expanded row, head, live}
@@ -204,7 +205,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if (ok) mbar_arrive_expect_tx(bar(full + st), kSlab);
         return st;
       };
-      publish(0);
+      if (ok) publish(0);
       for (int it = 0; ok; ++it) {
         const int* s = items + 12 * (it % kItems);
         const Item t = read_item(s);
@@ -215,6 +216,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           // the next item is taken near this one's end, so that the CTAs stay in balance
           if (j == max(nkv - kEarly, 0)) publish(it + 1);
           if (!ok) break;
+          if (skip == 1) continue;
           const int row = (int)(k0 + (int64_t)j * kKvTile), hrow = (int)((int64_t)t.hh * cap + row);
           for (int c = 0; c < 3 && ok; ++c) {
             const int st = slab(KF0, KE0, kKStages, ki);
@@ -235,17 +237,16 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           }
         }
       }
-      if (*abort_flag) {  // let the copies in flight land before the CTA can exit
-        const long long t0 = clock64();
-        auto drain = [&](int full, int stages, int i) {
-          for (int k = i > stages ? i - stages : 0; k < i; ++k)
-            while (!mbar_try_wait(bar(full + k % stages), (uint32_t)((k / stages) & 1)) &&
-                   clock64() - t0 < kWaitLimitCycles) {
-            }
-        };
-        drain(KF0, kKStages, ki);
-        drain(VF0, kVStages, vi);
-      }
+      // let the copies in flight land before the CTA can exit, whoever gives up and whenever
+      const long long t0 = clock64();
+      auto drain = [&](int full, int stages, int i) {
+        for (int k = i > stages ? i - stages : 0; k < i; ++k)
+          while (!mbar_try_wait(bar(full + k % stages), (uint32_t)((k / stages) & 1)) &&
+                 clock64() - t0 < wait_limit()) {
+          }
+      };
+      drain(KF0, kKStages, ki);
+      drain(VF0, kVStages, vi);
     }
   } else if (warp == 19) {
     // ------------------------------------------------------------ queries
@@ -254,7 +255,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       prefetch_tmap(&map_q);
       prefetch_tmap(&map_qr);
       const uint64_t once = policy_evict_first();
-      bool ok = true;
+      bool ok = skip_loads() != 2;
       int qn[2] = {0, 0};
       for (int it = 0; ok; ++it) {
         ok = wait_phase(bar(IF0 + it % kItems), (uint32_t)((it / kItems) & 1), abort_flag, err_word);
@@ -277,13 +278,11 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           tma_load_3d(dst + 2 * kSlab, &map_qr, bar(QL0 + x), 0, h0 + t.hh, row, once);
         }
       }
-      if (*abort_flag) {
-        const long long t0 = clock64();
-        for (int x = 0; x < 2; ++x)
-          while (qn[x] > 0 && !mbar_try_wait(bar(QL0 + x), (uint32_t)((qn[x] - 1) & 1)) &&
-                 clock64() - t0 < kWaitLimitCycles) {
-          }
-      }
+      const long long t0 = clock64();
+      for (int x = 0; x < 2; ++x)
+        while (qn[x] > 0 && !mbar_try_wait(bar(QL0 + x), (uint32_t)((qn[x] - 1) & 1)) &&
+               clock64() - t0 < wait_limit()) {
+        }
     }
   } else if (warp >= 17) {
     // ------------------------------------------------------------ MMA issuers
@@ -687,5 +686,9 @@ cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const u
   const int joins = chunk_max_items(B, T) < slots / 2 ? chunk_max_items(B, T) : slots / 2;  // two pieces at least
   return launch_pdl(join_kernel, dim3(joins, heads, 8), dim3(256), 0, s, plan, out, lse, H, h0, sl2);
 }
+
+#if MLA_DEBUG_CHECKS
+cudaError_t debug_attend(const long long* limit, const int* skip) { return sm100::debug_set(limit, skip); }
+#endif
 
 }  // namespace mla

@@ -223,4 +223,12 @@ cudaError_t launch_attend(const ChunkPlan& plan, const uint16_t* q_nope, const u
                           float* lse, int B, int T, int H, int h0, int heads, int64_t cap, int slots, int round,
                           float scale, bool f16, int32_t* err_word, cudaStream_t s);
 
+#if MLA_DEBUG_CHECKS
+// Test builds only: the wait limit and the loads left out (null: as they are) of the
+// kernels of one file.
+cudaError_t debug_append_chunk(const long long* limit, const int* skip);
+cudaError_t debug_expand(const long long* limit, const int* skip);
+cudaError_t debug_attend(const long long* limit, const int* skip);
+#endif
+
 }  // namespace mla

@@ -44,6 +44,7 @@
 // (one thread per head row, the CTA's 32 tokens of the page). The score MMAs
 // of page g+1 run while the softmax of page g is in flight; the value MMAs
 // trail by one page.
+#include "chunk.cuh"
 #include "mla_internal.cuh"
 #include "sm100.cuh"
 
@@ -1082,10 +1083,25 @@ int mla_debug_reset(void) {
   cudaError_t e = cudaMemcpyToSymbol(mla::g_dbg_counters, zero, sizeof(zero));
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(mla::g_dbg_skip_producer, &off, sizeof(off));
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(mla::sm100::g_wait_limit_override, &nolimit, sizeof(nolimit));
+  if (e == cudaSuccess) e = mla::debug_append_chunk(&nolimit, &off);
+  if (e == cudaSuccess) e = mla::debug_expand(&nolimit, &off);
+  if (e == cudaSuccess) e = mla::debug_attend(&nolimit, &off);
   return (int)e;
 }
 int mla_debug_set_wait_limit(long long cycles) {
-  return (int)cudaMemcpyToSymbol(mla::sm100::g_wait_limit_override, &cycles, sizeof(cycles));
+  cudaError_t e = cudaMemcpyToSymbol(mla::sm100::g_wait_limit_override, &cycles, sizeof(cycles));
+  if (e == cudaSuccess) e = mla::debug_append_chunk(&cycles, nullptr);
+  if (e == cudaSuccess) e = mla::debug_expand(&cycles, nullptr);
+  if (e == cudaSuccess) e = mla::debug_attend(&cycles, nullptr);
+  return (int)e;
+}
+int mla_debug_set_skip_loads(int kernel, int what) {
+  switch (kernel) {
+    case 0: return (int)mla::debug_append_chunk(nullptr, &what);
+    case 1: return (int)mla::debug_expand(nullptr, &what);
+    case 2: return (int)mla::debug_attend(nullptr, &what);
+    default: return (int)cudaErrorInvalidValue;
+  }
 }
 int mla_debug_set_skip_producer(int on) {
   return (int)cudaMemcpyToSymbol(mla::g_dbg_skip_producer, &on, sizeof(on));

@@ -115,9 +115,10 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
       const uint32_t af = mapa(bar(AF), 0);
       bool ok = true;
       int it = 0, loads = 0;
-      for (int64_t u = u0; u < u1 && ok; ++u) {
+      const int skip = skip_loads();
+      for (int64_t u = skip == 1 || (skip == 2 && rank == 1) ? u1 : u0; u < u1 && ok; ++u) {
         const int m = (int)(u / heads), h = h0 + (int)(u % heads);
-        if (u == u0 || u % heads == 0) {  // the next tokens, once the MMAs on the last ones are done
+        if (skip != 3 && (u == u0 || u % heads == 0)) {  // the next tokens, once the MMAs on the last ones are done
           if (loads > 0 && !wait_phase(bar(AE), (uint32_t)((loads - 1) & 1), abort_flag, err_word)) break;
           if (rank == 0) mbar_arrive_expect_tx(bar(AF), 2 * kABytes);
           for (int c = 0; c < 8; ++c)
@@ -134,14 +135,17 @@ expand_kernel(const __grid_constant__ CUtensorMap map_rows, const __grid_constan
           tma_load_2d_pair(sbase + kOffB + st * kBBytes, map_w, mapa(bar(FULL0 + st), 0), 64 * kb, h * 128, keep);
         }
       }
-      if (rank == 0 && *abort_flag) {
-        // let the pair's copies in flight land before the pair can exit (the odd CTA
-        // waits for this one below; where it issued fewer, the limit ends the wait)
+      if (rank == 0) {
+        // let the pair's copies in flight land before the pair can exit, whoever gives up
+        // and whenever (the odd CTA waits for this one below; where it issued fewer, the
+        // limit ends the wait)
         const long long t0 = clock64();
-        for (int i = it > kStages ? it - kStages : 0; i < it; ++i)
-          while (!mbar_try_wait(bar(FULL0 + i % kStages), (uint32_t)((i / kStages) & 1)) &&
-                 clock64() - t0 < kWaitLimitCycles) {
+        auto land = [&](int b, int use) {
+          while (!mbar_try_wait(bar(b), (uint32_t)(use & 1)) && clock64() - t0 < wait_limit()) {
           }
+        };
+        if (loads > 0) land(AF, loads - 1);
+        for (int i = it > kStages ? it - kStages : 0; i < it; ++i) land(FULL0 + i % kStages, i / kStages);
       }
     }
   } else if (warp == 9) {
@@ -244,5 +248,9 @@ cudaError_t launch_expand(const ChunkPlan& plan, const uint16_t* w_uk, const uin
                     plan, h0, heads, cap, f16 ? idesc_f16(256, 256, false, false) : idesc_bf16(256, 256, false, false),
                     err_word);
 }
+
+#if MLA_DEBUG_CHECKS
+cudaError_t debug_expand(const long long* limit, const int* skip) { return sm100::debug_set(limit, skip); }
+#endif
 
 }  // namespace mla

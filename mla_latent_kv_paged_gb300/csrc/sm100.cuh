@@ -116,8 +116,18 @@ __device__ __forceinline__ long long wait_limit() {
   const long long v = *reinterpret_cast<volatile long long*>(&g_wait_limit_override);
   return v > 0 ? v : kWaitLimitCycles;
 }
+// ... and which loads the kernels of this translation unit leave out, so that their
+// waits run out (0: none; see mla_debug_set_skip_loads)
+static __device__ int g_skip_loads;
+__device__ __forceinline__ int skip_loads() { return *reinterpret_cast<volatile int*>(&g_skip_loads); }
+static inline cudaError_t debug_set(const long long* limit, const int* skip) {
+  cudaError_t e = limit ? cudaMemcpyToSymbol(g_wait_limit_override, limit, sizeof(*limit)) : cudaSuccess;
+  if (e == cudaSuccess && skip) e = cudaMemcpyToSymbol(g_skip_loads, skip, sizeof(*skip));
+  return e;
+}
 #else
 __device__ __forceinline__ constexpr long long wait_limit() { return kWaitLimitCycles; }
+__device__ __forceinline__ constexpr int skip_loads() { return 0; }
 #endif
 
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort,
