@@ -466,7 +466,8 @@ mla_status mla_copy16(const void* src, void* dst, size_t bytes, void* stream);
  *   most 65536; workspace >= mla_append_chunk_workspace_bytes(T, d_model) bytes,
  *   no initial contents needed. w_dkr may be read while the kernel before is
  *   still finishing. Sums are added in a fixed order: results are reproducible
- *   bit for bit. Two rows that name the same cache row leave one of the two. */
+ *   bit for bit. Where two rows name the same cache row, each of its values is one
+ *   of the two (not all from the same row). */
 size_t mla_append_chunk_workspace_bytes(int T, int d_model);
 mla_status mla_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
                             const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,

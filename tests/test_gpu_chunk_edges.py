@@ -181,6 +181,30 @@ def test_append_rotation_keeps_small_sines(mla, err, last, d_model):
     assert (off <= (ref.U_BF16 + 2.0 ** -21) * want.abs() + 2.0 ** -29).all(), (off / want.abs()).max().item()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d_model", [64, 1024])
+def test_append_two_rows_for_one_cache_row(mla, err, d_model, fp8):
+    """Two sequences whose new tokens fall on the same cache rows: each value is one of the
+    two, and the rest of the pool is untouched."""
+    import torch
+    c = ref.Chunk([3, 3], [40, 40], H=1, fp8=fp8, seed=94)
+    h, w = hidden(6, d_model, 95)
+    mla.append_chunk(h, w, *c.paged(), fp8_scales=c.scales, err_word=err)
+    one, two = (c.cache.view(-1, 576)[c.rows(b, 37, 40)].clone() for b in (0, 1))
+    d = ref.Chunk([3, 3], [40, 40], H=1, fp8=fp8, seed=94)
+    before = d.cache.clone()
+    d.table[1] = d.table[0]
+    rows = d.rows(0, 37, 40)
+    mla.append_chunk(h, w, *d.paged(), fp8_scales=d.scales, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == OK
+    got = bits(d.cache.view(-1, 576)[rows])
+    assert ((got == bits(one)) | (got == bits(two))).all()
+    other = torch.ones(d.num_pages * d.page, dtype=torch.bool, device="cuda")
+    other[rows] = False
+    assert torch.equal(bits(d.cache).view(-1, 576)[other], bits(before).view(-1, 576)[other])
+
+
 # ------------------------------------------------------------------ read_kv
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("cu", CUTS)
