@@ -309,3 +309,36 @@ def test_absorbed_reports_scores_too_far_apart(mla, err, fp8):
     assert e == OK and torch.isfinite(out).all()
     out, e = run(2.0 ** 6)    # ... of +-2^21
     assert e == RANGE
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("form", ["expanded", "absorbed"])
+@pytest.mark.parametrize("what", ["values", "queries", "keys"])
+def test_attend_below_the_normal_range_of_fp16(mla, err, what, form, fp8):
+    """Weights or queries that bring keys, values or queries below 2^-14: the resolution is
+    2^-25 there, whatever the value. (Where a weight itself falls below it, each of the 512
+    products of a value is off by 2^-25 of its latent.)"""
+    import torch
+    c = ref.Chunk([30, 150], [200, 170], H=2, fp8=fp8, seed=100)
+    if what == "values":
+        c.w_uv *= 2.0 ** -15
+    elif what == "keys":
+        c.w_uk *= 2.0 ** -15
+        c.q_nope *= 2.0 ** 8
+    else:
+        c.q_nope *= 2.0 ** -17
+    want, _, bound = ref.attend(c)
+    got = mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=370, fp8_scales=c.scales,
+                           form=form, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == OK
+    extra = torch.zeros((), dtype=torch.float64, device="cuda")
+    lat = max(c.values(b)[:, :512].abs().sum(-1).max().item() for b in range(2))
+    if what == "values":
+        extra = ref.TINY_F16 * lat
+    elif what == "keys" and form == "expanded" and fp8:
+        # a key off by 2^-25 of the latents' sum: scores by q times that
+        qn = c.q_nope[:c.total].double().abs().sum(-1, keepdim=True)
+        v = max((c.values(b)[:, :512].abs() @ c.w_uv.double().abs().transpose(1, 2)).max().item() for b in range(2))
+        extra = torch.expm1(2 * ref.SCALE * ref.TINY_F16 * lat * qn) * v
+    assert ((got.double() - want).abs() <= bound[form] + extra).all()
