@@ -74,8 +74,9 @@ typedef enum {
     MLA_ERR_WORKSPACE_TOO_SMALL = 3,
     MLA_ERR_CUDA = 4,              /* a CUDA runtime call or launch failed */
     MLA_ERR_TIMEOUT = 5,           /* device: a bounded wait gave up */
-    MLA_ERR_BOUNDS = 6,            /* device: seq_len or page id out of range */
-    MLA_ERR_RANGE = 7              /* device: a split partial outside the fp16 range */
+    MLA_ERR_BOUNDS = 6,            /* device: seq_len, page id or row of a chunk out of range */
+    MLA_ERR_RANGE = 7              /* device: a value outside the fp16 range, of a split partial
+                                      or of what mla_attend_chunk rounds to fp16 */
 } mla_status;
 
 /* Human-readable name of a status code. Never NULL. */
@@ -490,8 +491,9 @@ mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t
  * own rows included (append them first):
  *   z_s = softmax_scale * (q_nope . (c_s W^UK) + q_rope . k^R_s),  s <= L_b - n_b + j
  *   out[t][h] = softmax(z) (c_s W^UV),  lse[t][h] = ln sum_s exp(z_s)
- * in one of two forms of the same sums (form = MLA_CHUNK_AUTO chooses by T / B,
- * H, max_tokens / B and the kind of cache, nothing on the device):
+ * in one of two forms of the same sums, one for the whole call (form =
+ * MLA_CHUNK_AUTO chooses by T / B, H, max_tokens / B and the kind of cache, nothing
+ * on the device; B counts sequences without new tokens too):
  *   MLA_CHUNK_EXPANDED  keys and values of every head are expanded from the latents
  *     first, and rounded to fp16 (so are content queries, the rows of an FP8 cache
  *     and, with one, the weights; fp32 sums everywhere). For long chunks.
@@ -510,8 +512,9 @@ mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t
  *   w_uk, w_uv as for mla_absorb_q and mla_out_proj, out [T][H][128] bf16,
  *   lse [T][H] float or NULL (both in device memory),
  *   max_tokens  at least the sum of the contexts of the sequences that have new
- *               tokens (it sizes the workspace; a sequence beyond it is skipped and
- *               reported), <= 2^30
+ *               tokens, <= 2^30. It sizes the expanded form's workspace and grids (that
+ *               form skips and reports a sequence beyond it) and stands for the contexts
+ *               in the choice of MLA_CHUNK_AUTO, so the nearer the better.
  *   workspace   >= mla_attend_chunk_workspace_bytes(B, T, H, max_tokens, form) bytes,
  *               no initial contents needed. Calls sharing a workspace must not
  *               overlap on the GPU. The size of the absorbed form depends on the

@@ -595,7 +595,8 @@ def append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, *, fp8_scales=None,
     tokens, at the end of its context (seq_lens [B] int32 already counts them). w_dkr
     [576, d_model] bf16 as for append_kv, cache [num_pages, page_size, 576] bf16, or
     uint8 e4m3 codes with their column scales fp8_scales [576] float32: the rows are
-    then quantised as they are written. Rows of h at and past cu[B] are ignored. The
+    then quantised as they are written. Rows of h at and past cu[B] are ignored; of a
+    sequence whose length or rows are out of range nothing is written (err_word tells). The
     workspace (allocated when none is given) is returned for reuse.
     """
     import torch
@@ -646,10 +647,14 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
     q_nope [T, H, 128], q_rope [T, H, 64] (rotated) bf16, rows cu[b] .. cu[b+1]-1 being
     sequence b's new tokens; row j of n sees tokens 0 .. seq_lens[b] - n + j. w_uk, w_uv
     [H, 128, 512] bf16; cache, block_table, seq_lens, cu, fp8_scales as for append_chunk.
-    max_tokens bounds the sum of the contexts (default: the block table's capacity) and
-    sizes the workspace. form: "expanded" (keys and values of every head expanded first),
-    "absorbed" (each token decoded over the latents) or "auto" (by T / B, H and max_tokens / B:
-    few new tokens on a context are absorbed).
+    max_tokens bounds the sum of the contexts of the sequences with new tokens. Pass it:
+    the default is the block table's capacity, which then sizes the workspace (1152 bytes a
+    token, beside up to 2 GiB, in the expanded form) and stands for the contexts when
+    "auto" chooses.
+    form, one for the whole call: "expanded" (keys and values of every head expanded first),
+    "absorbed" (each token decoded over the latents; on a bf16 cache the absorbed query and
+    the weights are rounded to bf16, as in decode_step) or "auto" (by T / B, H and
+    max_tokens / B: few new tokens on a context are absorbed).
     lse [T, H] float32, when given, receives the log-sum-exp of the scores. Rows at and
     past cu[B] of out and lse are left as they were.
     """
@@ -693,7 +698,8 @@ def chunk_step(h, q_nope, q_rope, w_dkr, w_uk, w_uv, cache, block_table, seq_len
     the cache that now holds the chunk (decode_step's counterpart for ragged chunks).
 
     ``bufs`` may hold preallocated append_workspace and attend_workspace tensors.
-    Returns out [T, H, 128] bf16.
+    max_tokens and form as for attend_chunk: without max_tokens the block table's capacity
+    sizes the workspace and goes into the choice of form. Returns out [T, H, 128] bf16.
     """
     bufs = bufs or {}
     append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, fp8_scales=fp8_scales, rope_theta=rope_theta,

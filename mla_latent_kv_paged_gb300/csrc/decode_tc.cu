@@ -250,7 +250,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
   tc_fence_after();
   cluster_sync();  // the peer's barriers are initialised before any remote arrive
   const uint32_t tmem = *tmem_slot;
-  // set-up above overlaps the plan kernel; the plan and q_abs are read below
+  // set-up above overlaps the plan kernel; the plan and q_abs are read below.
+  // (The order of these two matters to a chunk's rows: out_proj, two launches on, loads the
+  // fp16 copy of W^UV that their plan kernel writes before its own dependency wait, and
+  // may do so because it starts after this wait.)
   grid_dependency_wait();
   grid_launch_dependents();
   const int it0 = plan.range_item[worker], it1 = plan.range_item[worker + 1];
