@@ -76,7 +76,8 @@ __device__ inline int64_t ceil_div64(int64_t a, int64_t b) { return div_nn(a + b
 // Plan::seq_row). The chunk's inputs may come from the kernel before, so they are
 // read after it has finished.
 // Beside the planning threads (the first block, or its first warp) the rest of the
-// grid copies w_uv to fp16, in the time that the plan's chain of latencies takes.
+// grid copies w_uv to fp16, in the time that the plan's chain of latencies takes, and
+// some of it looks cu over (a sequence without a row of the array is met by no row).
 struct RowArgs {
   const int32_t* cu;   // [sequences + 1]
   int sequences;
@@ -129,6 +130,7 @@ plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bl
   if (kRows) {
     sm100::grid_dependency_wait();
     if (blockIdx.x > 0) {
+      if (blockIdx.x == 1) report_rows(rows.cu, rows.sequences, B, tid, kPlanThreads, err_word);
       copy_weights(rows, (blockIdx.x - 1) * kPlanThreads + tid, (gridDim.x - 1) * kPlanThreads, err_word);
       return;
     }
@@ -277,6 +279,7 @@ plan_small_kernel(const int32_t* __restrict__ seq_lens, int B, int n_q, int max_
     sm100::grid_dependency_wait();
     const int thread = blockIdx.x * kPlanThreads + lane - 32;
     if (thread >= 0) {
+      if (blockIdx.x == 0) report_rows(rows.cu, rows.sequences, B, thread, kPlanThreads - 32, err_word);
       copy_weights(rows, thread, gridDim.x * kPlanThreads - 32, err_word);
       return;
     }
@@ -389,7 +392,7 @@ cudaError_t launch_rows_plan(const int32_t* seq_lens, const int32_t* cu, int seq
   rows.w = reinterpret_cast<const uint4*>(w_uv);
   rows.w16 = reinterpret_cast<uint4*>(chunk.w16);
   rows.n8 = H * kDV * kDC / 8;
-  // four groups a thread, up to two blocks per SM
+  // four groups a thread, up to two blocks per SM (and at least two: block 1 looks cu over)
   const int want = (rows.n8 + 4 * kPlanThreads - 1) / (4 * kPlanThreads), blocks = 1 + (want < 304 ? want : 304);
   if (T <= 32)
     return launch_pdl(plan_small_kernel<true>, dim3(blocks), dim3(kPlanThreads), 0, s, seq_lens, T, 1, max_tokens, G,

@@ -224,6 +224,22 @@ def test_read_reports_rows_outside_the_array(mla, err, cu, fp8):
 
 
 # ------------------------------------------------------------------ attend_chunk
+@pytest.mark.parametrize("form", ["expanded", "absorbed"])
+@pytest.mark.parametrize("pad", [0, 60])  # up to 32 rows, more
+@pytest.mark.parametrize("cu", CUTS + [[3, 3, 9], [9, 9, 9], [0, 0, -1]])
+def test_attend_reports_rows_outside_the_array(mla, err, cu, pad, form):
+    """Also where no row of the array belongs to the sequence that is out of range."""
+    import torch
+    c = ref.Chunk([4, 5], [70, 100], H=2, seed=101, pad_rows=pad)
+    c.cu = ints(cu if pad == 0 else [v + pad if v > 9 else v for v in cu])
+    room = torch.full((c.T + 4, 2, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    mla.attend_chunk(c.q_nope, c.q_rope, c.w_uk, c.w_uv, *c.paged(), max_tokens=170, form=form, out=room[:c.T],
+                     err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == BOUNDS
+    assert (room[c.T:] == 3.0).all()
+
+
 def scored(c, q, kr):
     """Scores of position alone, on the first positional column: exact products."""
     c.q_nope.zero_()
