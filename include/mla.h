@@ -75,8 +75,9 @@ typedef enum {
     MLA_ERR_CUDA = 4,              /* a CUDA runtime call or launch failed */
     MLA_ERR_TIMEOUT = 5,           /* device: a bounded wait gave up */
     MLA_ERR_BOUNDS = 6,            /* device: seq_len, page id or row of a chunk out of range */
-    MLA_ERR_RANGE = 7              /* device: a value outside the fp16 range, of a split partial
+    MLA_ERR_RANGE = 7,             /* device: a value outside the fp16 range, of a split partial
                                       or of what mla_attend_chunk rounds to fp16 */
+    MLA_ERR_NO_PAGES = 8           /* device: mla_update_pages had fewer free pages than a sequence needs */
 } mla_status;
 
 /* Human-readable name of a status code. Never NULL. */
@@ -528,6 +529,104 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
                             int H, int num_pages, int page_size, int max_pages_per_seq, int64_t max_tokens,
                             float softmax_scale, int form, uint16_t* out, float* lse, void* workspace,
                             size_t workspace_bytes, int32_t* err_word, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A latent cache held in 8 bits with BLOCK SCALES (Huny's Dev Blog section 6, item 4: FP8 on
+ * the latent needs per-channel or per-block scale factors). Beside the per-column cache above,
+ * whose scales have to be known before the first token, these scales follow the data as it is
+ * written: for every block of block_tokens (16, 32 or 64) tokens of a page and each of five groups of
+ * columns (four of 128 latent columns, and the 64 positional columns) one power of two,
+ *   row_s[d] = 2^(entry[group of d] - 127) * e4m3(cache8[page][s % page_size][d])
+ *   cache8  [num_pages][page_size][576] uint8 codes, as above
+ *   entries [num_pages][page_size / block_tokens][8] uint8: bytes 0..4 the five groups', 5..7 zero
+ * (576 + 8 / block_tokens bytes a token). Such a value is a bf16 number
+ * exactly, and every call on this cache gives bit for bit what its counterpart gives on a bf16 cache
+ * that holds those values. e4m3's NaN code is a NaN. Entries outside [17, 247], which mla_write_kv
+ * never writes, give unspecified values.
+ *
+ * mla_write_kv — rows of a ragged chunk (B, T, cu, seq_lens as for mla_append_chunk) quantised into
+ * their pages:
+ *   e = the smallest power >= 2^-110 with |x| <= 448 * 2^e for all finite x of the new rows in the
+ *       block's columns of the group; where the block holds older tokens of the sequence (their
+ *       positions lie before the new ones), at least its power before
+ *   code = e4m3(x / 2^e), nearest even; what is not finite becomes NaN (0x7F)
+ * and where a power grows, the codes of those older tokens are requantised to it (exact but for
+ * values that become e4m3 subnormals). |x| up to 2^126. A page that is written belongs to one sequence.
+ * Of a sequence whose length or rows are out of range nothing is written, nor are rows whose page is;
+ * the first is told by err_word. Codes and entries behind the context are left as they were.
+ *   rows [T][576] bf16: the latent and the rotated positional key, as a bf16 cache holds them.
+ *
+ * mla_append_chunk_blocks — mla_append_chunk into such a cache: the rows in bf16, as it writes them
+ * into a bf16 cache, then mla_write_kv. workspace >= mla_append_chunk_blocks_workspace_bytes.
+ *
+ * mla_read_kv_blocks, mla_decode_paged_blocks, mla_decode_paged_planned_blocks,
+ * mla_attend_chunk_blocks — their counterparts without the suffix on such a cache, with the same
+ * ordering rules, workspaces and errors. */
+mla_status mla_write_kv(const uint16_t* rows, uint8_t* cache8, uint8_t* entries, int block_tokens,
+                        const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                        int num_pages, int page_size, int max_pages_per_seq, int32_t* err_word, void* stream);
+size_t mla_append_chunk_blocks_workspace_bytes(int T, int d_model);
+mla_status mla_append_chunk_blocks(const uint16_t* h, const uint16_t* w_dkr, uint8_t* cache8, uint8_t* entries,
+                                   int block_tokens, const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* cu, int B, int T, int d_model, int num_pages, int page_size,
+                                   int max_pages_per_seq, float rope_theta, void* workspace, size_t workspace_bytes,
+                                   int32_t* err_word, void* stream);
+mla_status mla_read_kv_blocks(const uint8_t* cache8, const uint8_t* entries, int block_tokens,
+                              const int32_t* block_table, const int32_t* seq_lens, const int32_t* first,
+                              const int32_t* cu, uint16_t* rows, int B, int n_rows, int num_pages, int page_size,
+                              int max_pages_per_seq, int32_t* err_word, void* stream);
+mla_status mla_decode_paged_blocks(const uint16_t* q_abs, const uint8_t* cache8, const uint8_t* entries,
+                                   int block_tokens, const int32_t* block_table, const int32_t* seq_lens, int B,
+                                   int n_q, int H, int num_pages, int page_size, int max_pages_per_seq,
+                                   float softmax_scale, int num_splits, void* workspace, size_t workspace_bytes,
+                                   int32_t* err_word, void* stream);
+mla_status mla_decode_paged_planned_blocks(const uint16_t* q_abs, const uint8_t* cache8, const uint8_t* entries,
+                                           int block_tokens, const int32_t* block_table, int B, int n_q, int H,
+                                           int num_pages, int page_size, int max_pages_per_seq, float softmax_scale,
+                                           int num_splits, void* workspace, size_t workspace_bytes,
+                                           int32_t* err_word, void* stream);
+mla_status mla_attend_chunk_blocks(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
+                                   const uint16_t* w_uv, const uint8_t* cache8, const uint8_t* entries,
+                                   int block_tokens, const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* cu, int B, int T, int H, int num_pages, int page_size,
+                                   int max_pages_per_seq, int64_t max_tokens, float softmax_scale, int form,
+                                   uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   int32_t* err_word, void* stream);
+
+/* ------------------------------------------------------------------------
+ * mla_update_pages — block tables, the pages that sequences hold, a stack of free pages and the
+ * slots of new tokens, brought up to date on the device from the sequences' lengths (the serving
+ * loop changes only seq_lens and cu; a sequence that has finished has length 0):
+ *   need_b = ceil(seq_lens[b] / page_size)
+ *   held_b > need_b: the pages of places need_b .. held_b - 1 of its block-table row go back to the
+ *                    stack, their places become -1
+ *   held_b < need_b: places held_b .. need_b - 1 are filled with pages taken from the stack
+ *   held_b = need_b afterwards
+ *   slots[cu[b] + i] = page * page_size + pos % page_size, the row of the pool (num_pages * page_size
+ *                    rows of a cache) of new token i, at position pos = seq_lens[b] - n_b + i
+ * in the order of the sequences, and of the places in each. The stack is free_pages[0 .. *free_count - 1],
+ * its top last. The first page given back comes to lie on top, and the first page taken is the top, so that
+ * pages given back are the first to be taken, and a call with the lengths of before undoes a call
+ * exactly. Entries of free_pages past the new count are left as they were. Results do not depend on timing.
+ * A sequence is served whole or not at all: the first one whose missing pages pass what the stack and
+ * the pages given back hold, and every one behind it that misses pages, keeps what it has, its slots
+ * become -1 and MLA_ERR_NO_PAGES is reported (give pages back and call again).
+ *   block_table [B][max_pages_per_seq], held [B], free_pages [num_pages], free_count [1] int32: updated
+ *   seq_lens [B] int32; cu [B + 1] int32 and slots [n_rows] int64, both or neither (n_rows 0):
+ *               sequence b's new tokens have rows cu[b] .. cu[b+1] - 1; slots of rows at and past
+ *               cu[B] become -1 (no row of the pool), so that a padded batch writes nothing stale
+ *   workspace   >= mla_update_pages_workspace_bytes(B) bytes, no initial contents needed. Calls
+ *               sharing a workspace must not overlap on the GPU.
+ * A sequence with a length outside [n_b, max_pages_per_seq * page_size], held outside
+ * [0, max_pages_per_seq] or rows outside the array is left as it is, its slots become -1; pages outside
+ * the pool that are met are moved all the same, their slots become -1; and if there are more pages on the
+ * stack and given back than num_pages (one is there twice) nothing is moved: MLA_ERR_BOUNDS. Every
+ * input is read after the kernel before has finished. 1 <= B <= MLA_MAX_BATCH, n_rows <= 2^20. */
+size_t mla_update_pages_workspace_bytes(int B);
+mla_status mla_update_pages(int32_t* block_table, int32_t* held, const int32_t* seq_lens, int32_t* free_pages,
+                            int32_t* free_count, const int32_t* cu, int64_t* slots, int B, int n_rows, int num_pages,
+                            int page_size, int max_pages_per_seq, void* workspace, size_t workspace_bytes,
+                            int32_t* err_word, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,6 +16,14 @@ and, for a ragged chunk of new tokens (the prompt side):
   append_chunk  the chunk's cache rows written into their pages, bf16 or FP8
   attend_chunk  attention of the chunk over the paged cache
   read_kv       cache rows read back from their pages
+  write_kv      rows quantised into the pages of an 8-bit cache with block scales
+  update_pages  block tables, free pages and slot maps kept on the GPU
+
+An 8-bit cache (uint8 e4m3 codes [num_pages, page_size, 576]) comes with ``fp8_scales``, in one of two
+forms: [576] float32, one fixed scale per column; or [num_pages, page_size / block, 8] uint8, block
+scales: for each block of 16, 32 or 64 tokens of a page the powers (plus 127) of two of its five groups of
+columns (four of 128 latent columns, the 64 positional ones), in bytes 0..4. The calls that write
+such a cache (write_kv, append_chunk) find and write the powers; start with a tensor of zeros.
 """
 from __future__ import annotations
 
@@ -40,6 +48,7 @@ STATUS = {
     5: "MLA_ERR_TIMEOUT",
     6: "MLA_ERR_BOUNDS",
     7: "MLA_ERR_RANGE",
+    8: "MLA_ERR_NO_PAGES",
 }
 
 EXPORTS = [
@@ -54,6 +63,9 @@ EXPORTS = [
     "mla_copy16",
     "mla_append_chunk_workspace_bytes", "mla_append_chunk", "mla_read_kv",
     "mla_attend_chunk_workspace_bytes", "mla_attend_chunk",
+    "mla_write_kv", "mla_append_chunk_blocks_workspace_bytes", "mla_append_chunk_blocks", "mla_read_kv_blocks",
+    "mla_decode_paged_blocks", "mla_decode_paged_planned_blocks", "mla_attend_chunk_blocks",
+    "mla_update_pages_workspace_bytes", "mla_update_pages",
 ]
 
 
@@ -173,6 +185,25 @@ def _load(path: str):
     L.mla_attend_chunk.restype = i
     L.mla_attend_chunk.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i64, f, i, vp, vp, vp, sz, vp,
                                    vp]
+    L.mla_write_kv.restype = i
+    L.mla_write_kv.argtypes = [vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, vp, vp]
+    L.mla_append_chunk_blocks_workspace_bytes.restype = sz
+    L.mla_append_chunk_blocks_workspace_bytes.argtypes = [i, i]
+    L.mla_append_chunk_blocks.restype = i
+    L.mla_append_chunk_blocks.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, f, vp, sz, vp, vp]
+    L.mla_read_kv_blocks.restype = i
+    L.mla_read_kv_blocks.argtypes = [vp, vp, i, vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
+    L.mla_decode_paged_blocks.restype = i
+    L.mla_decode_paged_blocks.argtypes = [vp, vp, vp, i, vp, vp, i, i, i, i, i, i, f, i, vp, sz, vp, vp]
+    L.mla_decode_paged_planned_blocks.restype = i
+    L.mla_decode_paged_planned_blocks.argtypes = [vp, vp, vp, i, vp, i, i, i, i, i, i, f, i, vp, sz, vp, vp]
+    L.mla_attend_chunk_blocks.restype = i
+    L.mla_attend_chunk_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i64, f, i, vp, vp, vp,
+                                          sz, vp, vp]
+    L.mla_update_pages_workspace_bytes.restype = sz
+    L.mla_update_pages_workspace_bytes.argtypes = [i]
+    L.mla_update_pages.restype = i
+    L.mla_update_pages.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, vp, vp]
     return L
 
 
@@ -388,12 +419,30 @@ def quantize_fp8(rows, scales, codes=None, stream=None):
     return codes
 
 
+def _block_tokens(cache, scales):
+    """Tokens of a block of a block-scaled cache, its scales' shape checked; 0 for other scales (or none)."""
+    import torch
+    if scales is None or scales.dtype is not torch.uint8:
+        return 0
+    num_pages, page_size = cache.shape[0], cache.shape[1]
+    if scales.dim() != 3 or scales.shape[1] < 1 or page_size // scales.shape[1] not in (16, 32, 64):
+        raise ValueError(f"fp8_scales: shape {tuple(scales.shape)}, expected [num_pages, page_size / block, 8] with "
+                         "blocks of 16, 32 or 64 tokens")
+    block = page_size // scales.shape[1]
+    _tensor("fp8_scales", scales, torch.uint8, (num_pages, page_size // block, 8), cache.get_device())
+    if block * scales.shape[1] != page_size:
+        raise ValueError(f"fp8_scales: {scales.shape[1]} blocks in a page of {page_size}")
+    return block
+
+
 def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, num_splits: int | None = None,
                      softmax_scale: float = DEFAULT_SCALE, workspace=None, err_word=None, stream=None,
                      planned: bool = False):
-    """decode_paged on an FP8 cache: cache8 [num_pages, 64, 576] uint8 e4m3 codes, scales [576]
-    float32 per column. Returns (workspace, num_splits) for ``combine``."""
+    """decode_paged on an FP8 cache: cache8 [num_pages, page_size, 576] uint8 e4m3 codes, scales [576]
+    float32 per column, or block scales [num_pages, page_size / block, 8] uint8. Returns
+    (workspace, num_splits) for ``combine``."""
     import torch
+    block = _block_tokens(cache8, scales)
     B, max_pages = block_table.shape
     H = q_abs.shape[-2]
     num_pages, page_size = cache8.shape[0], cache8.shape[1]
@@ -402,10 +451,20 @@ def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, 
     if workspace is None:
         workspace = torch.empty(workspace_bytes(B, n_q, H, num_splits), dtype=torch.uint8, device=q_abs.device)
     assert cache8.dtype == torch.uint8 and cache8.is_contiguous()
-    assert scales.dtype == torch.float32 and scales.is_contiguous()
+    assert block or (scales.dtype == torch.float32 and scales.is_contiguous())
     assert block_table.dtype == torch.int32 and block_table.is_contiguous()
     nb = workspace.numel() * workspace.element_size()
-    if planned:
+    if block:
+        if not planned:
+            assert seq_lens.dtype == torch.int32 and seq_lens.is_contiguous()
+        rest = (B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale), num_splits, _ptr(workspace), nb,
+                _ptr(err_word), _stream(stream))
+        head = (_ptr(_bits(q_abs)), _ptr(cache8), _ptr(scales), block, _ptr(block_table))
+        if planned:
+            _check(lib().mla_decode_paged_planned_blocks(*head, *rest), "mla_decode_paged_planned_blocks")
+        else:
+            _check(lib().mla_decode_paged_blocks(*head, _ptr(seq_lens), *rest), "mla_decode_paged_blocks")
+    elif planned:
         st = lib().mla_decode_paged_planned_fp8(_ptr(_bits(q_abs)), _ptr(cache8), _ptr(scales), _ptr(block_table),
                                                 B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale),
                                                 num_splits, _ptr(workspace), nb, _ptr(err_word), _stream(stream))
@@ -524,7 +583,7 @@ def _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word):
         raise ValueError(f"cache: on {cache.device}, a CUDA device is needed")
     fp8 = cache.dtype is torch.uint8
     if fp8 != (fp8_scales is not None):
-        raise ValueError("an FP8 cache (uint8 codes) needs its column scales fp8_scales, a bf16 cache has none")
+        raise ValueError("an FP8 cache (uint8 codes) needs its scales fp8_scales, a bf16 cache has none")
     num_pages, page_size, _ = _dims("cache", cache, 3)
     B, max_pages = _dims("block_table", block_table, 2)
     i32 = torch.int32
@@ -535,7 +594,7 @@ def _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word):
         _tensor("block_table", block_table, i32, (B, max_pages), dev)
         _tensor("seq_lens", seq_lens, i32, (B,), dev)
         _tensor("cu", cu, i32, (B + 1,), dev)
-    if fp8:
+    if fp8 and not _block_tokens(cache, fp8_scales):
         _tensor("fp8_scales", fp8_scales, torch.float32, (D_ROW,), dev)
     if err_word is not None and (err_word.dtype is not i32 or err_word.numel() < 1 or err_word.get_device() != dev):
         raise ValueError("err_word: an int32 tensor beside the cache")
@@ -595,7 +654,8 @@ def append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, *, fp8_scales=None,
     tokens, at the end of its context (seq_lens [B] int32 already counts them). w_dkr
     [576, d_model] bf16 as for append_kv, cache [num_pages, page_size, 576] bf16, or
     uint8 e4m3 codes with their column scales fp8_scales [576] float32: the rows are
-    then quantised as they are written. Rows of h at and past cu[B] are ignored; of a
+    then quantised as they are written; or with block scales (uint8): the rows are then
+    rounded to bf16 and written as by write_kv. Rows of h at and past cu[B] are ignored; of a
     sequence whose length or rows are out of range nothing is written (err_word tells). The
     workspace (allocated when none is given) is returned for reuse.
     """
@@ -604,6 +664,17 @@ def append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, *, fp8_scales=None,
     T, d_model = _dims("h", h, 2)
     _tensor("h", h, torch.bfloat16, (T, d_model), dev)
     _tensor("w_dkr", w_dkr, torch.bfloat16, (D_ROW, d_model), dev)
+    block = _block_tokens(cache, fp8_scales)
+    if block:
+        need = int(lib().mla_append_chunk_blocks_workspace_bytes(T, d_model))
+        if need == 0:
+            raise MlaError(1, "mla_append_chunk_blocks_workspace_bytes")
+        workspace, room = _room(workspace, need, cache, stream)
+        _call("mla_append_chunk_blocks", lib().mla_append_chunk_blocks, dev, stream, h.data_ptr(), w_dkr.data_ptr(),
+              cache.data_ptr(), fp8_scales.data_ptr(), block, block_table.data_ptr(), seq_lens.data_ptr(),
+              cu.data_ptr(), B, T, d_model, num_pages, page_size, max_pages, float(rope_theta), workspace.data_ptr(),
+              room, _address(err_word))
+        return workspace
     workspace, room = _room(workspace, append_chunk_workspace_bytes(T, d_model), cache, stream)
     _call("mla_append_chunk", lib().mla_append_chunk, dev, stream, h.data_ptr(), w_dkr.data_ptr(), cache.data_ptr(),
           _address(fp8_scales), block_table.data_ptr(), seq_lens.data_ptr(), cu.data_ptr(), B, T, d_model, num_pages,
@@ -611,11 +682,89 @@ def append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, *, fp8_scales=None,
     return workspace
 
 
+def append_chunk_blocks_workspace_bytes(T: int, d_model: int) -> int:
+    n = int(lib().mla_append_chunk_blocks_workspace_bytes(T, d_model))
+    if n == 0:
+        raise MlaError(1, "mla_append_chunk_blocks_workspace_bytes")
+    return n
+
+
+def write_kv(rows, cache, block_table, seq_lens, cu, *, fp8_scales, err_word=None, stream=None):
+    """Rows of a ragged chunk of new tokens quantised into the pages of a block-scaled cache.
+
+    rows [T, 576] bf16 (latent and rotated positional key, as a bf16 cache holds them), rows cu[b] ..
+    cu[b+1]-1 being sequence b's new tokens, at the end of its context as for append_chunk; cache
+    [num_pages, page_size, 576] uint8, fp8_scales [num_pages, page_size / block, 8] uint8. A block's powers
+    are the smallest that hold its new rows, and its older tokens' where it has some; these are
+    requantised where a power grows. What is not finite is stored as NaN. Rows at and past cu[B]
+    are ignored. A page that is written belongs to one sequence.
+    """
+    import torch
+    dev, B, num_pages, page_size, max_pages = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    block = _block_tokens(cache, fp8_scales)
+    if not block:
+        raise ValueError("write_kv: fp8_scales must be block scales (uint8)")
+    T, _ = _dims("rows", rows, 2)
+    _tensor("rows", rows, torch.bfloat16, (T, D_ROW), dev)
+    _call("mla_write_kv", lib().mla_write_kv, dev, stream, rows.data_ptr(), cache.data_ptr(), fp8_scales.data_ptr(), block,
+          block_table.data_ptr(), seq_lens.data_ptr(), cu.data_ptr(), B, T, num_pages, page_size, max_pages,
+          _address(err_word))
+
+
+def update_pages_workspace_bytes(B: int) -> int:
+    n = int(lib().mla_update_pages_workspace_bytes(B))
+    if n == 0:
+        raise MlaError(1, "mla_update_pages_workspace_bytes")
+    return n
+
+
+def update_pages(block_table, held, seq_lens, free_pages, free_count, *, page_size: int = PAGE, cu=None, slots=None,
+                 workspace=None, err_word=None, stream=None):
+    """Block tables, free pages and slots brought up to date from the sequences' lengths, on the GPU.
+
+    Sequence b needs ceil(seq_lens[b] / page_size) pages. Where it holds more (held [B] int32), the pages past
+    those go back to the stack of free pages (free_pages [num_pages] int32, of which the first free_count[0]
+    are free, the last of them on top) and their places in block_table [B, max_pages] int32 become -1; where it
+    holds fewer, the missing ones are taken. held, free_count, free_pages and block_table are updated.
+    A finished sequence has length 0. With cu [B+1] int32 (rows cu[b] .. cu[b+1]-1 are sequence b's new
+    tokens, at the end of its context) and slots [n_rows] int64, slots[t] becomes the row of the pool of
+    new token t, page * page_size + offset, and -1 for rows at and past cu[B].
+
+    The order is that of the sequences and of their pages; pages given back are the first to be taken, and a
+    call with the lengths of before undoes a call. A sequence is served whole or not at all: from the first one
+    that the free pages do not suffice for, sequences that miss pages keep what they have, their slots
+    become -1, and err_word tells MLA_ERR_NO_PAGES. Returns slots.
+    """
+    import torch
+    dev, i32 = block_table.get_device(), torch.int32
+    if dev < 0:
+        raise ValueError(f"block_table: on {block_table.device}, a CUDA device is needed")
+    B, max_pages = _dims("block_table", block_table, 2)
+    (num_pages,) = _dims("free_pages", free_pages, 1)
+    if (cu is None) != (slots is None):
+        raise ValueError("cu and slots: both or neither")
+    n_rows = 0 if slots is None else _dims("slots", slots, 1)[0]
+    for name, t, shape in (("block_table", block_table, (B, max_pages)), ("held", held, (B,)),
+                           ("seq_lens", seq_lens, (B,)), ("free_pages", free_pages, (num_pages,)),
+                           ("free_count", free_count, (1,))):
+        _tensor(name, t, i32, shape, dev)
+    if slots is not None:
+        _tensor("cu", cu, i32, (B + 1,), dev)
+        _tensor("slots", slots, torch.int64, (n_rows,), dev)
+    if err_word is not None and (err_word.dtype is not i32 or err_word.numel() < 1 or err_word.get_device() != dev):
+        raise ValueError("err_word: an int32 tensor beside the block table")
+    workspace, room = _room(workspace, update_pages_workspace_bytes(B), block_table, stream)
+    _call("mla_update_pages", lib().mla_update_pages, dev, stream, block_table.data_ptr(), held.data_ptr(),
+          seq_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), _address(cu), _address(slots), B, n_rows,
+          num_pages, page_size, max_pages, workspace.data_ptr(), room, _address(err_word))
+    return slots
+
+
 def read_kv(cache, block_table, seq_lens, cu, *, n_rows: int, first=None, fp8_scales=None, out=None, err_word=None,
             stream=None):
     """Cache rows read back: row cu[b] + i of the result [n_rows, 576] bf16 is token
     first[b] + i (first [B] int32, None = 0) of sequence b, dequantised from an FP8 cache
-    (uint8 codes with fp8_scales), zeros at and past seq_lens[b]. Rows at and past cu[B]
+    (uint8 codes with fp8_scales, of columns or of blocks), zeros at and past seq_lens[b]. Rows at and past cu[B]
     are left as they were in ``out`` (undefined in a new tensor)."""
     import torch
     dev, B, num_pages, page_size, max_pages = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
@@ -625,6 +774,12 @@ def read_kv(cache, block_table, seq_lens, cu, *, n_rows: int, first=None, fp8_sc
         out = _new((n_rows, D_ROW), torch.bfloat16, cache, stream)
     else:
         _tensor("out", out, torch.bfloat16, (n_rows, D_ROW), dev)
+    block = _block_tokens(cache, fp8_scales)
+    if block:
+        _call("mla_read_kv_blocks", lib().mla_read_kv_blocks, dev, stream, cache.data_ptr(), fp8_scales.data_ptr(), block,
+              block_table.data_ptr(), seq_lens.data_ptr(), _address(first), cu.data_ptr(), out.data_ptr(), B, n_rows,
+              num_pages, page_size, max_pages, _address(err_word))
+        return out
     _call("mla_read_kv", lib().mla_read_kv, dev, stream, cache.data_ptr(), _address(fp8_scales),
           block_table.data_ptr(), seq_lens.data_ptr(), _address(first), cu.data_ptr(), out.data_ptr(), B, n_rows,
           num_pages, page_size, max_pages, _address(err_word))
@@ -683,6 +838,14 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
             with torch.cuda.device(dev):
                 need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
     workspace, room = _room(workspace, need, cache, stream)
+    block = _block_tokens(cache, fp8_scales)
+    if block:
+        _call("mla_attend_chunk_blocks", lib().mla_attend_chunk_blocks, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(),
+              w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), fp8_scales.data_ptr(), block, block_table.data_ptr(),
+              seq_lens.data_ptr(), cu.data_ptr(), B, T, H, num_pages, page_size, max_pages, max_tokens,
+              float(softmax_scale), CHUNK_FORMS[form], out.data_ptr(), _address(lse), workspace.data_ptr(), room,
+              _address(err_word))
+        return out
     _call("mla_attend_chunk", lib().mla_attend_chunk, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(),
           w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), _address(fp8_scales), block_table.data_ptr(),
           seq_lens.data_ptr(), cu.data_ptr(), B, T, H, num_pages, page_size, max_pages, max_tokens,
@@ -717,7 +880,8 @@ def decode_step(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, *, n_q
 
     ``cache`` is the bf16 cache, or the FP8 cache (uint8 e4m3 codes of the same
     shape, from ``quantize_fp8``) together with its column scales ``fp8_scales``
-    [576] float32, which the decode then reads through decode_paged_fp8.
+    [576] float32, or a block-scaled one (from ``write_kv``) with its block scales
+    (uint8), which the decode then reads through decode_paged_fp8.
     ``bufs`` may hold preallocated q_abs, workspace, u, lse, out tensors; steps
     enqueued back to back may share one workspace (the step's up-projection lets
     the next step's plan start only once the step has finished).
@@ -733,7 +897,7 @@ def decode_step(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, *, n_q
     import torch
     if cache.dtype == torch.uint8:
         if fp8_scales is None:
-            raise ValueError("an FP8 cache (uint8 codes) needs its column scales fp8_scales")
+            raise ValueError("an FP8 cache (uint8 codes) needs its scales fp8_scales")
         decode_paged_fp8(q_abs, cache, fp8_scales, block_table, seq_lens, n_q=n_q, num_splits=g,
                          softmax_scale=softmax_scale, workspace=ws, err_word=err_word, stream=stream, planned=True)
     else:
@@ -755,7 +919,7 @@ class CapturedStep:
     the next replay: the split plan is derived on the device from seq_lens
     every time. Shapes (batch, max pages per sequence, heads, n_q) and
     num_splits are fixed at construction. An FP8 cache (uint8 codes) is given with
-    its column scales ``fp8_scales``, as for ``decode_step``. Calling the object copies the new
+    its scales ``fp8_scales`` (of columns or of blocks), as for ``decode_step``. Calling the object copies the new
     queries in (from host or device tensors, asynchronously) and replays the
     graph on the current stream; the returned tensors are the step's own
     buffers, overwritten by the next call.

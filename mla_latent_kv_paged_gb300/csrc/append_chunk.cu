@@ -22,6 +22,7 @@
 // epilogue does that.
 #include <math.h>
 
+#include "blocks.cuh"
 #include "chunk.cuh"
 #include "sm100.cuh"
 
@@ -186,6 +187,7 @@ struct Args {
   int32_t* err_word;
   double theta;
   int B, T, KB, S, num_pages, page_size, max_pages;
+  bool dense;  // row t goes to row t of `cache` (the rows of a block-scaled cache, quantised after)
 };
 
 template <bool kDirect, bool kF8>
@@ -298,6 +300,7 @@ append_chunk_gemm(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     if (kDirect && t < a.T)
       to = target_of(a.cu, a.seq_lens, a.block_table, a.B, a.T, t, a.num_pages, a.page_size, a.max_pages,
                      nt == 0, a.err_word);
+    if (a.dense && to.row >= 0) to.row = t;
     bool plain = true;  // the tile's scales, see quantise16
     for (int i = lane; kDirect && kF8 && i < kN; i += 32) {
       const float v = fabsf(__ldg(a.scales + nt * kN + i));
@@ -382,8 +385,9 @@ append_chunk_finalize(Args a) {
   const uint64_t per_pos = col >= kDC ? turn_fraction(a.theta, (col - kDC) / 2) : 0;
   // the GEMM before passed its own dependency wait before this kernel could
   // start, so the lengths and tables are final; the partials are not
-  const Target to = target_of(a.cu, a.seq_lens, a.block_table, a.B, a.T, t, a.num_pages, a.page_size, a.max_pages,
-                              c == 0, a.err_word);
+  Target to = target_of(a.cu, a.seq_lens, a.block_table, a.B, a.T, t, a.num_pages, a.page_size, a.max_pages, c == 0,
+                        a.err_word);
+  if (a.dense && to.row >= 0) to.row = t;
   float sn = 0.f, cs = 1.f;
   if (col >= kDC) turn_of(per_pos, to.pos, sn, cs);
   grid_dependency_wait();
@@ -431,10 +435,15 @@ size_t append_chunk_workspace_bytes(int T, int d_model) {
   return 256 + (sh.S > 1 ? (size_t)sh.tiles * 2 * sh.S * kM * kRow * 4 : 0);
 }
 
-cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
-                                const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
-                                int d_model, int num_pages, int page_size, int max_pages, double theta,
-                                void* workspace, int32_t* err_word, cudaStream_t s) {
+size_t append_blocks_workspace_bytes(int T, int d_model) {
+  return append_chunk_workspace_bytes(T, d_model) + (size_t)T * kRow * 2;
+}
+
+namespace {
+cudaError_t launch_rows(const uint16_t* h, const uint16_t* w_dkr, void* cache, bool dense, const float* fp8_scales,
+                        const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                        int d_model, int num_pages, int page_size, int max_pages, double theta, void* workspace,
+                        int32_t* err_word, cudaStream_t s) {
   const Shape sh = shape_of(T, d_model);
   CUtensorMap mw, mh;
   const uint64_t dw[2] = {(uint64_t)d_model, (uint64_t)kRow}, dh[2] = {(uint64_t)d_model, (uint64_t)T};
@@ -458,12 +467,36 @@ cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* 
   a.num_pages = num_pages;
   a.page_size = page_size;
   a.max_pages = max_pages;
+  a.dense = dense;
   if (sh.S == 1)
     return fp8_scales ? launch_gemm<true, true>(mw, mh, sh, a, s) : launch_gemm<true, false>(mw, mh, sh, a, s);
   cudaError_t e = launch_gemm<false, false>(mw, mh, sh, a, s);
   if (e != cudaSuccess) return e;
   return fp8_scales ? launch_pdl(append_chunk_finalize<true>, dim3(T), dim3(kRow / 2), 0, s, a)
                     : launch_pdl(append_chunk_finalize<false>, dim3(T), dim3(kRow / 2), 0, s, a);
+}
+}  // namespace
+
+cudaError_t launch_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
+                                const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                                int d_model, int num_pages, int page_size, int max_pages, double theta,
+                                void* workspace, int32_t* err_word, cudaStream_t s) {
+  return launch_rows(h, w_dkr, cache, false, fp8_scales, block_table, seq_lens, cu, B, T, d_model, num_pages, page_size,
+                     max_pages, theta, workspace, err_word, s);
+}
+
+// The rows in bf16 first (a block's power needs all of its rows), then quantised.
+cudaError_t launch_append_blocks(const uint16_t* h, const uint16_t* w_dkr, uint8_t* cache, const BlockScales& scales,
+                                 const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                                 int d_model, int num_pages, int page_size, int max_pages, double theta,
+                                 void* workspace, int32_t* err_word, cudaStream_t s) {
+  // behind the partial sums (a multiple of 256 bytes)
+  uint16_t* rows =
+      reinterpret_cast<uint16_t*>(workspace_base(workspace) + append_chunk_workspace_bytes(T, d_model) - 256);
+  cudaError_t e = launch_rows(h, w_dkr, rows, true, nullptr, block_table, seq_lens, cu, B, T, d_model, num_pages,
+                              page_size, max_pages, theta, workspace, err_word, s);
+  if (e != cudaSuccess) return e;
+  return launch_write_kv(rows, cache, scales, block_table, seq_lens, cu, B, T, num_pages, page_size, max_pages, err_word, s);
 }
 
 #if MLA_DEBUG_CHECKS

@@ -44,6 +44,7 @@
 // (one thread per head row, the CTA's 32 tokens of the page). The score MMAs
 // of page g+1 run while the softmax of page g is in flight; the value MMAs
 // trail by one page.
+#include "blocks.cuh"
 #include "chunk.cuh"
 #include "mla_internal.cuh"
 #include "sm100.cuh"
@@ -111,7 +112,9 @@ enum {
   kNumBars = CVR + 1
 };
 constexpr uint32_t kOffSlots = kOffBar + kNumBars * 8;
-constexpr uint32_t kSmemBytes = kOffSlots + 16;  // the base is checked to be 1024-byte aligned
+constexpr uint32_t kOffEntries = (kOffSlots + 15) / 16 * 16 + 16;  // block scales: the tile's 8-byte entries
+constexpr uint32_t kEntryStage = kTile / 16 * kEntryBytes;         // of a ring slot (blocks of 16 tokens or more)
+constexpr uint32_t kSmemBytes = kOffEntries + kStages * kEntryStage;  // the base is checked to be 1024-byte aligned
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(2 * kQBoxBytes + kQrBoxBytes <= kStageBytes, "a ring slot holds a query quarter");
 
@@ -165,17 +168,36 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
+// Block scales: four codes as bf16 pairs times a power of two (exact). The code's exponent
+// and mantissa, moved to bf16's, stand for the value times 2^-120 (e4m3's bias is 7,
+// bf16's 127; subnormals too), which `up` = 2^(120 + e) makes good.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t up, uint32_t& lo, uint32_t& hi) {
+  const uint32_t x = __byte_perm(w, 0u, 0x1404), y = __byte_perm(w, 0u, 0x3424);  // a code in each half's upper byte
+  lo = mul_bf16x2(((x >> 4) & 0x07F007F0u) | (x & 0x80008000u), up);
+  hi = mul_bf16x2(((y >> 4) & 0x07F007F0u) | (y & 0x80008000u), up);
+}
+// 0x80 in each byte that is e4m3's NaN
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 // bf16 pair times two scales, as an fp16 pair
 __device__ __forceinline__ uint32_t scale_bf16x2_to_f16x2(uint32_t w, float s0, float s1) {
   return cvt_f16x2(bf16_lo(w) * s0, bf16_hi(w) * s1);
 }
 
+// kBlocks (with kF8): codes with a power of two for each block of tokens and group of columns
+// (blocks.cuh). The expansion to 16 bits applies the powers, which bf16 holds exactly, so
+// everything else is the bf16 cache's path.
+//
 // kRows: the sequences are rows of a chunk (chunk.cuh): seq_row[b] is the block-table
 // row of sequence b, -1 for a row of no sequence (it reads zeros and its result is
 // not used); on an FP8 cache the absorbed query comes in fp16 and scaled. A template
 // parameter, because any change to the plain kernel's code costs it a few per cent
 // (decode call 38.8 -> 39.5 us with a run-time test).
-template <bool kF8, bool kRows>
+template <bool kF8, bool kRows, bool kBlocks>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_kr,
                  const __grid_constant__ CUtensorMap map_qkr, const __grid_constant__ CUtensorMap map_q,
@@ -184,6 +206,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
                  const int32_t* __restrict__ seq_row) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
+  constexpr bool kCol = kF8 && !kBlocks;  // a scale per column, fp16 operands
+  const uint8_t* entries = reinterpret_cast<const uint8_t*>(fp8_scales);  // with kBlocks
+  const int block_shift = kBlocks ? tile_shift >> 8 : 0;                  // (the launch packs both)
+  if (kBlocks) tile_shift &= 0xFF;
   if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) report_error(err_word, MLA_ERR_CUDA);
     return;
@@ -197,7 +223,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(FULL0 + i), 1);
+      mbar_init(bar(FULL0 + i), kBlocks ? 1 + kTile / 16 : 1);  // (and the lanes that copy entries)
       mbar_init(bar(EMPTY0 + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -339,6 +365,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
               tma_load_2d(dst + m * kQBoxBytes, &map_q, fb, 256 * (int)rank + 128 * q + 64 * m, qrow, pol_keep);
             tma_load_2d(dst + 2 * kQBoxBytes, &map_qkr, fb, kDC + 32 * (int)rank, qrow + 64 * q, pol_keep);
           }
+          if (kBlocks && lane < kTile / 16) mbar_arrive(bar(FULL0 + stage));
           last_ph[stage] = (int)ph;
           __syncwarp();
           if (++stage == kStages) { stage = 0; ph ^= 1u; }
@@ -375,6 +402,18 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           tma_load_2d(dst + 4 * kCBoxBytes, &map_kr, fb, kDC + 32 * (int)rank, y, pol_stream);
         }
       }
+      if (kBlocks && lane < kTile / 16) {
+        // lane i copies block i's entry (of a page outside the pool: zeros) and arrives once it is there
+        const uint32_t fb = bar(FULL0 + stage), dst = sbase + kOffEntries + stage * kEntryStage + 8 * lane;
+        if (lane < kTile >> block_shift && MLA_SMEM_OK(dst, 8)) {
+          const int64_t y = ((int64_t)pid << tile_shift) + sub;
+          if (pid >= 0 && pid < num_pages)
+            cp_async_8(dst, entries + ((y * kTile >> block_shift) + lane) * kEntryBytes);
+          else
+            asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(dst), "r"(0u) : "memory");
+        }
+        cp_async_arrive(fb);
+      }
       last_ph[stage] = (int)ph;
       __syncwarp();
       if (++stage == kStages) { stage = 0; ph ^= 1u; }
@@ -401,8 +440,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
     // (on chunk rows an elected lane issues: 134 -> 132 us for 128 rows on 4096 tokens;
     // for the plain calls it is within 1% either way, by workload)
     if (kRows ? elect() : lane == 0) {
-      constexpr uint32_t kIdQK = kF8 ? idesc_f16(128, 64, false, false) : idesc_bf16(128, 64, false, false);
-      constexpr uint32_t kIdPV = kF8 ? idesc_f16(128, 256, false, true) : idesc_bf16(128, 256, false, true);
+      constexpr uint32_t kIdQK = kCol ? idesc_f16(128, 64, false, false) : idesc_bf16(128, 64, false, false);
+      constexpr uint32_t kIdPV = kCol ? idesc_f16(128, 256, false, true) : idesc_bf16(128, 256, false, true);
       // descriptor templates; the start address is added per use
       const uint64_t dQK_c = smem_desc(0, 16, 1024, kSwizzle128B);
       const uint64_t dQK_r = smem_desc(0, 16, 512, kSwizzle64B);
@@ -543,10 +582,38 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             a1 = base + (((2 * kk + 1) ^ ((t >> 1) & 3)) * 16);
           }
           uint32_t o[8];
-          e4m3x4_to_f16(v[k][0], o[0], o[1]);
-          e4m3x4_to_f16(v[k][1], o[2], o[3]);
-          e4m3x4_to_f16(v[k][2], o[4], o[5]);
-          e4m3x4_to_f16(v[k][3], o[6], o[7]);
+          if (kBlocks) {
+            const uint32_t t = q < 1024 ? (q >> 2) & 63 : (q - 1024) >> 1, grp = q < 1024 ? 2 * rank + (q >> 9) : 4u;
+            uint32_t p;
+            asm volatile("ld.shared.u8 %0, [%1];"
+                         : "=r"(p)
+                         : "r"(sbase + kOffEntries + st * kEntryStage + ((t >> block_shift) << 3) + grp));
+            const uint32_t up = ((min(p, 127u) + 120u) << 7) * 0x00010001u;
+            uint32_t nan = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e4m3x4_to_bf16(v[k][i], up, o[2 * i], o[2 * i + 1]);
+              nan |= nan_codes(v[k][i]);
+            }
+            if (p > 127u) {  // powers above 2^0 in two steps: 2^(120 + e) alone may pass bf16's range
+              const uint32_t more = (p << 7) * 0x00010001u;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], more);
+            }
+            if (nan) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t bad = nan_codes(v[k][i]);
+                o[2 * i] |= (bad & 0x80u ? 0x7FFFu : 0u) | (bad & 0x8000u ? 0x7FFF0000u : 0u);
+                o[2 * i + 1] |= (bad & 0x800000u ? 0x7FFFu : 0u) | (bad & 0x80000000u ? 0x7FFF0000u : 0u);
+              }
+            }
+          } else {
+            e4m3x4_to_f16(v[k][0], o[0], o[1]);
+            e4m3x4_to_f16(v[k][1], o[2], o[3]);
+            e4m3x4_to_f16(v[k][2], o[4], o[5]);
+            e4m3x4_to_f16(v[k][3], o[6], o[7]);
+          }
           if (MLA_SMEM_OK(a0, 16) && MLA_SMEM_OK(a1, 16)) {
             st_shared_v4(a0, o[0], o[1], o[2], o[3]);
             st_shared_v4(a1, o[4], o[5], o[6], o[7]);
@@ -587,7 +654,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(r[4 * c]), "=r"(r[4 * c + 1]), "=r"(r[4 * c + 2]), "=r"(r[4 * c + 3])
                            : "r"(sq + m * kQBoxBytes + ((c ^ (row & 7)) * 16)));
-            if (kF8 && !kRows) {  // the FP8 cache's column scales fold into the query (fp16)
+            if (kCol && !kRows) {  // the FP8 cache's column scales fold into the query (fp16)
               const float* sc = fp8_scales + 256 * rank + 128 * q + 64 * m;
 #pragma unroll
               for (int k = 0; k < 32; ++k) r[k] = scale_bf16x2_to_f16x2(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
@@ -603,7 +670,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(r[4 * c]), "=r"(r[4 * c + 1]), "=r"(r[4 * c + 2]), "=r"(r[4 * c + 3])
                            : "r"(sr + rl * 64 + ((c ^ ((rl >> 1) & 3)) * 16)));
-            if (kF8 && !kRows) {
+            if (kCol && !kRows) {
               const float* sc = fp8_scales + kDC + 32 * rank;
 #pragma unroll
               for (int k = 0; k < 16; ++k) r[k] = scale_bf16x2_to_f16x2(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
@@ -721,7 +788,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             for (int e = 0; e < 8; ++e) {
               f[e] = __uint_as_float(r[8 * v + e]) * inv;
               // the FP8 cache's column scale (u = s * sum p code)
-              if (kF8) f[e] *= __ldg(fp8_scales + 256 * rank + 128 * half + 32 * c + 8 * v + e);
+              if (kCol) f[e] *= __ldg(fp8_scales + 256 * rank + 128 * half + 32 * c + 8 * v + e);
               amax = fmaxf(amax, fabsf(f[e]));
             }
             if (row < H)
@@ -884,7 +951,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           for (int v = 0; v < 16; ++v) {
             const float p0 = ex2(x[2 * v] - mref);
             const float p1 = ex2(x[2 * v + 1] - mref);
-            if (kF8) {  // fp16 operands with the FP8 cache
+            if (kCol) {  // fp16 operands with the FP8 cache
               pw[v] = cvt_f16x2(p0, p1);
               const float2 f = f16x2_to_f32(pw[v]);
               lsum0 += f.x;
@@ -985,7 +1052,7 @@ int decode_max_workers() {
     const int n = known[dev].load(std::memory_order_relaxed);
     if (n > 0) return n;
   }
-  if (smem_limit<decode_tc_kernel<false, false>>(kSmemBytes) != cudaSuccess) {
+  if (smem_limit<decode_tc_kernel<false, false, false>>(kSmemBytes) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
@@ -1001,7 +1068,7 @@ int decode_max_workers() {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, decode_tc_kernel<false, false>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, decode_tc_kernel<false, false, false>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
@@ -1012,12 +1079,12 @@ int decode_max_workers() {
 namespace {
 // The query maps and the launch, shared by the bf16 and FP8 caches (the page
 // maps differ: 16-bit swizzled boxes, or unswizzled 8-bit rows).
-template <bool kF8, bool kRows>
+template <bool kF8, bool kRows, bool kBlocks>
 cudaError_t launch_decode_as(const CUtensorMap& map_c, const CUtensorMap& map_kr, const uint16_t* q_abs,
                                const float* fp8_scales, const int32_t* block_table, int B, int n_q, int H,
                                int num_pages, int page_size, int max_pages, float scale, int G, const Plan& plan,
                                int32_t* err_word,
-                               cudaStream_t s) {
+                               cudaStream_t s, int block_shift = 0) {
   CUtensorMap map_qkr, map_q;
   const uint64_t q_dims[2] = {kRow, (uint64_t)B * n_q * H};
   const uint64_t row_stride[1] = {kRow * 2};
@@ -1025,17 +1092,17 @@ cudaError_t launch_decode_as(const CUtensorMap& map_c, const CUtensorMap& map_kr
   if (!make_tmap(&map_qkr, q_abs, 2, q_dims, row_stride, box_qkr, 64) ||
       !make_tmap(&map_q, q_abs, 2, q_dims, row_stride, box_q, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = smem_limit<decode_tc_kernel<kF8, kRows>>(kSmemBytes);
+  cudaError_t e = smem_limit<decode_tc_kernel<kF8, kRows, kBlocks>>(kSmemBytes);
   if (e != cudaSuccess) return e;
   const float sl2 = scale * 1.4426950408889634f;
   dim3 grid(2 * G, n_q, 1);
-  return launch_pdl(decode_tc_kernel<kF8, kRows>, grid, dim3(kThreads), kSmemBytes, s, map_c, map_kr, map_qkr, map_q,
-                    block_table, n_q, H, max_pages, num_pages, page_size == 2 * kTile ? 1 : 0, sl2, plan,
+  return launch_pdl(decode_tc_kernel<kF8, kRows, kBlocks>, grid, dim3(kThreads), kSmemBytes, s, map_c, map_kr, map_qkr, map_q,
+                    block_table, n_q, H, max_pages, num_pages, (page_size == 2 * kTile ? 1 : 0) | block_shift << 8, sl2, plan,
                     fp8_scales, err_word, plan.seq_row);
 }
-template <bool kF8, typename... Args>
+template <bool kF8, bool kBlocks = false, typename... Args>
 cudaError_t launch_decode_impl(const Plan& plan, const Args&... args) {
-  return plan.seq_row ? launch_decode_as<kF8, true>(args...) : launch_decode_as<kF8, false>(args...);
+  return plan.seq_row ? launch_decode_as<kF8, true, kBlocks>(args...) : launch_decode_as<kF8, false, kBlocks>(args...);
 }
 }  // namespace
 
@@ -1053,17 +1120,34 @@ cudaError_t launch_decode(const uint16_t* q_abs, const uint16_t* cache, const in
                                    max_pages, scale, G, plan, err_word, s);
 }
 
+namespace {
+// unswizzled 8-bit rows of a page half
+bool code_maps(CUtensorMap* map_c, CUtensorMap* map_kr, const uint8_t* cache8, int num_pages, int page_size) {
+  const uint64_t cache_dims[2] = {kRow, (uint64_t)num_pages * page_size};
+  const uint64_t row_stride[1] = {kRow};
+  const uint32_t box_c[2] = {64, 64}, box_kr[2] = {32, 16};
+  return make_tmap(map_c, cache8, 2, cache_dims, row_stride, box_c, 0, true) &&
+         make_tmap(map_kr, cache8, 2, cache_dims, row_stride, box_kr, 0, true);
+}
+}  // namespace
+
+cudaError_t launch_decode_blocks(const uint16_t* q_abs, const uint8_t* cache8, const BlockScales& scales,
+                                 const int32_t* block_table, int B, int n_q, int H, int num_pages, int page_size,
+                                 int max_pages, float scale, int G, const Plan& plan, int32_t* err_word,
+                                 cudaStream_t s) {
+  CUtensorMap map_c, map_kr;
+  if (!code_maps(&map_c, &map_kr, cache8, num_pages, page_size)) return cudaErrorInvalidValue;
+  return launch_decode_impl<true, true>(plan, map_c, map_kr, q_abs, reinterpret_cast<const float*>(scales.entries),
+                                        block_table, B, n_q, H, num_pages, page_size, max_pages, scale, G, plan,
+                                        err_word, s, scales.shift);
+}
+
 cudaError_t launch_decode_fp8(const uint16_t* q_abs, const uint8_t* cache8, const float* fp8_scales,
                               const int32_t* block_table, int B, int n_q, int H, int num_pages, int page_size,
                               int max_pages, float scale, int G, const Plan& plan, int32_t* err_word,
                               cudaStream_t s) {
   CUtensorMap map_c, map_kr;
-  const uint64_t cache_dims[2] = {kRow, (uint64_t)num_pages * page_size};
-  const uint64_t row_stride[1] = {kRow};
-  const uint32_t box_c[2] = {64, 64}, box_kr[2] = {32, 16};
-  if (!make_tmap(&map_c, cache8, 2, cache_dims, row_stride, box_c, 0, true) ||
-      !make_tmap(&map_kr, cache8, 2, cache_dims, row_stride, box_kr, 0, true))
-    return cudaErrorInvalidValue;
+  if (!code_maps(&map_c, &map_kr, cache8, num_pages, page_size)) return cudaErrorInvalidValue;
   return launch_decode_impl<true>(plan, map_c, map_kr, q_abs, fp8_scales, block_table, B, n_q, H, num_pages, page_size,
                                   max_pages, scale, G, plan, err_word, s);
 }

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "blocks.cuh"
 #include "chunk.cuh"
 #include "mla_internal.cuh"
 
@@ -58,6 +59,7 @@ const char* mla_status_string(int status) {
     case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT";
     case MLA_ERR_BOUNDS: return "MLA_ERR_BOUNDS";
     case MLA_ERR_RANGE: return "MLA_ERR_RANGE";
+    case MLA_ERR_NO_PAGES: return "MLA_ERR_NO_PAGES";
     default: return "MLA_ERR_UNKNOWN";
   }
 }
@@ -330,6 +332,61 @@ mla_status mla_append_kv(const uint16_t* h, const uint16_t* w_dkr, uint16_t* cac
                                      (cudaStream_t)stream));
 }
 
+// ------------------------------------------------------------------ block scales
+namespace {
+// the checks of the arguments that name a block-scaled cache; fills `out` on success
+mla_status block_args(const void* cache8, const void* entries, int block_tokens, BlockScales* out) {
+  if (!cache8 || !entries || !aligned16(cache8) || !aligned16(entries)) return MLA_ERR_INVALID_ARG;
+  if (!block_tokens_ok(block_tokens)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  out->entries = static_cast<uint8_t*>(const_cast<void*>(entries));
+  out->shift = block_shift(block_tokens);
+  return MLA_OK;
+}
+}  // namespace
+
+mla_status mla_decode_paged_blocks(const uint16_t* q_abs, const uint8_t* cache8, const uint8_t* entries,
+                                   int block_tokens, const int32_t* block_table, const int32_t* seq_lens, int B,
+                                   int n_q, int H, int num_pages, int page_size, int max_pages_per_seq,
+                                   float softmax_scale, int num_splits, void* workspace, size_t workspace_bytes,
+                                   int32_t* err_word, void* stream) {
+  if (!q_abs || !block_table || !seq_lens) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_abs) || !aligned16(block_table) || !aligned16(seq_lens)) return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  BlockScales scales;
+  mla_status st = block_args(cache8, entries, block_tokens, &scales);
+  Plan plan;
+  if (st == MLA_OK)
+    st = decode_args(workspace, workspace_bytes, B, n_q, H, num_pages, page_size, max_pages_per_seq, num_splits, &plan);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (st == MLA_OK)
+    st = launch_status(launch_plan(seq_lens, block_table, B, n_q, max_pages_per_seq, page_size, num_pages, num_splits,
+                                   plan, err_word, s));
+  if (st == MLA_OK)
+    st = launch_status(launch_decode_blocks(q_abs, cache8, scales, block_table, B, n_q, H, num_pages, page_size,
+                                            max_pages_per_seq, softmax_scale, num_splits, plan, err_word, s));
+  return st;
+}
+
+mla_status mla_decode_paged_planned_blocks(const uint16_t* q_abs, const uint8_t* cache8, const uint8_t* entries,
+                                           int block_tokens, const int32_t* block_table, int B, int n_q, int H,
+                                           int num_pages, int page_size, int max_pages_per_seq, float softmax_scale,
+                                           int num_splits, void* workspace, size_t workspace_bytes,
+                                           int32_t* err_word, void* stream) {
+  if (!q_abs || !block_table) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_abs) || !aligned16(block_table)) return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  BlockScales scales;
+  mla_status st = block_args(cache8, entries, block_tokens, &scales);
+  Plan plan;
+  if (st == MLA_OK)
+    st = decode_args(workspace, workspace_bytes, B, n_q, H, num_pages, page_size, max_pages_per_seq, num_splits, &plan);
+  if (st == MLA_OK)
+    st = launch_status(launch_decode_blocks(q_abs, cache8, scales, block_table, B, n_q, H, num_pages, page_size,
+                                            max_pages_per_seq, softmax_scale, num_splits, plan, err_word,
+                                            (cudaStream_t)stream));
+  return st;
+}
+
 // ------------------------------------------------------------------ chunks of new tokens
 namespace {
 bool chunk_counts_ok(int B, int T) { return B <= MLA_MAX_BATCH && T <= kMaxChunkRows; }
@@ -368,10 +425,11 @@ size_t chunk_form_bytes(int form, int B, int T, int H, int64_t max_tokens) {
 }
 }  // namespace
 
-mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t* block_table,
-                       const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* rows, int B,
-                       int n_rows, int num_pages, int page_size, int max_pages_per_seq, int32_t* err_word,
-                       void* stream) {
+namespace {
+mla_status read_rows(const void* cache, const float* fp8_scales, const BlockScales* blocks, const int32_t* block_table,
+                     const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* rows, int B,
+                     int n_rows, int num_pages, int page_size, int max_pages_per_seq, int32_t* err_word,
+                     cudaStream_t s) {
   if (!cache || !block_table || !seq_lens || !cu || !rows) return MLA_ERR_INVALID_ARG;
   if (!aligned16(cache) || !aligned16(fp8_scales) || !aligned16(block_table) || !aligned16(seq_lens) ||
       !aligned16(first) || !aligned16(cu) || !aligned16(rows))
@@ -379,8 +437,68 @@ mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t
   if (B < 1 || n_rows < 1 || num_pages < 1 || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
   if (B > MLA_MAX_BATCH || n_rows > kMaxTokens || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
   if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (blocks)
+    return launch_status(launch_read_blocks(static_cast<const uint8_t*>(cache), *blocks, block_table, seq_lens, first,
+                                            cu, rows, B, n_rows, num_pages, page_size, max_pages_per_seq, err_word, s));
   return launch_status(launch_read_kv(cache, fp8_scales, block_table, seq_lens, first, cu, rows, B, n_rows, num_pages,
-                                      page_size, max_pages_per_seq, err_word, (cudaStream_t)stream));
+                                      page_size, max_pages_per_seq, err_word, s));
+}
+}  // namespace
+
+mla_status mla_read_kv(const void* cache, const float* fp8_scales, const int32_t* block_table,
+                       const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* rows, int B,
+                       int n_rows, int num_pages, int page_size, int max_pages_per_seq, int32_t* err_word,
+                       void* stream) {
+  return read_rows(cache, fp8_scales, nullptr, block_table, seq_lens, first, cu, rows, B, n_rows, num_pages, page_size,
+                   max_pages_per_seq, err_word, (cudaStream_t)stream);
+}
+
+mla_status mla_read_kv_blocks(const uint8_t* cache8, const uint8_t* entries, int block_tokens,
+                              const int32_t* block_table, const int32_t* seq_lens, const int32_t* first,
+                              const int32_t* cu, uint16_t* rows, int B, int n_rows, int num_pages, int page_size,
+                              int max_pages_per_seq, int32_t* err_word, void* stream) {
+  BlockScales scales;
+  const mla_status st = block_args(cache8, entries, block_tokens, &scales);
+  if (st != MLA_OK) return st;
+  return read_rows(cache8, nullptr, &scales, block_table, seq_lens, first, cu, rows, B, n_rows, num_pages, page_size,
+                   max_pages_per_seq, err_word, (cudaStream_t)stream);
+}
+
+mla_status mla_write_kv(const uint16_t* rows, uint8_t* cache8, uint8_t* entries, int block_tokens,
+                        const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                        int num_pages, int page_size, int max_pages_per_seq, int32_t* err_word, void* stream) {
+  if (!rows || !block_table || !seq_lens || !cu) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(rows) || !aligned16(block_table) || !aligned16(seq_lens) || !aligned16(cu)) return MLA_ERR_INVALID_ARG;
+  BlockScales scales;
+  const mla_status st = block_args(cache8, entries, block_tokens, &scales);
+  if (st != MLA_OK) return st;
+  if (B < 1 || T < 1 || num_pages < 1 || max_pages_per_seq < 1) return MLA_ERR_INVALID_ARG;
+  if (!chunk_counts_ok(B, T) || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  return launch_status(launch_write_kv(rows, cache8, scales, block_table, seq_lens, cu, B, T, num_pages, page_size,
+                                       max_pages_per_seq, err_word, (cudaStream_t)stream));
+}
+
+size_t mla_update_pages_workspace_bytes(int B) {
+  return B < 1 || B > MLA_MAX_BATCH ? 0 : update_pages_workspace_bytes(B);
+}
+
+mla_status mla_update_pages(int32_t* block_table, int32_t* held, const int32_t* seq_lens, int32_t* free_pages,
+                            int32_t* free_count, const int32_t* cu, int64_t* slots, int B, int n_rows, int num_pages,
+                            int page_size, int max_pages_per_seq, void* workspace, size_t workspace_bytes,
+                            int32_t* err_word, void* stream) {
+  if (!block_table || !held || !seq_lens || !free_pages || !free_count || !workspace) return MLA_ERR_INVALID_ARG;
+  if (!aligned16(block_table) || !aligned16(held) || !aligned16(seq_lens) || !aligned16(free_pages) ||
+      !aligned16(free_count) || !aligned16(cu) || !aligned16(slots) || !aligned16(workspace))
+    return MLA_ERR_INVALID_ARG;
+  if ((cu == nullptr) != (slots == nullptr)) return MLA_ERR_INVALID_ARG;
+  if (B < 1 || num_pages < 1 || max_pages_per_seq < 1 || n_rows < (slots ? 1 : 0)) return MLA_ERR_INVALID_ARG;
+  if (!chunk_counts_ok(B, n_rows) || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
+  if (workspace_bytes < update_pages_workspace_bytes(B)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  Pages p = {block_table, held, seq_lens, free_pages, free_count, cu, slots, B, slots ? n_rows : 0, num_pages, page_size,
+             max_pages_per_seq};
+  return launch_status(launch_update_pages(p, workspace, err_word, (cudaStream_t)stream));
 }
 
 size_t mla_append_chunk_workspace_bytes(int T, int d_model) {
@@ -388,10 +506,16 @@ size_t mla_append_chunk_workspace_bytes(int T, int d_model) {
   return append_chunk_workspace_bytes(T, d_model);
 }
 
-mla_status mla_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
-                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
-                            int d_model, int num_pages, int page_size, int max_pages_per_seq, float rope_theta,
-                            void* workspace, size_t workspace_bytes, int32_t* err_word, void* stream) {
+size_t mla_append_chunk_blocks_workspace_bytes(int T, int d_model) {
+  return mla_append_chunk_workspace_bytes(T, d_model) == 0 ? 0 : append_blocks_workspace_bytes(T, d_model);
+}
+
+namespace {
+mla_status append_rows(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
+                       const BlockScales* blocks, const int32_t* block_table, const int32_t* seq_lens,
+                       const int32_t* cu, int B, int T, int d_model, int num_pages, int page_size,
+                       int max_pages_per_seq, float rope_theta, void* workspace, size_t workspace_bytes,
+                       int32_t* err_word, cudaStream_t s) {
   if (!h || !w_dkr || !cache || !block_table || !seq_lens || !cu || !workspace) return MLA_ERR_INVALID_ARG;
   if (!aligned16(h) || !aligned16(w_dkr) || !aligned16(cache) || !aligned16(fp8_scales) || !aligned16(block_table) ||
       !aligned16(seq_lens) || !aligned16(cu) || !aligned16(workspace))
@@ -401,10 +525,37 @@ mla_status mla_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cach
   if (!chunk_counts_ok(B, T) || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
   if (d_model < 64 || d_model % 64 != 0 || d_model > 65536) return MLA_ERR_UNSUPPORTED_SHAPE;
   if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
-  if (workspace_bytes < append_chunk_workspace_bytes(T, d_model)) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < (blocks ? append_blocks_workspace_bytes(T, d_model) : append_chunk_workspace_bytes(T, d_model)))
+    return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (blocks)
+    return launch_status(launch_append_blocks(h, w_dkr, static_cast<uint8_t*>(cache), *blocks, block_table, seq_lens,
+                                              cu, B, T, d_model, num_pages, page_size, max_pages_per_seq,
+                                              (double)rope_theta, workspace, err_word, s));
   return launch_status(launch_append_chunk(h, w_dkr, cache, fp8_scales, block_table, seq_lens, cu, B, T, d_model,
                                            num_pages, page_size, max_pages_per_seq, (double)rope_theta, workspace,
-                                           err_word, (cudaStream_t)stream));
+                                           err_word, s));
+}
+}  // namespace
+
+mla_status mla_append_chunk(const uint16_t* h, const uint16_t* w_dkr, void* cache, const float* fp8_scales,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                            int d_model, int num_pages, int page_size, int max_pages_per_seq, float rope_theta,
+                            void* workspace, size_t workspace_bytes, int32_t* err_word, void* stream) {
+  return append_rows(h, w_dkr, cache, fp8_scales, nullptr, block_table, seq_lens, cu, B, T, d_model, num_pages,
+                     page_size, max_pages_per_seq, rope_theta, workspace, workspace_bytes, err_word,
+                     (cudaStream_t)stream);
+}
+
+mla_status mla_append_chunk_blocks(const uint16_t* h, const uint16_t* w_dkr, uint8_t* cache8, uint8_t* entries,
+                                   int block_tokens, const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* cu, int B, int T, int d_model, int num_pages, int page_size,
+                                   int max_pages_per_seq, float rope_theta, void* workspace, size_t workspace_bytes,
+                                   int32_t* err_word, void* stream) {
+  BlockScales scales;
+  const mla_status st = block_args(cache8, entries, block_tokens, &scales);
+  if (st != MLA_OK) return st;
+  return append_rows(h, w_dkr, cache8, nullptr, &scales, block_table, seq_lens, cu, B, T, d_model, num_pages, page_size,
+                     max_pages_per_seq, rope_theta, workspace, workspace_bytes, err_word, (cudaStream_t)stream);
 }
 
 size_t mla_attend_chunk_workspace_bytes(int B, int T, int H, int64_t max_tokens, int form) {
@@ -417,12 +568,13 @@ size_t mla_attend_chunk_workspace_bytes(int B, int T, int H, int64_t max_tokens,
   return a == 0 || b == 0 ? 0 : a > b ? a : b;
 }
 
-mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
-                            const uint16_t* w_uv, const void* cache, const float* fp8_scales,
-                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
-                            int H, int num_pages, int page_size, int max_pages_per_seq, int64_t max_tokens,
-                            float softmax_scale, int form, uint16_t* out, float* lse, void* workspace,
-                            size_t workspace_bytes, int32_t* err_word, void* stream) {
+namespace {
+mla_status attend_rows(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk, const uint16_t* w_uv,
+                       const void* cache, const float* fp8_scales, const BlockScales* blocks,
+                       const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T, int H,
+                       int num_pages, int page_size, int max_pages_per_seq, int64_t max_tokens, float softmax_scale,
+                       int form, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                       int32_t* err_word, cudaStream_t s) {
   if (!q_nope || !q_rope || !w_uk || !w_uv || !cache || !block_table || !seq_lens || !cu || !out || !workspace)
     return MLA_ERR_INVALID_ARG;
   if (!aligned16(q_nope) || !aligned16(q_rope) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(cache) ||
@@ -436,7 +588,6 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
     return MLA_ERR_UNSUPPORTED_SHAPE;
   if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
   const int max_tokens_seq = max_pages_per_seq * page_size;
-  cudaStream_t s = (cudaStream_t)stream;
   form = chunk_form(form, B, T, H, max_tokens, fp8_scales != nullptr);
   if (form == MLA_CHUNK_ABSORBED) {
     if (T > MLA_MAX_BATCH) return MLA_ERR_UNSUPPORTED_SHAPE;
@@ -454,7 +605,10 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
                                                    G, plan, r, w_uv, err_word, s));
     if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s, r.hdr, fp8_scales, err_word));
     if (st == MLA_OK)
-      st = launch_status(fp8_scales ? launch_decode_fp8(r.q_abs, static_cast<const uint8_t*>(cache), fp8_scales,
+      st = launch_status(blocks ? launch_decode_blocks(r.q_abs, static_cast<const uint8_t*>(cache), *blocks, block_table,
+                                                       T, 1, H, num_pages, page_size, max_pages_per_seq,
+                                                       softmax_scale, G, plan, err_word, s)
+                         : fp8_scales ? launch_decode_fp8(r.q_abs, static_cast<const uint8_t*>(cache), fp8_scales,
                                                         block_table, T, 1, H, num_pages, page_size,
                                                         max_pages_per_seq, softmax_scale, G, plan, err_word, s)
                                     : launch_decode(r.q_abs, static_cast<const uint16_t*>(cache), block_table, T, 1,
@@ -479,6 +633,11 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
     if (st == MLA_OK) st = launch_status(launch_weights_f16(w_uk, w_uv, plan.w16, H, err_word, s));
     w_uk = plan.w16;
     w_uv = plan.w16 + (size_t)H * kDNope * kDC;
+  } else if (st == MLA_OK && blocks) {
+    // (bf16 holds a code times a power of two exactly)
+    st = launch_status(launch_read_blocks(static_cast<const uint8_t*>(cache), *blocks, block_table, plan.len_eff, nullptr,
+                                          plan.pstart, plan.rows, B, (int)cap, num_pages, page_size,
+                                          max_pages_per_seq, err_word, s));
   } else if (st == MLA_OK) {
     st = launch_status(launch_read_kv(cache, nullptr, block_table, plan.len_eff, nullptr, plan.pstart, plan.rows, B,
                                       (int)cap, num_pages, page_size, max_pages_per_seq, err_word, s));
@@ -491,6 +650,33 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
                                        softmax_scale, f16, err_word, s));
   }
   return st;
+}
+}  // namespace
+
+mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
+                            const uint16_t* w_uv, const void* cache, const float* fp8_scales,
+                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
+                            int H, int num_pages, int page_size, int max_pages_per_seq, int64_t max_tokens,
+                            float softmax_scale, int form, uint16_t* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* err_word, void* stream) {
+  return attend_rows(q_nope, q_rope, w_uk, w_uv, cache, fp8_scales, nullptr, block_table, seq_lens, cu, B, T, H,
+                     num_pages, page_size, max_pages_per_seq, max_tokens, softmax_scale, form, out, lse, workspace,
+                     workspace_bytes, err_word, (cudaStream_t)stream);
+}
+
+mla_status mla_attend_chunk_blocks(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
+                                   const uint16_t* w_uv, const uint8_t* cache8, const uint8_t* entries,
+                                   int block_tokens, const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* cu, int B, int T, int H, int num_pages, int page_size,
+                                   int max_pages_per_seq, int64_t max_tokens, float softmax_scale, int form,
+                                   uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   int32_t* err_word, void* stream) {
+  BlockScales scales;
+  const mla_status st = block_args(cache8, entries, block_tokens, &scales);
+  if (st != MLA_OK) return st;
+  return attend_rows(q_nope, q_rope, w_uk, w_uv, cache8, nullptr, &scales, block_table, seq_lens, cu, B, T, H, num_pages,
+                     page_size, max_pages_per_seq, max_tokens, softmax_scale, form, out, lse, workspace,
+                     workspace_bytes, err_word, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 // Rows of the sequences read back from their pages into one bf16 array: row
 // cu[b] + i is token first[b] + i of sequence b (zeros at and past the context's
-// end), an FP8 row as bf16(scales[d] * e4m3(code)).
+// end), an FP8 row as bf16(scales[d] * e4m3(code)), a row of a block-scaled cache as
+// code * 2^power (exact in bf16).
 //
 // A copy: HBM-bound, each cached byte read once and each output byte written
 // once. One thread owns one 8-value column group of every fourth row of its
@@ -10,6 +11,7 @@
 // source of each of its rows (search in cu, one block-table entry).
 // 4 x 131072 rows of a bf16 cache: 176 us, 6.86 TB/s, the measured copy rate; a few
 // hundred rows: 3.2 us, the latency of one launch and three dependent reads.
+#include "blocks.cuh"
 #include "chunk.cuh"
 #include "sm100.cuh"
 
@@ -21,13 +23,14 @@ constexpr int kRowsAtOnce = 4;
 constexpr int kThreads = kGroups * kRowsAtOnce;  // 288
 constexpr int kInFlight = 8;
 
-// kF16: fp16 rows instead of bf16 (the workspace of attend_chunk)
-template <bool kF8, bool kF16, int kRows>
+// kF16: fp16 rows instead of bf16 (the workspace of attend_chunk). kBlocks: codes with an
+// 8-byte entry of powers for each block of 1 << shift rows (blocks.cuh) in place of scales.
+template <bool kF8, bool kF16, bool kBlocks, int kRows>
 __global__ void __launch_bounds__(kThreads)
 read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales, const int32_t* __restrict__ block_table,
                const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ first, const int32_t* __restrict__ cu,
                uint4* __restrict__ out, int B, int n_rows, int num_pages, int page_size, int max_pages,
-               int32_t* err_word) {
+               int32_t* err_word, const uint8_t* __restrict__ entries, int shift) {
   __shared__ int64_t src[kRows];  // row of the pool; -1 zeros, -2 not a sequence's row
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
@@ -55,7 +58,7 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
   if (blockIdx.x == 0) report_rows(cu, B, n_rows, threadIdx.x, kThreads, err_word);
   const int g = threadIdx.x % kGroups, r0 = threadIdx.x / kGroups;
   float sc[8];
-  if (kF8) {
+  if (kF8 && !kBlocks) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) sc[i] = __ldg(scales + 8 * g + i);
   }
@@ -71,6 +74,7 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
       const int64_t s = src[(k0 + k) * kRowsAtOnce + r0];
       v[k] = make_uint4(0, 0, 0, 0);
       if (s >= 0) {
+        if (kBlocks) v[k].z = __ldg(entries + ((s >> shift) << 3) + (g < 64 ? g >> 4 : 4));
         if (kF8) {
           const uint2 c = __ldg(static_cast<const uint2*>(cache) + s * kGroups + g);
           v[k].x = c.x;
@@ -98,7 +102,8 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float2 x = sm100::f16x2_to_f32(f[q]);
-          const float a = x.x * sc[2 * q], b = x.y * sc[2 * q + 1];
+          const float s0 = kBlocks ? step_of(v[k].z) : sc[2 * q], s1 = kBlocks ? s0 : sc[2 * q + 1];
+          const float a = x.x * s0, b = x.y * s1;
           p[q] = kF16 ? sm100::cvt_f16x2(a, b) : sm100::cvt_bf16x2(a, b);
           if (kF16 && src[i] >= 0) top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));
         }
@@ -125,13 +130,14 @@ weights_f16_kernel(const uint4* __restrict__ w_uk, const uint4* __restrict__ w_u
   if (top >= kF16Limit && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
 }
 
-template <bool kF8, bool kF16, int kRows>
+template <bool kF8, bool kF16, bool kBlocks, int kRows>
 cudaError_t launch(const void* cache, const float* scales, const int32_t* block_table, const int32_t* seq_lens,
                    const int32_t* first, const int32_t* cu, uint16_t* out, int B, int n_rows, int num_pages,
-                   int page_size, int max_pages, int32_t* err_word, cudaStream_t s) {
-  return launch_pdl(read_kv_kernel<kF8, kF16, kRows>, dim3((n_rows + kRows - 1) / kRows), dim3(kThreads), 0, s, cache,
+                   int page_size, int max_pages, int32_t* err_word, cudaStream_t s,
+                   const BlockScales& blocks = BlockScales{nullptr, 0}) {
+  return launch_pdl(read_kv_kernel<kF8, kF16, kBlocks, kRows>, dim3((n_rows + kRows - 1) / kRows), dim3(kThreads), 0, s, cache,
                     scales, block_table, seq_lens, first, cu, reinterpret_cast<uint4*>(out), B, n_rows, num_pages,
-                    page_size, max_pages, err_word);
+                    page_size, max_pages, err_word, static_cast<const uint8_t*>(blocks.entries), blocks.shift);
 }
 
 }  // namespace
@@ -140,16 +146,24 @@ cudaError_t launch_read_kv(const void* cache, const float* fp8_scales, const int
                            const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* out, int B,
                            int n_rows, int num_pages, int page_size, int max_pages, int32_t* err_word,
                            cudaStream_t s) {
-  return fp8_scales ? launch<true, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows, num_pages,
+  return fp8_scales ? launch<true, false, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows, num_pages,
                                        page_size, max_pages, err_word, s)
-                    : launch<false, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows,
+                    : launch<false, false, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows,
                                         num_pages, page_size, max_pages, err_word, s);
+}
+
+cudaError_t launch_read_blocks(const uint8_t* cache, const BlockScales& scales, const int32_t* block_table,
+                               const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* out, int B,
+                               int n_rows, int num_pages, int page_size, int max_pages, int32_t* err_word,
+                               cudaStream_t s) {
+  return launch<true, false, true, 32>(cache, nullptr, block_table, seq_lens, first, cu, out, B, n_rows, num_pages,
+                                       page_size, max_pages, err_word, s, scales);
 }
 
 cudaError_t launch_rows_f16(const void* cache8, const float* fp8_scales, const int32_t* block_table,
                             const int32_t* seq_lens, const int32_t* cu, uint16_t* out, int B, int n_rows,
                             int num_pages, int page_size, int max_pages, int32_t* err_word, cudaStream_t s) {
-  return launch<true, true, 32>(cache8, fp8_scales, block_table, seq_lens, nullptr, cu, out, B, n_rows, num_pages,
+  return launch<true, true, false, 32>(cache8, fp8_scales, block_table, seq_lens, nullptr, cu, out, B, n_rows, num_pages,
                                 page_size, max_pages, err_word, s);
 }
 

@@ -1,0 +1,287 @@
+// Block tables, the pages that sequences hold, a stack of free pages and the slots of
+// new tokens, brought up to date from the sequences' lengths on the GPU:
+//   need_b = ceil(lens_b / page_size); where held_b is larger the pages past need_b
+//   go back to the stack, where it is smaller the missing ones are taken from it;
+//   slots[cu_b + i] = table_b[pos / page_size] * page_size + pos % page_size,
+//   pos = lens_b - n_b + i.
+// Pages given back are numbered q = 0 .. R - 1 and pages taken k = 0 .. K - 1, both in
+// order of the sequences and of the pages in each. The given back lie on the stack of F
+// free pages with q = 0 on top (q at F + R - 1 - q), and k takes from the top: k < R is
+// q = k, then the stack's own, k at F - 1 - (k - R). So a step and the step back leave
+// stack and tables as they were, and the result does not depend on timing. Sequences
+// are served whole and in order: one whose pages would pass F + R gets none, nor
+// does one behind it.
+//
+// Latency-bound: a step of a few hundred sequences moves some kilobytes. One block
+// counts and scans (three running sums over the sequences), then the pages are dealt out
+// to groups of eight lanes, a page with the slots in it to a group; no two groups
+// touch one entry: a page that goes from one sequence to another in the same call is
+// read and cleared by the group that takes it. While the slots are few the scanning
+// block does that work itself (one launch); else a grid does, after it.
+#include "blocks.cuh"
+#include "chunk.cuh"
+
+namespace mla {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kPerThread = MLA_MAX_BATCH / kThreads;
+constexpr int kLanes = 8;  // of a page
+constexpr int kGridThreads = 256;
+// One launch up to these sizes (see the file's head).
+constexpr int kSmallRows = 4096, kSmallBatch = 1024;
+
+struct Sequence {  // one read of what a page's group needs
+  int32_t page0;   // its first page
+  int32_t held;    // pages held before
+  int32_t need;    // ... and after
+  int32_t row0;    // row of its first new token
+  int32_t pos0;    // ... and its position
+  int32_t end;     // the context's length; its new tokens are pos0 .. end - 1
+  int32_t refused;
+  int32_t unused;
+};
+struct Work {
+  int32_t* give;   // [B + 1] pages given back by the sequences before
+  int32_t* take;   // [B + 1] pages taken by those before
+  int32_t* unit;   // [B + 1] pages worked on for those before
+  Sequence* seq;   // [B]
+  int32_t* total;  // [4] free pages before, given back, taken, units
+};
+size_t work_layout(void* base, int B, Work* w) {
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = off;
+    off = align256(off + bytes);
+    return o;
+  };
+  const size_t og = take((size_t)(B + 1) * 4), ot = take((size_t)(B + 1) * 4), ou = take((size_t)(B + 1) * 4);
+  const size_t os = take((size_t)B * sizeof(Sequence)), on = take(16);
+  if (base && w) {
+    char* c = workspace_base(base);
+    w->give = reinterpret_cast<int32_t*>(c + og);
+    w->take = reinterpret_cast<int32_t*>(c + ot);
+    w->unit = reinterpret_cast<int32_t*>(c + ou);
+    w->seq = reinterpret_cast<Sequence*>(c + os);
+    w->total = reinterpret_cast<int32_t*>(c + on);
+  }
+  return off + 256;
+}
+
+// the last i in [0, n) with sum[i] <= x (sum[0] = 0 <= x)
+__device__ __forceinline__ int last_at(const int32_t* sum, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sum[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The pages, each by one group of lanes; then the pages given back and not taken, each
+// by a thread; then the rows behind the last sequence.
+__device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, int thread, int threads, int32_t* err_word) {
+  const int F = w.total[0], R = w.total[1], K = w.total[2], units = w.total[3];
+  const int lane = thread % kLanes;
+  bool bad = false;
+  for (int i = thread / kLanes; i < units; i += threads / kLanes) {
+    const int b = last_at(w.unit, p.B, i);
+    const Sequence s = w.seq[b];
+    const int pi = s.page0 + i - w.unit[b];
+    int32_t* place = p.block_table + (int64_t)b * p.max_pages + pi;
+    int page = -1;
+    if (pi < s.held) {
+      page = *place;
+    } else if (pi < s.need) {
+      const int k = w.take[b] + pi - s.held;
+      if (k < R) {
+        const int from = last_at(w.give, p.B, k);
+        int32_t* old = p.block_table + (int64_t)from * p.max_pages + w.seq[from].need + k - w.give[from];
+        page = *old;
+        __syncwarp(0xFFu << ((threadIdx.x & 31) & ~(kLanes - 1)));  // every lane has read it
+        if (lane == 0) *old = -1;
+      } else {
+        page = p.free_pages[F - 1 - (k - R)];
+      }
+      if (lane == 0) *place = page;
+    }
+    const bool good = page >= 0 && page < p.num_pages && !s.refused;
+    bad |= !good && !s.refused;
+    const int a = max(s.pos0, pi * p.page_size), e = min(s.end, (pi + 1) * p.page_size);
+    for (int pos = a + lane; pos < e; pos += kLanes)
+      p.slots[s.row0 + pos - s.pos0] = good ? (int64_t)page * p.page_size + (pos - pi * p.page_size) : -1;
+  }
+  for (int q = K + thread; q < R; q += threads) {
+    const int b = last_at(w.give, p.B, q);
+    int32_t* old = p.block_table + (int64_t)b * p.max_pages + w.seq[b].need + q - w.give[b];
+    const int page = *old;
+    bad |= page < 0 || page >= p.num_pages;
+    p.free_pages[F + R - 1 - q] = page;
+    *old = -1;
+  }
+  if (p.slots)
+    for (int t = max(p.cu[p.B], 0) + thread; t < p.n_rows; t += threads) p.slots[t] = -1;
+  if (bad) report_error(err_word, MLA_ERR_BOUNDS);
+}
+
+// Exclusive sums over the block's threads of one value each; the total in *all.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* shared, int64_t* all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) shared[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t y = shared[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t z = __shfl_up_sync(0xffffffffu, y, d);
+      if (lane >= d) y += z;
+    }
+    shared[lane] = y;
+  }
+  __syncthreads();
+  const int64_t r = x - v + (warp > 0 ? shared[warp - 1] : 0);
+  *all = shared[31];
+  __syncthreads();
+  return r;
+}
+
+template <bool kAll>
+__global__ void __launch_bounds__(kThreads)
+update_pages_scan(Pages p, Work w, int32_t* err_word) {
+  __shared__ int64_t sums[32];
+  __shared__ int served;  // pages taken in all
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
+  const int tid = threadIdx.x, per = (p.B + kThreads - 1) / kThreads, b0 = tid * per;
+  const int max_tokens = p.max_pages * p.page_size;
+  if (tid == 0) served = 0;
+  bool bad = false;
+  Sequence s[kPerThread];
+  int64_t give = 0, take = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int b = b0 + i;
+    if (i >= per || b >= p.B) continue;
+    const int L = p.lens[b], h = p.held[b];
+    int c0 = 0, n = 0;
+    bool ok = L >= 0 && L <= max_tokens && h >= 0 && h <= p.max_pages;
+    if (p.slots) {
+      const int a = p.cu[b], e = p.cu[b + 1];
+      c0 = min(max(a, 0), p.n_rows);
+      n = min(max(e, c0), p.n_rows) - c0;
+      ok = ok && a == c0 && e == c0 + n && (b > 0 || a == 0);
+    }
+    ok = ok && n <= L;
+    bad |= !ok;
+    s[i].held = ok ? h : 0;  // a sequence whose numbers are out of range is left as it is
+    s[i].need = ok ? (L + p.page_size - 1) / p.page_size : 0;
+    s[i].row0 = c0;
+    s[i].end = ok ? L : n;
+    s[i].pos0 = s[i].end - n;
+    s[i].refused = !ok;
+    if (ok) {
+      give += max(s[i].held - s[i].need, 0);
+      take += max(s[i].need - s[i].held, 0);
+    }
+  }
+  int64_t all_give, all_take;
+  int64_t g = block_scan(give, sums, &all_give), k = block_scan(take, sums, &all_take);
+  int F = *p.free_count;
+  if (F < 0 || F > p.num_pages) {
+    bad = true;
+    F = min(max(F, 0), p.num_pages);
+  }
+  // more pages than there are: some are held or free twice, and nothing is moved
+  const bool broken = F + all_give > p.num_pages;
+  bad |= broken;
+  const int R = broken ? 0 : (int)all_give;
+  const int64_t room = broken ? 0 : (int64_t)F + R;
+  int64_t units = 0;
+  bool short_of = false;
+  int gives[kPerThread], takes[kPerThread], count[kPerThread], most = 0;
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int b = b0 + i;
+    if (i >= per || b >= p.B) continue;
+    const int back = max(s[i].held - s[i].need, 0), more = max(s[i].need - s[i].held, 0);
+    const bool valid = !s[i].refused;
+    gives[i] = broken ? 0 : (int)g;
+    takes[i] = (int)min(k, room);
+    g += back;
+    k += more;
+    bool refused = !valid || broken;
+    if (valid && more > 0 && k > room) {
+      refused = true;
+      short_of |= !broken;
+    }
+    if (valid && more > 0 && !refused) most = (int)k;
+    const int held = s[i].held;
+    if (refused) s[i].need = s[i].held;
+    s[i].refused = refused;
+    const int n = s[i].end - s[i].pos0, first = n > 0 ? s[i].pos0 / p.page_size : INT32_MAX;
+    int u0 = first, u1 = n > 0 ? (s[i].end + p.page_size - 1) / p.page_size : 0;
+    if (!refused && more > 0) {
+      u0 = min(u0, held);
+      u1 = max(u1, s[i].need);
+    }
+    s[i].page0 = u0;
+    count[i] = max(u1 - u0, 0);
+    units += count[i];
+    if (valid && !refused && s[i].need != held) p.held[b] = s[i].need;
+  }
+  if (most > 0) atomicMax(&served, most);
+  int64_t all_units;
+  int64_t u = block_scan(units, sums, &all_units);
+#pragma unroll
+  for (int i = 0; i < kPerThread; ++i) {
+    const int b = b0 + i;
+    if (i >= per || b >= p.B) continue;
+    w.give[b] = gives[i];
+    w.take[b] = takes[i];
+    w.unit[b] = (int)u;
+    w.seq[b] = s[i];
+    u += count[i];
+  }
+  if (tid == 0) {
+    w.total[0] = F;
+    w.total[1] = R;
+    w.total[2] = served;
+    w.total[3] = (int)all_units;
+    if (R != served) *p.free_count = F + R - served;
+  }
+  if (short_of) report_error(err_word, MLA_ERR_NO_PAGES);
+  else if (bad) report_error(err_word, MLA_ERR_BOUNDS);
+  if (kAll) {
+    __syncthreads();
+    deal_pages(p, w, tid, kThreads, err_word);
+  }
+}
+
+__global__ void __launch_bounds__(kGridThreads)
+update_pages_deal(Pages p, Work w, int32_t* err_word) {
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
+  deal_pages(p, w, blockIdx.x * kGridThreads + threadIdx.x, gridDim.x * kGridThreads, err_word);
+}
+
+}  // namespace
+
+size_t update_pages_workspace_bytes(int B) { return work_layout(nullptr, B, nullptr); }
+
+cudaError_t launch_update_pages(const Pages& p, void* workspace, int32_t* err_word, cudaStream_t s) {
+  Work w;
+  work_layout(workspace, p.B, &w);
+  if (p.n_rows <= kSmallRows && p.B <= kSmallBatch)
+    return launch_pdl(update_pages_scan<true>, dim3(1), dim3(kThreads), 0, s, p, w, err_word);
+  cudaError_t e = launch_pdl(update_pages_scan<false>, dim3(1), dim3(kThreads), 0, s, p, w, err_word);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(update_pages_deal, dim3(2 * 152), dim3(kGridThreads), 0, s, p, w, err_word);
+}
+
+}  // namespace mla
