@@ -603,7 +603,8 @@ mla_status attend_rows(const uint16_t* q_nope, const uint16_t* q_rope, const uin
     plan.seq_row = r.seq_row;
     mla_status st = launch_status(launch_rows_plan(seq_lens, cu, B, T, H, max_pages_per_seq, page_size, num_pages,
                                                    G, plan, r, w_uv, err_word, s));
-    if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s, r.hdr, fp8_scales, err_word));
+    if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s, r.hdr, fp8_scales, err_word,
+                                                          fp8_scales || blocks));
     if (st == MLA_OK)
       st = launch_status(blocks ? launch_decode_blocks(r.q_abs, static_cast<const uint8_t*>(cache), *blocks, block_table,
                                                        T, 1, H, num_pages, page_size, max_pages_per_seq,

@@ -171,11 +171,11 @@ int decode_max_workers();
 // only, and u is fp16
 cudaError_t launch_combine(const Plan& plan, int B, int n_q, int H, uint16_t* u, float* lse,
                            cudaStream_t s, const int32_t* rows_live = nullptr);
-// col_scales (device, may be null): a chunk's rows on an FP8 cache, q_abs in fp16 and
+// f16: a chunk's rows on an FP8 cache, q_abs in fp16, with col_scales (device, may be null)
 // scaled by column; of rows < *rows_live a value outside fp16 is reported
 cudaError_t launch_absorb_q(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
                             uint16_t* q_abs, int T, int H, cudaStream_t s, const int32_t* rows_live = nullptr,
-                            const float* col_scales = nullptr, int32_t* err_word = nullptr);
+                            const float* col_scales = nullptr, int32_t* err_word = nullptr, bool f16 = false);
 // rows_live (device, may be null): a chunk's rows; only rows t < *rows_live are written,
 // and u and w_uv are fp16
 cudaError_t launch_out_proj(const uint16_t* u, const uint16_t* w_uv, uint16_t* out, int T, int H,

@@ -175,11 +175,13 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         const int t = i / (kDR / 8), v = i % (kDR / 8);
         uint4 w = reinterpret_cast<const uint4*>(q_rope + ((size_t)t * H + h) * kDR)[v];
         if (kScaled) {
-          const float* sc = col_scales + kDC + 8 * v;
           uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            e[k] = cvt_f16x2(scaled(bf16_lo(e[k]), sc[2 * k], t), scaled(bf16_hi(e[k]), sc[2 * k + 1], t));
+          for (int k = 0; k < 4; ++k) {
+            const int d = kDC + 8 * v + 2 * k;
+            const float s0 = col_scales ? col_scales[d] : 1.f, s1 = col_scales ? col_scales[d + 1] : 1.f;
+            e[k] = cvt_f16x2(scaled(bf16_lo(e[k]), s0, t), scaled(bf16_hi(e[k]), s1, t));
+          }
           w = make_uint4(e[0], e[1], e[2], e[3]);
         }
         reinterpret_cast<uint4*>(out + ((size_t)t * H + h) * out_row + kDC)[v] = w;
@@ -196,7 +198,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     const int col = warp * 32 + lane;
     const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t tile = sbase + C::kOffB;
-    const float col_scale = kScaled ? col_scales[cblk * 128 + col] : 1.f;
+    const float col_scale = kScaled && col_scales ? col_scales[cblk * 128 + col] : 1.f;
 #pragma unroll 1
     for (int c0 = 0; c0 < C::NT; c0 += 32) {
       uint32_t r[32];
@@ -275,9 +277,9 @@ cudaError_t absorb_rows(const uint16_t* q_nope, const uint16_t* q_rope, const ui
 
 cudaError_t launch_absorb_q(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
                             uint16_t* q_abs, int T, int H, cudaStream_t s, const int32_t* rows_live,
-                            const float* col_scales, int32_t* err_word) {
-  return col_scales ? absorb_rows<true>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s, rows_live, col_scales, err_word)
-                    : absorb_rows<false>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s);
+                            const float* col_scales, int32_t* err_word, bool f16) {
+  return f16 ? absorb_rows<true>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s, rows_live, col_scales, err_word)
+             : absorb_rows<false>(q_nope, q_rope, w_uk, q_abs, T, H, kRow, s);
 }
 
 cudaError_t launch_merge_w_kq(const uint16_t* w_uq, const uint16_t* w_uk, uint16_t* w_kq, int d_q, int H,

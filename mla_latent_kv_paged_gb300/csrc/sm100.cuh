@@ -28,6 +28,18 @@ __device__ __forceinline__ bool elect() {
 }
 __device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
 
+// ---------------------------------------------------------------- registers
+// A warpgroup's registers a thread (a multiple of 8), executed by all of its warps. The sum over
+// the block's warpgroups stays within what the block was launched with.
+template <int kRegs>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // ---------------------------------------------------------------- cluster
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -144,6 +156,20 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
       return false;
     }
   }
+}
+
+// The same in few instructions, for a kernel with many waits: the caller reports once, at its end,
+// if *abort is set. (The limit is compared on the clock's low 32 bits, which wrap above it.)
+__device__ __forceinline__ bool wait_short(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = (uint32_t)clock();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort || (uint32_t)clock() - t0 > (uint32_t)wait_limit()) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
 }
 
 // ---------------------------------------------------------------- proxies
