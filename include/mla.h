@@ -540,9 +540,8 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
  *   cache8  [num_pages][page_size][576] uint8 codes, as above
  *   entries [num_pages][page_size / block_tokens][8] uint8: bytes 0..4 the five groups', 5..7 zero
  * (576 + 8 / block_tokens bytes a token). Such a value is a bf16 number
- * exactly, and every call on this cache gives bit for bit what its counterpart gives on a bf16 cache
- * that holds those values. e4m3's NaN code is a NaN. Entries outside [17, 247], which mla_write_kv
- * never writes, give unspecified values.
+ * exactly. e4m3's NaN code is a NaN. Entries outside [17, 247], which mla_write_kv never writes, give
+ * unspecified values.
  *
  * mla_write_kv — rows of a ragged chunk (B, T, cu, seq_lens as for mla_append_chunk) quantised into
  * their pages:
@@ -561,7 +560,17 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
  *
  * mla_read_kv_blocks, mla_decode_paged_blocks, mla_decode_paged_planned_blocks,
  * mla_attend_chunk_blocks — their counterparts without the suffix on such a cache, with the same
- * ordering rules, workspaces and errors. */
+ * ordering rules, workspaces and errors. Reading back and the expanded form of the attention give bit for
+ * bit what they give on a bf16 cache that holds the values. The decode and the absorbed form take fp16
+ * operands, as on the per-column cache: values, absorbed query and weights are rounded to fp16 (exact from 2^-14
+ * on, below it their resolution is 2^-25), and a value of the context or of a query that fp16 does not
+ * hold (65520 and more) is reported as MLA_ERR_RANGE. q_f16: q_abs holds fp16 and not bf16.
+ *
+ * mla_decode_step_blocks — a whole decode step on such a cache in one call: mla_decode_plan, mla_absorb_q
+ * with its result rounded once, to fp16, mla_decode_paged_planned_blocks, mla_combine and mla_out_proj.
+ *   q_abs [B * n_q][H][576] fp16 (output), u, lse (may be NULL) and out as there (lse and out may be pinned
+ *   host memory), workspace >= mla_decode_workspace_bytes(B, n_q, H, num_splits) bytes, which
+ *   consecutive steps may share. */
 mla_status mla_write_kv(const uint16_t* rows, uint8_t* cache8, uint8_t* entries, int block_tokens,
                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu, int B, int T,
                         int num_pages, int page_size, int max_pages_per_seq, int32_t* err_word, void* stream);
@@ -575,16 +584,23 @@ mla_status mla_read_kv_blocks(const uint8_t* cache8, const uint8_t* entries, int
                               const int32_t* block_table, const int32_t* seq_lens, const int32_t* first,
                               const int32_t* cu, uint16_t* rows, int B, int n_rows, int num_pages, int page_size,
                               int max_pages_per_seq, int32_t* err_word, void* stream);
-mla_status mla_decode_paged_blocks(const uint16_t* q_abs, const uint8_t* cache8, const uint8_t* entries,
+mla_status mla_decode_paged_blocks(const uint16_t* q_abs, int q_f16, const uint8_t* cache8, const uint8_t* entries,
                                    int block_tokens, const int32_t* block_table, const int32_t* seq_lens, int B,
                                    int n_q, int H, int num_pages, int page_size, int max_pages_per_seq,
                                    float softmax_scale, int num_splits, void* workspace, size_t workspace_bytes,
                                    int32_t* err_word, void* stream);
-mla_status mla_decode_paged_planned_blocks(const uint16_t* q_abs, const uint8_t* cache8, const uint8_t* entries,
-                                           int block_tokens, const int32_t* block_table, int B, int n_q, int H,
+mla_status mla_decode_paged_planned_blocks(const uint16_t* q_abs, int q_f16, const uint8_t* cache8,
+                                           const uint8_t* entries, int block_tokens, const int32_t* block_table,
+                                           int B, int n_q, int H,
                                            int num_pages, int page_size, int max_pages_per_seq, float softmax_scale,
                                            int num_splits, void* workspace, size_t workspace_bytes,
                                            int32_t* err_word, void* stream);
+mla_status mla_decode_step_blocks(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
+                                  const uint16_t* w_uv, const uint8_t* cache8, const uint8_t* entries, int block_tokens,
+                                  const int32_t* block_table, const int32_t* seq_lens, int B, int n_q, int H,
+                                  int num_pages, int page_size, int max_pages_per_seq, float softmax_scale,
+                                  int num_splits, uint16_t* q_abs, uint16_t* u, float* lse, uint16_t* out,
+                                  void* workspace, size_t workspace_bytes, int32_t* err_word, void* stream);
 mla_status mla_attend_chunk_blocks(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
                                    const uint16_t* w_uv, const uint8_t* cache8, const uint8_t* entries,
                                    int block_tokens, const int32_t* block_table, const int32_t* seq_lens,

@@ -27,6 +27,7 @@ such a cache (write_kv, append_chunk) find and write the powers; start with a te
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -64,7 +65,7 @@ EXPORTS = [
     "mla_append_chunk_workspace_bytes", "mla_append_chunk", "mla_read_kv",
     "mla_attend_chunk_workspace_bytes", "mla_attend_chunk",
     "mla_write_kv", "mla_append_chunk_blocks_workspace_bytes", "mla_append_chunk_blocks", "mla_read_kv_blocks",
-    "mla_decode_paged_blocks", "mla_decode_paged_planned_blocks", "mla_attend_chunk_blocks",
+    "mla_decode_paged_blocks", "mla_decode_paged_planned_blocks", "mla_decode_step_blocks", "mla_attend_chunk_blocks",
     "mla_update_pages_workspace_bytes", "mla_update_pages",
 ]
 
@@ -194,9 +195,12 @@ def _load(path: str):
     L.mla_read_kv_blocks.restype = i
     L.mla_read_kv_blocks.argtypes = [vp, vp, i, vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
     L.mla_decode_paged_blocks.restype = i
-    L.mla_decode_paged_blocks.argtypes = [vp, vp, vp, i, vp, vp, i, i, i, i, i, i, f, i, vp, sz, vp, vp]
+    L.mla_decode_paged_blocks.argtypes = [vp, i, vp, vp, i, vp, vp, i, i, i, i, i, i, f, i, vp, sz, vp, vp]
     L.mla_decode_paged_planned_blocks.restype = i
-    L.mla_decode_paged_planned_blocks.argtypes = [vp, vp, vp, i, vp, i, i, i, i, i, i, f, i, vp, sz, vp, vp]
+    L.mla_decode_paged_planned_blocks.argtypes = [vp, i, vp, vp, i, vp, i, i, i, i, i, i, f, i, vp, sz, vp, vp]
+    L.mla_decode_step_blocks.restype = i
+    L.mla_decode_step_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, f, i, vp, vp, vp, vp, vp, sz,
+                                         vp, vp]
     L.mla_attend_chunk_blocks.restype = i
     L.mla_attend_chunk_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i64, f, i, vp, vp, vp,
                                           sz, vp, vp]
@@ -425,13 +429,18 @@ def _block_tokens(cache, scales):
     if scales is None or scales.dtype is not torch.uint8:
         return 0
     num_pages, page_size = cache.shape[0], cache.shape[1]
+    for block in (64, 32, 16):
+        if scales.shape == (num_pages, page_size // block, 8):
+            if page_size % block == 0 and scales.get_device() == cache.get_device() and scales.is_contiguous():
+                return block
+            break
     if scales.dim() != 3 or scales.shape[1] < 1 or page_size // scales.shape[1] not in (16, 32, 64):
         raise ValueError(f"fp8_scales: shape {tuple(scales.shape)}, expected [num_pages, page_size / block, 8] with "
                          "blocks of 16, 32 or 64 tokens")
     block = page_size // scales.shape[1]
-    _tensor("fp8_scales", scales, torch.uint8, (num_pages, page_size // block, 8), cache.get_device())
     if block * scales.shape[1] != page_size:
         raise ValueError(f"fp8_scales: {scales.shape[1]} blocks in a page of {page_size}")
+    _tensor("fp8_scales", scales, torch.uint8, (num_pages, page_size // block, 8), cache.get_device())
     return block
 
 
@@ -439,8 +448,8 @@ def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, 
                      softmax_scale: float = DEFAULT_SCALE, workspace=None, err_word=None, stream=None,
                      planned: bool = False):
     """decode_paged on an FP8 cache: cache8 [num_pages, page_size, 576] uint8 e4m3 codes, scales [576]
-    float32 per column, or block scales [num_pages, page_size / block, 8] uint8. Returns
-    (workspace, num_splits) for ``combine``."""
+    float32 per column, or block scales [num_pages, page_size / block, 8] uint8 (q_abs then may be
+    float16). Returns (workspace, num_splits) for ``combine``."""
     import torch
     block = _block_tokens(cache8, scales)
     B, max_pages = block_table.shape
@@ -459,7 +468,9 @@ def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, 
             assert seq_lens.dtype == torch.int32 and seq_lens.is_contiguous()
         rest = (B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale), num_splits, _ptr(workspace), nb,
                 _ptr(err_word), _stream(stream))
-        head = (_ptr(_bits(q_abs)), _ptr(cache8), _ptr(scales), block, _ptr(block_table))
+        f16 = q_abs.dtype is torch.float16
+        assert q_abs.is_contiguous(), "tensors must be contiguous"
+        head = (_ptr(q_abs if f16 else _bits(q_abs)), int(f16), _ptr(cache8), _ptr(scales), block, _ptr(block_table))
         if planned:
             _check(lib().mla_decode_paged_planned_blocks(*head, *rest), "mla_decode_paged_planned_blocks")
         else:
@@ -576,7 +587,7 @@ def _dims(name, t, n):
 
 def _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word):
     """Check the paged-cache arguments of the chunk calls; returns (device number, B, pages,
-    page size, pages per sequence)."""
+    page size, pages per sequence, tokens of a block of a block-scaled cache or 0)."""
     import torch
     dev = cache.get_device()
     if dev < 0:
@@ -594,11 +605,12 @@ def _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word):
         _tensor("block_table", block_table, i32, (B, max_pages), dev)
         _tensor("seq_lens", seq_lens, i32, (B,), dev)
         _tensor("cu", cu, i32, (B + 1,), dev)
-    if fp8 and not _block_tokens(cache, fp8_scales):
+    block = _block_tokens(cache, fp8_scales) if fp8 else 0
+    if fp8 and not block:
         _tensor("fp8_scales", fp8_scales, torch.float32, (D_ROW,), dev)
     if err_word is not None and (err_word.dtype is not i32 or err_word.numel() < 1 or err_word.get_device() != dev):
         raise ValueError("err_word: an int32 tensor beside the cache")
-    return dev, B, num_pages, page_size, max_pages
+    return dev, B, num_pages, page_size, max_pages, block
 
 
 def _address(t):
@@ -660,16 +672,12 @@ def append_chunk(h, w_dkr, cache, block_table, seq_lens, cu, *, fp8_scales=None,
     workspace (allocated when none is given) is returned for reuse.
     """
     import torch
-    dev, B, num_pages, page_size, max_pages = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    dev, B, num_pages, page_size, max_pages, block = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
     T, d_model = _dims("h", h, 2)
     _tensor("h", h, torch.bfloat16, (T, d_model), dev)
     _tensor("w_dkr", w_dkr, torch.bfloat16, (D_ROW, d_model), dev)
-    block = _block_tokens(cache, fp8_scales)
     if block:
-        need = int(lib().mla_append_chunk_blocks_workspace_bytes(T, d_model))
-        if need == 0:
-            raise MlaError(1, "mla_append_chunk_blocks_workspace_bytes")
-        workspace, room = _room(workspace, need, cache, stream)
+        workspace, room = _room(workspace, append_chunk_blocks_workspace_bytes(T, d_model), cache, stream)
         _call("mla_append_chunk_blocks", lib().mla_append_chunk_blocks, dev, stream, h.data_ptr(), w_dkr.data_ptr(),
               cache.data_ptr(), fp8_scales.data_ptr(), block, block_table.data_ptr(), seq_lens.data_ptr(),
               cu.data_ptr(), B, T, d_model, num_pages, page_size, max_pages, float(rope_theta), workspace.data_ptr(),
@@ -700,8 +708,7 @@ def write_kv(rows, cache, block_table, seq_lens, cu, *, fp8_scales, err_word=Non
     are ignored. A page that is written belongs to one sequence.
     """
     import torch
-    dev, B, num_pages, page_size, max_pages = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
-    block = _block_tokens(cache, fp8_scales)
+    dev, B, num_pages, page_size, max_pages, block = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
     if not block:
         raise ValueError("write_kv: fp8_scales must be block scales (uint8)")
     T, _ = _dims("rows", rows, 2)
@@ -744,10 +751,13 @@ def update_pages(block_table, held, seq_lens, free_pages, free_count, *, page_si
     if (cu is None) != (slots is None):
         raise ValueError("cu and slots: both or neither")
     n_rows = 0 if slots is None else _dims("slots", slots, 1)[0]
-    for name, t, shape in (("block_table", block_table, (B, max_pages)), ("held", held, (B,)),
-                           ("seq_lens", seq_lens, (B,)), ("free_pages", free_pages, (num_pages,)),
-                           ("free_count", free_count, (1,))):
-        _tensor(name, t, i32, shape, dev)
+    if not (_fits(block_table, i32, (B, max_pages), dev) and _fits(held, i32, (B,), dev)
+            and _fits(seq_lens, i32, (B,), dev) and _fits(free_pages, i32, (num_pages,), dev)
+            and _fits(free_count, i32, (1,), dev)):
+        for name, t, shape in (("block_table", block_table, (B, max_pages)), ("held", held, (B,)),
+                               ("seq_lens", seq_lens, (B,)), ("free_pages", free_pages, (num_pages,)),
+                               ("free_count", free_count, (1,))):
+            _tensor(name, t, i32, shape, dev)
     if slots is not None:
         _tensor("cu", cu, i32, (B + 1,), dev)
         _tensor("slots", slots, torch.int64, (n_rows,), dev)
@@ -767,14 +777,13 @@ def read_kv(cache, block_table, seq_lens, cu, *, n_rows: int, first=None, fp8_sc
     (uint8 codes with fp8_scales, of columns or of blocks), zeros at and past seq_lens[b]. Rows at and past cu[B]
     are left as they were in ``out`` (undefined in a new tensor)."""
     import torch
-    dev, B, num_pages, page_size, max_pages = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    dev, B, num_pages, page_size, max_pages, block = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
     if first is not None:
         _tensor("first", first, torch.int32, (B,), dev)
     if out is None:
         out = _new((n_rows, D_ROW), torch.bfloat16, cache, stream)
     else:
         _tensor("out", out, torch.bfloat16, (n_rows, D_ROW), dev)
-    block = _block_tokens(cache, fp8_scales)
     if block:
         _call("mla_read_kv_blocks", lib().mla_read_kv_blocks, dev, stream, cache.data_ptr(), fp8_scales.data_ptr(), block,
               block_table.data_ptr(), seq_lens.data_ptr(), _address(first), cu.data_ptr(), out.data_ptr(), B, n_rows,
@@ -814,7 +823,7 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
     past cu[B] of out and lse are left as they were.
     """
     import torch
-    dev, B, num_pages, page_size, max_pages = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
+    dev, B, num_pages, page_size, max_pages, block = _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word)
     if form not in CHUNK_FORMS:
         raise ValueError(f"form: {form!r}, expected one of {sorted(CHUNK_FORMS)}")
     bf = torch.bfloat16
@@ -838,7 +847,6 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
             with torch.cuda.device(dev):
                 need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
     workspace, room = _room(workspace, need, cache, stream)
-    block = _block_tokens(cache, fp8_scales)
     if block:
         _call("mla_attend_chunk_blocks", lib().mla_attend_chunk_blocks, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(),
               w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), fp8_scales.data_ptr(), block, block_table.data_ptr(),
@@ -885,9 +893,13 @@ def decode_step(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, *, n_q
     ``bufs`` may hold preallocated q_abs, workspace, u, lse, out tensors; steps
     enqueued back to back may share one workspace (the step's up-projection lets
     the next step's plan start only once the step has finished).
-    Returns dict(q_abs, u, lse, out).
+    Returns dict(q_abs, u, lse, out); q_abs is float16 with block scales, else bfloat16.
     """
     bufs = bufs or {}
+    block = _block_tokens(cache, fp8_scales)
+    if block:
+        return _decode_step_blocks(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, n_q, num_splits,
+                                   softmax_scale, bufs, err_word, stream, fp8_scales, block)
     B, max_pages = block_table.shape
     T, H = q_nope.shape[0], q_nope.shape[1]
     ws, g = decode_plan(seq_lens, n_q=n_q, H=H, max_pages=max_pages, num_pages=cache.shape[0],
@@ -907,6 +919,57 @@ def decode_step(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, *, n_q
                      stream=stream)
     out = out_proj(u, w_uv, bufs.get("out"), stream)
     return dict(q_abs=q_abs, u=u, lse=lse, out=out, workspace=ws, num_splits=g)
+
+
+def _decode_step_blocks(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, n_q, num_splits, softmax_scale, bufs,
+                        err_word, stream, scales, block):
+    """decode_step on a block-scaled cache: one call of the library."""
+    import torch
+    bf, i32 = torch.bfloat16, torch.int32
+    dev = cache.get_device()
+    if dev < 0:
+        raise ValueError(f"cache: on {cache.device}, a CUDA device is needed")
+    num_pages, page_size, _ = _dims("cache", cache, 3)
+    B, max_pages = _dims("block_table", block_table, 2)
+    T, H, _ = _dims("q_nope", q_nope, 3)
+    if T != B * n_q:
+        raise ValueError(f"q_nope: {T} rows, expected {B} x {n_q}")
+    shapes = ((cache, torch.uint8, (num_pages, page_size, D_ROW)), (block_table, i32, (B, max_pages)),
+              (seq_lens, i32, (B,)), (q_nope, bf, (T, H, D_NOPE)), (q_rope, bf, (T, H, D_R)),
+              (w_uk, bf, (H, D_NOPE, D_C)), (w_uv, bf, (H, D_V, D_C)))
+    for k, (t, dtype, shape) in enumerate(shapes):
+        if not _fits(t, dtype, shape, dev):
+            _tensor(("cache", "block_table", "seq_lens", "q_nope", "q_rope", "w_uk", "w_uv")[k], t, dtype, shape, dev)
+    if err_word is not None and (err_word.dtype is not i32 or err_word.numel() < 1 or err_word.get_device() != dev):
+        raise ValueError("err_word: an int32 tensor beside the cache")
+    if num_splits is None:
+        with torch.cuda.device(dev) if torch.cuda.current_device() != dev else contextlib.nullcontext():
+            num_splits = default_splits(n_q)
+    q_abs, u, lse, out, workspace = (bufs.get(k) for k in ("q_abs", "u", "lse", "out", "workspace"))
+    if q_abs is None:
+        q_abs = _new((T, H, D_ROW), torch.float16, cache, stream)
+    else:
+        _tensor("q_abs", q_abs, torch.float16, (T, H, D_ROW), dev)
+    if u is None:
+        u = _new((T, H, D_C), bf, cache, stream)
+    else:
+        _tensor("u", u, bf, (T, H, D_C), dev)
+    # (lse and out may be pinned host memory)
+    if lse is None:
+        lse = _new((T, H), torch.float32, cache, stream)
+    elif not _fits(lse, torch.float32, (T, H), lse.get_device()):
+        _tensor("lse", lse, torch.float32, (T, H), lse.get_device())
+    if out is None:
+        out = _new((T, H, D_V), bf, cache, stream)
+    elif not _fits(out, bf, (T, H, D_V), out.get_device()):
+        _tensor("out", out, bf, (T, H, D_V), out.get_device())
+    need = workspace_bytes(B, n_q, H, num_splits) if workspace is None else 0
+    workspace, room = _room(workspace, need, cache, stream)
+    _call("mla_decode_step_blocks", lib().mla_decode_step_blocks, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(),
+          w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), scales.data_ptr(), block, block_table.data_ptr(),
+          seq_lens.data_ptr(), B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale), num_splits,
+          q_abs.data_ptr(), u.data_ptr(), lse.data_ptr(), out.data_ptr(), workspace.data_ptr(), room, _address(err_word))
+    return dict(q_abs=q_abs, u=u, lse=lse, out=out, workspace=workspace, num_splits=num_splits)
 
 
 class CapturedStep:
@@ -946,7 +1009,8 @@ class CapturedStep:
         bf = torch.bfloat16
         self.q_nope = torch.empty((T, H, D_NOPE), dtype=bf, device=dev)
         self.q_rope = torch.empty((T, H, D_R), dtype=bf, device=dev)
-        self.bufs = dict(q_abs=torch.empty((T, H, D_ROW), dtype=bf, device=dev),
+        q_type = torch.float16 if _block_tokens(cache, fp8_scales) else bf
+        self.bufs = dict(q_abs=torch.empty((T, H, D_ROW), dtype=q_type, device=dev),
                          workspace=torch.empty(workspace_bytes(B, n_q, H, g), dtype=torch.uint8, device=dev),
                          u=torch.empty((T, H, D_C), dtype=bf, device=dev),
                          lse=torch.empty((T, H), dtype=torch.float32, device=dev),

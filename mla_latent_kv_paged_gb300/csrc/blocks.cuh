@@ -53,8 +53,8 @@ cudaError_t launch_read_blocks(const uint8_t* cache, const BlockScales& scales, 
                                const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* out, int B,
                                int n_rows, int num_pages, int page_size, int max_pages, int32_t* err_word,
                                cudaStream_t s);
-// decode on a block-scaled cache
-cudaError_t launch_decode_blocks(const uint16_t* q_abs, const uint8_t* cache, const BlockScales& scales,
+// decode on a block-scaled cache; q_abs bf16, or fp16 with q_f16 (a chunk's rows: fp16 always)
+cudaError_t launch_decode_blocks(const uint16_t* q_abs, bool q_f16, const uint8_t* cache, const BlockScales& scales,
                                  const int32_t* block_table, int B, int n_q, int H, int num_pages, int page_size,
                                  int max_pages, float scale, int G, const Plan& plan, int32_t* err_word,
                                  cudaStream_t s);

@@ -302,7 +302,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
   constexpr int kSlots = kBlocks ? kOpSlots : kStages;
   using R = Roles<kBlocks>;
   const uint8_t* entries = reinterpret_cast<const uint8_t*>(fp8_scales);  // with kBlocks
-  const int block_shift = kBlocks ? tile_shift >> 8 : 0;                  // (the launch packs both)
+  const int block_shift = kBlocks ? tile_shift >> 8 & 0xFF : 0;           // (the launch packs these)
+  const bool q_f16 = kBlocks && (kRows || tile_shift >> 16);
   if (kBlocks) tile_shift &= 0xFF;
   if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) report_error(err_word, MLA_ERR_CUDA);
@@ -743,7 +744,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
 #pragma unroll
               for (int k = 0; k < 32; ++k) r[k] = scale_bf16x2_to_f16x2(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
             }
-            if (kBlocks && !kRows) query_f16(r, row < H, err_word);
+            if (kBlocks && !q_f16) query_f16(r, row < H, err_word);
             tmem_st32(tQ + 64 * q + 32 * m, r);
           }
           if ((row >> 6) == q) {  // this row's positional half: 64 bytes, 64B-swizzled (warp-uniform)
@@ -760,7 +761,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
 #pragma unroll
               for (int k = 0; k < 16; ++k) r[k] = scale_bf16x2_to_f16x2(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
             }
-            if (kBlocks && !kRows) query_f16(r, row < H, err_word);
+            if (kBlocks && !q_f16) query_f16(r, row < H, err_word);
             tmem_st16(tmem + lane_off + kTmQr, r);
           }
           // every use of a ring slot completes its CVF once (the query's too)
@@ -1332,7 +1333,7 @@ cudaError_t launch_decode_as(const CUtensorMap& map_c, const CUtensorMap& map_kr
                                const float* fp8_scales, const int32_t* block_table, int B, int n_q, int H,
                                int num_pages, int page_size, int max_pages, float scale, int G, const Plan& plan,
                                int32_t* err_word,
-                               cudaStream_t s, int block_shift = 0) {
+                               cudaStream_t s, int blocks = 0) {
   CUtensorMap map_qkr, map_q;
   const uint64_t q_dims[2] = {kRow, (uint64_t)B * n_q * H};
   const uint64_t row_stride[1] = {kRow * 2};
@@ -1346,7 +1347,7 @@ cudaError_t launch_decode_as(const CUtensorMap& map_c, const CUtensorMap& map_kr
   dim3 grid(2 * G, n_q, 1);
   return launch_pdl(decode_tc_kernel<kF8, kRows, kBlocks>, grid, dim3(Roles<kBlocks>::kThreads), kSmemBytes, s, map_c,
                     map_kr, map_qkr, map_q, block_table, n_q, H, max_pages, num_pages,
-                    (page_size == 2 * kTile ? 1 : 0) | block_shift << 8, sl2, plan, fp8_scales, err_word,
+                    (page_size == 2 * kTile ? 1 : 0) | blocks << 8, sl2, plan, fp8_scales, err_word,
                     plan.seq_row);
 }
 template <bool kF8, bool kBlocks = false, typename... Args>
@@ -1380,7 +1381,7 @@ bool code_maps(CUtensorMap* map_c, CUtensorMap* map_kr, const uint8_t* cache8, i
 }
 }  // namespace
 
-cudaError_t launch_decode_blocks(const uint16_t* q_abs, const uint8_t* cache8, const BlockScales& scales,
+cudaError_t launch_decode_blocks(const uint16_t* q_abs, bool q_f16, const uint8_t* cache8, const BlockScales& scales,
                                  const int32_t* block_table, int B, int n_q, int H, int num_pages, int page_size,
                                  int max_pages, float scale, int G, const Plan& plan, int32_t* err_word,
                                  cudaStream_t s) {
@@ -1388,7 +1389,7 @@ cudaError_t launch_decode_blocks(const uint16_t* q_abs, const uint8_t* cache8, c
   if (!code_maps(&map_c, &map_kr, cache8, num_pages, page_size)) return cudaErrorInvalidValue;
   return launch_decode_impl<true, true>(plan, map_c, map_kr, q_abs, reinterpret_cast<const float*>(scales.entries),
                                         block_table, B, n_q, H, num_pages, page_size, max_pages, scale, G, plan,
-                                        err_word, s, scales.shift);
+                                        err_word, s, scales.shift | (q_f16 ? 1 : 0) << 8);
 }
 
 cudaError_t launch_decode_fp8(const uint16_t* q_abs, const uint8_t* cache8, const float* fp8_scales,

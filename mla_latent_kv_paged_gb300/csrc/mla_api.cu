@@ -344,7 +344,7 @@ mla_status block_args(const void* cache8, const void* entries, int block_tokens,
 }
 }  // namespace
 
-mla_status mla_decode_paged_blocks(const uint16_t* q_abs, const uint8_t* cache8, const uint8_t* entries,
+mla_status mla_decode_paged_blocks(const uint16_t* q_abs, int q_f16, const uint8_t* cache8, const uint8_t* entries,
                                    int block_tokens, const int32_t* block_table, const int32_t* seq_lens, int B,
                                    int n_q, int H, int num_pages, int page_size, int max_pages_per_seq,
                                    float softmax_scale, int num_splits, void* workspace, size_t workspace_bytes,
@@ -362,13 +362,13 @@ mla_status mla_decode_paged_blocks(const uint16_t* q_abs, const uint8_t* cache8,
     st = launch_status(launch_plan(seq_lens, block_table, B, n_q, max_pages_per_seq, page_size, num_pages, num_splits,
                                    plan, err_word, s));
   if (st == MLA_OK)
-    st = launch_status(launch_decode_blocks(q_abs, cache8, scales, block_table, B, n_q, H, num_pages, page_size,
+    st = launch_status(launch_decode_blocks(q_abs, q_f16 != 0, cache8, scales, block_table, B, n_q, H, num_pages, page_size,
                                             max_pages_per_seq, softmax_scale, num_splits, plan, err_word, s));
   return st;
 }
 
-mla_status mla_decode_paged_planned_blocks(const uint16_t* q_abs, const uint8_t* cache8, const uint8_t* entries,
-                                           int block_tokens, const int32_t* block_table, int B, int n_q, int H,
+mla_status mla_decode_paged_planned_blocks(const uint16_t* q_abs, int q_f16, const uint8_t* cache8,
+                                           const uint8_t* entries, int block_tokens, const int32_t* block_table, int B, int n_q, int H,
                                            int num_pages, int page_size, int max_pages_per_seq, float softmax_scale,
                                            int num_splits, void* workspace, size_t workspace_bytes,
                                            int32_t* err_word, void* stream) {
@@ -381,9 +381,47 @@ mla_status mla_decode_paged_planned_blocks(const uint16_t* q_abs, const uint8_t*
   if (st == MLA_OK)
     st = decode_args(workspace, workspace_bytes, B, n_q, H, num_pages, page_size, max_pages_per_seq, num_splits, &plan);
   if (st == MLA_OK)
-    st = launch_status(launch_decode_blocks(q_abs, cache8, scales, block_table, B, n_q, H, num_pages, page_size,
+    st = launch_status(launch_decode_blocks(q_abs, q_f16 != 0, cache8, scales, block_table, B, n_q, H, num_pages, page_size,
                                             max_pages_per_seq, softmax_scale, num_splits, plan, err_word,
                                             (cudaStream_t)stream));
+  return st;
+}
+
+mla_status mla_decode_step_blocks(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w_uk,
+                                  const uint16_t* w_uv, const uint8_t* cache8, const uint8_t* entries, int block_tokens,
+                                  const int32_t* block_table, const int32_t* seq_lens, int B, int n_q, int H,
+                                  int num_pages, int page_size, int max_pages_per_seq, float softmax_scale,
+                                  int num_splits, uint16_t* q_abs, uint16_t* u, float* lse, uint16_t* out,
+                                  void* workspace, size_t workspace_bytes, int32_t* err_word, void* stream) {
+  if (!q_nope || !q_rope || !w_uk || !w_uv || !block_table || !seq_lens || !q_abs || !u || !out)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(q_nope) || !aligned16(q_rope) || !aligned16(w_uk) || !aligned16(w_uv) || !aligned16(block_table) ||
+      !aligned16(seq_lens) || !aligned16(q_abs) || !aligned16(u) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.f)) return MLA_ERR_INVALID_ARG;
+  BlockScales scales;
+  mla_status st = block_args(cache8, entries, block_tokens, &scales);
+  Plan plan;
+  if (st == MLA_OK)
+    st = decode_args(workspace, workspace_bytes, B, n_q, H, num_pages, page_size, max_pages_per_seq, num_splits, &plan);
+  if (st != MLA_OK) return st;
+  // lse and out may be pinned host memory, written over the host link
+  const void *lse_dev = nullptr, *out_dev = nullptr;
+  if ((lse && !device_address(lse, &lse_dev)) || !device_address(out, &out_dev)) return MLA_ERR_INVALID_ARG;
+  const int T = B * n_q;
+  cudaStream_t s = (cudaStream_t)stream;
+  st = launch_status(launch_plan(seq_lens, nullptr, B, n_q, max_pages_per_seq, page_size, num_pages, num_splits, plan,
+                                 err_word, s));
+  if (st == MLA_OK)
+    st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, q_abs, T, H, s, nullptr, nullptr, err_word, true));
+  if (st == MLA_OK)
+    st = launch_status(launch_decode_blocks(q_abs, true, cache8, scales, block_table, B, n_q, H, num_pages, page_size,
+                                            max_pages_per_seq, softmax_scale, num_splits, plan, err_word, s));
+  if (st == MLA_OK)
+    st = launch_status(launch_combine(plan, B, n_q, H, u, static_cast<float*>(const_cast<void*>(lse_dev)), s));
+  if (st == MLA_OK)
+    st = launch_status(launch_out_proj(u, w_uv, static_cast<uint16_t*>(const_cast<void*>(out_dev)), T, H, s));
   return st;
 }
 
@@ -606,7 +644,7 @@ mla_status attend_rows(const uint16_t* q_nope, const uint16_t* q_rope, const uin
     if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s, r.hdr, fp8_scales, err_word,
                                                           fp8_scales || blocks));
     if (st == MLA_OK)
-      st = launch_status(blocks ? launch_decode_blocks(r.q_abs, static_cast<const uint8_t*>(cache), *blocks, block_table,
+      st = launch_status(blocks ? launch_decode_blocks(r.q_abs, true, static_cast<const uint8_t*>(cache), *blocks, block_table,
                                                        T, 1, H, num_pages, page_size, max_pages_per_seq,
                                                        softmax_scale, G, plan, err_word, s)
                          : fp8_scales ? launch_decode_fp8(r.q_abs, static_cast<const uint8_t*>(cache), fp8_scales,

@@ -52,8 +52,8 @@ struct ProjCfg {
 
 // kRows: rows of a chunk. absorb_q (for the decode on an FP8 cache) scales the query by
 // the cache's column scales and writes fp16, so that it is rounded once and its range is
-// that of the product that the decode takes; of the rows below *rows_live it reports
-// values that fp16 does not hold. out_proj takes fp16 u and weights, and writes only the
+// that of the product that the decode takes; of the rows below *rows_live (null: of all T) it
+// reports values that fp16 does not hold. Without column scales it only writes fp16. out_proj takes fp16 u and weights, and writes only the
 // rows below *rows_live.
 template <bool kAbsorb, int kNT, bool kRows>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -115,7 +115,7 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   if (!kAbsorb) grid_launch_dependents();
   // rows at and past *rows_live are computed at most as part of a tile, never
   // written; the first tile always runs, since its loads are under way
-  const int live = kRows ? min(T, *rows_live) : T;
+  const int live = kRows && rows_live ? min(T, *rows_live) : T;
   if (kRows && !kAbsorb) T = max(live, 1);
   constexpr bool kScaled = kRows && kAbsorb;
   bool beyond = false;  // a scaled query outside fp16

@@ -69,7 +69,7 @@ def test_decode_blocks_refusals(lib, planned):
     ws = lib.mla_decode_workspace_bytes(2, 1, 16, 4)
 
     def call(**kw):
-        a = dict(q=P, cache=P, entries=P, block=16, bt=P, sl=P, B=2, n_q=1, H=16, pages=8, page=64, maxp=4, scale=0.07,
+        a = dict(q=P, f16=0, cache=P, entries=P, block=16, bt=P, sl=P, B=2, n_q=1, H=16, pages=8, page=64, maxp=4, scale=0.07,
                  splits=4, ws=P, wsb=ws)
         a.update(kw)
         if planned:
@@ -80,6 +80,21 @@ def test_decode_blocks_refusals(lib, planned):
     refusals(call, ("q", "cache", "entries", "bt", "ws") + (() if planned else ("sl",)))
     assert call(block=0) == 2 and call(scale=0.0) == 1 and call(scale=float("nan")) == 1 and call(B=0) == 1
     assert call(n_q=3) == 2 and call(H=129) == 2 and call(page=32) == 2 and call(wsb=ws - 1) == 3
+
+
+def test_decode_step_blocks_refusals(lib):
+    """(out and lse come last among the checks: their kind of memory is asked of the runtime.)"""
+    ws = lib.mla_decode_workspace_bytes(2, 1, 16, 4)
+
+    def call(**kw):
+        a = dict(qn=P, qr=P, uk=P, uv=P, cache=P, entries=P, block=16, bt=P, sl=P, B=2, n_q=1, H=16, pages=8, page=64,
+                 maxp=4, scale=0.07, splits=4, qa=P, u=P, lse=None, out=P, ws=P, wsb=ws)
+        a.update(kw)
+        return lib.mla_decode_step_blocks(*a.values(), None, None)
+
+    refusals(call, ("qn", "qr", "uk", "uv", "cache", "entries", "bt", "sl", "qa", "u", "out", "ws"))
+    assert call(lse=P + 2) == 1 and call(block=8) == 2 and call(scale=0.0) == 1 and call(B=0) == 1
+    assert call(n_q=3) == 2 and call(H=0) == 2 and call(page=96) == 2 and call(wsb=ws - 1) == 3 and call(splits=0) == 1
 
 
 def test_attend_chunk_blocks_refusals(lib):

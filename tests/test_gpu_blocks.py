@@ -227,9 +227,10 @@ def decode(mla, c, cache, scales, n_q, err=None, scale=ref.SCALE):
 
 
 def check_decode(c, r, n_q, scale=ref.SCALE, skip=()):
-    """A step's u, lse and out within the bounds of its roundings, given the q_abs that it returns (bf16).
+    """A step's q_abs, u, lse and out within the bounds of its roundings, each given those before it.
 
-    A score is off by dz: query and values in fp16 are exact from 2^-14 on and off by 2^-25 below, the
+    q_abs is a sum of 128 products in fp32, rounded to fp16. A score is off by dz: values in fp16 are exact from
+    2^-14 on and off by 2^-25 below, the
     sums of 576 products are in fp32, the half of them that comes from the other CTA goes through fp16 as an
     offset of at most half the half's spread (2^-11 relative), and scaling and shifting round a few times
     in fp32. That moves weights by a factor exp(+-2 dz). A weight is rounded to fp16 (2^-11, below 2^-14 of the largest
@@ -237,6 +238,13 @@ def check_decode(c, r, n_q, scale=ref.SCALE, skip=()):
     merged u to bf16. out is W^UV times that u, in fp32, rounded to bf16."""
     import torch
     tiny, f16, bf = ref.TINY_F16, ref.U_F16, ref.U_BF16
+    qn, wk = c.q_nope.double(), c.w_uk.double()
+    qa = torch.cat([torch.einsum("thd,hdc->thc", qn, wk), c.q_rope.double()], 2)
+    bound = 1.01 * f16 * qa.abs() + tiny
+    bound[..., :512] += 128 * ref.U_F32 * torch.einsum("thd,hdc->thc", qn.abs(), wk.abs())
+    assert r["q_abs"].dtype == torch.float16
+    rows = [b * n_q + j for b in range(len(c.lens)) if b not in skip for j in range(n_q)]
+    assert ((r["q_abs"].double() - qa).abs() <= bound)[rows].all()
     for b, L in enumerate(c.lens):
         if b in skip:
             continue
@@ -367,7 +375,27 @@ def test_decode_calls_without_the_step(mla, err):
         u, lse = mla.combine(ws, B=2, n_q=1, H=24, num_splits=g)
         torch.cuda.synchronize()
         assert torch.equal(bits(u), bits(want["u"])) and torch.equal(bits(lse), bits(want["lse"]))
-    assert int(err.item()) == 0
+    # a bf16 query is taken as it is: its values are fp16 numbers too
+    q = mla.absorb_q(c.q_nope, c.q_rope, c.w_uk)
+    assert (q.to(torch.float16).float() == q.float()).all()
+    res = []
+    for query in (q, q.to(torch.float16)):
+        ws, g = mla.decode_paged_fp8(query, c.codes, c.entries, c.table, c.seq_lens, n_q=1, err_word=err)
+        res.append(mla.combine(ws, B=2, n_q=1, H=24, num_splits=g))
+        torch.cuda.synchronize()
+    assert all(torch.equal(bits(a), bits(b)) for a, b in zip(*res)) and int(err.item()) == 0
+
+
+def test_queries_in_bf16_outside_fp16_are_reported(mla, err):
+    import torch
+    c = Blocks([1, 1], [70, 70], H=16, seed=8)
+    for d, value, want in ((3, 65536.0, RANGE), (560, -65536.0, RANGE), (3, 65280.0, 0)):
+        q = mla.absorb_q(c.q_nope, c.q_rope, c.w_uk)
+        q[1, 5, d] = value
+        err.zero_()
+        mla.decode_paged_fp8(q, c.codes, c.entries, c.table, c.seq_lens, n_q=1, err_word=err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == want
 
 
 def test_decode_reports_bad_pages(mla, err):
@@ -413,7 +441,7 @@ def test_test_build_finds_no_bad_address(mla):
         ws = torch.empty(mla.workspace_bytes(5, 2, 40, g), dtype=torch.uint8, device="cuda")
         e = torch.zeros(1, dtype=torch.int32, device="cuda")
         s = torch.cuda.current_stream().cuda_stream
-        st = L.mla_decode_paged_blocks(q.data_ptr(), c.codes.data_ptr(), c.entries.data_ptr(), 16, c.table.data_ptr(),
+        st = L.mla_decode_paged_blocks(q.data_ptr(), 0, c.codes.data_ptr(), c.entries.data_ptr(), 16, c.table.data_ptr(),
                                        c.seq_lens.data_ptr(), 5, 2, 40, c.num_pages, 128, c.max_pages, ref.SCALE, g,
                                        ws.data_ptr(), ws.numel(), e.data_ptr(), s)
         assert st == 0
@@ -440,7 +468,7 @@ def test_waits_that_run_out_are_reported(mla, lens):
     torch.cuda.synchronize()
     try:
         assert dbg.mla_debug_set_wait_limit(2_000_000) == 0 and dbg.mla_debug_set_skip_producer(1) == 0
-        st = dbg.mla_decode_paged_blocks(q.data_ptr(), c.codes.data_ptr(), c.entries.data_ptr(), 16, c.table.data_ptr(),
+        st = dbg.mla_decode_paged_blocks(q.data_ptr(), 0, c.codes.data_ptr(), c.entries.data_ptr(), 16, c.table.data_ptr(),
                                          c.seq_lens.data_ptr(), len(lens), 1, 16, c.num_pages, 64, c.max_pages,
                                          ref.SCALE, g, ws.data_ptr(), ws.numel(), e.data_ptr(),
                                          torch.cuda.current_stream().cuda_stream)
@@ -725,6 +753,15 @@ def test_python_checks(mla):
         mla.read_kv(*c.paged8(), n_rows=9, fp8_scales=c.entries[:1])
     with pytest.raises(ValueError, match="on cpu"):
         mla.read_kv(*c.paged8(), n_rows=9, fp8_scales=c.entries.cpu())
+    step = (c.q_nope[:1], c.q_rope[:1], c.w_uk, c.w_uv, c.codes, c.table, c.seq_lens)
+    for k, bad in ((0, c.q_nope[:2]), (1, c.q_rope[:1].float()), (2, c.w_uk[:1]), (3, c.w_uv.transpose(0, 1)),
+                   (5, c.table[:, ::2]), (6, c.seq_lens.long())):
+        with pytest.raises(ValueError):
+            mla.decode_step(*step[:k], bad, *step[k + 1:], n_q=1, fp8_scales=c.entries)
+    with pytest.raises(ValueError, match="q_abs"):
+        mla.decode_step(*step, n_q=1, fp8_scales=c.entries, bufs=dict(q_abs=mla.absorb_q(*step[:3])))
+    with pytest.raises(mla.MlaError, match="WORKSPACE"):
+        mla.decode_step(*step, n_q=1, fp8_scales=c.entries, bufs=dict(workspace=c.codes[0]))
     with pytest.raises(ValueError, match="shape"):
         q = mla.absorb_q(c.q_nope[:1], c.q_rope[:1], c.w_uk)
         mla.decode_paged_fp8(q, c.codes, c.entries[1:], c.table, c.seq_lens, n_q=1)
