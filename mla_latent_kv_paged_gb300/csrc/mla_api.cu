@@ -534,8 +534,8 @@ mla_status mla_update_pages(int32_t* block_table, int32_t* held, const int32_t* 
   if (!chunk_counts_ok(B, n_rows) || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
   if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
   if (workspace_bytes < update_pages_workspace_bytes(B)) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  Pages p = {block_table, held, seq_lens, free_pages, free_count, cu, slots, B, slots ? n_rows : 0, num_pages, page_size,
-             max_pages_per_seq};
+  Pages p = {block_table, held, seq_lens, free_pages, free_count, cu, slots, B, slots ? n_rows : 0, num_pages,
+             page_size == 64 ? 6 : 7, max_pages_per_seq};
   return launch_status(launch_update_pages(p, workspace, err_word, (cudaStream_t)stream));
 }
 

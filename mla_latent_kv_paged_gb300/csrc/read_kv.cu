@@ -32,6 +32,7 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
                uint4* __restrict__ out, int B, int n_rows, int num_pages, int page_size, int max_pages,
                int32_t* err_word, const uint8_t* __restrict__ entries, int shift) {
   __shared__ int64_t src[kRows];  // row of the pool; -1 zeros, -2 not a sequence's row
+  __shared__ uint2 entry[kBlocks ? kRows : 1];  // the row's block's
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
   const int t0 = blockIdx.x * kRows;
@@ -54,6 +55,7 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
       }
     }
     src[i] = r;
+    if (kBlocks && r >= 0) entry[i] = __ldg(reinterpret_cast<const uint2*>(entries) + (r >> shift));
   }
   if (blockIdx.x == 0) report_rows(cu, B, n_rows, threadIdx.x, kThreads, err_word);
   const int g = threadIdx.x % kGroups, r0 = threadIdx.x / kGroups;
@@ -74,7 +76,6 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
       const int64_t s = src[(k0 + k) * kRowsAtOnce + r0];
       v[k] = make_uint4(0, 0, 0, 0);
       if (s >= 0) {
-        if (kBlocks) v[k].z = __ldg(entries + ((s >> shift) << 3) + (g < 64 ? g >> 4 : 4));
         if (kF8) {
           const uint2 c = __ldg(static_cast<const uint2*>(cache) + s * kGroups + g);
           v[k].x = c.x;
@@ -93,6 +94,8 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
         // e4m3 -> fp16 (exact) -> fp32, times the scale in fp32, rounded once to bf16
         const uint32_t w[2] = {v[k].x, v[k].y};
         uint32_t f[4], p[4];
+        const float step =
+            kBlocks ? step_of(reinterpret_cast<const uint8_t*>(entry)[8 * i + (g < 64 ? g >> 4 : 4)]) : 0.f;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
@@ -102,7 +105,7 @@ read_kv_kernel(const void* __restrict__ cache, const float* __restrict__ scales,
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float2 x = sm100::f16x2_to_f32(f[q]);
-          const float s0 = kBlocks ? step_of(v[k].z) : sc[2 * q], s1 = kBlocks ? s0 : sc[2 * q + 1];
+          const float s0 = kBlocks ? step : sc[2 * q], s1 = kBlocks ? s0 : sc[2 * q + 1];
           const float a = x.x * s0, b = x.y * s1;
           p[q] = kF16 ? sm100::cvt_f16x2(a, b) : sm100::cvt_bf16x2(a, b);
           if (kF16 && src[i] >= 0) top = fmaxf(top, fmaxf(fabsf(a), fabsf(b)));

@@ -25,11 +25,11 @@ namespace mla {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kPerThread = MLA_MAX_BATCH / kThreads;
+static_assert(MLA_MAX_BATCH == 4 * kThreads, "one, two or four sequences a thread");
 constexpr int kLanes = 8;  // of a page
 constexpr int kGridThreads = 256;
 // One launch up to these sizes (see the file's head).
-constexpr int kSmallRows = 4096, kSmallBatch = 1024;
+constexpr int kSmallRows = 4096, kSmallBatch = kThreads;
 
 struct Sequence {  // one read of what a page's group needs
   int32_t page0;   // its first page
@@ -39,12 +39,11 @@ struct Sequence {  // one read of what a page's group needs
   int32_t pos0;    // ... and its position
   int32_t end;     // the context's length; its new tokens are pos0 .. end - 1
   int32_t refused;
-  int32_t unused;
+  int32_t taken;   // pages taken by those before
 };
 struct Work {
-  int32_t* give;   // [B + 1] pages given back by the sequences before
-  int32_t* take;   // [B + 1] pages taken by those before
-  int32_t* unit;   // [B + 1] pages worked on for those before
+  int32_t* give;   // [B] pages given back by the sequences before
+  int32_t* unit;   // [B] pages worked on for those before
   Sequence* seq;   // [B]
   int32_t* total;  // [4] free pages before, given back, taken, units
 };
@@ -55,12 +54,11 @@ size_t work_layout(void* base, int B, Work* w) {
     off = align256(off + bytes);
     return o;
   };
-  const size_t og = take((size_t)(B + 1) * 4), ot = take((size_t)(B + 1) * 4), ou = take((size_t)(B + 1) * 4);
+  const size_t og = take((size_t)B * 4), ou = take((size_t)B * 4);
   const size_t os = take((size_t)B * sizeof(Sequence)), on = take(16);
   if (base && w) {
     char* c = workspace_base(base);
     w->give = reinterpret_cast<int32_t*>(c + og);
-    w->take = reinterpret_cast<int32_t*>(c + ot);
     w->unit = reinterpret_cast<int32_t*>(c + ou);
     w->seq = reinterpret_cast<Sequence*>(c + os);
     w->total = reinterpret_cast<int32_t*>(c + on);
@@ -79,26 +77,28 @@ __device__ __forceinline__ int last_at(const int32_t* sum, int n, int x) {
 }
 
 // The pages, each by one group of lanes; then the pages given back and not taken, each
-// by a thread; then the rows behind the last sequence.
-__device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, int thread, int threads, int32_t* err_word) {
+// by a thread; then the rows behind the last sequence. give, unit: copies of w's in shared memory.
+__device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, const int32_t* give, const int32_t* unit,
+                                           int thread, int threads, int32_t* err_word) {
   const int F = w.total[0], R = w.total[1], K = w.total[2], units = w.total[3];
-  const int lane = thread % kLanes;
+  const int lane = thread % kLanes, shift = p.page_shift;
+  const uint32_t group = 0xFFu << ((threadIdx.x & 31) & ~(kLanes - 1));
   bool bad = false;
   for (int i = thread / kLanes; i < units; i += threads / kLanes) {
-    const int b = last_at(w.unit, p.B, i);
+    const int b = last_at(unit, p.B, i);
     const Sequence s = w.seq[b];
-    const int pi = s.page0 + i - w.unit[b];
+    const int pi = s.page0 + i - unit[b];
     int32_t* place = p.block_table + (int64_t)b * p.max_pages + pi;
     int page = -1;
     if (pi < s.held) {
       page = *place;
     } else if (pi < s.need) {
-      const int k = w.take[b] + pi - s.held;
+      const int k = s.taken + pi - s.held;
       if (k < R) {
-        const int from = last_at(w.give, p.B, k);
-        int32_t* old = p.block_table + (int64_t)from * p.max_pages + w.seq[from].need + k - w.give[from];
+        const int from = last_at(give, p.B, k);
+        int32_t* old = p.block_table + (int64_t)from * p.max_pages + w.seq[from].need + k - give[from];
         page = *old;
-        __syncwarp(0xFFu << ((threadIdx.x & 31) & ~(kLanes - 1)));  // every lane has read it
+        __syncwarp(group);  // every lane has read it
         if (lane == 0) *old = -1;
       } else {
         page = p.free_pages[F - 1 - (k - R)];
@@ -107,13 +107,13 @@ __device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, int th
     }
     const bool good = page >= 0 && page < p.num_pages && !s.refused;
     bad |= !good && !s.refused;
-    const int a = max(s.pos0, pi * p.page_size), e = min(s.end, (pi + 1) * p.page_size);
+    const int a = max(s.pos0, pi << shift), e = min(s.end, (pi + 1) << shift);
     for (int pos = a + lane; pos < e; pos += kLanes)
-      p.slots[s.row0 + pos - s.pos0] = good ? (int64_t)page * p.page_size + (pos - pi * p.page_size) : -1;
+      p.slots[s.row0 + pos - s.pos0] = good ? (int64_t)(page - pi) * (1 << shift) + pos : -1;
   }
   for (int q = K + thread; q < R; q += threads) {
-    const int b = last_at(w.give, p.B, q);
-    int32_t* old = p.block_table + (int64_t)b * p.max_pages + w.seq[b].need + q - w.give[b];
+    const int b = last_at(give, p.B, q);
+    int32_t* old = p.block_table + (int64_t)b * p.max_pages + w.seq[b].need + q - give[b];
     const int page = *old;
     bad |= page < 0 || page >= p.num_pages;
     p.free_pages[F + R - 1 - q] = page;
@@ -124,50 +124,63 @@ __device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, int th
   if (bad) report_error(err_word, MLA_ERR_BOUNDS);
 }
 
-// Exclusive sums over the block's threads of one value each; the total in *all.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* shared, int64_t* all) {
+// Sums that stay at kMany once they reach it: more pages than a pool can have (2^25).
+constexpr int kMany = 1 << 26;
+__device__ __forceinline__ int plus(int a, int b) { return min(a + b, kMany); }
+
+// Exclusive sums over the block's threads of kN values each, in v; the totals in all.
+template <int kN>
+__device__ __forceinline__ void block_scan(int (&v)[kN], int (&all)[kN], int (*shared)[kN]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t x = v;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) shared[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int64_t y = shared[lane];
+  for (int k = 0; k < kN; ++k) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t z = __shfl_up_sync(0xffffffffu, y, d);
-      if (lane >= d) y += z;
+      const int y = __shfl_up_sync(0xffffffffu, v[k], d);
+      if (lane >= d) v[k] = plus(v[k], y);
     }
-    shared[lane] = y;
+    if (lane == 31) shared[warp][k] = v[k];
+    v[k] = __shfl_up_sync(0xffffffffu, v[k], 1);
+    if (lane == 0) v[k] = 0;
   }
   __syncthreads();
-  const int64_t r = x - v + (warp > 0 ? shared[warp - 1] : 0);
-  *all = shared[31];
-  __syncthreads();
-  return r;
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {  // every warp adds up the warps' sums for itself
+    int y = shared[lane][k];
+    all[k] = y;
+    if (lane >= warp) y = 0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      y = plus(y, __shfl_xor_sync(0xffffffffu, y, d));
+      all[k] = plus(all[k], __shfl_xor_sync(0xffffffffu, all[k], d));
+    }
+    v[k] = plus(v[k], y);
+  }
 }
 
-template <bool kAll>
+// kPer: sequences a thread. kAll: this block also deals out the pages (kPer is 1).
+template <int kPer, bool kAll>
 __global__ void __launch_bounds__(kThreads)
 update_pages_scan(Pages p, Work w, int32_t* err_word) {
-  __shared__ int64_t sums[32];
+  __shared__ int sums[32][2], unit_sums[32][1];
   __shared__ int served;  // pages taken in all
+  __shared__ int32_t give[kAll ? kThreads : 1], unit[kAll ? kThreads : 1];
+  static_assert(!kAll || kPer == 1, "shared memory");
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
-  const int tid = threadIdx.x, per = (p.B + kThreads - 1) / kThreads, b0 = tid * per;
-  const int max_tokens = p.max_pages * p.page_size;
+  const int tid = threadIdx.x, b0 = tid * kPer;
+  const int shift = p.page_shift, round = (1 << shift) - 1, max_tokens = p.max_pages << shift;
   if (tid == 0) served = 0;
+  int F = *p.free_count;
   bool bad = false;
-  Sequence s[kPerThread];
-  int64_t give = 0, take = 0;
+  Sequence s[kPer];
+  int moved[2] = {0, 0}, all[2];  // pages given back, taken
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const int b = b0 + i;
-    if (i >= per || b >= p.B) continue;
+    s[i] = Sequence{};
+    s[i].refused = 1;
+    if (b >= p.B) continue;
     const int L = p.lens[b], h = p.held[b];
     int c0 = 0, n = 0;
     bool ok = L >= 0 && L <= max_tokens && h >= 0 && h <= p.max_pages;
@@ -179,95 +192,105 @@ update_pages_scan(Pages p, Work w, int32_t* err_word) {
     }
     ok = ok && n <= L;
     bad |= !ok;
-    s[i].held = ok ? h : 0;  // a sequence whose numbers are out of range is left as it is
-    s[i].need = ok ? (L + p.page_size - 1) / p.page_size : 0;
+    // a sequence whose numbers are out of range is left as it is
+    s[i].held = ok ? h : 0;
+    s[i].need = ok ? (L + round) >> shift : 0;
     s[i].row0 = c0;
     s[i].end = ok ? L : n;
     s[i].pos0 = s[i].end - n;
     s[i].refused = !ok;
-    if (ok) {
-      give += max(s[i].held - s[i].need, 0);
-      take += max(s[i].need - s[i].held, 0);
-    }
+    moved[0] = plus(moved[0], max(s[i].held - s[i].need, 0));
+    moved[1] = plus(moved[1], max(s[i].need - s[i].held, 0));
   }
-  int64_t all_give, all_take;
-  int64_t g = block_scan(give, sums, &all_give), k = block_scan(take, sums, &all_take);
-  int F = *p.free_count;
+  block_scan<2>(moved, all, sums);
+  int g = moved[0], k = moved[1];
   if (F < 0 || F > p.num_pages) {
     bad = true;
     F = min(max(F, 0), p.num_pages);
   }
   // more pages than there are: some are held or free twice, and nothing is moved
-  const bool broken = F + all_give > p.num_pages;
+  const bool broken = F + all[0] > p.num_pages;
   bad |= broken;
-  const int R = broken ? 0 : (int)all_give;
-  const int64_t room = broken ? 0 : (int64_t)F + R;
-  int64_t units = 0;
+  const int R = broken ? 0 : all[0], room = broken ? 0 : F + R;
+  int units[1] = {0}, all_units[1];
   bool short_of = false;
-  int gives[kPerThread], takes[kPerThread], count[kPerThread], most = 0;
+  int gives[kPer], count[kPer], most = 0;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = b0 + i;
-    if (i >= per || b >= p.B) continue;
-    const int back = max(s[i].held - s[i].need, 0), more = max(s[i].need - s[i].held, 0);
-    const bool valid = !s[i].refused;
-    gives[i] = broken ? 0 : (int)g;
-    takes[i] = (int)min(k, room);
-    g += back;
-    k += more;
-    bool refused = !valid || broken;
-    if (valid && more > 0 && k > room) {
-      refused = true;
-      short_of |= !broken;
+  for (int i = 0; i < kPer; ++i) {
+    const int held = s[i].held, back = max(held - s[i].need, 0), more = max(s[i].need - held, 0);
+    gives[i] = broken ? 0 : g;
+    s[i].taken = k;
+    g = plus(g, back);
+    k = plus(k, more);
+    if (more > 0 && !broken) {
+      if (k > room) {
+        s[i].refused = 1;
+        short_of = true;
+      } else {
+        most = k;
+      }
     }
-    if (valid && more > 0 && !refused) most = (int)k;
-    const int held = s[i].held;
-    if (refused) s[i].need = s[i].held;
-    s[i].refused = refused;
-    const int n = s[i].end - s[i].pos0, first = n > 0 ? s[i].pos0 / p.page_size : INT32_MAX;
-    int u0 = first, u1 = n > 0 ? (s[i].end + p.page_size - 1) / p.page_size : 0;
-    if (!refused && more > 0) {
+    if (broken) s[i].refused = 1;
+    if (s[i].refused) {
+      s[i].need = held;
+    } else if (s[i].need != held) {
+      p.held[b0 + i] = s[i].need;
+    }
+    const int n = s[i].end - s[i].pos0;
+    int u0 = n > 0 ? s[i].pos0 >> shift : INT32_MAX, u1 = n > 0 ? (s[i].end + round) >> shift : 0;
+    if (s[i].need > held) {
       u0 = min(u0, held);
       u1 = max(u1, s[i].need);
     }
     s[i].page0 = u0;
     count[i] = max(u1 - u0, 0);
-    units += count[i];
-    if (valid && !refused && s[i].need != held) p.held[b] = s[i].need;
+    units[0] = plus(units[0], count[i]);
   }
   if (most > 0) atomicMax(&served, most);
-  int64_t all_units;
-  int64_t u = block_scan(units, sums, &all_units);
+  block_scan<1>(units, all_units, unit_sums);
+  int u = units[0];
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const int b = b0 + i;
-    if (i >= per || b >= p.B) continue;
-    w.give[b] = gives[i];
-    w.take[b] = takes[i];
-    w.unit[b] = (int)u;
-    w.seq[b] = s[i];
-    u += count[i];
+    if (b < p.B) {
+      if (kAll) {
+        give[b] = gives[i];
+        unit[b] = u;
+      } else {
+        w.give[b] = gives[i];
+        w.unit[b] = u;
+      }
+      w.seq[b] = s[i];
+    }
+    u = plus(u, count[i]);
   }
   if (tid == 0) {
     w.total[0] = F;
     w.total[1] = R;
     w.total[2] = served;
-    w.total[3] = (int)all_units;
+    w.total[3] = all_units[0];
     if (R != served) *p.free_count = F + R - served;
   }
   if (short_of) report_error(err_word, MLA_ERR_NO_PAGES);
   else if (bad) report_error(err_word, MLA_ERR_BOUNDS);
   if (kAll) {
     __syncthreads();
-    deal_pages(p, w, tid, kThreads, err_word);
+    deal_pages(p, w, give, unit, tid, kThreads, err_word);
   }
 }
 
 __global__ void __launch_bounds__(kGridThreads)
 update_pages_deal(Pages p, Work w, int32_t* err_word) {
+  extern __shared__ int32_t prefix[];
+  int32_t *give = prefix, *unit = prefix + p.B;
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
-  deal_pages(p, w, blockIdx.x * kGridThreads + threadIdx.x, gridDim.x * kGridThreads, err_word);
+  for (int b = threadIdx.x; b < p.B; b += kGridThreads) {
+    give[b] = w.give[b];
+    unit[b] = w.unit[b];
+  }
+  __syncthreads();
+  deal_pages(p, w, give, unit, blockIdx.x * kGridThreads + threadIdx.x, gridDim.x * kGridThreads, err_word);
 }
 
 }  // namespace
@@ -278,10 +301,13 @@ cudaError_t launch_update_pages(const Pages& p, void* workspace, int32_t* err_wo
   Work w;
   work_layout(workspace, p.B, &w);
   if (p.n_rows <= kSmallRows && p.B <= kSmallBatch)
-    return launch_pdl(update_pages_scan<true>, dim3(1), dim3(kThreads), 0, s, p, w, err_word);
-  cudaError_t e = launch_pdl(update_pages_scan<false>, dim3(1), dim3(kThreads), 0, s, p, w, err_word);
+    return launch_pdl(update_pages_scan<1, true>, dim3(1), dim3(kThreads), 0, s, p, w, err_word);
+  const auto scan = p.B <= kThreads       ? update_pages_scan<1, false>
+                    : p.B <= 2 * kThreads ? update_pages_scan<2, false>
+                                          : update_pages_scan<4, false>;
+  cudaError_t e = launch_pdl(scan, dim3(1), dim3(kThreads), 0, s, p, w, err_word);
   if (e != cudaSuccess) return e;
-  return launch_pdl(update_pages_deal, dim3(2 * 152), dim3(kGridThreads), 0, s, p, w, err_word);
+  return launch_pdl(update_pages_deal, dim3(2 * 152), dim3(kGridThreads), 8 * (size_t)p.B, s, p, w, err_word);
 }
 
 }  // namespace mla

@@ -7,10 +7,10 @@
 // 2^(before - e). What is not finite becomes the NaN code and does not count in e.
 //
 // HBM-bound for prompts (1152 bytes read, 576 written a token), latency-bound for a
-// decode step's one row a sequence. A CTA owns 64 positions of one sequence (a tile:
-// whole blocks), so a power is decided in one place and no two CTAs write one entry: its
-// rows are read once into registers, the magnitudes meet in shared memory, and the
-// codes are written from the registers. CTA c belongs to the last sequence b with
+// decode step's one row a sequence. A CTA owns one group of columns at 64 positions of one
+// sequence (a tile: whole blocks), so a power is decided in one place and no two CTAs write one
+// byte: its values are read once into registers, the magnitudes meet in shared memory, and
+// the codes are written from the registers. CTA c of a group belongs to the last sequence b with
 // cu[b] / 64 + 2b <= c: a run of n rows touches at most n / 64 + 2 tiles, so every
 // tile has a CTA without a plan on the device before (the CTAs left over end at once).
 #include "blocks.cuh"
@@ -19,25 +19,37 @@
 namespace mla {
 namespace {
 
-constexpr int kChunks = kRow / 8;              // 72 chunks of 8 columns per row
-constexpr int kRowsAtOnce = 4;
-constexpr int kThreads = kChunks * kRowsAtOnce;  // 288
-constexpr int kPer = kTile / kRowsAtOnce;      // rows of a tile per thread
-constexpr int kSub = kTile / 16;               // a block is at least 16 tokens: four rows of a thread
+constexpr int kChunks = kRow / 8;  // 72 chunks of 8 columns per row
+constexpr int kThreads = 128;
+constexpr int kSub = kTile / 16;   // a block is at least 16 tokens
+static_assert(kGroups == 5, "four groups of 16 chunks, one of 8");
 
-// the last sequence whose first CTA is at or before c, by all lanes of a warp: each
-// round cuts the candidates by 32. Inside [0, B) whatever cu holds.
-__device__ __forceinline__ int sequence_of_cta(const int32_t* __restrict__ cu, int B, int c) {
+struct Rows {
+  int b, first, end, L;  // the sequence, its rows of the array, its context
+};
+// The last sequence whose first CTA is at or before c, by all lanes of a warp: a round cuts the
+// candidates by 32, the last one brings what is needed of the sequence along. Inside [0, B) whatever cu holds.
+__device__ __forceinline__ Rows sequence_of_cta(const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_lens, int B,
+                                                int c) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = B;
-  while (n > 1) {
+  while (n > 32) {
     const int step = (n + 31) / 32, at = lane * step;
     const bool before = at < n && (__ldg(cu + lo + at) >> 6) + 2 * (lo + at) <= c;
     const int k = max(__popc(__ballot_sync(0xffffffffu, before)) - 1, 0);
     lo += k * step;
     n = min(step, n - k * step);
   }
-  return lo;
+  Rows r = {lo + min(lane, n - 1), 0, 0, 0};
+  r.first = __ldg(cu + r.b);
+  r.end = __ldg(cu + r.b + 1);
+  r.L = __ldg(seq_lens + r.b);
+  const int k = max(__popc(__ballot_sync(0xffffffffu, lane < n && (r.first >> 6) + 2 * r.b <= c)) - 1, 0);
+  r.b = lo + k;
+  r.first = __shfl_sync(0xffffffffu, r.first, k);
+  r.end = __shfl_sync(0xffffffffu, r.end, k);
+  r.L = __shfl_sync(0xffffffffu, r.L, k);
+  return r;
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -53,120 +65,146 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
 // 0x8000 in each half that is infinite or NaN (bf16 pair)
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
 
-__global__ void __launch_bounds__(kThreads)
-write_kv_kernel(const uint4* __restrict__ rows, uint8_t* __restrict__ cache, uint8_t* __restrict__ entries, int shift,
-                const int32_t* __restrict__ block_table, const int32_t* __restrict__ seq_lens,
-                const int32_t* __restrict__ cu, int B, int T, int num_pages, int page_size, int max_pages,
-                int32_t* err_word) {
-  __shared__ uint32_t top[kSub][kEntryBytes];    // largest magnitude of block j's new rows, bf16 bits
-  __shared__ uint32_t power[kSub][kEntryBytes];  // the block's powers from now on
-  __shared__ uint32_t before[kSub][kEntryBytes];  // ... and those of its older tokens' codes
-  const int tid = threadIdx.x;
-  if (tid < kSub * kEntryBytes) top[tid / kEntryBytes][tid % kEntryBytes] = 0;
-  sm100::grid_dependency_wait();
-  sm100::grid_launch_dependents();
-  if (blockIdx.x == 0) report_rows(cu, B, T, tid, kThreads, err_word);
-  const int b = sequence_of_cta(cu, B, blockIdx.x);
-  const int first = __ldg(cu + b), end = __ldg(cu + b + 1), n = end - first, L = __ldg(seq_lens + b);
-  const int tile = blockIdx.x - ((first >> 6) + 2 * b);  // of those of this sequence's new rows
-  if (tile < 0 || n <= 0) return;
-  if (first < 0 || end > T || L < n || L > max_pages * page_size) {  // nothing of it is written
-    if (tile == 0 && tid == 0) report_error(err_word, MLA_ERR_BOUNDS);
-    return;
-  }
-  const int p0 = L - n, t0 = (p0 / kTile + tile) * kTile;  // the first new position; the tile's first
-  if (t0 >= L) return;
-  const int lo = max(p0 - t0, 0), hi = min(L - t0, kTile);  // new rows of the tile
-  const int page = __ldg(block_table + (int64_t)b * max_pages + t0 / page_size);
-  if (page < 0 || page >= num_pages) {
-    if (tid == 0) report_error(err_word, MLA_ERR_BOUNDS);
-    return;
-  }
-  const int64_t row0 = (int64_t)page * page_size + t0 % page_size;  // of the pool
-  uint8_t* entry = entries + ((row0 >> shift) << 3);
+// What a CTA knows before it reads its rows.
+struct Tile {
+  const uint4* src;       // the group's first chunk at the tile's first position (rows before `lo` are not read)
+  const int32_t* page;    // the tile's page, read beside the rows
+  int64_t row;            // the tile's row in its page
+  int lo, hi;             // the tile's new rows
+  bool older;             // tokens older than the chunk lie in the block of row lo
+};
+struct Cache {
+  uint8_t *codes, *entries;
+  int shift, num_pages, page_size;
+};
 
-  const int g = tid % kChunks, r0 = tid / kChunks;
-  const int group = g < 64 ? g >> 4 : 4;
-  const uint4* src = rows + ((int64_t)first + t0 - p0) * kChunks + g;
+// kWide: chunks of the group in a row
+template <int kWide>
+__device__ __forceinline__ void write_tile(const Tile& tile, const Cache& cache, int group, uint32_t* top, uint32_t* power,
+                                           uint32_t* before, int32_t* err_word) {
+  constexpr int kAtOnce = kThreads / kWide, kPer = kTile / kAtOnce;  // rows of a pass, passes
+  const int tid = threadIdx.x, r0 = tid / kWide, c = tid % kWide, shift = cache.shift;
+  const uint4* src = tile.src + c;
+  const int lo = tile.lo, hi = tile.hi;
+  const int page = __ldg(tile.page);
   uint4 v[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const int r = kRowsAtOnce * k + r0;
+    const int r = kAtOnce * k + r0;
     v[k] = r >= lo && r < hi ? __ldg(src + (int64_t)r * kChunks) : make_uint4(0, 0, 0, 0);
   }
+  if (page < 0 || page >= cache.num_pages) {
+    if (tid == 0) report_error(err_word, MLA_ERR_BOUNDS);
+    return;
+  }
+  const int64_t row0 = (int64_t)page * cache.page_size + tile.row;  // of the pool
+  uint2* dst = reinterpret_cast<uint2*>(cache.codes + row0 * kRow) + 16 * group + c;
+  // thread j < blocks of a tile: its block's entry
+  uint8_t* entry = cache.entries + ((row0 >> shift) + tid) * kEntryBytes + group;
+  const int at = tid << shift;
+  const bool owner = tid < kTile >> shift && max(at, lo) < min(at + (1 << shift), hi);
+  uint32_t old = 0;
+  if (owner && at < lo && tile.older) old = *entry;
   uint32_t m[kSub];  // this thread's largest magnitudes of 16 positions (bf16 pairs)
 #pragma unroll
-  for (int j = 0; j < kSub; ++j) {
-    m[j] = 0;
+  for (int j = 0; j < kSub; ++j) m[j] = 0;
 #pragma unroll
-    for (int k = 4 * j; k < 4 * j + 4; ++k) {
-      uint32_t* w = &v[k].x;
+  for (int k = 0; k < kPer; ++k) {
+    uint32_t* w = &v[k].x;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t bad = not_finite(w[q]);
-        w[q] |= bad - (bad >> 15);  // 0x7FFF: infinities are stored as NaN
-        m[j] = __vmaxu2(m[j], w[q] & 0x7FFF7FFFu & ~((bad >> 15) * 0xFFFFu));
-      }
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t bad = not_finite(w[q]);
+      w[q] |= bad - (bad >> 15);  // 0x7FFF: infinities are stored as NaN
+      uint32_t& mj = m[k * kAtOnce / 16];
+      mj = __vmaxu2(mj, w[q] & 0x7FFF7FFFu & ~((bad >> 15) * 0xFFFFu));
     }
-    m[j] = max(m[j] & 0xFFFFu, m[j] >> 16);
   }
-  // over the eight threads of 64 columns of a row (part of one group, and of one warp)
-  uint32_t m01 = m[0] | m[1] << 16, m23 = m[2] | m[3] << 16;
+  uint32_t m01 = __vmaxu2(m[0] & 0xFFFFu, m[0] >> 16) | __vmaxu2(m[1] & 0xFFFFu, m[1] >> 16) << 16;
+  uint32_t m23 = __vmaxu2(m[2] & 0xFFFFu, m[2] >> 16) | __vmaxu2(m[3] & 0xFFFFu, m[3] >> 16) << 16;
 #pragma unroll
-  for (int d = 1; d < 8; d <<= 1) {
+  for (int d = 1; d < 32; d <<= 1) {
     m01 = __vmaxu2(m01, __shfl_xor_sync(0xffffffffu, m01, d));
     m23 = __vmaxu2(m23, __shfl_xor_sync(0xffffffffu, m23, d));
   }
-  __syncthreads();
-  if ((tid & 7) == 0) {
-    atomicMax(&top[0][group], m01 & 0xFFFFu);
-    atomicMax(&top[16 >> shift][group], m01 >> 16);
-    atomicMax(&top[32 >> shift][group], m23 & 0xFFFFu);
-    atomicMax(&top[48 >> shift][group], m23 >> 16);
+  if ((tid & 31) == 0) {
+    atomicMax(top, m01 & 0xFFFFu);
+    atomicMax(top + (16 >> shift), m01 >> 16);
+    atomicMax(top + (32 >> shift), m23 & 0xFFFFu);
+    atomicMax(top + (48 >> shift), m23 >> 16);
   }
   __syncthreads();
-  if (tid < (kTile >> shift) * kEntryBytes) {
-    const int j = tid / kEntryBytes, e = tid % kEntryBytes, at = j << shift;
-    if (max(at, lo) < min(at + (1 << shift), hi)) {
-      uint32_t p = e < kGroups ? power_of(top[j][e] << 16) : 0u, old = p;
-      if (e < kGroups && at < lo && t0 + at < p0) {  // the block holds older tokens
-        old = entry[tid];
-        p = max(p, old);
-      }
-      power[j][e] = p;
-      before[j][e] = old;
-      entry[tid] = (uint8_t)p;
-    }
+  if (owner) {
+    const uint32_t p = max(power_of(top[tid] << 16), old);
+    power[tid] = p;
+    before[tid] = at < lo && tile.older ? old : p;
+    *entry = (uint8_t)p;
+    if (group == kGroups - 1)
+      for (int k = 1; k <= kEntryBytes - kGroups; ++k) entry[k] = 0;
   }
   __syncthreads();
-  uint2* dst = reinterpret_cast<uint2*>(cache + row0 * kRow) + g;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    const int r = kRowsAtOnce * k + r0;
+    const int r = kAtOnce * k + r0;
     if (r >= lo && r < hi) {
-      const float inv = inverse_step_of(power[r >> shift][group]);
+      const float inv = inverse_step_of(power[r >> shift]);
       const uint32_t* w = &v[k].x;
-      uint32_t c[4];
+      uint32_t e[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) c[q] = e4m3x2(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
-      dst[(int64_t)r * kChunks] = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+      for (int q = 0; q < 4; ++q) e[q] = e4m3x2(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
+      dst[(int64_t)r * kChunks] = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
     }
   }
-  // the older tokens of the block in which the new rows start
+  // the older tokens of the block in which the new rows start, where its power grew
   const int start = lo >> shift << shift;
-  if (t0 + lo == p0 && start < lo) {
-    const uint32_t now = power[lo >> shift][group], old = before[lo >> shift][group];
-    if (now != old) {  // now is the larger
+  if (tile.older && start < lo) {
+    const uint32_t now = power[lo >> shift], old = before[lo >> shift];
+    if (now != old) {
       const float f = now - old < 127 ? step_of(127 + old - now) : 0.f;
-      for (int r = start + r0; r < lo; r += kRowsAtOnce) {
+      for (int r = start + r0; r < lo; r += kAtOnce) {
         const uint2 w = dst[(int64_t)r * kChunks];
-        const float2 a = from_e4m3x2(w.x & 0xFFFFu), b2 = from_e4m3x2(w.x >> 16), c = from_e4m3x2(w.y & 0xFFFFu),
-                     d = from_e4m3x2(w.y >> 16);
-        dst[(int64_t)r * kChunks] = make_uint2(e4m3x2(a.x * f, a.y * f) | e4m3x2(b2.x * f, b2.y * f) << 16,
-                                               e4m3x2(c.x * f, c.y * f) | e4m3x2(d.x * f, d.y * f) << 16);
+        const float2 e0 = from_e4m3x2(w.x & 0xFFFFu), e1 = from_e4m3x2(w.x >> 16), e2 = from_e4m3x2(w.y & 0xFFFFu),
+                     e3 = from_e4m3x2(w.y >> 16);
+        dst[(int64_t)r * kChunks] = make_uint2(e4m3x2(e0.x * f, e0.y * f) | e4m3x2(e1.x * f, e1.y * f) << 16,
+                                               e4m3x2(e2.x * f, e2.y * f) | e4m3x2(e3.x * f, e3.y * f) << 16);
       }
     }
   }
+}
+
+__global__ void __launch_bounds__(kThreads)
+write_kv_kernel(const uint4* __restrict__ rows, Cache cache, const int32_t* __restrict__ block_table,
+                const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ cu, int B, int T, int max_pages,
+                int32_t* err_word) {
+  __shared__ uint32_t top[kSub];     // largest magnitude of block j's new rows, bf16 bits
+  __shared__ uint32_t power[kSub];   // the block's power from now on
+  __shared__ uint32_t before[kSub];  // ... and that of its older tokens' codes
+  const int tid = threadIdx.x, cta = blockIdx.x / kGroups, group = blockIdx.x % kGroups;
+  if (tid < kSub) top[tid] = 0;
+  sm100::grid_dependency_wait();
+  sm100::grid_launch_dependents();
+  if (blockIdx.x == 0) report_rows(cu, B, T, tid, kThreads, err_word);
+  const Rows s = sequence_of_cta(cu, seq_lens, B, cta);
+  const int n = s.end - s.first;
+  const int number = cta - ((s.first >> 6) + 2 * s.b);  // of the tiles of this sequence's new rows
+  if (number < 0 || n <= 0) return;
+  if (s.first < 0 || s.end > T || s.L < n || s.L > max_pages * cache.page_size) {  // nothing of it is written
+    if (number == 0 && tid == 0) report_error(err_word, MLA_ERR_BOUNDS);
+    return;
+  }
+  const int p0 = s.L - n, t0 = (p0 / kTile + number) * kTile;  // the first new position; the tile's first
+  if (t0 >= s.L) return;
+  Tile tile;
+  tile.src = rows + ((int64_t)s.first + t0 - p0) * kChunks + 16 * group;
+  tile.page = block_table + (int64_t)s.b * max_pages + t0 / cache.page_size;
+  tile.row = t0 % cache.page_size;
+  tile.lo = max(p0 - t0, 0);
+  tile.hi = min(s.L - t0, kTile);
+  tile.older = p0 > t0;
+  __syncthreads();  // top is cleared
+  if (group < kGroups - 1)
+    write_tile<16>(tile, cache, group, top, power, before, err_word);
+  else
+    write_tile<8>(tile, cache, group, top, power, before, err_word);
 }
 
 }  // namespace
@@ -174,9 +212,9 @@ write_kv_kernel(const uint4* __restrict__ rows, uint8_t* __restrict__ cache, uin
 cudaError_t launch_write_kv(const uint16_t* rows, uint8_t* cache, const BlockScales& scales, const int32_t* block_table,
                             const int32_t* seq_lens, const int32_t* cu, int B, int T, int num_pages, int page_size,
                             int max_pages, int32_t* err_word, cudaStream_t s) {
-  return launch_pdl(write_kv_kernel, dim3(T / kTile + 2 * B), dim3(kThreads), 0, s, reinterpret_cast<const uint4*>(rows),
-                    cache, scales.entries, scales.shift, block_table, seq_lens, cu, B, T, num_pages, page_size,
-                    max_pages, err_word);
+  const Cache to = {cache, scales.entries, scales.shift, num_pages, page_size};
+  return launch_pdl(write_kv_kernel, dim3(kGroups * (T / kTile + 2 * B)), dim3(kThreads), 0, s,
+                    reinterpret_cast<const uint4*>(rows), to, block_table, seq_lens, cu, B, T, max_pages, err_word);
 }
 
 }  // namespace mla
