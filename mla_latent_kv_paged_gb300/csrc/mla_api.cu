@@ -445,12 +445,15 @@ int chunk_head_group(int H, int64_t cap) {
 // n = c H L / (L + 950), c = 1.37 (bf16) or 1.0 (FP8). Both sides at H = 128, bf16
 // (absorbed / expanded): L = 512: n = 32 35/44, 64 48/44; L = 4096: n = 128 162/184,
 // 160 203/191; L = 16384: n = 160 603/655, 192 714/659; FP8, L = 4096: n = 96 172/195,
-// 128 216/197; H = 16, L = 16384: n = 16 84/111, 32 139/112.
-int chunk_form(int form, int B, int T, int H, int64_t max_tokens, bool fp8) {
+// 128 216/197; H = 16, L = 16384: n = 16 84/111, 32 139/112. With block scales c = 1.12,
+// H = 128: L = 512: n = 48 38/39, 64 42/39; L = 4096: n = 112 161/166, 128 180/167; L = 16384:
+// n = 128 566/576, 160 712/598; H = 16, L = 16384: n = 16 99/112, 24 126/103.
+enum CacheKind { kBf16Cache, kColumnScales, kBlockScales };
+int chunk_form(int form, int B, int T, int H, int64_t max_tokens, CacheKind kind) {
   if (form != MLA_CHUNK_AUTO) return form;
   const double L = (double)max_tokens / B, n = (double)T / B;
-  return T <= MLA_MAX_BATCH && n * (L + 950.0) <= (fp8 ? 1.0 : 1.37) * H * L ? MLA_CHUNK_ABSORBED
-                                                                           : MLA_CHUNK_EXPANDED;
+  const double c = kind == kBf16Cache ? 1.37 : kind == kColumnScales ? 1.0 : 1.12;
+  return T <= MLA_MAX_BATCH && n * (L + 950.0) <= c * H * L ? MLA_CHUNK_ABSORBED : MLA_CHUNK_EXPANDED;
 }
 // bytes of workspace of a form that is not AUTO; 0 without a device
 size_t chunk_form_bytes(int form, int B, int T, int H, int64_t max_tokens) {
@@ -600,10 +603,14 @@ size_t mla_attend_chunk_workspace_bytes(int B, int T, int H, int64_t max_tokens,
   if (B < 1 || T < 1 || !chunk_counts_ok(B, T) || !heads_ok(H) || max_tokens < 1 || max_tokens > kMaxTokens ||
       form < MLA_CHUNK_AUTO || form > MLA_CHUNK_ABSORBED)
     return 0;
-  // the larger of what the two kinds of cache need
-  const size_t a = chunk_form_bytes(chunk_form(form, B, T, H, max_tokens, false), B, T, H, max_tokens);
-  const size_t b = chunk_form_bytes(chunk_form(form, B, T, H, max_tokens, true), B, T, H, max_tokens);
-  return a == 0 || b == 0 ? 0 : a > b ? a : b;
+  // the largest of what the kinds of cache need
+  size_t most = 0;
+  for (const CacheKind kind : {kBf16Cache, kColumnScales, kBlockScales}) {
+    const size_t n = chunk_form_bytes(chunk_form(form, B, T, H, max_tokens, kind), B, T, H, max_tokens);
+    if (n == 0) return 0;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 namespace {
@@ -626,7 +633,7 @@ mla_status attend_rows(const uint16_t* q_nope, const uint16_t* q_rope, const uin
     return MLA_ERR_UNSUPPORTED_SHAPE;
   if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
   const int max_tokens_seq = max_pages_per_seq * page_size;
-  form = chunk_form(form, B, T, H, max_tokens, fp8_scales != nullptr);
+  form = chunk_form(form, B, T, H, max_tokens, blocks ? kBlockScales : fp8_scales ? kColumnScales : kBf16Cache);
   if (form == MLA_CHUNK_ABSORBED) {
     if (T > MLA_MAX_BATCH) return MLA_ERR_UNSUPPORTED_SHAPE;
     // the plan counts the tiles of all rows' contexts, each row's by itself, in 32 bits
