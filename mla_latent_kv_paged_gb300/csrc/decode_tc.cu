@@ -71,7 +71,7 @@ struct Roles {
   static constexpr int kRead0 = kBlocks ? 4 : 3, kSoft0 = kRead0 + kAWarps, kWide0 = kSoft0 + kBWarps;
   static constexpr int kThreads = kBlocks ? 32 * kWide0 + kWThreads : 96 + kAThreads + kBThreads;
 };
-constexpr int kRegsIssue = 48, kRegsRead = 96, kRegsSoftmax = 128, kRegsWiden = 40;
+constexpr int kRegsIssue = 48, kRegsRead = 96, kRegsSoftmax = 112, kRegsWiden = 56;
 static_assert(kRegsIssue + kRegsRead + 2 * kRegsSoftmax + 2 * kRegsWiden <= 6 * 80, "the launch's registers");
 constexpr uint32_t kCBoxBytes = 64 * 128;   // [64 tokens][64 latent cols] bf16, 128B swizzle
 constexpr uint32_t kKrBoxBytes = 64 * 64;   // [64 tokens][32 positional cols] bf16, 64B swizzle
@@ -326,7 +326,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
       for (int i = 0; i < kOpSlots; ++i) mbar_init(bar(EMPTY0 + i), 1);
       for (int i = 0; i < kCodeSlots; ++i) {
         mbar_init(bar(CF0 + i), 1 + kTile / 16);  // the copies of the codes and of the entries
-        mbar_init(bar(CE0 + i), kWThreads);
+        mbar_init(bar(CE0 + i), kWThreads / 32);
       }
     } else {
       for (int i = 0; i < kStages; ++i) {
@@ -356,7 +356,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
     mbar_init(bar(OFREE), 2 * kGThreads);        // both halves of O drained
     mbar_init(bar(MMAD), 2);  // both MMA issuers done
     if (kF8) {
-      for (int i = 0; i < kSlots; ++i) mbar_init(bar(CVF0 + i), kBlocks ? kWThreads : kAThreads);
+      for (int i = 0; i < kSlots; ++i) mbar_init(bar(CVF0 + i), kBlocks ? kWThreads / 32 : kAThreads);
       mbar_init(bar(CVR), kAThreads);
     }
     *abort_flag = 0;
@@ -1199,7 +1199,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             tma_load_2d(dst + m * kQBoxBytes, &map_q, fb, 256 * (int)rank + 128 * q + 64 * m, qrow, keep);
           tma_load_2d(dst + 2 * kQBoxBytes, &map_qkr, fb, kDC + 32 * (int)rank, qrow + 64 * q, keep);
           asked = slot + 1;
-        } else {
+        } else if ((wtid & 31) == 0) {
           mbar_arrive(fb);
         }
       }
@@ -1224,16 +1224,16 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           }
         };
         if (!next_slot()) break;
-#pragma unroll 1
+#pragma unroll 2
         for (uint32_t k = 0; k < 4; ++k) {
           const bool beyond = widen16(v, k < 2 ? by0 : by1, k < 2 ? pw & 0xFFu : pw >> 8, o);
           if (k < 3 || wtid < 128) ld_shared_v4(sc + 4096 * (k + 1), v[0], v[1], v[2], v[3]);  // the next chunk
           put(dst + k * kCBoxBytes + w0, dst + k * kCBoxBytes + w1, beyond, t);
         }
         if (wtid < 128) put(dst + x0, dst + x1, widen16(v, power_f16x2(pr), pr, o), tr);
-        mbar_arrive(bar(CE0 + cs));
         fence_proxy_async_smem();  // read by the MMAs (async proxy)
-        mbar_arrive(bar(CVF0 + slot % kOpSlots));
+        __syncwarp();
+        if ((wtid & 31) == 0) { mbar_arrive(bar(CE0 + cs)); mbar_arrive(bar(CVF0 + slot % kOpSlots)); }
       }
     }
     if (!ok && wtid == 0) {
