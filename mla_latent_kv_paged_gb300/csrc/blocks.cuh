@@ -59,6 +59,12 @@ cudaError_t launch_decode_blocks(const uint16_t* q_abs, bool q_f16, const uint8_
                                  int max_pages, float scale, int G, const Plan& plan, int32_t* err_word,
                                  cudaStream_t s);
 
+#if MLA_DEBUG_CHECKS
+// Test builds only: the wait limit, the producer switch and the counters (n < 0: set to zero) of the
+// block-scaled decode (null: as they are).
+cudaError_t debug_decode_blocks(const long long* limit, const int* skip_producer, unsigned long long* counters, int n);
+#endif
+
 // Page tables (update_pages.cu)
 struct Pages {
   int32_t* block_table;   // [B][max_pages]

@@ -60,19 +60,6 @@ constexpr int kBWarps = 8;  // softmax: two groups of four (one per lane quadran
 constexpr int kAThreads = kAWarps * 32, kBThreads = kBWarps * 32;
 constexpr int kGThreads = kBThreads / 2;  // one softmax group: a thread per head row
 constexpr int kThreads = 96 + kAThreads + kBThreads;
-// Where the roles lie. On a block-scaled cache eight warps of their own widen the codes: the score
-// readers, which do it on a cache with column scales, have no time left for the powers (138 us
-// for the step of 32 x 4096). Every role then is a warpgroup of its own (an idle warp 3, score
-// readers 4..7, softmax 8..15, wideners 16..23) and registers are dealt out by role, from the
-// launch's 80 a thread.
-constexpr int kWThreads = 8 * 32;
-template <bool kBlocks>
-struct Roles {
-  static constexpr int kRead0 = kBlocks ? 4 : 3, kSoft0 = kRead0 + kAWarps, kWide0 = kSoft0 + kBWarps;
-  static constexpr int kThreads = kBlocks ? 32 * kWide0 + kWThreads : 96 + kAThreads + kBThreads;
-};
-constexpr int kRegsIssue = 48, kRegsRead = 96, kRegsSoftmax = 112, kRegsWiden = 56;
-static_assert(kRegsIssue + kRegsRead + 2 * kRegsSoftmax + 2 * kRegsWiden <= 6 * 80, "the launch's registers");
 constexpr uint32_t kCBoxBytes = 64 * 128;   // [64 tokens][64 latent cols] bf16, 128B swizzle
 constexpr uint32_t kKrBoxBytes = 64 * 64;   // [64 tokens][32 positional cols] bf16, 64B swizzle
 constexpr uint32_t kStageBytes = 4 * kCBoxBytes + kKrBoxBytes;  // 36864
@@ -96,10 +83,7 @@ constexpr uint32_t kF8CBoxBytes = 64 * 64;   // [64 tokens][64 latent cols] e4m3
 constexpr uint32_t kF8KrBoxBytes = 16 * 32;  // [16 tokens][32 positional cols] e4m3, four per page half
 constexpr uint32_t kF8StageBytes = 4 * kF8CBoxBytes + 4 * kF8KrBoxBytes;  // 18432
 constexpr uint32_t kF8Off = kStageBytes - kF8StageBytes;              // 18432
-// Block scales: four operand slots (queries and widened pages) and, in the fifth slot's place, two
-// slots of codes, which are free again as soon as they are widened.
-constexpr int kOpSlots = 4, kCodeSlots = 2;
-static_assert(kCodeSlots * kF8StageBytes <= (kStages - kOpSlots) * kStageBytes, "the slots of codes");
+constexpr int kF8Chunks = kF8StageBytes / 16;  // 16-byte chunks of a page half: 1152
 
 constexpr uint32_t kOffStage = 0;
 constexpr uint32_t kOffX = kOffStage + kStages * kStageBytes;  // peer partial scores, one buffer per group
@@ -125,15 +109,10 @@ enum {
   // (every use of a slot completes it once, so its phases follow FULL's); CVR =
   // every score reader has read its share of the codes of the page being expanded
   CVF0 = MMAD + 1, CVR = CVF0 + kStages,
-  kNumBars = CVR + 1,
-  // block scales: CVF as above (an operand slot filled, by the wideners or with a query), and the
-  // codes' slots filled (CF) and widened (CE)
-  CF0 = FULL0, CE0 = CF0 + kCodeSlots
+  kNumBars = CVR + 1
 };
 constexpr uint32_t kOffSlots = kOffBar + kNumBars * 8;
-constexpr uint32_t kOffEntries = (kOffSlots + 15) / 16 * 16 + 16;  // block scales: the tile's 8-byte entries
-constexpr uint32_t kEntryStage = kTile / 16 * kEntryBytes;         // of a slot of codes (blocks of 16 tokens or more)
-constexpr uint32_t kSmemBytes = kOffEntries + kCodeSlots * kEntryStage;  // the base is checked to be 1024-byte aligned
+constexpr uint32_t kSmemBytes = kOffSlots + 16;  // the base is checked to be 1024-byte aligned
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(2 * kQBoxBytes + kQrBoxBytes <= kStageBytes, "a ring slot holds a query quarter");
 
@@ -187,110 +166,18 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
-// Block scales: 16 codes times 2^(p - 127), as fp16 pairs. Exact but below fp16's normal range
-// (2^-14), where the product is rounded to 2^-24's multiples. fp16 holds the powers 2^-24 .. 2^15:
-// one below takes a second product, one above stands for values that fp16 does not hold. Returns
-// whether one of the values became infinite.
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-constexpr uint32_t kLeastF16 = 127 - 24, kMostF16 = 127 + 15, kSafeF16 = 127 + 7;  // 448 * 2^7 < 65504
-__device__ __forceinline__ uint32_t power_f16x2(uint32_t p) {
-  const float step = step_of(min(max(p, kLeastF16), kMostF16));
-  return cvt_f16x2(step, step);
-}
-// by: power_f16x2(p)
-__device__ __forceinline__ bool widen16(const uint32_t (&v)[4], uint32_t by, uint32_t p, uint32_t (&o)[8]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    e4m3x4_to_f16(v[c], o[2 * c], o[2 * c + 1]);
-    o[2 * c] = mul_f16x2(o[2 * c], by);
-    o[2 * c + 1] = mul_f16x2(o[2 * c + 1], by);
-  }
-  bool beyond = false;
-  if (__builtin_expect(p < kLeastF16 || p > kSafeF16, 0)) {
-    // what is left of the power (at most 2^15 of it: every value but zero then is infinite)
-    const float rest = step_of(p < kLeastF16 ? p + 24 : p > kMostF16 ? min(p - 15, kMostF16) : 127);
-    const uint32_t more = cvt_f16x2(rest, rest);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      o[c] = mul_f16x2(o[c], more);
-      beyond |= (o[c] & 0x7FFFu) == 0x7C00u || (o[c] & 0x7FFF0000u) == 0x7C000000u;
-    }
-  }
-  return beyond;
-}
 // bf16 pair times two scales, as an fp16 pair
 __device__ __forceinline__ uint32_t scale_bf16x2_to_f16x2(uint32_t w, float s0, float s1) {
   return cvt_f16x2(bf16_lo(w) * s0, bf16_hi(w) * s1);
 }
 
-// Pairs of fp32 in one instruction, and the largest or smallest of three. The block-scaled
-// kernel's score readers and softmax use them to be short: more roles share the instruction
-// caches there (62.9 us without, for the step of 32 x 4096).
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float r;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// an fp16 pair's two values, each plus c
-__device__ __forceinline__ uint64_t f16x2_plus(uint32_t w, float c) {
-  float lo, hi;
-  asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tadd.rn.f32.f16 %0, l, %3;\n\tadd.rn.f32.f16 %1, h, %3;\n\t}"
-      : "=f"(lo), "=f"(hi)
-      : "r"(w), "f"(c));
-  return pair(lo, hi);
-}
-// A head's query, from bf16 to fp16; what fp16 does not hold is reported.
-template <int kN>
-__device__ __forceinline__ void query_f16(uint32_t (&r)[kN], bool live, int32_t* err_word) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int k = 0; k < kN; ++k) {
-    top = max(top, max((r[k] << 16) & 0x7FFFFFFFu, r[k] & 0x7FFF0000u));
-    r[k] = cvt_f16x2(bf16_lo(r[k]), bf16_hi(r[k]));
-  }
-  if (live && top >= kF16Limit && top < 0x7F800000u) report_error(err_word, MLA_ERR_RANGE);
-}
-// kBlocks (with kF8): codes with a power of two for each block of tokens and group of columns
-// (blocks.cuh). The widening to fp16 applies the powers; the query is rounded from bf16 to fp16
-// as it is. (As bf16 pairs, which hold every power, a code took three times the instructions:
-// 72 us for the step of 32 x 4096.)
-//
 // kRows: the sequences are rows of a chunk (chunk.cuh): seq_row[b] is the block-table
 // row of sequence b, -1 for a row of no sequence (it reads zeros and its result is
 // not used); on an FP8 cache the absorbed query comes in fp16 and scaled. A template
 // parameter, because any change to the plain kernel's code costs it a few per cent
 // (decode call 38.8 -> 39.5 us with a run-time test).
-template <bool kF8, bool kRows, bool kBlocks>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Roles<kBlocks>::kThreads, 1)
+template <bool kF8, bool kRows>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constant__ CUtensorMap map_kr,
                  const __grid_constant__ CUtensorMap map_qkr, const __grid_constant__ CUtensorMap map_q,
                  const int32_t* __restrict__ block_table, int n_q, int H, int max_pages, int num_pages,
@@ -298,41 +185,21 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
                  const int32_t* __restrict__ seq_row) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  constexpr bool kCol = kF8 && !kBlocks;  // a scale per column, fp16 operands
-  constexpr int kSlots = kBlocks ? kOpSlots : kStages;
-  using R = Roles<kBlocks>;
-  const uint8_t* entries = reinterpret_cast<const uint8_t*>(fp8_scales);  // with kBlocks
-  const int block_shift = kBlocks ? tile_shift >> 8 & 0xFF : 0;           // (the launch packs these)
-  const bool q_f16 = kBlocks && (kRows || tile_shift >> 16);
-  if (kBlocks) tile_shift &= 0xFF;
   if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
     if (threadIdx.x == 0) report_error(err_word, MLA_ERR_CUDA);
     return;
   }
-  const int warp = kRows || kBlocks ? warp_index() : threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = kRows ? warp_index() : threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank(), peer = rank ^ 1u;
   const int worker = blockIdx.x >> 1, j = blockIdx.y;
   auto bar = [&](int i) -> uint32_t { return sbase + kOffBar + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffSlots + 4);
 
-  auto wait = [&](uint32_t b, uint32_t parity) -> bool {
-    if constexpr (kBlocks) return wait_short(b, parity, abort_flag);
-    return wait_phase(b, parity, abort_flag, err_word);
-  };
-
   if (threadIdx.x == 0) {
-    if (kBlocks) {
-      for (int i = 0; i < kOpSlots; ++i) mbar_init(bar(EMPTY0 + i), 1);
-      for (int i = 0; i < kCodeSlots; ++i) {
-        mbar_init(bar(CF0 + i), 1 + kTile / 16);  // the copies of the codes and of the entries
-        mbar_init(bar(CE0 + i), kWThreads / 32);
-      }
-    } else {
-      for (int i = 0; i < kStages; ++i) {
-        mbar_init(bar(FULL0 + i), 1);
-        mbar_init(bar(EMPTY0 + i), 1);
-      }
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(FULL0 + i), 1);
+      mbar_init(bar(EMPTY0 + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(LXF0 + i), 1);
@@ -356,7 +223,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
     mbar_init(bar(OFREE), 2 * kGThreads);        // both halves of O drained
     mbar_init(bar(MMAD), 2);  // both MMA issuers done
     if (kF8) {
-      for (int i = 0; i < kSlots; ++i) mbar_init(bar(CVF0 + i), kBlocks ? kWThreads / 32 : kAThreads);
+      for (int i = 0; i < kStages; ++i) mbar_init(bar(CVF0 + i), kAThreads);
       mbar_init(bar(CVR), kAThreads);
     }
     *abort_flag = 0;
@@ -392,7 +259,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
   grid_launch_dependents();
   const int it0 = plan.range_item[worker], it1 = plan.range_item[worker + 1];
 
-  auto produce = [&]() {
+  if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
     // Loads this CTA's half of each page into the stage ring.
     const uint64_t pol_stream = policy_evict_first();
@@ -457,14 +324,14 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
     if (*reinterpret_cast<volatile int*>(&g_dbg_skip_producer)) ld.it = it1;  // load nothing
 #endif
     while (ok && ld.it < it1) {
-      if (!kBlocks && ld.pg == ld.pg0) {
+      if (ld.pg == ld.pg0) {
         // first page of a range: the CTA's half of its query into the next two
         // ring slots (the score readers move it into tensor memory). Slot q holds
         // latent boxes [128 heads][64] for columns 256r + 128q + {0, 64} and, in
         // its last 4 KB, positional rows [64q, 64q + 64) of columns 512 + 32r.
         const int qrow = (ld.seq * n_q + j) * H;
         for (int q = 0; q < kQSlots && ok; ++q) {
-          if (!wait(bar(EMPTY0 + stage), ph ^ 1u)) { ok = false; break; }
+          if (!wait_phase(bar(EMPTY0 + stage), ph ^ 1u, abort_flag, err_word)) { ok = false; break; }
           if (lane == 0 && MLA_SMEM_OK(sbase + kOffStage + stage * kStageBytes, kStageBytes)) {
             const uint32_t fb = bar(FULL0 + stage);
             const uint32_t dst = sbase + kOffStage + stage * kStageBytes;
@@ -484,13 +351,10 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
       const int pid = cur_next(ld);
       // an id outside the pool loads zeros (TMA bounds) and is reported
       if (lane == 0 && !none && (pid < 0 || pid >= num_pages)) report_error(err_word, MLA_ERR_BOUNDS);
-      if (!wait(bar((kBlocks ? CE0 : EMPTY0) + stage), ph ^ 1u)) { ok = false; break; }
-      // (the codes of a block-scaled cache: a slot of their own; else of an FP8 cache: the slot's upper half)
-      const uint32_t slot0 = sbase + kOffStage + (kBlocks ? kOpSlots * kStageBytes - kF8Off + stage * kF8StageBytes
-                                                          : stage * kStageBytes);
-      if (lane == 0 && MLA_SMEM_OK(slot0, kStageBytes)) {
+      if (!wait_phase(bar(EMPTY0 + stage), ph ^ 1u, abort_flag, err_word)) { ok = false; break; }
+      if (lane == 0 && MLA_SMEM_OK(sbase + kOffStage + stage * kStageBytes, kStageBytes)) {
         const uint32_t fb = bar(FULL0 + stage);
-        const uint32_t dst = slot0;
+        const uint32_t dst = sbase + kOffStage + stage * kStageBytes;
         const int y = ((pid << tile_shift) + sub) * kTile;
         if (kF8) {
           // the codes into the upper half of the slot, unswizzled rows
@@ -512,21 +376,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           tma_load_2d(dst + 4 * kCBoxBytes, &map_kr, fb, kDC + 32 * (int)rank, y, pol_stream);
         }
       }
-      if (kBlocks && lane < kTile / 16) {
-        // lane i copies block i's entry (of a page outside the pool: zeros) and arrives once it is there
-        const uint32_t dst = sbase + kOffEntries + stage * kEntryStage + 8 * lane;
-        if (lane < kTile >> block_shift && MLA_SMEM_OK(dst, 8)) {
-          const int64_t tile = ((int64_t)pid << tile_shift) + sub;
-          if (pid >= 0 && pid < num_pages)
-            cp_async_8(dst, entries + ((tile * kTile >> block_shift) + lane) * kEntryBytes);
-          else
-            asm volatile("st.shared.v2.b32 [%0], {%1, %1};" ::"r"(dst), "r"(0u) : "memory");
-        }
-        cp_async_arrive(bar(CF0 + stage));
-      }
       last_ph[stage] = (int)ph;
       __syncwarp();
-      if (++stage == (kBlocks ? kCodeSlots : kStages)) { stage = 0; ph ^= 1u; }
+      if (++stage == kStages) { stage = 0; ph ^= 1u; }
     }
     if (!ok) {
       // let every issued copy land before this CTA can exit
@@ -539,8 +391,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
         }
       }
     }
-  };
-  auto issue = [&]() {
+  } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------ MMA issuers
     // Two threads feed the tensor pipe: warp 1 the score MMAs, warp 2 the value
     // MMAs. An MMA issue stalls at the pipe's execution rate, so with one
@@ -550,7 +401,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
     // also covers the page's score MMAs.
     // (on chunk rows an elected lane issues: 134 -> 132 us for 128 rows on 4096 tokens;
     // for the plain calls it is within 1% either way, by workload)
-    if (kRows || kBlocks ? elect() : lane == 0) {
+    if (kRows ? elect() : lane == 0) {
       constexpr uint32_t kIdQK = kF8 ? idesc_f16(128, 64, false, false) : idesc_bf16(128, 64, false, false);
       constexpr uint32_t kIdPV = kF8 ? idesc_f16(128, 256, false, true) : idesc_bf16(128, 256, false, true);
       // descriptor templates; the start address is added per use
@@ -573,15 +424,15 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           // the range's query: the score readers have moved the latent and
           // positional halves from their two ring slots into tensor memory (and
           // read the slots: free them)
-          if (!wait(bar(QCF), li & 1)) { ok = false; break; }
+          if (!wait_phase(bar(QCF), li & 1, abort_flag, err_word)) { ok = false; break; }
           for (int q = 0; q < kQSlots; ++q) {
             mbar_arrive(bar(EMPTY0 + stage));
-            if (++stage == kSlots) { stage = 0; ph ^= 1u; }
+            if (++stage == kStages) { stage = 0; ph ^= 1u; }
           }
           for (int i = 0; i < ntiles; ++i, ++g) {
             // an FP8 page is expanded by the score readers after it lands (CVF)
-            if (!wait(bar((kF8 ? CVF0 : FULL0) + stage), ph) ||
-                !wait(bar(SFREE), (g & 1) ^ 1)) { ok = false; break; }
+            if (!wait_phase(bar((kF8 ? CVF0 : FULL0) + stage), ph, abort_flag, err_word) ||
+                !wait_phase(bar(SFREE), (g & 1) ^ 1, abort_flag, err_word)) { ok = false; break; }
             tc_fence_after();
             const uint32_t d = tmem + kTmS;
             const uint64_t bc = dQK_c + da(sbase + kOffStage + stage * kStageBytes);
@@ -594,7 +445,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             mma_ts(d, tmem + kTmQr, br, kIdQK, 1u);
             mma_ts(d, tmem + kTmQr + 8, br + 2, kIdQK, 1u);
             mma_commit(bar(SF0 + (g & 1)));
-            if (++stage == kSlots) { stage = 0; ph ^= 1u; }
+            if (++stage == kStages) { stage = 0; ph ^= 1u; }
           }
         }
       } else {
@@ -604,13 +455,13 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           const int li = it - it0;
           const int ntiles = plan.item_tile1[it] - plan.item_tile0[it];
           for (int q = 0; q < kQSlots; ++q)  // the range's query slots (released by the score issuer)
-            if (++stage == kSlots) { stage = 0; ph ^= 1u; }
+            if (++stage == kStages) { stage = 0; ph ^= 1u; }
           for (int i = 0; i < ntiles; ++i, ++g) {
             const int pb = g % kPBufs;
-            if (!wait(bar(PF0 + pb), (g / kPBufs) & 1)) { ok = false; break; }
+            if (!wait_phase(bar(PF0 + pb), (g / kPBufs) & 1, abort_flag, err_word)) { ok = false; break; }
             // the first value MMA of a range overwrites O: the previous range's
             // epilogue must have read it
-            if (i == 0 && li > 0 && !wait(bar(OFREE), (li - 1) & 1)) { ok = false; break; }
+            if (i == 0 && li > 0 && !wait_phase(bar(OFREE), (li - 1) & 1, abort_flag, err_word)) { ok = false; break; }
             // arm the P buffer for page g+2; its peer half can only come after
             // this page's value MMAs (waited through PVD by the peer)
             mbar_arrive_expect_tx(bar(PF0 + pb), kPHalfBytes);
@@ -628,7 +479,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             }
             mma_commit_multicast(bar(PVD0 + pb), 0x3);
             mma_commit(bar(EMPTY0 + stage));
-            if (++stage == kSlots) { stage = 0; ph ^= 1u; }
+            if (++stage == kStages) { stage = 0; ph ^= 1u; }
           }
         }
       }
@@ -636,8 +487,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
       mma_commit(bar(MMAD));
     }
     __syncwarp();
-  };
-  auto score = [&]() {
+  } else {
     // ------------------------------------------------------------ score readers and softmax
     const int quad = warp & 3;
     const int row = quad * 32 + lane;  // head row == TMEM lane
@@ -649,12 +499,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
     const uint32_t r_lxf = mapa(bar(LXF0), peer), r_mxf = mapa(bar(MXF0), peer);
     const uint32_t r_tok = mapa(sbase + kOffTok, peer);
 
-    if (warp < R::kSoft0) {
-      if (kBlocks) reg_inc<kRegsRead>();
+    if (warp < 3 + kAWarps) {
       // -------------------------------------------------------- A: score readers
       // Per page: read the peer's 32 tokens of this CTA's partial scores and send
       // them (log2 units, fp16) into the peer's shared memory.
-      const int atid = threadIdx.x - 32 * R::kRead0;  // 0 .. 127
+      const int atid = threadIdx.x - 96;  // 0 .. 127
       const uint32_t tQ = tmem + lane_off + kTmQ;
       int g = 0;
       bool ok = true;
@@ -670,14 +519,14 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
       auto expand = [&](int gg, int lii) -> bool {
         const int slot = gg + kQSlots * (lii + 1);
         const int st = slot % kStages;
-        if (!wait(bar(FULL0 + st), (slot / kStages) & 1)) return false;
+        if (!wait_phase(bar(FULL0 + st), (slot / kStages) & 1, abort_flag, err_word)) return false;
         const uint32_t sb = sbase + kOffStage + st * kStageBytes;
         uint32_t v[9][4];
 #pragma unroll
         for (int k = 0; k < 9; ++k)
           ld_shared_v4(sb + kF8Off + (uint32_t)(atid + 128 * k) * 16, v[k][0], v[k][1], v[k][2], v[k][3]);
         mbar_arrive(bar(CVR));
-        if (!wait(bar(CVR), cv_n & 1)) return false;
+        if (!wait_phase(bar(CVR), cv_n & 1, abort_flag, err_word)) return false;
         ++cv_n;
 #pragma unroll
         for (int k = 0; k < 9; ++k) {
@@ -728,8 +577,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
         // (this warp read the S of its last page), so Q may be overwritten.
         for (int q = 0; q < kQSlots && ok; ++q) {
           const int slot = g + kQSlots * li + q;
-          if (!wait(bar((kBlocks ? CVF0 : FULL0) + slot % kSlots), (slot / kSlots) & 1)) { ok = false; break; }
-          const uint32_t sq = sbase + kOffStage + (slot % kSlots) * kStageBytes + (uint32_t)row * 128;
+          if (!wait_phase(bar(FULL0 + slot % kStages), (slot / kStages) & 1, abort_flag, err_word)) { ok = false; break; }
+          const uint32_t sq = sbase + kOffStage + (slot % kStages) * kStageBytes + (uint32_t)row * 128;
           (void)MLA_SMEM_OK(sq + kQBoxBytes, 128);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
@@ -739,16 +588,15 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(r[4 * c]), "=r"(r[4 * c + 1]), "=r"(r[4 * c + 2]), "=r"(r[4 * c + 3])
                            : "r"(sq + m * kQBoxBytes + ((c ^ (row & 7)) * 16)));
-            if (kCol && !kRows) {  // the FP8 cache's column scales fold into the query (fp16)
+            if (kF8 && !kRows) {  // the FP8 cache's column scales fold into the query (fp16)
               const float* sc = fp8_scales + 256 * rank + 128 * q + 64 * m;
 #pragma unroll
               for (int k = 0; k < 32; ++k) r[k] = scale_bf16x2_to_f16x2(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
             }
-            if (kBlocks && !q_f16) query_f16(r, row < H, err_word);
             tmem_st32(tQ + 64 * q + 32 * m, r);
           }
           if ((row >> 6) == q) {  // this row's positional half: 64 bytes, 64B-swizzled (warp-uniform)
-            const uint32_t sr = sbase + kOffStage + (slot % kSlots) * kStageBytes + 2 * kQBoxBytes;
+            const uint32_t sr = sbase + kOffStage + (slot % kStages) * kStageBytes + 2 * kQBoxBytes;
             const int rl = row & 63;
             uint32_t r[16];
 #pragma unroll
@@ -756,28 +604,27 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
               asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(r[4 * c]), "=r"(r[4 * c + 1]), "=r"(r[4 * c + 2]), "=r"(r[4 * c + 3])
                            : "r"(sr + rl * 64 + ((c ^ ((rl >> 1) & 3)) * 16)));
-            if (kCol && !kRows) {
+            if (kF8 && !kRows) {
               const float* sc = fp8_scales + kDC + 32 * rank;
 #pragma unroll
               for (int k = 0; k < 16; ++k) r[k] = scale_bf16x2_to_f16x2(r[k], __ldg(sc + 2 * k), __ldg(sc + 2 * k + 1));
             }
-            if (kBlocks && !q_f16) query_f16(r, row < H, err_word);
             tmem_st16(tmem + lane_off + kTmQr, r);
           }
           // every use of a ring slot completes its CVF once (the query's too)
-          if (kCol) mbar_arrive(bar(CVF0 + slot % kStages));
+          if (kF8) mbar_arrive(bar(CVF0 + slot % kStages));
         }
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(QCF));
-        if (kCol) {  // the range's first page, expanded before its score MMAs
+        if (kF8) {  // the range's first page, expanded before its score MMAs
           cv_next = g;
           cv_last = g + ntiles - 1;
           if (!expand_upto(g, li)) { ok = false; break; }
         }
         for (int i = 0; i < ntiles; ++i, ++g) {
-          if (!wait(bar(SF0 + (g & 1)), (g >> 1) & 1)) { ok = false; break; }
+          if (!wait_phase(bar(SF0 + (g & 1)), (g >> 1) & 1, abort_flag, err_word)) { ok = false; break; }
           tc_fence_after();
           uint32_t r[32];
           tmem_ld32(tS + 32 * peer, r);
@@ -786,7 +633,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           mbar_arrive(bar(SFREE));
           // the peer has read this CTA's partial of page g-2 (same buffer)
           if (g >= 2) {
-            if (!wait(bar(XE0 + (g & 1)), ((g >> 1) & 1) ^ 1)) { ok = false; break; }
+            if (!wait_phase(bar(XE0 + (g & 1)), ((g >> 1) & 1) ^ 1, abort_flag, err_word)) { ok = false; break; }
             if (atid == 0) mbar_arrive_expect_tx(bar(XE0 + (g & 1)), kTokBytes);  // arm for this page
           }
           // The partial scores go out as fp16 offsets from the midpoint of this head's
@@ -794,80 +641,50 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           // scores within the 32 tokens, not their size (a score shared by the tokens
           // costs no precision). Only tokens the query attends count toward the
           // midpoint; slack rows past the context may hold any bits.
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]) * sl2;
           const int nvp = n_att - ((pg0 + i) * kTile + 32 * (int)peer);  // attended among the 32
-          float v[32], mid;
-          if constexpr (kBlocks) {
-            // (what is not attended is masked where it arrives: any of the others will do)
-            if (nvp < 32) {
+          float hi = -INFINITY, lo = INFINITY;
+          if (nvp >= 32) {
 #pragma unroll
-              for (int k = 1; k < 32; ++k)
-                if (k >= nvp) r[k] = r[0];
+            for (int k = 0; k < 32; ++k) {
+              hi = fmaxf(hi, v[k]);
+              lo = fminf(lo, v[k]);
             }
-            float hi = __uint_as_float(r[0]), lo = hi;
-#pragma unroll
-            for (int k = 1; k < 31; k += 2) {
-              hi = max3(hi, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-              lo = min3(lo, __uint_as_float(r[k]), __uint_as_float(r[k + 1]));
-            }
-            hi = fmaxf(hi, __uint_as_float(r[31])) * sl2;
-            lo = fminf(lo, __uint_as_float(r[31])) * sl2;
-            mid = 0.5f * lo + 0.5f * hi;
-            if (kRows && row < H && 0.5f * hi - 0.5f * lo >= 65520.f && hi < INFINITY && lo > -INFINITY)
-              report_error(err_word, MLA_ERR_RANGE);
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]) * sl2;
-            float hi = -INFINITY, lo = INFINITY;
-            if (nvp >= 32) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
+            for (int k = 0; k < 32; ++k)
+              if (k < nvp) {
                 hi = fmaxf(hi, v[k]);
                 lo = fminf(lo, v[k]);
               }
-            } else {
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (k < nvp) {
-                  hi = fmaxf(hi, v[k]);
-                  lo = fminf(lo, v[k]);
-                }
-            }
-            mid = lo <= hi ? 0.5f * lo + 0.5f * hi : 0.f;
-            // offsets that fp16 does not hold (the difference of halves: both ends may be large)
-            if (kRows && row < H && 0.5f * hi - 0.5f * lo >= 65520.f && hi < INFINITY && lo > -INFINITY)
-              report_error(err_word, MLA_ERR_RANGE);
           }
+          const float mid = lo <= hi ? 0.5f * lo + 0.5f * hi : 0.f;
+          // offsets that fp16 does not hold (the difference of halves: both ends may be large)
+          if (kRows && row < H && 0.5f * hi - 0.5f * lo >= 65520.f && hi < INFINITY && lo > -INFINITY)
+            report_error(err_word, MLA_ERR_RANGE);
           const uint32_t xoff = (uint32_t)(g & 1) * kXBytes;
           const uint32_t xa = r_x + xoff + (uint32_t)row * 16;
           const uint32_t xf = r_xf + 8u * (uint32_t)(g & 1);
           if (MLA_SMEM_OK(sbase + kOffX + xoff + (uint32_t)row * 16 + 3 * 128 * 16, 16) &&
               MLA_SMEM_OK(sbase + kOffX + xoff + kXDataBytes + (uint32_t)row * 4, 4)) {
-            const uint64_t by = pair(sl2, sl2), off = pair(-mid, -mid);
-            auto offset = [&](int k) -> uint32_t {  // tokens k and k + 1
-              if constexpr (kBlocks) {
-                const float2 e = unpair(fma2(pair(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), by, off));
-                return cvt_f16x2(e.x, e.y);
-              } else {
-                return cvt_f16x2(v[k] - mid, v[k + 1] - mid);
-              }
-            };
 #pragma unroll
             for (int q8 = 0; q8 < 4; ++q8) {
               uint4 w;
-              w.x = offset(8 * q8);
-              w.y = offset(8 * q8 + 2);
-              w.z = offset(8 * q8 + 4);
-              w.w = offset(8 * q8 + 6);
+              w.x = cvt_f16x2(v[8 * q8 + 0] - mid, v[8 * q8 + 1] - mid);
+              w.y = cvt_f16x2(v[8 * q8 + 2] - mid, v[8 * q8 + 3] - mid);
+              w.z = cvt_f16x2(v[8 * q8 + 4] - mid, v[8 * q8 + 5] - mid);
+              w.w = cvt_f16x2(v[8 * q8 + 6] - mid, v[8 * q8 + 7] - mid);
               st_async_v4(xa + q8 * 128 * 16, w, xf);
             }
             st_async_b32(r_x + xoff + kXDataBytes + (uint32_t)row * 4, __float_as_uint(mid), xf);
           }
           // FP8 cache: expand the range's pages up to two ahead of this one
-          if (kCol && !expand_upto(g + 2, li)) { ok = false; break; }
+          if (kF8 && !expand_upto(g + 2, li)) { ok = false; break; }
         }
       }
     } else {
-      if (kBlocks) reg_inc<kRegsSoftmax>();
       // -------------------------------------------------------- B: softmax + epilogue
       // Two groups of four warps (one per TMEM lane quadrant) take alternate
       // pages: group grp handles the pages g with g % 2 == grp, one thread per
@@ -876,8 +693,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
       // shared memory the groups pass the reference maximum of each head
       // (decided page by page, in page order) and, at the end of a range, the
       // softmax sum of the group that does not write the output.
-      const int grp = (warp - R::kSoft0) >> 2;
-      const int gwarp = (warp - R::kSoft0) & 3;
+      const int grp = (warp - 3 - kAWarps) >> 2;
+      const int gwarp = (warp - 3 - kAWarps) & 3;
       const int gtid = gwarp * 32 + lane;  // 0 .. 127
       const uint32_t vec_off = (uint32_t)row * 4;
       float x[32];
@@ -905,7 +722,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             for (int e = 0; e < 8; ++e) {
               f[e] = __uint_as_float(r[8 * v + e]) * inv;
               // the FP8 cache's column scale (u = s * sum p code)
-              if (kCol) f[e] *= __ldg(fp8_scales + 256 * rank + 128 * half + 32 * c + 8 * v + e);
+              if (kF8) f[e] *= __ldg(fp8_scales + 256 * rank + 128 * half + 32 * c + 8 * v + e);
               amax = fmaxf(amax, fabsf(f[e]));
             }
             if (row < H)
@@ -927,11 +744,11 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           if ((g & 1) != grp) {
             if (i == ntiles - 1) {
               // helper at the end of the range handled by the other group
-              if (!wait(bar(IVF0 + grp), iv_n & 1)) { ok = false; break; }
+              if (!wait_phase(bar(IVF0 + grp), iv_n & 1, abort_flag, err_word)) { ok = false; break; }
               ++iv_n;
               float inv;
               asm volatile("ld.shared.f32 %0, [%1];" : "=f"(inv) : "r"(sbase + kOffIV + vec_off));
-              if (!wait(bar(PVD0 + g % kPBufs), (g / kPBufs) & 1)) { ok = false; break; }
+              if (!wait_phase(bar(PVD0 + g % kPBufs), (g / kPBufs) & 1, abort_flag, err_word)) { ok = false; break; }
               tc_fence_after();
               drain_o(it, 1, inv);
               tc_fence_before();
@@ -942,7 +759,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           const int xb = g & 1;
           // this CTA's partial scores of its 32 tokens
           const int nv = n_att - ((pg0 + i) * kTile + 32 * (int)rank);  // valid tokens among these 32
-          if (!wait(bar(SF0 + xb), (g >> 1) & 1)) { ok = false; break; }
+          if (!wait_phase(bar(SF0 + xb), (g >> 1) & 1, abort_flag, err_word)) { ok = false; break; }
           tc_fence_after();
           {
             uint32_t r[32];
@@ -954,7 +771,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           tc_fence_before();
           mbar_arrive(bar(SFREE));
           // add the peer's partial for these tokens: its midpoint plus the fp16 offsets
-          if (!wait(bar(XF0 + xb), (g >> 1) & 1)) { ok = false; break; }
+          if (!wait_phase(bar(XF0 + xb), (g >> 1) & 1, abort_flag, err_word)) { ok = false; break; }
           if (gtid == 0) mbar_arrive_expect_tx(bar(XF0 + xb), kXBytes);  // arm for page g+2
           float mid_p;
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(mid_p) : "r"(sbase + kOffX + xb * kXBytes + kXDataBytes + vec_off));
@@ -967,13 +784,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              if constexpr (kBlocks) {
-                const int e = 8 * q8 + 2 * k;
-                const float2 f = unpair(fma2(pair(x[e], x[e + 1]), pair(sl2, sl2), f16x2_plus(ww[k], mid_p)));
-                x[e] = f.x;
-                x[e + 1] = f.y;
-                continue;
-              }
               const float2 f = f16x2_to_f32(ww[k]);
               x[8 * q8 + 2 * k] = fmaf(x[8 * q8 + 2 * k], sl2, mid_p) + f.x;
               x[8 * q8 + 2 * k + 1] = fmaf(x[8 * q8 + 2 * k + 1], sl2, mid_p) + f.y;
@@ -992,13 +802,13 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           // previous phase, page g-6, is complete: the value MMAs complete in page
           // order and this group waited for page g-5 at page g-2.)
           const int pb = g % kPBufs;
-          if (g >= kPBufs && !wait(bar(PVD0 + pb), ((g / kPBufs) & 1) ^ 1)) { ok = false; break; }
+          if (g >= kPBufs && !wait_phase(bar(PVD0 + pb), ((g / kPBufs) & 1) ^ 1, abort_flag, err_word)) { ok = false; break; }
           const int rows_valid = L - (pg0 + i) * kTile;
           if (rows_valid < kTile) {
             // slack rows past the context may hold any bits: zero this CTA's latent
             // half so 0-weight x NaN cannot reach O. The score MMAs have read the
             // stage (SF); the value MMAs read it after this group's P-ready arrive.
-            const int stage = (g + kQSlots * (li + 1)) % kSlots;  // ring slot of page g
+            const int stage = (g + kQSlots * (li + 1)) % kStages;  // ring slot of page g
             const uint32_t sa = sbase + kOffStage + stage * kStageBytes;
             (void)MLA_SMEM_OK(sa, 4 * kCBoxBytes);
             const int nz = (kTile - rows_valid) * 4 * 8;  // 16-byte chunks
@@ -1011,23 +821,17 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             fence_proxy_async_smem();
           }
           float m = x[0];
-          if constexpr (kBlocks) {
 #pragma unroll
-            for (int jj = 1; jj < 31; jj += 2) m = max3(m, x[jj], x[jj + 1]);
-            m = fmaxf(m, x[31]);
-          } else {
-#pragma unroll
-            for (int jj = 1; jj < 32; ++jj) m = fmaxf(m, x[jj]);
-          }
+          for (int jj = 1; jj < 32; ++jj) m = fmaxf(m, x[jj]);
           st_async_b32(r_mx + xb * kVecBytes + vec_off, __float_as_uint(m), r_mxf + 8u * xb);
-          if (!wait(bar(MXF0 + xb), (g >> 1) & 1)) { ok = false; break; }
+          if (!wait_phase(bar(MXF0 + xb), (g >> 1) & 1, abort_flag, err_word)) { ok = false; break; }
           if (gtid == 0) mbar_arrive_expect_tx(bar(MXF0 + xb), kVecBytes);
           float m_p;
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m_p) : "r"(sbase + kOffMX + xb * kVecBytes + vec_off));
           const float mt = fmaxf(m, m_p);
           // the reference maximum: the previous page's decision (the other group's)
           // is raised lazily, only when this page exceeds it by the threshold
-          if (g >= 1 && !wait(bar(MRF), (g - 1) & 1)) { ok = false; break; }
+          if (g >= 1 && !wait_phase(bar(MRF), (g - 1) & 1, abort_flag, err_word)) { ok = false; break; }
           float m_new = mt, alpha = 1.f;
           bool need = false;
           if (i > 0) {
@@ -1047,7 +851,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             if (lane == 0) atomicAdd(&g_dbg_counters[0], 1ull);
 #endif
             // O must hold every earlier page before it is rescaled
-            if (!wait(bar(PVD0 + (g - 1) % kPBufs), ((g - 1) / kPBufs) & 1)) { ok = false; break; }
+            if (!wait_phase(bar(PVD0 + (g - 1) % kPBufs), ((g - 1) / kPBufs) & 1, abort_flag, err_word)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
@@ -1077,23 +881,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           (void)MLA_TMEM_OK(kTmP + 16 * pb, 16);
           float lsum0 = 0.f, lsum1 = 0.f;
           uint32_t pw[16];
-          if constexpr (kBlocks) {
-            // (the sum of the weights before their rounding to fp16: off by less than 2^-12 of itself)
-            uint64_t sum = pair(0.f, 0.f);
-            const uint64_t off = pair(-mref, -mref);
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-              const float2 d = unpair(add2(pair(x[2 * v], x[2 * v + 1]), off));
-              const float p0 = ex2(d.x), p1 = ex2(d.y);
-              pw[v] = cvt_f16x2(p0, p1);
-              sum = add2(sum, pair(p0, p1));
-            }
-            const float2 both = unpair(sum);
-            lsum0 = both.x;
-            lsum1 = both.y;
-          }
-#pragma unroll
-          for (int v = 0; v < 16 && !kBlocks; ++v) {
+          for (int v = 0; v < 16; ++v) {
             const float p0 = ex2(x[2 * v] - mref);
             const float p1 = ex2(x[2 * v + 1] - mref);
             if (kF8) {  // fp16 operands with the FP8 cache
@@ -1127,7 +916,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             // epilogue: the CTA's sum (both groups), the peer's, the normalised output
             float l_c = l_g;
             if (ntiles >= 2) {
-              if (!wait(bar(LGF0 + (lg_n & 1)), (lg_n >> 1) & 1)) { ok = false; break; }
+              if (!wait_phase(bar(LGF0 + (lg_n & 1)), (lg_n >> 1) & 1, abort_flag, err_word)) { ok = false; break; }
               const uint32_t lg = sbase + kOffLG + (uint32_t)(lg_n & 1) * 2 * kVecBytes;
               float l_o, m_o;
               asm volatile("ld.shared.f32 %0, [%1];" : "=f"(l_o) : "r"(lg + vec_off));
@@ -1136,7 +925,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             }
             const int lb = li & 1;
             st_async_b32(r_lx + lb * kVecBytes + vec_off, __float_as_uint(l_c), r_lxf + 8u * lb);
-            if (!wait(bar(LXF0 + lb), (li >> 1) & 1)) { ok = false; break; }
+            if (!wait_phase(bar(LXF0 + lb), (li >> 1) & 1, abort_flag, err_word)) { ok = false; break; }
             if (gtid == 0) mbar_arrive_expect_tx(bar(LXF0 + lb), kVecBytes);  // arm for range li+2
             float l_p;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(l_p) : "r"(sbase + kOffLX + lb * kVecBytes + vec_off));
@@ -1146,7 +935,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
             // 1/l for the helper group, which drains the other half of O
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sbase + kOffIV + vec_off), "f"(inv) : "memory");
             mbar_arrive(bar(IVF0 + (grp ^ 1)));
-            if (!wait(bar(PVD0 + pb), (g / kPBufs) & 1)) { ok = false; break; }
+            if (!wait_phase(bar(PVD0 + pb), (g / kPBufs) & 1, abort_flag, err_word)) { ok = false; break; }
             tc_fence_after();
             const size_t orow = ((size_t)it * n_q + j) * H + row;
             drain_o(it, 0, inv);
@@ -1161,109 +950,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
         if (ntiles >= 2) ++lg_n;
       }
     }
-  };
-  auto widen = [&]() {
-    // ------------------------------------------------------------ wideners
-    // Block scales: they hand out the operand slots in ring order. A query's two slots are filled by
-    // TMA; a page's codes become the fp16 page half the MMAs read, in the swizzled layout of the
-    // bf16 path's boxes. The loop stays short: unrolled over all of a thread's chunks it kept the other
-    // roles waiting for their instructions (102 us for the step of 32 x 4096).
-    const int wtid = threadIdx.x - 32 * R::kWide0;  // 0 .. 255
-    // 16-byte chunks wtid + 256 k of the page half: box k, token wtid / 4, 16 of its 64 columns;
-    // then, for the first half of the threads, the positional box: token wtid / 2, 16 of its 32
-    // columns (64B swizzle)
-    const uint32_t t = (uint32_t)wtid >> 2, kk = wtid & 3, tr = (uint32_t)wtid >> 1, kr = 2 * (wtid & 1);
-    const uint32_t w0 = t * 128 + ((2 * kk) ^ (t & 7)) * 16, w1 = t * 128 + ((2 * kk + 1) ^ (t & 7)) * 16;
-    const uint32_t x0 = 4 * kCBoxBytes + tr * 64 + (kr ^ ((tr >> 1) & 3)) * 16;
-    const uint32_t x1 = 4 * kCBoxBytes + tr * 64 + ((kr + 1) ^ ((tr >> 1) & 3)) * 16;
-    int slot = 0, page = 0;  // uses of operand slots, and of slots of codes
-    int asked = 0;           // uses of operand slots up to the last query's
-    bool ok = true;
-    auto next_slot = [&]() -> bool {  // the next operand slot, once its last use is over
-      const bool free = wait(bar(EMPTY0 + slot % kOpSlots), ((slot / kOpSlots) & 1) ^ 1);
-      if (!free) ok = false;
-      return free;
-    };
-    for (int it = it0; it < it1 && ok; ++it) {
-      const int ntiles = plan.item_tile1[it] - plan.item_tile0[it];
-      const int seq = plan.item_seq[it], qrow = (seq * n_q + j) * H;
-      const int end = plan.seq_len_eff[seq] - plan.item_tile0[it] * kTile;  // of the context, from the first tile on
-      for (int q = 0; q < kQSlots && next_slot(); ++q, ++slot) {
-        // as the producer of the bf16 path: latent boxes [128 heads][64] for columns 256r + 128q + {0, 64}
-        // and positional rows [64q, 64q + 64) of columns 512 + 32r
-        const uint32_t fb = bar(CVF0 + slot % kOpSlots), dst = sbase + kOffStage + (slot % kOpSlots) * kStageBytes;
-        if (wtid == 0 && MLA_SMEM_OK(dst, kStageBytes)) {
-          const uint64_t keep = policy_evict_last();
-          mbar_arrive_expect_tx(fb, 2 * kQBoxBytes + kQrBoxBytes);
-          for (int m = 0; m < 2; ++m)
-            tma_load_2d(dst + m * kQBoxBytes, &map_q, fb, 256 * (int)rank + 128 * q + 64 * m, qrow, keep);
-          tma_load_2d(dst + 2 * kQBoxBytes, &map_qkr, fb, kDC + 32 * (int)rank, qrow + 64 * q, keep);
-          asked = slot + 1;
-        } else if ((wtid & 31) == 0) {
-          mbar_arrive(fb);
-        }
-      }
-      for (int i = 0; i < ntiles && ok; ++i, ++slot, ++page) {
-        const int cs = page % kCodeSlots;
-        if (!wait(bar(CF0 + cs), (page / kCodeSlots) & 1)) { ok = false; break; }
-        const uint32_t sc = sbase + kOffStage + kOpSlots * kStageBytes + cs * kF8StageBytes + wtid * 16;
-        const uint32_t se = sbase + kOffEntries + cs * kEntryStage;
-        const uint32_t dst = sbase + kOffStage + (slot % kOpSlots) * kStageBytes;
-        const int left = end - i * kTile;  // tokens of the context from this tile on
-        // the powers of the CTA's two groups in this thread's block, and of the positional columns
-        uint32_t pw, pr, v[4], o[8];
-        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(pw) : "r"(se + ((t >> block_shift) << 3) + 2 * rank));
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(pr) : "r"(se + ((tr >> block_shift) << 3) + 4));
-        ld_shared_v4(sc, v[0], v[1], v[2], v[3]);
-        const uint32_t by0 = power_f16x2(pw & 0xFFu), by1 = power_f16x2(pw >> 8);
-        auto put = [&](uint32_t a0, uint32_t a1, bool beyond, uint32_t token) {
-          if (beyond && (int)token < left) report_error(err_word, MLA_ERR_RANGE);
-          if (MLA_SMEM_OK(a0, 16) && MLA_SMEM_OK(a1, 16)) {
-            st_shared_v4(a0, o[0], o[1], o[2], o[3]);
-            st_shared_v4(a1, o[4], o[5], o[6], o[7]);
-          }
-        };
-        if (!next_slot()) break;
-#pragma unroll 2
-        for (uint32_t k = 0; k < 4; ++k) {
-          const bool beyond = widen16(v, k < 2 ? by0 : by1, k < 2 ? pw & 0xFFu : pw >> 8, o);
-          if (k < 3 || wtid < 128) ld_shared_v4(sc + 4096 * (k + 1), v[0], v[1], v[2], v[3]);  // the next chunk
-          put(dst + k * kCBoxBytes + w0, dst + k * kCBoxBytes + w1, beyond, t);
-        }
-        if (wtid < 128) put(dst + x0, dst + x1, widen16(v, power_f16x2(pr), pr, o), tr);
-        fence_proxy_async_smem();  // read by the MMAs (async proxy)
-        __syncwarp();
-        if ((wtid & 31) == 0) { mbar_arrive(bar(CE0 + cs)); mbar_arrive(bar(CVF0 + slot % kOpSlots)); }
-      }
-    }
-    if (!ok && wtid == 0) {
-      // let the last query's copies land before this CTA can exit (where another thread gave up before
-      // it arrived, the limit ends the wait)
-      const long long start = clock64();
-      for (int u = asked > kQSlots ? asked - kQSlots : 0; u < asked; ++u)
-        while (!mbar_try_wait(bar(CVF0 + u % kOpSlots), (u / kOpSlots) & 1) && clock64() - start < wait_limit()) {
-        }
-    }
-  };
-  if constexpr (kBlocks) {
-    if (warp < R::kRead0) {
-      reg_dec<kRegsIssue>();
-      if (warp == 0) produce();
-      else if (warp < 3) issue();
-    } else if (warp < R::kWide0) {
-      score();
-    } else {
-      reg_dec<kRegsWiden>();
-      widen();
-    }
-  } else {
-    if (warp == 0) {
-      produce();
-    } else if (warp == 1 || warp == 2) {
-      issue();
-    } else {
-      score();
-    }
   }
 
   // ------------------------------------------------------------ teardown
@@ -1275,7 +961,6 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (kBlocks && threadIdx.x == 0 && *abort_flag) report_error(err_word, MLA_ERR_TIMEOUT);
   cluster_sync();  // the peer has finished writing into this CTA's shared memory
   if (warp == 1) {
     tc_fence_after();
@@ -1301,7 +986,7 @@ int decode_max_workers() {
     const int n = known[dev].load(std::memory_order_relaxed);
     if (n > 0) return n;
   }
-  if (smem_limit<decode_tc_kernel<false, false, false>>(kSmemBytes) != cudaSuccess) {
+  if (smem_limit<decode_tc_kernel<false, false>>(kSmemBytes) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
@@ -1317,7 +1002,7 @@ int decode_max_workers() {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, decode_tc_kernel<false, false, false>, &cfg) != cudaSuccess) {
+  if (cudaOccupancyMaxActiveClusters(&n, decode_tc_kernel<false, false>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     return -1;
   }
@@ -1328,12 +1013,12 @@ int decode_max_workers() {
 namespace {
 // The query maps and the launch, shared by the bf16 and FP8 caches (the page
 // maps differ: 16-bit swizzled boxes, or unswizzled 8-bit rows).
-template <bool kF8, bool kRows, bool kBlocks>
+template <bool kF8, bool kRows>
 cudaError_t launch_decode_as(const CUtensorMap& map_c, const CUtensorMap& map_kr, const uint16_t* q_abs,
                                const float* fp8_scales, const int32_t* block_table, int B, int n_q, int H,
                                int num_pages, int page_size, int max_pages, float scale, int G, const Plan& plan,
                                int32_t* err_word,
-                               cudaStream_t s, int blocks = 0) {
+                               cudaStream_t s) {
   CUtensorMap map_qkr, map_q;
   const uint64_t q_dims[2] = {kRow, (uint64_t)B * n_q * H};
   const uint64_t row_stride[1] = {kRow * 2};
@@ -1341,18 +1026,17 @@ cudaError_t launch_decode_as(const CUtensorMap& map_c, const CUtensorMap& map_kr
   if (!make_tmap(&map_qkr, q_abs, 2, q_dims, row_stride, box_qkr, 64) ||
       !make_tmap(&map_q, q_abs, 2, q_dims, row_stride, box_q, 128))
     return cudaErrorInvalidValue;
-  cudaError_t e = smem_limit<decode_tc_kernel<kF8, kRows, kBlocks>>(kSmemBytes);
+  cudaError_t e = smem_limit<decode_tc_kernel<kF8, kRows>>(kSmemBytes);
   if (e != cudaSuccess) return e;
   const float sl2 = scale * 1.4426950408889634f;
   dim3 grid(2 * G, n_q, 1);
-  return launch_pdl(decode_tc_kernel<kF8, kRows, kBlocks>, grid, dim3(Roles<kBlocks>::kThreads), kSmemBytes, s, map_c,
-                    map_kr, map_qkr, map_q, block_table, n_q, H, max_pages, num_pages,
-                    (page_size == 2 * kTile ? 1 : 0) | blocks << 8, sl2, plan, fp8_scales, err_word,
-                    plan.seq_row);
+  return launch_pdl(decode_tc_kernel<kF8, kRows>, grid, dim3(kThreads), kSmemBytes, s, map_c, map_kr, map_qkr, map_q,
+                    block_table, n_q, H, max_pages, num_pages, page_size == 2 * kTile ? 1 : 0, sl2, plan,
+                    fp8_scales, err_word, plan.seq_row);
 }
-template <bool kF8, bool kBlocks = false, typename... Args>
+template <bool kF8, typename... Args>
 cudaError_t launch_decode_impl(const Plan& plan, const Args&... args) {
-  return plan.seq_row ? launch_decode_as<kF8, true, kBlocks>(args...) : launch_decode_as<kF8, false, kBlocks>(args...);
+  return plan.seq_row ? launch_decode_as<kF8, true>(args...) : launch_decode_as<kF8, false>(args...);
 }
 }  // namespace
 
@@ -1370,34 +1054,17 @@ cudaError_t launch_decode(const uint16_t* q_abs, const uint16_t* cache, const in
                                    max_pages, scale, G, plan, err_word, s);
 }
 
-namespace {
-// unswizzled 8-bit rows of a page half
-bool code_maps(CUtensorMap* map_c, CUtensorMap* map_kr, const uint8_t* cache8, int num_pages, int page_size) {
-  const uint64_t cache_dims[2] = {kRow, (uint64_t)num_pages * page_size};
-  const uint64_t row_stride[1] = {kRow};
-  const uint32_t box_c[2] = {64, 64}, box_kr[2] = {32, 16};
-  return make_tmap(map_c, cache8, 2, cache_dims, row_stride, box_c, 0, true) &&
-         make_tmap(map_kr, cache8, 2, cache_dims, row_stride, box_kr, 0, true);
-}
-}  // namespace
-
-cudaError_t launch_decode_blocks(const uint16_t* q_abs, bool q_f16, const uint8_t* cache8, const BlockScales& scales,
-                                 const int32_t* block_table, int B, int n_q, int H, int num_pages, int page_size,
-                                 int max_pages, float scale, int G, const Plan& plan, int32_t* err_word,
-                                 cudaStream_t s) {
-  CUtensorMap map_c, map_kr;
-  if (!code_maps(&map_c, &map_kr, cache8, num_pages, page_size)) return cudaErrorInvalidValue;
-  return launch_decode_impl<true, true>(plan, map_c, map_kr, q_abs, reinterpret_cast<const float*>(scales.entries),
-                                        block_table, B, n_q, H, num_pages, page_size, max_pages, scale, G, plan,
-                                        err_word, s, scales.shift | (q_f16 ? 1 : 0) << 8);
-}
-
 cudaError_t launch_decode_fp8(const uint16_t* q_abs, const uint8_t* cache8, const float* fp8_scales,
                               const int32_t* block_table, int B, int n_q, int H, int num_pages, int page_size,
                               int max_pages, float scale, int G, const Plan& plan, int32_t* err_word,
                               cudaStream_t s) {
   CUtensorMap map_c, map_kr;
-  if (!code_maps(&map_c, &map_kr, cache8, num_pages, page_size)) return cudaErrorInvalidValue;
+  const uint64_t cache_dims[2] = {kRow, (uint64_t)num_pages * page_size};
+  const uint64_t row_stride[1] = {kRow};
+  const uint32_t box_c[2] = {64, 64}, box_kr[2] = {32, 16};
+  if (!make_tmap(&map_c, cache8, 2, cache_dims, row_stride, box_c, 0, true) ||
+      !make_tmap(&map_kr, cache8, 2, cache_dims, row_stride, box_kr, 0, true))
+    return cudaErrorInvalidValue;
   return launch_decode_impl<true>(plan, map_c, map_kr, q_abs, fp8_scales, block_table, B, n_q, H, num_pages, page_size,
                                   max_pages, scale, G, plan, err_word, s);
 }
@@ -1411,7 +1078,11 @@ cudaError_t launch_decode_fp8(const uint16_t* q_abs, const uint8_t* cache8, cons
 extern "C" {
 int mla_debug_read_counters(unsigned long long* out, int n) {
   if (!out || n < 1 || n > 4) return (int)cudaErrorInvalidValue;
-  return (int)cudaMemcpyFromSymbol(out, mla::g_dbg_counters, sizeof(unsigned long long) * (size_t)n);
+  unsigned long long blocks[4] = {0, 0, 0, 0};  // the kernel of a block-scaled cache counts on its own
+  cudaError_t e = cudaMemcpyFromSymbol(out, mla::g_dbg_counters, sizeof(unsigned long long) * (size_t)n);
+  if (e == cudaSuccess) e = mla::debug_decode_blocks(nullptr, nullptr, blocks, n);
+  for (int i = 0; i < n; ++i) out[i] += blocks[i];
+  return (int)e;
 }
 int mla_debug_reset(void) {
   const unsigned long long zero[4] = {0, 0, 0, 0};
@@ -1420,6 +1091,8 @@ int mla_debug_reset(void) {
   cudaError_t e = cudaMemcpyToSymbol(mla::g_dbg_counters, zero, sizeof(zero));
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(mla::g_dbg_skip_producer, &off, sizeof(off));
   if (e == cudaSuccess) e = cudaMemcpyToSymbol(mla::sm100::g_wait_limit_override, &nolimit, sizeof(nolimit));
+  unsigned long long none;
+  if (e == cudaSuccess) e = mla::debug_decode_blocks(&nolimit, &off, &none, -1);
   if (e == cudaSuccess) e = mla::debug_append_chunk(&nolimit, &off);
   if (e == cudaSuccess) e = mla::debug_expand(&nolimit, &off);
   if (e == cudaSuccess) e = mla::debug_attend(&nolimit, &off);
@@ -1427,6 +1100,7 @@ int mla_debug_reset(void) {
 }
 int mla_debug_set_wait_limit(long long cycles) {
   cudaError_t e = cudaMemcpyToSymbol(mla::sm100::g_wait_limit_override, &cycles, sizeof(cycles));
+  if (e == cudaSuccess) e = mla::debug_decode_blocks(&cycles, nullptr, nullptr, 0);
   if (e == cudaSuccess) e = mla::debug_append_chunk(&cycles, nullptr);
   if (e == cudaSuccess) e = mla::debug_expand(&cycles, nullptr);
   if (e == cudaSuccess) e = mla::debug_attend(&cycles, nullptr);
@@ -1441,7 +1115,9 @@ int mla_debug_set_skip_loads(int kernel, int what) {
   }
 }
 int mla_debug_set_skip_producer(int on) {
-  return (int)cudaMemcpyToSymbol(mla::g_dbg_skip_producer, &on, sizeof(on));
+  cudaError_t e = cudaMemcpyToSymbol(mla::g_dbg_skip_producer, &on, sizeof(on));
+  if (e == cudaSuccess) e = mla::debug_decode_blocks(nullptr, &on, nullptr, 0);
+  return (int)e;
 }
 }  // extern "C"
 #endif
