@@ -589,18 +589,20 @@ def _paged(cache, block_table, seq_lens, cu, fp8_scales, err_word):
     """Check the paged-cache arguments of the chunk calls; returns (device number, B, pages,
     page size, pages per sequence, tokens of a block of a block-scaled cache or 0)."""
     import torch
-    dev = cache.get_device()
+    dev, i32, kind = cache.get_device(), torch.int32, cache.dtype
     if dev < 0:
         raise ValueError(f"cache: on {cache.device}, a CUDA device is needed")
-    fp8 = cache.dtype is torch.uint8
+    fp8 = kind is torch.uint8
     if fp8 != (fp8_scales is not None):
         raise ValueError("an FP8 cache (uint8 codes) needs its scales fp8_scales, a bf16 cache has none")
-    num_pages, page_size, _ = _dims("cache", cache, 3)
-    B, max_pages = _dims("block_table", block_table, 2)
-    i32 = torch.int32
-    if not (_fits(cache, torch.uint8 if fp8 else torch.bfloat16, (num_pages, page_size, D_ROW), dev)
-            and _fits(block_table, i32, (B, max_pages), dev) and _fits(seq_lens, i32, (B,), dev)
-            and _fits(cu, i32, (B + 1,), dev)):
+    num_pages, page_size, width = cache.shape if cache.dim() == 3 else _dims("cache", cache, 3)
+    B, max_pages = block_table.shape if block_table.dim() == 2 else _dims("block_table", block_table, 2)
+    # (written out: a call of _fits for each takes a microsecond more)
+    if not ((fp8 or kind is torch.bfloat16) and width == D_ROW and cache.is_contiguous()
+            and block_table.dtype is i32 and block_table.get_device() == dev and block_table.is_contiguous()
+            and seq_lens.dtype is i32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev
+            and seq_lens.is_contiguous()
+            and cu.dtype is i32 and cu.shape == (B + 1,) and cu.get_device() == dev and cu.is_contiguous()):
         _tensor("cache", cache, torch.uint8 if fp8 else torch.bfloat16, (num_pages, page_size, D_ROW), dev)
         _tensor("block_table", block_table, i32, (B, max_pages), dev)
         _tensor("seq_lens", seq_lens, i32, (B,), dev)
@@ -622,7 +624,7 @@ def _call(name, fn, dev, stream, *args):
     import torch
     # the stream's number alone: a Stream object takes a microsecond
     handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -718,6 +720,9 @@ def write_kv(rows, cache, block_table, seq_lens, cu, *, fp8_scales, err_word=Non
           _address(err_word))
 
 
+PAGES_SMALL_BATCH, PAGES_SMALL_ROWS = 1024, 4096  # update_pages needs no workspace up to these
+
+
 def update_pages_workspace_bytes(B: int) -> int:
     n = int(lib().mla_update_pages_workspace_bytes(B))
     if n == 0:
@@ -740,7 +745,8 @@ def update_pages(block_table, held, seq_lens, free_pages, free_count, *, page_si
     The order is that of the sequences and of their pages; pages given back are the first to be taken, and a
     call with the lengths of before undoes a call. A sequence is served whole or not at all: from the first one
     that the free pages do not suffice for, sequences that miss pages keep what they have, their slots
-    become -1, and err_word tells MLA_ERR_NO_PAGES. Returns slots.
+    become -1, and err_word tells MLA_ERR_NO_PAGES. A workspace is taken for more than 1024 sequences or 4096
+    slots only (one is allocated when none is given). Returns slots.
     """
     import torch
     dev, i32 = block_table.get_device(), torch.int32
@@ -750,23 +756,34 @@ def update_pages(block_table, held, seq_lens, free_pages, free_count, *, page_si
     (num_pages,) = _dims("free_pages", free_pages, 1)
     if (cu is None) != (slots is None):
         raise ValueError("cu and slots: both or neither")
-    n_rows = 0 if slots is None else _dims("slots", slots, 1)[0]
-    if not (_fits(block_table, i32, (B, max_pages), dev) and _fits(held, i32, (B,), dev)
-            and _fits(seq_lens, i32, (B,), dev) and _fits(free_pages, i32, (num_pages,), dev)
-            and _fits(free_count, i32, (1,), dev)):
+    # (written out: a call of _fits for each takes a microsecond more)
+    if not (block_table.dtype is i32 and block_table.is_contiguous()
+            and held.dtype is i32 and held.shape == (B,) and held.get_device() == dev and held.is_contiguous()
+            and seq_lens.dtype is i32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev
+            and seq_lens.is_contiguous()
+            and free_pages.dtype is i32 and free_pages.get_device() == dev and free_pages.is_contiguous()
+            and free_count.dtype is i32 and free_count.shape == (1,) and free_count.get_device() == dev):
         for name, t, shape in (("block_table", block_table, (B, max_pages)), ("held", held, (B,)),
                                ("seq_lens", seq_lens, (B,)), ("free_pages", free_pages, (num_pages,)),
                                ("free_count", free_count, (1,))):
             _tensor(name, t, i32, shape, dev)
+    n_rows = at_cu = at_slots = 0
     if slots is not None:
-        _tensor("cu", cu, i32, (B + 1,), dev)
-        _tensor("slots", slots, torch.int64, (n_rows,), dev)
+        (n_rows,) = _dims("slots", slots, 1)
+        if not (cu.dtype is i32 and cu.shape == (B + 1,) and cu.get_device() == dev and cu.is_contiguous()):
+            _tensor("cu", cu, i32, (B + 1,), dev)
+        if not (slots.dtype is torch.int64 and slots.get_device() == dev and slots.is_contiguous()):
+            _tensor("slots", slots, torch.int64, (n_rows,), dev)
+        at_cu, at_slots = cu.data_ptr(), slots.data_ptr()
     if err_word is not None and (err_word.dtype is not i32 or err_word.numel() < 1 or err_word.get_device() != dev):
         raise ValueError("err_word: an int32 tensor beside the block table")
-    workspace, room = _room(workspace, update_pages_workspace_bytes(B), block_table, stream)
+    at_workspace = room = 0
+    if workspace is not None or B > PAGES_SMALL_BATCH or n_rows > PAGES_SMALL_ROWS:
+        workspace, room = _room(workspace, update_pages_workspace_bytes(B), block_table, stream)
+        at_workspace = workspace.data_ptr()
     _call("mla_update_pages", lib().mla_update_pages, dev, stream, block_table.data_ptr(), held.data_ptr(),
-          seq_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), _address(cu), _address(slots), B, n_rows,
-          num_pages, page_size, max_pages, workspace.data_ptr(), room, _address(err_word))
+          seq_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), at_cu, at_slots, B, n_rows, num_pages,
+          page_size, max_pages, at_workspace, room, _address(err_word))
     return slots
 
 

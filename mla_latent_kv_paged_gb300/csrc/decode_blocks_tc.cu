@@ -246,11 +246,9 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffSlots + 4);
 
-  // one thread's wait, and a warp's: its lanes go on, or give up, together
+  // (as in decode_tc.cu, a warp's lanes wait in step: one try, one look at the flag and the clock for all
+  // of them. A vote on the result in every wait cost 3%.)
   auto wait = [&](uint32_t b, uint32_t parity) -> bool { return wait_short(b, parity, abort_flag); };
-  auto wait_warp = [&](uint32_t b, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, wait_short(b, parity, abort_flag));
-  };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kOpSlots; ++i) {
@@ -384,7 +382,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
       const int pid = cur_next(ld);
       // an id outside the pool loads zeros (TMA bounds) and is reported
       if (lane == 0 && !none && (pid < 0 || pid >= num_pages)) report_error(err_word, MLA_ERR_BOUNDS);
-      if (!wait_warp(bar(CE0 + stage), ph ^ 1u)) { ok = false; break; }
+      if (!wait(bar(CE0 + stage), ph ^ 1u)) { ok = false; break; }
       const uint32_t fb = bar(CF0 + stage), dst = sbase + kOffCode + stage * kCodeBytes;
       if (lane == 0 && MLA_SMEM_OK(dst, kCodeBytes)) {
         const int y = ((pid << tile_shift) + sub) * kTile;
@@ -552,7 +550,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
         // (this warp read the S of its last page), so Q may be overwritten.
         for (int q = 0; q < kQSlots && ok; ++q) {
           const int slot = g + kQSlots * li + q;
-          if (!wait_warp(bar(OPF0 + slot % kOpSlots), (slot / kOpSlots) & 1)) { ok = false; break; }
+          if (!wait(bar(OPF0 + slot % kOpSlots), (slot / kOpSlots) & 1)) { ok = false; break; }
           const uint32_t sq = sbase + kOffOp + (slot % kOpSlots) * kOpBytes + (uint32_t)row * 128;
           (void)MLA_SMEM_OK(sq + kQBoxBytes, 128);
 #pragma unroll
@@ -584,7 +582,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
         tc_fence_before();
         mbar_arrive(bar(QCF));
         for (int i = 0; i < ntiles; ++i, ++g) {
-          if (!wait_warp(bar(SF0 + (g & 1)), (g >> 1) & 1)) { ok = false; break; }
+          if (!wait(bar(SF0 + (g & 1)), (g >> 1) & 1)) { ok = false; break; }
           tc_fence_after();
           uint32_t r[32];
           tmem_ld32(tS + 32 * peer, r);
@@ -593,7 +591,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
           mbar_arrive(bar(SFREE));
           // the peer has read this CTA's partial of page g-2 (same buffer)
           if (g >= 2) {
-            if (!wait_warp(bar(XE0 + (g & 1)), ((g >> 1) & 1) ^ 1)) { ok = false; break; }
+            if (!wait(bar(XE0 + (g & 1)), ((g >> 1) & 1) ^ 1)) { ok = false; break; }
             if (atid == 0) mbar_arrive_expect_tx(bar(XE0 + (g & 1)), kTokBytes);  // arm for this page
           }
           // The partial scores go out as fp16 offsets from the midpoint of this head's
@@ -701,11 +699,11 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
           if ((g & 1) != grp) {
             if (i == ntiles - 1) {
               // helper at the end of the range handled by the other group
-              if (!wait_warp(bar(IVF0 + grp), iv_n & 1)) { ok = false; break; }
+              if (!wait(bar(IVF0 + grp), iv_n & 1)) { ok = false; break; }
               ++iv_n;
               float inv;
               asm volatile("ld.shared.f32 %0, [%1];" : "=f"(inv) : "r"(sbase + kOffIV + vec_off));
-              if (!wait_warp(bar(PVD0 + g % kPBufs), (g / kPBufs) & 1)) { ok = false; break; }
+              if (!wait(bar(PVD0 + g % kPBufs), (g / kPBufs) & 1)) { ok = false; break; }
               tc_fence_after();
               drain_o(it, 1, inv);
               tc_fence_before();
@@ -716,7 +714,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
           const int xb = g & 1;
           // this CTA's partial scores of its 32 tokens
           const int nv = n_att - ((pg0 + i) * kTile + 32 * (int)rank);  // valid tokens among these 32
-          if (!wait_warp(bar(SF0 + xb), (g >> 1) & 1)) { ok = false; break; }
+          if (!wait(bar(SF0 + xb), (g >> 1) & 1)) { ok = false; break; }
           tc_fence_after();
           {
             uint32_t r[32];
@@ -728,7 +726,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
           tc_fence_before();
           mbar_arrive(bar(SFREE));
           // add the peer's partial for these tokens: its midpoint plus the fp16 offsets
-          if (!wait_warp(bar(XF0 + xb), (g >> 1) & 1)) { ok = false; break; }
+          if (!wait(bar(XF0 + xb), (g >> 1) & 1)) { ok = false; break; }
           if (gtid == 0) mbar_arrive_expect_tx(bar(XF0 + xb), kXBytes);  // arm for page g+2
           float mid_p;
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(mid_p) : "r"(sbase + kOffX + xb * kXBytes + kXDataBytes + vec_off));
@@ -760,7 +758,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
           // previous phase, page g-6, is complete: the value MMAs complete in page
           // order and this group waited for page g-5 at page g-2.)
           const int pb = g % kPBufs;
-          if (g >= kPBufs && !wait_warp(bar(PVD0 + pb), ((g / kPBufs) & 1) ^ 1)) { ok = false; break; }
+          if (g >= kPBufs && !wait(bar(PVD0 + pb), ((g / kPBufs) & 1) ^ 1)) { ok = false; break; }
           const int rows_valid = L - (pg0 + i) * kTile;
           if (rows_valid < kTile) {
             // slack rows past the context may hold any bits: zero this CTA's latent
@@ -783,14 +781,14 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
           for (int jj = 1; jj < 31; jj += 2) m = max3(m, x[jj], x[jj + 1]);
           m = fmaxf(m, x[31]);
           st_async_b32(r_mx + xb * kVecBytes + vec_off, __float_as_uint(m), r_mxf + 8u * xb);
-          if (!wait_warp(bar(MXF0 + xb), (g >> 1) & 1)) { ok = false; break; }
+          if (!wait(bar(MXF0 + xb), (g >> 1) & 1)) { ok = false; break; }
           if (gtid == 0) mbar_arrive_expect_tx(bar(MXF0 + xb), kVecBytes);
           float m_p;
           asm volatile("ld.shared.f32 %0, [%1];" : "=f"(m_p) : "r"(sbase + kOffMX + xb * kVecBytes + vec_off));
           const float mt = fmaxf(m, m_p);
           // the reference maximum: the previous page's decision (the other group's)
           // is raised lazily, only when this page exceeds it by the threshold
-          if (g >= 1 && !wait_warp(bar(MRF), (g - 1) & 1)) { ok = false; break; }
+          if (g >= 1 && !wait(bar(MRF), (g - 1) & 1)) { ok = false; break; }
           float m_new = mt, alpha = 1.f;
           bool need = false;
           if (i > 0) {
@@ -810,7 +808,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
             if (lane == 0) atomicAdd(&g_dbg_counters[0], 1ull);
 #endif
             // O must hold every earlier page before it is rescaled
-            if (!wait_warp(bar(PVD0 + (g - 1) % kPBufs), ((g - 1) / kPBufs) & 1)) { ok = false; break; }
+            if (!wait(bar(PVD0 + (g - 1) % kPBufs), ((g - 1) / kPBufs) & 1)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
@@ -870,7 +868,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
             // epilogue: the CTA's sum (both groups), the peer's, the normalised output
             float l_c = l_g;
             if (ntiles >= 2) {
-              if (!wait_warp(bar(LGF0 + (lg_n & 1)), (lg_n >> 1) & 1)) { ok = false; break; }
+              if (!wait(bar(LGF0 + (lg_n & 1)), (lg_n >> 1) & 1)) { ok = false; break; }
               const uint32_t lg = sbase + kOffLG + (uint32_t)(lg_n & 1) * 2 * kVecBytes;
               float l_o, m_o;
               asm volatile("ld.shared.f32 %0, [%1];" : "=f"(l_o) : "r"(lg + vec_off));
@@ -879,7 +877,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
             }
             const int lb = li & 1;
             st_async_b32(r_lx + lb * kVecBytes + vec_off, __float_as_uint(l_c), r_lxf + 8u * lb);
-            if (!wait_warp(bar(LXF0 + lb), (li >> 1) & 1)) { ok = false; break; }
+            if (!wait(bar(LXF0 + lb), (li >> 1) & 1)) { ok = false; break; }
             if (gtid == 0) mbar_arrive_expect_tx(bar(LXF0 + lb), kVecBytes);  // arm for range li+2
             float l_p;
             asm volatile("ld.shared.f32 %0, [%1];" : "=f"(l_p) : "r"(sbase + kOffLX + lb * kVecBytes + vec_off));
@@ -889,7 +887,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
             // 1/l for the helper group, which drains the other half of O
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(sbase + kOffIV + vec_off), "f"(inv) : "memory");
             mbar_arrive(bar(IVF0 + (grp ^ 1)));
-            if (!wait_warp(bar(PVD0 + pb), (g / kPBufs) & 1)) { ok = false; break; }
+            if (!wait(bar(PVD0 + pb), (g / kPBufs) & 1)) { ok = false; break; }
             tc_fence_after();
             const size_t orow = ((size_t)it * n_q + j) * H + row;
             drain_o(it, 0, inv);
@@ -922,7 +920,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
     int asked = 0;           // uses of operand slots up to the last query's
     bool ok = true;
     auto next_slot = [&]() -> bool {  // the next operand slot, once its last use is over
-      const bool free = wait_warp(bar(EMPTY0 + slot % kOpSlots), ((slot / kOpSlots) & 1) ^ 1);
+      const bool free = wait(bar(EMPTY0 + slot % kOpSlots), ((slot / kOpSlots) & 1) ^ 1);
       if (!free) ok = false;
       return free;
     };
@@ -947,7 +945,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
       }
       for (int i = 0; i < ntiles && ok; ++i, ++slot, ++page) {
         const int cs = page % kCodeSlots;
-        if (!wait_warp(bar(CF0 + cs), (page / kCodeSlots) & 1)) { ok = false; break; }
+        if (!wait(bar(CF0 + cs), (page / kCodeSlots) & 1)) { ok = false; break; }
         const uint32_t sc = sbase + kOffCode + cs * kCodeBytes + wtid * 16;
         const uint32_t se = sbase + kOffEntries + cs * kEntriesBytes;
         const uint32_t dst = sbase + kOffOp + (slot % kOpSlots) * kOpBytes;

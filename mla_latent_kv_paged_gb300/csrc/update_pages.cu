@@ -28,8 +28,9 @@ constexpr int kThreads = 1024;
 static_assert(MLA_MAX_BATCH == 4 * kThreads, "one, two or four sequences a thread");
 constexpr int kLanes = 8;  // of a page
 constexpr int kGridThreads = 256;
-// One launch up to these sizes (see the file's head).
-constexpr int kSmallRows = 4096, kSmallBatch = kThreads;
+// One launch up to these sizes, without a workspace.
+constexpr int kSmallRows = MLA_PAGES_SMALL_ROWS, kSmallBatch = MLA_PAGES_SMALL_BATCH;
+static_assert(kSmallBatch <= kThreads, "a sequence a thread");
 
 struct Sequence {  // one read of what a page's group needs
   int32_t page0;   // its first page
@@ -77,10 +78,10 @@ __device__ __forceinline__ int last_at(const int32_t* sum, int n, int x) {
 }
 
 // The pages, each by one group of lanes; then the pages given back and not taken, each
-// by a thread; then the rows behind the last sequence. give, unit: copies of w's in shared memory.
-__device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, const int32_t* give, const int32_t* unit,
-                                           int thread, int threads, int32_t* err_word) {
+// by a thread; then the rows behind the last sequence. w's give and unit lie in shared memory.
+__device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, int thread, int threads, int32_t* err_word) {
   const int F = w.total[0], R = w.total[1], K = w.total[2], units = w.total[3];
+  const int32_t *give = w.give, *unit = w.unit;
   const int lane = thread % kLanes, shift = p.page_shift;
   const uint32_t group = 0xFFu << ((threadIdx.x & 31) & ~(kLanes - 1));
   bool bad = false;
@@ -164,8 +165,10 @@ __global__ void __launch_bounds__(kThreads)
 update_pages_scan(Pages p, Work w, int32_t* err_word) {
   __shared__ int sums[32][2], unit_sums[32][1];
   __shared__ int served;  // pages taken in all
-  __shared__ int32_t give[kAll ? kThreads : 1], unit[kAll ? kThreads : 1];
   static_assert(!kAll || kPer == 1, "shared memory");
+  __shared__ int32_t give[kAll ? kThreads : 1], unit[kAll ? kThreads : 1], total[4];
+  __shared__ Sequence seq[kAll ? kThreads : 1];
+  if (kAll) w = Work{give, unit, seq, total};
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
   const int tid = threadIdx.x, b0 = tid * kPer;
@@ -253,13 +256,8 @@ update_pages_scan(Pages p, Work w, int32_t* err_word) {
   for (int i = 0; i < kPer; ++i) {
     const int b = b0 + i;
     if (b < p.B) {
-      if (kAll) {
-        give[b] = gives[i];
-        unit[b] = u;
-      } else {
-        w.give[b] = gives[i];
-        w.unit[b] = u;
-      }
+      w.give[b] = gives[i];
+      w.unit[b] = u;
       w.seq[b] = s[i];
     }
     u = plus(u, count[i]);
@@ -275,14 +273,14 @@ update_pages_scan(Pages p, Work w, int32_t* err_word) {
   else if (bad) report_error(err_word, MLA_ERR_BOUNDS);
   if (kAll) {
     __syncthreads();
-    deal_pages(p, w, give, unit, tid, kThreads, err_word);
+    deal_pages(p, w, tid, kThreads, err_word);
   }
 }
 
 __global__ void __launch_bounds__(kGridThreads)
 update_pages_deal(Pages p, Work w, int32_t* err_word) {
   extern __shared__ int32_t prefix[];
-  int32_t *give = prefix, *unit = prefix + p.B;
+  int32_t *give = prefix, *unit = prefix + p.B;  // every search is in these
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
   for (int b = threadIdx.x; b < p.B; b += kGridThreads) {
@@ -290,7 +288,9 @@ update_pages_deal(Pages p, Work w, int32_t* err_word) {
     unit[b] = w.unit[b];
   }
   __syncthreads();
-  deal_pages(p, w, give, unit, blockIdx.x * kGridThreads + threadIdx.x, gridDim.x * kGridThreads, err_word);
+  w.give = give;
+  w.unit = unit;
+  deal_pages(p, w, blockIdx.x * kGridThreads + threadIdx.x, gridDim.x * kGridThreads, err_word);
 }
 
 }  // namespace
@@ -298,7 +298,7 @@ update_pages_deal(Pages p, Work w, int32_t* err_word) {
 size_t update_pages_workspace_bytes(int B) { return work_layout(nullptr, B, nullptr); }
 
 cudaError_t launch_update_pages(const Pages& p, void* workspace, int32_t* err_word, cudaStream_t s) {
-  Work w;
+  Work w = {};
   work_layout(workspace, p.B, &w);
   if (p.n_rows <= kSmallRows && p.B <= kSmallBatch)
     return launch_pdl(update_pages_scan<1, true>, dim3(1), dim3(kThreads), 0, s, p, w, err_word);

@@ -120,12 +120,13 @@ def test_update_pages_refusals(lib):
         a.update(kw)
         return lib.mla_update_pages(*a.values(), None, None)
 
-    refusals(call, ("bt", "held", "sl", "free", "count", "cu", "slots", "ws"))
+    refusals(call, ("bt", "held", "sl", "free", "count", "cu", "slots"))
+    assert call(ws=P + 4) == 1 and call(ws=None, n=4097) == 1  # (up to 1024 sequences and 4096 rows it may be null)
     assert call(B=0) == 1 and call(n=0) == 1 and call(n=-1) == 1 and call(pages=0) == 1 and call(maxp=0) == 1
     assert call(cu=None, slots=None, n=-1) == 1
     assert call(B=4097) == 2 and call(n=(1 << 20) + 1) == 2 and call(page=32) == 2
     assert call(maxp=(1 << 24) + 1) == 2 and call(pages=1 << 26) == 2
-    assert call(wsb=ws - 1) == 3
+    assert call(wsb=ws - 1, n=4097) == 3 and call(B=1025, ws=None) == 1 and call(B=1025) == 3
 
 
 def test_python_refusals():

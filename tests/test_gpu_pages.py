@@ -255,4 +255,5 @@ def test_python_checks(mla):
     with pytest.raises(ValueError, match="slots"):
         mla.update_pages(**good, cu=s.i([0, 1, 2]), slots=s.i([0, 0]))
     with pytest.raises(mla.MlaError, match="WORKSPACE"):
-        mla.update_pages(**good, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+        mla.update_pages(**good, cu=s.i([0, 1, 2]), slots=torch.zeros(4097, dtype=torch.int64, device="cuda"),
+                         workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
