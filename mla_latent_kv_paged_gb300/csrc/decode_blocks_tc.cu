@@ -5,26 +5,32 @@
 // every 64-token tile; partial scores, page maxima and weights exchanged between the two; the head
 // rows as the M = 128 rows of both products. It differs in
 //   - the tile: e4m3 codes with a power of two for each block of tokens and group of columns, which
-//     eight warps of their own widen to the fp16 boxes that the MMAs read, powers applied
+//     twelve warps of their own widen to the fp16 boxes that the MMAs read, powers applied
 //     (exact from 2^-14 on). Column scales can be folded into the query and the output instead, as
 //     decode_tc.cu does for its 8-bit cache; a block's cannot;
 //   - the ring: four operand slots (queries and widened tiles, 36 KB) and two slots of codes (18 KB),
 //     each free again as soon as its codes are widened;
 //   - the operands: query, weights and tiles in fp16, fp32 sums;
-//   - the roles: a warpgroup each, with registers dealt out by setmaxnreg (24 warps: producer, two
-//     MMA issuers and an idle one; score readers; softmax 2 x 4; wideners 2 x 4).
+//   - the roles: a warpgroup each, with registers dealt out by setmaxnreg (28 warps: producer, two
+//     MMA issuers and an idle one; score readers; softmax 2 x 4; wideners 3 x 4).
 // It is a kernel of its own because a change to the other's code, even one that its template
 // folds away, costs it up to 2%.
 //
-// What bounds it: a tile's chain of work, as there, and beside it the widening. 32 sequences of 4096
-// tokens, 128 heads (decode call and its step, us): 8-bit with column scales 59 / 75; here 45 / 56; bf16
-// 42 / 56. Steps on the way (step of 32 x 4096): widened by the score readers 102; by four warps of their
+// What bounds it: a tile's chain of work, as there (2300 cycles a tile at long contexts), and the wideners'
+// share of the issue slots and of shared memory. More room does not help: five operand slots in place of
+// four (with the positional columns in a ring of two, and P in two buffers) took the same time.
+// 32 sequences of 4096 tokens, 128 heads (this kernel alone with cold caches / decode step, us): 8-bit with
+// column scales 60 / 75; here 45 / 57; bf16 44 / 56. Four sequences of 131072 (step): 166; 132; 122.
+// Steps on the way (step of 32 x 4096): widened by the score readers 102; by four warps of their
 // own, to bf16 73 (83 instructions for 16 codes), to fp16 72; by eight 63; with the roles' code made
 // short (packed fp32 pairs, maxima of three, waits of few instructions, loops left rolled) and the next
 // codes read ahead 60: five roles share the SM's instruction caches, and every unrolled loop was
-// slower; with 56 registers for the wideners 56. Measured and not taken: tiles prefetched
-// into L2 (65), codes as 256-byte rows (60), the entries read ahead (60 to 63), score MMAs started on the
-// first half of a widened tile (60).
+// slower; with registers dealt by need 58.5; by twelve, three chunks each, all read before the wait for the
+// operand slot, 57 (and the long contexts from 139 to 132).
+// Measured and not taken: tiles prefetched into L2 (65), codes as 256-byte rows (60), the entries read ahead
+// (60 to 63), score MMAs started on the first half of a widened tile (60). A slot of codes is given back
+// after the widened values are stored, not once its codes are read: given back right after the loads,
+// the next copy overtook some of them, for 0.2% of the time.
 //
 // Tensor memory (512 columns x 128 lanes of 32 bits): O [0,256), S [256,320), this CTA's P half for three
 // tiles [320,368), positional query half [368,384), latent query half [384,512).
@@ -43,11 +49,11 @@ constexpr int kAWarps = 4;  // score readers: one per TMEM lane quadrant
 constexpr int kBWarps = 8;  // softmax: two groups of four (one per lane quadrant), alternate pages
 constexpr int kAThreads = kAWarps * 32, kBThreads = kBWarps * 32;
 constexpr int kGThreads = kBThreads / 2;  // one softmax group: a thread per head row
-constexpr int kWThreads = 8 * 32;  // wideners
+constexpr int kWThreads = 12 * 32;  // wideners: three 16-byte chunks of a tile each
 constexpr int kRead0 = 4, kSoft0 = kRead0 + kAWarps, kWide0 = kSoft0 + kBWarps;  // first warps of the roles
 constexpr int kThreads = 32 * kWide0 + kWThreads;
-constexpr int kRegsIssue = 48, kRegsRead = 96, kRegsSoftmax = 112, kRegsWiden = 56;
-static_assert(kRegsIssue + kRegsRead + 2 * kRegsSoftmax + 2 * kRegsWiden <= 6 * 80, "the launch's registers");
+constexpr int kRegsIssue = 56, kRegsRead = 96, kRegsSoftmax = 104, kRegsWiden = 48;
+static_assert(kRegsIssue + kRegsRead + 2 * kRegsSoftmax + 3 * kRegsWiden <= 7 * 72, "the launch's registers");
 constexpr uint32_t kCBoxBytes = 64 * 128;   // [64 tokens][64 latent cols] fp16, 128B swizzle
 constexpr uint32_t kKrBoxBytes = 64 * 64;   // [64 tokens][32 positional cols] fp16, 64B swizzle
 constexpr uint32_t kOpBytes = 4 * kCBoxBytes + kKrBoxBytes;  // 36864: an operand slot
@@ -906,16 +912,23 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
   auto widen = [&]() {
     // ------------------------------------------------------------ wideners
     // They hand out the operand slots in ring order. A query's two slots are filled by TMA; a tile's codes become
-    // the fp16 half that the MMAs read, in the swizzled layout of decode_tc.cu's boxes. The loop stays short:
-    // unrolled over all of a thread's chunks it kept the other roles waiting for their instructions.
-    const int wtid = threadIdx.x - 32 * kWide0;  // 0 .. 255
-    // 16-byte chunks wtid + 256 k of the page half: box k, token wtid / 4, 16 of its 64 columns;
-    // then, for the first half of the threads, the positional box: token wtid / 2, 16 of its 32
-    // columns (64B swizzle)
-    const uint32_t t = (uint32_t)wtid >> 2, kk = wtid & 3, tr = (uint32_t)wtid >> 1, kr = 2 * (wtid & 1);
-    const uint32_t w0 = t * 128 + ((2 * kk) ^ (t & 7)) * 16, w1 = t * 128 + ((2 * kk + 1) ^ (t & 7)) * 16;
-    const uint32_t x0 = 4 * kCBoxBytes + tr * 64 + (kr ^ ((tr >> 1) & 3)) * 16;
-    const uint32_t x1 = 4 * kCBoxBytes + tr * 64 + ((kr + 1) ^ ((tr >> 1) & 3)) * 16;
+    // the fp16 half that the MMAs read, in the swizzled layout of decode_tc.cu's boxes. The code stays short:
+    // longer code kept the other roles waiting for their instructions.
+    const int wtid = threadIdx.x - 32 * kWide0;  // 0 .. 383
+    // 16-byte chunks q = wtid + 384 k of the 1152 of a tile's half: q < 1024: box q / 256, token q / 4 % 64, 16 of
+    // its 64 columns; then the positional box: token (q - 1024) / 2, 16 of its 32 columns (64B swizzle)
+    constexpr int kChunks = kCodeBytes / 16 / kWThreads;
+    static_assert(kChunks * kWThreads * 16 == kCodeBytes, "the same number for every thread");
+    // where a chunk's first eight values go (the other eight: 16 bytes on or back), and its power's place
+    uint32_t to[kChunks], at[kChunks];
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      const uint32_t q = wtid + kWThreads * k, latent = q < 1024;
+      const uint32_t t = latent ? q >> 2 & 63 : (q - 1024) >> 1, kk = latent ? 2 * (q & 3) : 2 * (q & 1);
+      to[k] = latent ? (q >> 8) * kCBoxBytes + t * 128 + (kk ^ (t & 7)) * 16
+                     : 4 * kCBoxBytes + t * 64 + (kk ^ (t >> 1 & 3)) * 16;
+      at[k] = (t >> block_shift) * kEntryBytes + (latent ? 2 * rank + (q >> 9) : 4u);
+    }
     int slot = 0, page = 0;  // uses of operand slots, and of slots of codes
     int asked = 0;           // uses of operand slots up to the last query's
     bool ok = true;
@@ -949,28 +962,26 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
         const uint32_t sc = sbase + kOffCode + cs * kCodeBytes + wtid * 16;
         const uint32_t se = sbase + kOffEntries + cs * kEntriesBytes;
         const uint32_t dst = sbase + kOffOp + (slot % kOpSlots) * kOpBytes;
-        const int left = end - i * kTile;  // tokens of the context from this tile on
-        // the powers of the CTA's two groups in this thread's block, and of the positional columns
-        uint32_t pw, pr, v[4], o[8] = {};
-        asm volatile("ld.shared.u16 %0, [%1];" : "=r"(pw) : "r"(se + ((t >> block_shift) << 3) + 2 * rank));
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(pr) : "r"(se + ((tr >> block_shift) << 3) + 4));
-        ld_shared_v4(sc, v[0], v[1], v[2], v[3]);
-        const uint32_t by0 = power_f16x2(pw & 0xFFu), by1 = power_f16x2(pw >> 8);
-        auto put = [&](uint32_t a0, uint32_t a1, bool beyond, uint32_t token) {
-          if (beyond && (int)token < left) report_error(err_word, MLA_ERR_RANGE);
+        uint32_t v[kChunks][4], p[kChunks], o[8] = {};
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          ld_shared_v4(sc + 16 * kWThreads * k, v[k][0], v[k][1], v[k][2], v[k][3]);
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(p[k]) : "r"(se + at[k]));
+        }
+        if (!next_slot()) break;
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) {
+          const bool beyond = widen16(v[k], power_f16x2(p[k]), p[k], o);
+          const uint32_t a0 = dst + to[k], a1 = a0 ^ 16u;
+          if (beyond) {
+            const int q = wtid + kWThreads * k, t = q < 1024 ? q >> 2 & 63 : (q - 1024) >> 1;
+            if (t < end - i * kTile) report_error(err_word, MLA_ERR_RANGE);  // a token of the context
+          }
           if (MLA_SMEM_OK(a0, 16) && MLA_SMEM_OK(a1, 16)) {
             st_shared_v4(a0, o[0], o[1], o[2], o[3]);
             st_shared_v4(a1, o[4], o[5], o[6], o[7]);
           }
-        };
-        if (!next_slot()) break;
-#pragma unroll 2
-        for (uint32_t k = 0; k < 4; ++k) {
-          const bool beyond = widen16(v, k < 2 ? by0 : by1, k < 2 ? pw & 0xFFu : pw >> 8, o);
-          if (k < 3 || wtid < 128) ld_shared_v4(sc + 4096 * (k + 1), v[0], v[1], v[2], v[3]);  // the next chunk
-          put(dst + k * kCBoxBytes + w0, dst + k * kCBoxBytes + w1, beyond, t);
         }
-        if (wtid < 128) put(dst + x0, dst + x1, widen16(v, power_f16x2(pr), pr, o), tr);
         fence_proxy_async_smem();  // read by the MMAs (async proxy)
         __syncwarp();
         if ((wtid & 31) == 0) {

@@ -542,6 +542,19 @@ def test_absorbed_attention(mla, err, H, page, block, new, lens, pad):
     assert ((lse[:c.total].double() - want_lse).abs() <= lse_bound).all()
 
 
+@pytest.mark.parametrize("H,page,block,new,lens,pad", CHUNKS[3:])
+def test_calls_repeat_their_bits(mla, err, H, page, block, new, lens, pad):
+    """Slots of codes and operands pass between the roles of a CTA hundreds of times in a call: one handed on too
+    early shows as bits that change from call to call."""
+    import torch
+    c = Blocks(new, lens, H=H, page=page, block=block, seed=11, pad_rows=pad, spread=0.5)
+    want = [bits(x) for x in attend(mla, c, c.codes, c.entries, "absorbed", err)]
+    for _ in range(60):
+        got = [bits(x) for x in attend(mla, c, c.codes, c.entries, "absorbed", err)]
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert int(err.item()) == 0
+
+
 def test_expanded_and_auto_against_64_bits(mla, err):
     """A ragged chunk within the bounds that chunk_reference derives for a bf16 cache (the values are the
     cache's own, so its quantisation is no part of the error)."""
