@@ -2,11 +2,12 @@
  * mla_debug.h — entry points of the test build of the library
  * (libmla_gb300_debug.so, compiled from the same sources with
  * MLA_DEBUG_CHECKS=1). The release library libmla_gb300.so does not export
- * them. No page has a counterpart: they instrument the decode kernel so tests
- * can see that rarely taken branches ran and that a bounded wait gives up, there
+ * them. No page has a counterpart: they instrument the decode kernels (that of the
+ * block-scaled cache is one of its own; both are meant below, and their counters are added
+ * up) so tests can see that rarely taken branches ran and that a bounded wait gives up, there
  * and in the MMA kernels of the chunk calls.
  *
- * In the test build the decode kernel also checks every shared-memory
+ * In the test build a decode kernel also checks every shared-memory
  * address it computes for a plain or cluster store or load (and the tensor
  * memory columns of the P operand) against its own allocation; an address
  * outside it is counted, reported as MLA_ERR_BOUNDS in err_word, and the

@@ -6,8 +6,10 @@
 // Why powers of two: e4m3 is a floating format, so a scale only moves its window of
 // 17 binades and a power of two loses no precision against amax / 448; requantising
 // a block whose power grows then is exact but for values that fall into e4m3's
-// subnormals; and a value is a bf16 number exactly (four significant bits), so what
-// follows (the MMAs, the keys' expansion) is that of the bf16 cache, bit for bit.
+// subnormals; and a value is a bf16 number exactly (four significant bits), so rows read
+// back and the keys' expansion are those of a bf16 cache, bit for bit. It is an fp16 number as well
+// (below 2^-14 rounded to multiples of 2^-24), which the decode takes: codes widen to fp16 in two
+// instructions for four, and weights in fp16 carry three bits more than in bf16.
 #pragma once
 
 #include "mla_internal.cuh"

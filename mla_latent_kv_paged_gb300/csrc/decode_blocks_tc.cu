@@ -28,7 +28,8 @@
 // slower; with registers dealt by need 58.5; by twelve, three chunks each, all read before the wait for the
 // operand slot, 57 (and the long contexts from 139 to 132).
 // Measured and not taken: tiles prefetched into L2 (65), codes as 256-byte rows (60), the entries read ahead
-// (60 to 63), score MMAs started on the first half of a widened tile (60). A slot of codes is given back
+// (60 to 63), score MMAs started on the first half of a widened tile (60), weights taken with an older reference
+// while the maxima travel (58). A slot of codes is given back
 // after the widened values are stored, not once its codes are read: given back right after the loads,
 // the next copy overtook some of them, for 0.2% of the time.
 //

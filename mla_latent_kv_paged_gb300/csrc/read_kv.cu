@@ -11,6 +11,7 @@
 // source of each of its rows (search in cu, one block-table entry).
 // 4 x 131072 rows of a bf16 cache: 176 us, 6.86 TB/s, the measured copy rate; a few
 // hundred rows: 3.2 us, the latency of one launch and three dependent reads.
+// 4 x 65536 rows of a block-scaled cache: 69.7 us, 6.5 TB/s; 2000 rows of seven sequences 3.3 us.
 #include "blocks.cuh"
 #include "chunk.cuh"
 #include "sm100.cuh"

@@ -13,6 +13,11 @@
 // the codes are written from the registers. CTA c of a group belongs to the last sequence b with
 // cu[b] / 64 + 2b <= c: a run of n rows touches at most n / 64 + 2 tiles, so every
 // tile has a CTA without a plan on the device before (the CTAs left over end at once).
+//
+// Measured: 42026 rows of 24 prompt pieces 16.3 us (72.7 MB, 4.5 TB/s: the reads that come before a row's,
+// of cu, length and page, are as long as the row's own), one row for each of 128 sequences 4.9 us, a launch and five
+// dependent reads. These two with all five groups in one CTA 21.9 and 6.8, with 256 threads 17.5 and 5.8,
+// with 64 17.1 and 5.2; held to more CTAs an SM by fewer registers no change.
 #include "blocks.cuh"
 #include "chunk.cuh"
 
