@@ -14,10 +14,12 @@
 // cu[b] / 64 + 2b <= c: a run of n rows touches at most n / 64 + 2 tiles, so every
 // tile has a CTA without a plan on the device before (the CTAs left over end at once).
 //
-// Measured: 42026 rows of 24 prompt pieces 16.3 us (72.7 MB, 4.5 TB/s: the reads that come before a row's,
-// of cu, length and page, are as long as the row's own), one row for each of 128 sequences 4.9 us, a launch and five
-// dependent reads. These two with all five groups in one CTA 21.9 and 6.8, with 256 threads 17.5 and 5.8,
-// with 64 17.1 and 5.2; held to more CTAs an SM by fewer registers no change.
+// Measured: 42026 rows of 24 prompt pieces 14.5 us (72.7 MB, 5.0 TB/s: the reads that come before a row's,
+// of cu, length and page, are as long as the row's own, and two thirds of the issue slots are taken), one row for
+// each of 128 sequences 4.0 us, a launch and five dependent reads. With magnitudes looked over two by two first and
+// what is not finite only where there is some, and the products two by two in bf16 (exact: powers): 16.3 and
+// 4.8 before. With 256 threads 15.2 and 4.9, held to 48 registers (ten CTAs an SM) 14.0 and 4.3; before that step
+// all five groups in one CTA took 21.9 and 6.8.
 #include "blocks.cuh"
 #include "chunk.cuh"
 
@@ -67,6 +69,11 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
   asm("{\n\t.reg .b16 a;\n\tcvt.u16.u32 a, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(w));
   return sm100::f16x2_to_f32(h);
 }
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // 0x8000 in each half that is infinite or NaN (bf16 pair)
 __device__ __forceinline__ uint32_t not_finite(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
 
@@ -115,27 +122,30 @@ __device__ __forceinline__ void write_tile(const Tile& tile, const Cache& cache,
   for (int j = 0; j < kSub; ++j) m[j] = 0;
 #pragma unroll
   for (int k = 0; k < kPer; ++k) {
-    uint32_t* w = &v[k].x;
+    const uint32_t* w = &v[k].x;
+    uint32_t& mj = m[k * kAtOnce / 16];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t bad = not_finite(w[q]);
-      w[q] |= bad - (bad >> 15);  // 0x7FFF: infinities are stored as NaN
+    for (int q = 0; q < 4; ++q) mj = __vmaxu2(mj, w[q] & 0x7FFF7FFFu);
+  }
+  if (not_finite(__vmaxu2(__vmaxu2(m[0], m[1]), __vmaxu2(m[2], m[3])))) {  // some value is: the maxima without those
+#pragma unroll
+    for (int j = 0; j < kSub; ++j) m[j] = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      uint32_t* w = &v[k].x;
       uint32_t& mj = m[k * kAtOnce / 16];
-      mj = __vmaxu2(mj, w[q] & 0x7FFF7FFFu & ~((bad >> 15) * 0xFFFFu));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t bad = not_finite(w[q]);
+        w[q] |= bad - (bad >> 15);  // 0x7FFF: infinities are stored as NaN
+        mj = __vmaxu2(mj, w[q] & 0x7FFF7FFFu & ~((bad >> 15) * 0xFFFFu));
+      }
     }
   }
-  uint32_t m01 = __vmaxu2(m[0] & 0xFFFFu, m[0] >> 16) | __vmaxu2(m[1] & 0xFFFFu, m[1] >> 16) << 16;
-  uint32_t m23 = __vmaxu2(m[2] & 0xFFFFu, m[2] >> 16) | __vmaxu2(m[3] & 0xFFFFu, m[3] >> 16) << 16;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    m01 = __vmaxu2(m01, __shfl_xor_sync(0xffffffffu, m01, d));
-    m23 = __vmaxu2(m23, __shfl_xor_sync(0xffffffffu, m23, d));
-  }
-  if ((tid & 31) == 0) {
-    atomicMax(top, m01 & 0xFFFFu);
-    atomicMax(top + (16 >> shift), m01 >> 16);
-    atomicMax(top + (32 >> shift), m23 & 0xFFFFu);
-    atomicMax(top + (48 >> shift), m23 >> 16);
+  for (int j = 0; j < kSub; ++j) {
+    const uint32_t most = __reduce_max_sync(0xffffffffu, max(m[j] & 0xFFFFu, m[j] >> 16));
+    if ((tid & 31) == 0) atomicMax(top + (16 * j >> shift), most);
   }
   __syncthreads();
   if (owner) {
@@ -151,11 +161,14 @@ __device__ __forceinline__ void write_tile(const Tile& tile, const Cache& cache,
   for (int k = 0; k < kPer; ++k) {
     const int r = kAtOnce * k + r0;
     if (r >= lo && r < hi) {
-      const float inv = inverse_step_of(power[r >> shift]);
+      const uint32_t inv = (254u - power[r >> shift]) * 0x00800080u;  // 2^-e, a bf16 pair
       const uint32_t* w = &v[k].x;
       uint32_t e[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) e[q] = e4m3x2(bf16_lo(w[q]) * inv, bf16_hi(w[q]) * inv);
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t x = mul_bf16x2(w[q], inv);  // exact wherever a code is not zero
+        e[q] = e4m3x2(bf16_lo(x), bf16_hi(x));
+      }
       dst[(int64_t)r * kChunks] = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
     }
   }
