@@ -14,14 +14,16 @@
 //
 // Latency-bound: a step of a few hundred sequences moves some kilobytes. One block
 // counts and scans (three running sums over the sequences), then the pages are dealt out
-// to groups of eight lanes, a page with the slots in it to a group; no two groups
-// touch one entry: a page that goes from one sequence to another in the same call is
+// to groups of eight lanes (without slots: to lanes), a page with the slots in it to a group; no two
+// groups touch one entry: a page that goes from one sequence to another in the same call is
 // read and cleared by the group that takes it. While the slots are few the scanning
 // block does that work itself (one launch); else a grid does, after it.
-// Measured (calls back to back in a graph): 32 sequences 4.1 us, about a launch; 2048 sequences, prompts of up to
-// 4096 tokens started in an eighth of them, 9.6 us, 4.4 of it the scanning block. In that: a
+// Measured (calls back to back in a graph): 32 sequences 4.0 us, about a launch; 2048 sequences, prompts of up to
+// 4096 tokens started in an eighth of them, 9.8 us, 4.4 of it the scanning block. In that: a
 // sequence stored by one instruction, and warp totals added by one reduction each (five shuffles: 0.4 us more).
-// Grids of 152 x 512 and 608 x 256 took the same, 152 x 1024 2.4 us more.
+// Grids of 152 x 512 and 608 x 256 took the same, 152 x 1024 2.4 us more. The one block without slots, all
+// pages taken or given back: 2048 pages 4.3 us, 8192 7.4, 65536 47 (a page to eight lanes, one read after another: 9.5,
+// 28, 239).
 #include "blocks.cuh"
 #include "chunk.cuh"
 
@@ -30,7 +32,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 static_assert(MLA_MAX_BATCH == 4 * kThreads, "one, two or four sequences a thread");
-constexpr int kLanes = 8;  // of a page
+constexpr int kLanesOfAPage = 8;  // with slots to fill
 constexpr int kGridThreads = 256;
 // One launch up to these sizes, without a workspace.
 constexpr int kSmallRows = MLA_PAGES_SMALL_ROWS, kSmallBatch = MLA_PAGES_SMALL_BATCH;
@@ -94,11 +96,12 @@ __device__ __forceinline__ int last_at(const int32_t* sum, int n, int x) {
 
 // The pages, each by one group of lanes; then the pages given back and not taken, each
 // by a thread; then the rows behind the last sequence. w's give and unit lie in shared memory.
+template <int kLanes>
 __device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, int thread, int threads, int32_t* err_word) {
   const int F = w.total[0], R = w.total[1], K = w.total[2], units = w.total[3];
   const int32_t *give = w.give, *unit = w.unit;
   const int lane = thread % kLanes, shift = p.page_shift;
-  const uint32_t group = 0xFFu << ((threadIdx.x & 31) & ~(kLanes - 1));
+  const uint32_t group = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) & ~(kLanes - 1));
   bool bad = false;
   for (int i = thread / kLanes; i < units; i += threads / kLanes) {
     const int b = last_at(unit, p.B, i);
@@ -127,13 +130,26 @@ __device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, int th
     for (int pos = a + lane; pos < e; pos += kLanes)
       p.slots[s.row0 + pos - s.pos0] = good ? (int64_t)(page - pi) * (1 << shift) + pos : -1;
   }
-  for (int q = K + thread; q < R; q += threads) {
-    const int b = last_at(give, p.B, q);
-    int32_t* old = p.block_table + (int64_t)b * p.max_pages + w.seq[b].need + q - give[b];
-    const int page = *old;
-    bad |= page < 0 || page >= p.num_pages;
-    p.free_pages[F + R - 1 - q] = page;
-    *old = -1;
+  constexpr int kAtOnce = 4;  // one read after another cost 2 us for every 8192 pages
+  for (int q0 = K + thread; q0 < R; q0 += kAtOnce * threads) {
+    int32_t* old[kAtOnce];
+    int page[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int q = q0 + k * threads;
+      if (q >= R) break;
+      const int b = last_at(give, p.B, q);
+      old[k] = p.block_table + (int64_t)b * p.max_pages + w.seq[b].need + q - give[b];
+      page[k] = *old[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int q = q0 + k * threads;
+      if (q >= R) break;
+      bad |= page[k] < 0 || page[k] >= p.num_pages;
+      p.free_pages[F + R - 1 - q] = page[k];
+      *old[k] = -1;
+    }
   }
   if (p.slots)
     for (int t = max(p.cu[p.B], 0) + thread; t < p.n_rows; t += threads) p.slots[t] = -1;
@@ -285,7 +301,8 @@ update_pages_scan(Pages p, Work w, int32_t* err_word) {
   else if (bad) report_error(err_word, MLA_ERR_BOUNDS);
   if (kAll) {
     __syncthreads();
-    deal_pages(p, w, tid, kThreads, err_word);
+    if (p.slots) deal_pages<kLanesOfAPage>(p, w, tid, kThreads, err_word);
+    else deal_pages<1>(p, w, tid, kThreads, err_word);
   }
 }
 
@@ -302,7 +319,9 @@ update_pages_deal(Pages p, Work w, int32_t* err_word) {
   __syncthreads();
   w.give = give;
   w.unit = unit;
-  deal_pages(p, w, blockIdx.x * kGridThreads + threadIdx.x, gridDim.x * kGridThreads, err_word);
+  const int thread = blockIdx.x * kGridThreads + threadIdx.x, threads = gridDim.x * kGridThreads;
+  if (p.slots) deal_pages<kLanesOfAPage>(p, w, thread, threads, err_word);
+  else deal_pages<1>(p, w, thread, threads, err_word);
 }
 
 }  // namespace

@@ -426,6 +426,25 @@ def test_captured_step(mla, err):
     assert int(err.item()) == 0
 
 
+def test_captured_step_with_host_buffers(mla, err):
+    """replay_host reads queries, table and lengths from pinned memory and writes out and lse there."""
+    import torch
+    c = Blocks([2, 2, 2], [70, 300, 2], H=24, block=32, seed=9)
+    step = mla.CapturedStep(c.w_uk, c.w_uv, c.codes, c.table, c.seq_lens, n_q=2, fp8_scales=c.entries, err_word=err,
+                            host_io=True)
+    for k in range(2):
+        step.host["q_nope"].copy_(c.q_nope)
+        step.host["q_rope"].copy_(c.q_rope)
+        step.host["seq_lens"].copy_(c.seq_lens)
+        torch.cuda.synchronize()
+        step.replay_host()
+        want = decode(mla, c, c.codes, c.entries, 2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(bits(step.host[key].cuda()), bits(want[key])) for key in ("lse", "out"))
+        c.seq_lens.sub_(torch.tensor([5, 200, 0], dtype=torch.int32, device="cuda"))
+    assert int(err.item()) == 0
+
+
 def test_test_build_finds_no_bad_address(mla):
     """The same decode in the test build, whose kernel checks every shared and tensor memory address."""
     import ctypes

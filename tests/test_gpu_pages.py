@@ -63,6 +63,15 @@ class State:
         assert self.table.tolist() == self.want.table
 
 
+def test_many_pages_and_no_rows(mla, err):
+    """All the pages of a large batch taken, most given back, taken again: no slots, so one launch does it."""
+    s = State(1000, 40, 41000, 64, seed=4)
+    s.update(mla, [40 * 64 - b % 64 for b in range(1000)], err=err)
+    s.update(mla, [0 if b % 3 else 100 + b for b in range(1000)], err=err)
+    s.update(mla, [64 * (b % 41) for b in range(1000)], err=err)
+    assert int(err.item()) == 0
+
+
 @pytest.mark.parametrize("B,page,steps", [(1, 64, 12), (7, 128, 12), (33, 64, 8), (500, 64, 4), (1024, 128, 3),
                                           (1025, 64, 3), (4096, 128, 3)])
 def test_serving_loop(mla, err, B, page, steps):
