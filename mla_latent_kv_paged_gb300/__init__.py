@@ -464,17 +464,20 @@ def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, 
     assert block_table.dtype == torch.int32 and block_table.is_contiguous()
     nb = workspace.numel() * workspace.element_size()
     if block:
+        dev, f16 = cache8.get_device(), q_abs.dtype is torch.float16
+        _tensor("q_abs", q_abs, torch.float16 if f16 else torch.bfloat16, tuple(q_abs.shape[:-2]) + (H, D_ROW), dev)
+        if q_abs.numel() != B * n_q * H * D_ROW:
+            raise ValueError(f"q_abs: shape {tuple(q_abs.shape)}, expected {B} x {n_q} rows of {H} heads")
+        _tensor("block_table", block_table, torch.int32, (B, max_pages), dev)
         if not planned:
-            assert seq_lens.dtype == torch.int32 and seq_lens.is_contiguous()
-        rest = (B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale), num_splits, _ptr(workspace), nb,
-                _ptr(err_word), _stream(stream))
-        f16 = q_abs.dtype is torch.float16
-        assert q_abs.is_contiguous(), "tensors must be contiguous"
-        head = (_ptr(q_abs if f16 else _bits(q_abs)), int(f16), _ptr(cache8), _ptr(scales), block, _ptr(block_table))
+            _tensor("seq_lens", seq_lens, torch.int32, (B,), dev)
+        head = (q_abs.data_ptr(), int(f16), cache8.data_ptr(), scales.data_ptr(), block, block_table.data_ptr())
+        rest = (B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale), num_splits, workspace.data_ptr(), nb,
+                _address(err_word))
         if planned:
-            _check(lib().mla_decode_paged_planned_blocks(*head, *rest), "mla_decode_paged_planned_blocks")
+            _call("mla_decode_paged_planned_blocks", lib().mla_decode_paged_planned_blocks, dev, stream, *head, *rest)
         else:
-            _check(lib().mla_decode_paged_blocks(*head, _ptr(seq_lens), *rest), "mla_decode_paged_blocks")
+            _call("mla_decode_paged_blocks", lib().mla_decode_paged_blocks, dev, stream, *head, seq_lens.data_ptr(), *rest)
     elif planned:
         st = lib().mla_decode_paged_planned_fp8(_ptr(_bits(q_abs)), _ptr(cache8), _ptr(scales), _ptr(block_table),
                                                 B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale),

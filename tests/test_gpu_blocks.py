@@ -794,6 +794,12 @@ def test_python_checks(mla):
         mla.decode_step(*step, n_q=1, fp8_scales=c.entries, bufs=dict(q_abs=mla.absorb_q(*step[:3])))
     with pytest.raises(mla.MlaError, match="WORKSPACE"):
         mla.decode_step(*step, n_q=1, fp8_scales=c.entries, bufs=dict(workspace=c.codes[0]))
+    with pytest.raises(ValueError, match="rows of 2 heads"):  # nine tokens' queries for one sequence
+        mla.decode_paged_fp8(mla.absorb_q(c.q_nope, c.q_rope, c.w_uk), c.codes, c.entries, c.table, c.seq_lens, n_q=1)
+    with pytest.raises(ValueError, match="q_abs"):
+        mla.decode_paged_fp8(mla.absorb_q(*step[:3]).float(), c.codes, c.entries, c.table, c.seq_lens, n_q=1)
+    with pytest.raises(ValueError, match="seq_lens"):
+        mla.decode_paged_fp8(mla.absorb_q(*step[:3]), c.codes, c.entries, c.table, c.seq_lens.long(), n_q=1)
     with pytest.raises(ValueError, match="shape"):
         q = mla.absorb_q(c.q_nope[:1], c.q_rope[:1], c.w_uk)
         mla.decode_paged_fp8(q, c.codes, c.entries[1:], c.table, c.seq_lens, n_q=1)
