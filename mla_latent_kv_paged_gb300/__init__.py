@@ -27,8 +27,8 @@ such a cache (write_kv, append_chunk) find and write the powers; start with a te
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -733,6 +733,12 @@ def update_pages_workspace_bytes(B: int) -> int:
     return n
 
 
+@functools.lru_cache(maxsize=64)
+def _pages_bytes(B):
+    """update_pages_workspace_bytes, asked of the library once."""
+    return update_pages_workspace_bytes(B)
+
+
 def update_pages(block_table, held, seq_lens, free_pages, free_count, *, page_size: int = PAGE, cu=None, slots=None,
                  workspace=None, err_word=None, stream=None):
     """Block tables, free pages and slots brought up to date from the sequences' lengths, on the GPU.
@@ -782,7 +788,7 @@ def update_pages(block_table, held, seq_lens, free_pages, free_count, *, page_si
         raise ValueError("err_word: an int32 tensor beside the block table")
     at_workspace = room = 0
     if workspace is not None or B > PAGES_SMALL_BATCH or n_rows > PAGES_SMALL_ROWS:
-        workspace, room = _room(workspace, update_pages_workspace_bytes(B), block_table, stream)
+        workspace, room = _room(workspace, 0 if workspace is not None else _pages_bytes(B), block_table, stream)
         at_workspace = workspace.data_ptr()
     _call("mla_update_pages", lib().mla_update_pages, dev, stream, block_table.data_ptr(), held.data_ptr(),
           seq_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), at_cu, at_slots, B, n_rows, num_pages,
@@ -941,6 +947,20 @@ def decode_step(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, *, n_q
     return dict(q_abs=q_abs, u=u, lse=lse, out=out, workspace=ws, num_splits=g)
 
 
+@functools.lru_cache(maxsize=64)
+def _splits_on(dev, n_q):
+    """default_splits on a device, asked of the library once."""
+    import torch
+    with torch.cuda.device(dev):
+        return default_splits(n_q)
+
+
+@functools.lru_cache(maxsize=256)
+def _step_bytes(B, n_q, H, num_splits):
+    """workspace_bytes, asked of the library once."""
+    return workspace_bytes(B, n_q, H, num_splits)
+
+
 def _decode_step_blocks(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, n_q, num_splits, softmax_scale, bufs,
                         err_word, stream, scales, block):
     """decode_step on a block-scaled cache: one call of the library."""
@@ -949,22 +969,31 @@ def _decode_step_blocks(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens
     dev = cache.get_device()
     if dev < 0:
         raise ValueError(f"cache: on {cache.device}, a CUDA device is needed")
-    num_pages, page_size, _ = _dims("cache", cache, 3)
+    num_pages, page_size, width = _dims("cache", cache, 3)
     B, max_pages = _dims("block_table", block_table, 2)
-    T, H, _ = _dims("q_nope", q_nope, 3)
+    T, H, d = _dims("q_nope", q_nope, 3)
     if T != B * n_q:
         raise ValueError(f"q_nope: {T} rows, expected {B} x {n_q}")
-    shapes = ((cache, torch.uint8, (num_pages, page_size, D_ROW)), (block_table, i32, (B, max_pages)),
-              (seq_lens, i32, (B,)), (q_nope, bf, (T, H, D_NOPE)), (q_rope, bf, (T, H, D_R)),
-              (w_uk, bf, (H, D_NOPE, D_C)), (w_uv, bf, (H, D_V, D_C)))
-    for k, (t, dtype, shape) in enumerate(shapes):
-        if not _fits(t, dtype, shape, dev):
-            _tensor(("cache", "block_table", "seq_lens", "q_nope", "q_rope", "w_uk", "w_uv")[k], t, dtype, shape, dev)
+    # (written out: a call of _fits for each takes three microseconds more)
+    if not (cache.dtype is torch.uint8 and width == D_ROW and cache.is_contiguous()
+            and block_table.dtype is i32 and block_table.get_device() == dev and block_table.is_contiguous()
+            and seq_lens.dtype is i32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev
+            and seq_lens.is_contiguous()
+            and q_nope.dtype is bf and d == D_NOPE and q_nope.get_device() == dev and q_nope.is_contiguous()
+            and q_rope.dtype is bf and q_rope.shape == (T, H, D_R) and q_rope.get_device() == dev
+            and q_rope.is_contiguous()
+            and w_uk.dtype is bf and w_uk.shape == (H, D_NOPE, D_C) and w_uk.get_device() == dev
+            and w_uk.is_contiguous()
+            and w_uv.dtype is bf and w_uv.shape == (H, D_V, D_C) and w_uv.get_device() == dev
+            and w_uv.is_contiguous()):
+        for name, t, dtype, shape in (("cache", cache, torch.uint8, (num_pages, page_size, D_ROW)),
+                                      ("block_table", block_table, i32, (B, max_pages)), ("seq_lens", seq_lens, i32, (B,)),
+                                      ("q_nope", q_nope, bf, (T, H, D_NOPE)), ("q_rope", q_rope, bf, (T, H, D_R)),
+                                      ("w_uk", w_uk, bf, (H, D_NOPE, D_C)), ("w_uv", w_uv, bf, (H, D_V, D_C))):
+            _tensor(name, t, dtype, shape, dev)
     if err_word is not None and (err_word.dtype is not i32 or err_word.numel() < 1 or err_word.get_device() != dev):
         raise ValueError("err_word: an int32 tensor beside the cache")
-    if num_splits is None:
-        with torch.cuda.device(dev) if torch.cuda.current_device() != dev else contextlib.nullcontext():
-            num_splits = default_splits(n_q)
+    num_splits = _splits_on(dev, n_q) if num_splits is None else num_splits
     q_abs, u, lse, out, workspace = (bufs.get(k) for k in ("q_abs", "u", "lse", "out", "workspace"))
     if q_abs is None:
         q_abs = _new((T, H, D_ROW), torch.float16, cache, stream)
@@ -983,8 +1012,7 @@ def _decode_step_blocks(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens
         out = _new((T, H, D_V), bf, cache, stream)
     elif not _fits(out, bf, (T, H, D_V), out.get_device()):
         _tensor("out", out, bf, (T, H, D_V), out.get_device())
-    need = workspace_bytes(B, n_q, H, num_splits) if workspace is None else 0
-    workspace, room = _room(workspace, need, cache, stream)
+    workspace, room = _room(workspace, 0 if workspace is not None else _step_bytes(B, n_q, H, num_splits), cache, stream)
     _call("mla_decode_step_blocks", lib().mla_decode_step_blocks, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(),
           w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), scales.data_ptr(), block, block_table.data_ptr(),
           seq_lens.data_ptr(), B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale), num_splits,
