@@ -199,11 +199,11 @@ def _load(path: str):
     L.mla_decode_paged_planned_blocks.restype = i
     L.mla_decode_paged_planned_blocks.argtypes = [vp, i, vp, vp, i, vp, i, i, i, i, i, i, f, i, vp, sz, vp, vp]
     L.mla_decode_step_blocks.restype = i
-    L.mla_decode_step_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, f, i, vp, vp, vp, vp, vp, sz,
-                                         vp, vp]
+    L.mla_decode_step_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, i, i, i, i, i, i, f, i, vp, vp, vp, vp,
+                                         vp, sz, vp, vp]
     L.mla_attend_chunk_blocks.restype = i
-    L.mla_attend_chunk_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i64, f, i, vp, vp, vp,
-                                          sz, vp, vp]
+    L.mla_attend_chunk_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i64, f, i, vp, vp,
+                                          vp, sz, vp, vp]
     L.mla_update_pages_workspace_bytes.restype = sz
     L.mla_update_pages_workspace_bytes.argtypes = [i]
     L.mla_update_pages.restype = i
@@ -477,7 +477,8 @@ def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, 
         if planned:
             _call("mla_decode_paged_planned_blocks", lib().mla_decode_paged_planned_blocks, dev, stream, *head, *rest)
         else:
-            _call("mla_decode_paged_blocks", lib().mla_decode_paged_blocks, dev, stream, *head, seq_lens.data_ptr(), *rest)
+            _call("mla_decode_paged_blocks", lib().mla_decode_paged_blocks, dev, stream, *head, seq_lens.data_ptr(),
+                  *rest)
     elif planned:
         st = lib().mla_decode_paged_planned_fp8(_ptr(_bits(q_abs)), _ptr(cache8), _ptr(scales), _ptr(block_table),
                                                 B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale),
@@ -718,8 +719,8 @@ def write_kv(rows, cache, block_table, seq_lens, cu, *, fp8_scales, err_word=Non
         raise ValueError("write_kv: fp8_scales must be block scales (uint8)")
     T, _ = _dims("rows", rows, 2)
     _tensor("rows", rows, torch.bfloat16, (T, D_ROW), dev)
-    _call("mla_write_kv", lib().mla_write_kv, dev, stream, rows.data_ptr(), cache.data_ptr(), fp8_scales.data_ptr(), block,
-          block_table.data_ptr(), seq_lens.data_ptr(), cu.data_ptr(), B, T, num_pages, page_size, max_pages,
+    _call("mla_write_kv", lib().mla_write_kv, dev, stream, rows.data_ptr(), cache.data_ptr(), fp8_scales.data_ptr(),
+          block, block_table.data_ptr(), seq_lens.data_ptr(), cu.data_ptr(), B, T, num_pages, page_size, max_pages,
           _address(err_word))
 
 
@@ -811,8 +812,8 @@ def read_kv(cache, block_table, seq_lens, cu, *, n_rows: int, first=None, fp8_sc
     else:
         _tensor("out", out, torch.bfloat16, (n_rows, D_ROW), dev)
     if block:
-        _call("mla_read_kv_blocks", lib().mla_read_kv_blocks, dev, stream, cache.data_ptr(), fp8_scales.data_ptr(), block,
-              block_table.data_ptr(), seq_lens.data_ptr(), _address(first), cu.data_ptr(), out.data_ptr(), B, n_rows,
+        _call("mla_read_kv_blocks", lib().mla_read_kv_blocks, dev, stream, cache.data_ptr(), fp8_scales.data_ptr(),
+              block, block_table.data_ptr(), seq_lens.data_ptr(), _address(first), cu.data_ptr(), out.data_ptr(), B, n_rows,
               num_pages, page_size, max_pages, _address(err_word))
         return out
     _call("mla_read_kv", lib().mla_read_kv, dev, stream, cache.data_ptr(), _address(fp8_scales),
@@ -874,8 +875,8 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
                 need = attend_chunk_workspace_bytes(B, T, H, max_tokens, form)
     workspace, room = _room(workspace, need, cache, stream)
     if block:
-        _call("mla_attend_chunk_blocks", lib().mla_attend_chunk_blocks, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(),
-              w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), fp8_scales.data_ptr(), block, block_table.data_ptr(),
+        _call("mla_attend_chunk_blocks", lib().mla_attend_chunk_blocks, dev, stream, q_nope.data_ptr(),
+              q_rope.data_ptr(), w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), fp8_scales.data_ptr(), block, block_table.data_ptr(),
               seq_lens.data_ptr(), cu.data_ptr(), B, T, H, num_pages, page_size, max_pages, max_tokens,
               float(softmax_scale), CHUNK_FORMS[form], out.data_ptr(), _address(lse), workspace.data_ptr(), room,
               _address(err_word))
@@ -987,7 +988,8 @@ def _decode_step_blocks(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens
             and w_uv.dtype is bf and w_uv.shape == (H, D_V, D_C) and w_uv.get_device() == dev
             and w_uv.is_contiguous()):
         for name, t, dtype, shape in (("cache", cache, torch.uint8, (num_pages, page_size, D_ROW)),
-                                      ("block_table", block_table, i32, (B, max_pages)), ("seq_lens", seq_lens, i32, (B,)),
+                                      ("block_table", block_table, i32, (B, max_pages)),
+                                      ("seq_lens", seq_lens, i32, (B,)),
                                       ("q_nope", q_nope, bf, (T, H, D_NOPE)), ("q_rope", q_rope, bf, (T, H, D_R)),
                                       ("w_uk", w_uk, bf, (H, D_NOPE, D_C)), ("w_uv", w_uv, bf, (H, D_V, D_C))):
             _tensor(name, t, dtype, shape, dev)
@@ -1012,11 +1014,13 @@ def _decode_step_blocks(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens
         out = _new((T, H, D_V), bf, cache, stream)
     elif not _fits(out, bf, (T, H, D_V), out.get_device()):
         _tensor("out", out, bf, (T, H, D_V), out.get_device())
-    workspace, room = _room(workspace, 0 if workspace is not None else _step_bytes(B, n_q, H, num_splits), cache, stream)
+    workspace, room = _room(workspace, 0 if workspace is not None else _step_bytes(B, n_q, H, num_splits), cache,
+                            stream)
     _call("mla_decode_step_blocks", lib().mla_decode_step_blocks, dev, stream, q_nope.data_ptr(), q_rope.data_ptr(),
           w_uk.data_ptr(), w_uv.data_ptr(), cache.data_ptr(), scales.data_ptr(), block, block_table.data_ptr(),
           seq_lens.data_ptr(), B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale), num_splits,
-          q_abs.data_ptr(), u.data_ptr(), lse.data_ptr(), out.data_ptr(), workspace.data_ptr(), room, _address(err_word))
+          q_abs.data_ptr(), u.data_ptr(), lse.data_ptr(), out.data_ptr(), workspace.data_ptr(), room,
+          _address(err_word))
     return dict(q_abs=q_abs, u=u, lse=lse, out=out, workspace=workspace, num_splits=num_splits)
 
 

@@ -496,7 +496,8 @@ cudaError_t launch_append_blocks(const uint16_t* h, const uint16_t* w_dkr, uint8
   cudaError_t e = launch_rows(h, w_dkr, rows, true, nullptr, block_table, seq_lens, cu, B, T, d_model, num_pages,
                               page_size, max_pages, theta, workspace, err_word, s);
   if (e != cudaSuccess) return e;
-  return launch_write_kv(rows, cache, scales, block_table, seq_lens, cu, B, T, num_pages, page_size, max_pages, err_word, s);
+  return launch_write_kv(rows, cache, scales, block_table, seq_lens, cu, B, T, num_pages, page_size, max_pages,
+                         err_word, s);
 }
 
 #if MLA_DEBUG_CHECKS

@@ -362,14 +362,15 @@ mla_status mla_decode_paged_blocks(const uint16_t* q_abs, int q_f16, const uint8
     st = launch_status(launch_plan(seq_lens, block_table, B, n_q, max_pages_per_seq, page_size, num_pages, num_splits,
                                    plan, err_word, s));
   if (st == MLA_OK)
-    st = launch_status(launch_decode_blocks(q_abs, q_f16 != 0, cache8, scales, block_table, B, n_q, H, num_pages, page_size,
-                                            max_pages_per_seq, softmax_scale, num_splits, plan, err_word, s));
+    st = launch_status(launch_decode_blocks(q_abs, q_f16 != 0, cache8, scales, block_table, B, n_q, H, num_pages,
+                                            page_size, max_pages_per_seq, softmax_scale, num_splits, plan, err_word, s));
   return st;
 }
 
 mla_status mla_decode_paged_planned_blocks(const uint16_t* q_abs, int q_f16, const uint8_t* cache8,
-                                           const uint8_t* entries, int block_tokens, const int32_t* block_table, int B, int n_q, int H,
-                                           int num_pages, int page_size, int max_pages_per_seq, float softmax_scale,
+                                           const uint8_t* entries, int block_tokens, const int32_t* block_table,
+                                           int B, int n_q, int H, int num_pages, int page_size, int max_pages_per_seq,
+                                           float softmax_scale,
                                            int num_splits, void* workspace, size_t workspace_bytes,
                                            int32_t* err_word, void* stream) {
   if (!q_abs || !block_table) return MLA_ERR_INVALID_ARG;
@@ -381,8 +382,8 @@ mla_status mla_decode_paged_planned_blocks(const uint16_t* q_abs, int q_f16, con
   if (st == MLA_OK)
     st = decode_args(workspace, workspace_bytes, B, n_q, H, num_pages, page_size, max_pages_per_seq, num_splits, &plan);
   if (st == MLA_OK)
-    st = launch_status(launch_decode_blocks(q_abs, q_f16 != 0, cache8, scales, block_table, B, n_q, H, num_pages, page_size,
-                                            max_pages_per_seq, softmax_scale, num_splits, plan, err_word,
+    st = launch_status(launch_decode_blocks(q_abs, q_f16 != 0, cache8, scales, block_table, B, n_q, H, num_pages,
+                                            page_size, max_pages_per_seq, softmax_scale, num_splits, plan, err_word,
                                             (cudaStream_t)stream));
   return st;
 }
@@ -651,11 +652,12 @@ mla_status attend_rows(const uint16_t* q_nope, const uint16_t* q_rope, const uin
     plan.seq_row = r.seq_row;
     mla_status st = launch_status(launch_rows_plan(seq_lens, cu, B, T, H, max_pages_per_seq, page_size, num_pages,
                                                    G, plan, r, w_uv, err_word, s));
-    if (st == MLA_OK) st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s, r.hdr, fp8_scales, err_word,
-                                                          fp8_scales || blocks));
     if (st == MLA_OK)
-      st = launch_status(blocks ? launch_decode_blocks(r.q_abs, true, static_cast<const uint8_t*>(cache), *blocks, block_table,
-                                                       T, 1, H, num_pages, page_size, max_pages_per_seq,
+      st = launch_status(launch_absorb_q(q_nope, q_rope, w_uk, r.q_abs, T, H, s, r.hdr, fp8_scales, err_word,
+                                         fp8_scales || blocks));
+    if (st == MLA_OK)
+      st = launch_status(blocks ? launch_decode_blocks(r.q_abs, true, static_cast<const uint8_t*>(cache), *blocks,
+                                                       block_table, T, 1, H, num_pages, page_size, max_pages_per_seq,
                                                        softmax_scale, G, plan, err_word, s)
                          : fp8_scales ? launch_decode_fp8(r.q_abs, static_cast<const uint8_t*>(cache), fp8_scales,
                                                         block_table, T, 1, H, num_pages, page_size,
@@ -684,8 +686,8 @@ mla_status attend_rows(const uint16_t* q_nope, const uint16_t* q_rope, const uin
     w_uv = plan.w16 + (size_t)H * kDNope * kDC;
   } else if (st == MLA_OK && blocks) {
     // (bf16 holds a code times a power of two exactly)
-    st = launch_status(launch_read_blocks(static_cast<const uint8_t*>(cache), *blocks, block_table, plan.len_eff, nullptr,
-                                          plan.pstart, plan.rows, B, (int)cap, num_pages, page_size,
+    st = launch_status(launch_read_blocks(static_cast<const uint8_t*>(cache), *blocks, block_table, plan.len_eff,
+                                          nullptr, plan.pstart, plan.rows, B, (int)cap, num_pages, page_size,
                                           max_pages_per_seq, err_word, s));
   } else if (st == MLA_OK) {
     st = launch_status(launch_read_kv(cache, nullptr, block_table, plan.len_eff, nullptr, plan.pstart, plan.rows, B,
@@ -723,8 +725,8 @@ mla_status mla_attend_chunk_blocks(const uint16_t* q_nope, const uint16_t* q_rop
   BlockScales scales;
   const mla_status st = block_args(cache8, entries, block_tokens, &scales);
   if (st != MLA_OK) return st;
-  return attend_rows(q_nope, q_rope, w_uk, w_uv, cache8, nullptr, &scales, block_table, seq_lens, cu, B, T, H, num_pages,
-                     page_size, max_pages_per_seq, max_tokens, softmax_scale, form, out, lse, workspace,
+  return attend_rows(q_nope, q_rope, w_uk, w_uv, cache8, nullptr, &scales, block_table, seq_lens, cu, B, T, H,
+                     num_pages, page_size, max_pages_per_seq, max_tokens, softmax_scale, form, out, lse, workspace,
                      workspace_bytes, err_word, (cudaStream_t)stream);
 }
 

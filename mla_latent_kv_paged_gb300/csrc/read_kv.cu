@@ -139,7 +139,8 @@ cudaError_t launch(const void* cache, const float* scales, const int32_t* block_
                    const int32_t* first, const int32_t* cu, uint16_t* out, int B, int n_rows, int num_pages,
                    int page_size, int max_pages, int32_t* err_word, cudaStream_t s,
                    const BlockScales& blocks = BlockScales{nullptr, 0}) {
-  return launch_pdl(read_kv_kernel<kF8, kF16, kBlocks, kRows>, dim3((n_rows + kRows - 1) / kRows), dim3(kThreads), 0, s, cache,
+  return launch_pdl(read_kv_kernel<kF8, kF16, kBlocks, kRows>, dim3((n_rows + kRows - 1) / kRows), dim3(kThreads), 0,
+                    s, cache,
                     scales, block_table, seq_lens, first, cu, reinterpret_cast<uint4*>(out), B, n_rows, num_pages,
                     page_size, max_pages, err_word, static_cast<const uint8_t*>(blocks.entries), blocks.shift);
 }
@@ -150,10 +151,10 @@ cudaError_t launch_read_kv(const void* cache, const float* fp8_scales, const int
                            const int32_t* seq_lens, const int32_t* first, const int32_t* cu, uint16_t* out, int B,
                            int n_rows, int num_pages, int page_size, int max_pages, int32_t* err_word,
                            cudaStream_t s) {
-  return fp8_scales ? launch<true, false, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows, num_pages,
-                                       page_size, max_pages, err_word, s)
-                    : launch<false, false, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B, n_rows,
-                                        num_pages, page_size, max_pages, err_word, s);
+  return fp8_scales ? launch<true, false, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B,
+                                                     n_rows, num_pages, page_size, max_pages, err_word, s)
+                    : launch<false, false, false, 32>(cache, fp8_scales, block_table, seq_lens, first, cu, out, B,
+                                                      n_rows, num_pages, page_size, max_pages, err_word, s);
 }
 
 cudaError_t launch_read_blocks(const uint8_t* cache, const BlockScales& scales, const int32_t* block_table,
@@ -167,8 +168,8 @@ cudaError_t launch_read_blocks(const uint8_t* cache, const BlockScales& scales, 
 cudaError_t launch_rows_f16(const void* cache8, const float* fp8_scales, const int32_t* block_table,
                             const int32_t* seq_lens, const int32_t* cu, uint16_t* out, int B, int n_rows,
                             int num_pages, int page_size, int max_pages, int32_t* err_word, cudaStream_t s) {
-  return launch<true, true, false, 32>(cache8, fp8_scales, block_table, seq_lens, nullptr, cu, out, B, n_rows, num_pages,
-                                page_size, max_pages, err_word, s);
+  return launch<true, true, false, 32>(cache8, fp8_scales, block_table, seq_lens, nullptr, cu, out, B, n_rows,
+                                       num_pages, page_size, max_pages, err_word, s);
 }
 
 cudaError_t launch_weights_f16(const uint16_t* w_uk, const uint16_t* w_uv, uint16_t* out, int H, int32_t* err_word,

@@ -36,8 +36,8 @@ struct Rows {
 };
 // The last sequence whose first CTA is at or before c, by all lanes of a warp: a round cuts the
 // candidates by 32, the last one brings what is needed of the sequence along. Inside [0, B) whatever cu holds.
-__device__ __forceinline__ Rows sequence_of_cta(const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_lens, int B,
-                                                int c) {
+__device__ __forceinline__ Rows sequence_of_cta(const int32_t* __restrict__ cu, const int32_t* __restrict__ seq_lens,
+                                                int B, int c) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = B;
   while (n > 32) {
@@ -92,8 +92,8 @@ struct Cache {
 
 // kWide: chunks of the group in a row
 template <int kWide>
-__device__ __forceinline__ void write_tile(const Tile& tile, const Cache& cache, int group, uint32_t* top, uint32_t* power,
-                                           uint32_t* before, int32_t* err_word) {
+__device__ __forceinline__ void write_tile(const Tile& tile, const Cache& cache, int group, uint32_t* top,
+                                           uint32_t* power, uint32_t* before, int32_t* err_word) {
   constexpr int kAtOnce = kThreads / kWide, kPer = kTile / kAtOnce;  // rows of a pass, passes
   const int tid = threadIdx.x, r0 = tid / kWide, c = tid % kWide, shift = cache.shift;
   const uint4* src = tile.src + c;

@@ -69,8 +69,8 @@ def test_decode_blocks_refusals(lib, planned):
     ws = lib.mla_decode_workspace_bytes(2, 1, 16, 4)
 
     def call(**kw):
-        a = dict(q=P, f16=0, cache=P, entries=P, block=16, bt=P, sl=P, B=2, n_q=1, H=16, pages=8, page=64, maxp=4, scale=0.07,
-                 splits=4, ws=P, wsb=ws)
+        a = dict(q=P, f16=0, cache=P, entries=P, block=16, bt=P, sl=P, B=2, n_q=1, H=16, pages=8, page=64, maxp=4,
+                 scale=0.07, splits=4, ws=P, wsb=ws)
         a.update(kw)
         if planned:
             a.pop("sl")

@@ -460,7 +460,8 @@ def test_test_build_finds_no_bad_address(mla):
         ws = torch.empty(mla.workspace_bytes(5, 2, 40, g), dtype=torch.uint8, device="cuda")
         e = torch.zeros(1, dtype=torch.int32, device="cuda")
         s = torch.cuda.current_stream().cuda_stream
-        st = L.mla_decode_paged_blocks(q.data_ptr(), 0, c.codes.data_ptr(), c.entries.data_ptr(), 16, c.table.data_ptr(),
+        st = L.mla_decode_paged_blocks(q.data_ptr(), 0, c.codes.data_ptr(), c.entries.data_ptr(), 16,
+                                       c.table.data_ptr(),
                                        c.seq_lens.data_ptr(), 5, 2, 40, c.num_pages, 128, c.max_pages, ref.SCALE, g,
                                        ws.data_ptr(), ws.numel(), e.data_ptr(), s)
         assert st == 0
@@ -487,7 +488,8 @@ def test_waits_that_run_out_are_reported(mla, lens):
     torch.cuda.synchronize()
     try:
         assert dbg.mla_debug_set_wait_limit(2_000_000) == 0 and dbg.mla_debug_set_skip_producer(1) == 0
-        st = dbg.mla_decode_paged_blocks(q.data_ptr(), 0, c.codes.data_ptr(), c.entries.data_ptr(), 16, c.table.data_ptr(),
+        st = dbg.mla_decode_paged_blocks(q.data_ptr(), 0, c.codes.data_ptr(), c.entries.data_ptr(), 16,
+                                         c.table.data_ptr(),
                                          c.seq_lens.data_ptr(), len(lens), 1, 16, c.num_pages, 64, c.max_pages,
                                          ref.SCALE, g, ws.data_ptr(), ws.numel(), e.data_ptr(),
                                          torch.cuda.current_stream().cuda_stream)
