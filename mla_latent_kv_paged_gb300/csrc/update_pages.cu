@@ -21,6 +21,7 @@
 // Measured (calls back to back in a graph): 32 sequences 4.0 us, about a launch; 2048 sequences, prompts of up to
 // 4096 tokens started in an eighth of them, 9.8 us, 4.4 of it the scanning block. In that: a
 // sequence stored by one instruction, and warp totals added by one reduction each (five shuffles: 0.4 us more).
+// One cluster of 8 or 16 CTAs that scan each for itself and deal together (no workspace): 23 and 16 us.
 // Grids of 152 x 512 and 608 x 256 took the same, 152 x 1024 2.4 us more. The one block without slots, all
 // pages taken or given back: 2048 pages 4.3 us, 8192 7.4, 65536 47 (a page to eight lanes, one read after another: 9.5,
 // 28, 239).
