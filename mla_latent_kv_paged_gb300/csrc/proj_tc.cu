@@ -53,8 +53,8 @@ struct ProjCfg {
 // kRows: rows of a chunk. absorb_q (for the decode on an FP8 cache) scales the query by
 // the cache's column scales and writes fp16, so that it is rounded once and its range is
 // that of the product that the decode takes; of the rows below *rows_live (null: of all T) it
-// reports values that fp16 does not hold. Without column scales it only writes fp16. out_proj takes fp16 u and weights, and writes only the
-// rows below *rows_live.
+// reports values that fp16 does not hold. Without column scales it only writes fp16. out_proj
+// takes fp16 u and weights, and writes only the rows below *rows_live.
 template <bool kAbsorb, int kNT, bool kRows>
 __global__ void __launch_bounds__(kThreads, 1)
 proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
