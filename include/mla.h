@@ -631,21 +631,14 @@ mla_status mla_attend_chunk_blocks(const uint16_t* q_nope, const uint16_t* q_rop
  *   seq_lens [B] int32; cu [B + 1] int32 and slots [n_rows] int64, both or neither (n_rows 0):
  *               sequence b's new tokens have rows cu[b] .. cu[b+1] - 1; slots of rows at and past
  *               cu[B] become -1 (no row of the pool), so that a padded batch writes nothing stale
- *   workspace   >= mla_update_pages_workspace_bytes(B) bytes, no initial contents needed. Calls
- *               sharing a workspace must not overlap on the GPU. May be NULL for B <= MLA_PAGES_SMALL_BATCH
- *               and n_rows <= MLA_PAGES_SMALL_ROWS, which work without.
  * A sequence with a length outside [n_b, max_pages_per_seq * page_size], held outside
  * [0, max_pages_per_seq] or rows outside the array is left as it is, its slots become -1; pages outside
  * the pool that are met are moved all the same, their slots become -1; and if there are more pages on the
  * stack and given back than num_pages (one is there twice) nothing is moved: MLA_ERR_BOUNDS. Every
  * input is read after the kernel before has finished. 1 <= B <= MLA_MAX_BATCH, n_rows <= 2^20. */
-#define MLA_PAGES_SMALL_BATCH 1024
-#define MLA_PAGES_SMALL_ROWS 4096
-size_t mla_update_pages_workspace_bytes(int B);
 mla_status mla_update_pages(int32_t* block_table, int32_t* held, const int32_t* seq_lens, int32_t* free_pages,
                             int32_t* free_count, const int32_t* cu, int64_t* slots, int B, int n_rows, int num_pages,
-                            int page_size, int max_pages_per_seq, void* workspace, size_t workspace_bytes,
-                            int32_t* err_word, void* stream);
+                            int page_size, int max_pages_per_seq, int32_t* err_word, void* stream);
 
 #ifdef __cplusplus
 }

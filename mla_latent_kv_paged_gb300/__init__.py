@@ -66,7 +66,7 @@ EXPORTS = [
     "mla_attend_chunk_workspace_bytes", "mla_attend_chunk",
     "mla_write_kv", "mla_append_chunk_blocks_workspace_bytes", "mla_append_chunk_blocks", "mla_read_kv_blocks",
     "mla_decode_paged_blocks", "mla_decode_paged_planned_blocks", "mla_decode_step_blocks", "mla_attend_chunk_blocks",
-    "mla_update_pages_workspace_bytes", "mla_update_pages",
+    "mla_update_pages",
 ]
 
 
@@ -204,10 +204,8 @@ def _load(path: str):
     L.mla_attend_chunk_blocks.restype = i
     L.mla_attend_chunk_blocks.argtypes = [vp, vp, vp, vp, vp, vp, i, vp, vp, vp, i, i, i, i, i, i, i64, f, i, vp, vp,
                                           vp, sz, vp, vp]
-    L.mla_update_pages_workspace_bytes.restype = sz
-    L.mla_update_pages_workspace_bytes.argtypes = [i]
     L.mla_update_pages.restype = i
-    L.mla_update_pages.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, sz, vp, vp]
+    L.mla_update_pages.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp]
     return L
 
 
@@ -724,24 +722,8 @@ def write_kv(rows, cache, block_table, seq_lens, cu, *, fp8_scales, err_word=Non
           _address(err_word))
 
 
-PAGES_SMALL_BATCH, PAGES_SMALL_ROWS = 1024, 4096  # update_pages needs no workspace up to these
-
-
-def update_pages_workspace_bytes(B: int) -> int:
-    n = int(lib().mla_update_pages_workspace_bytes(B))
-    if n == 0:
-        raise MlaError(1, "mla_update_pages_workspace_bytes")
-    return n
-
-
-@functools.lru_cache(maxsize=64)
-def _pages_bytes(B):
-    """update_pages_workspace_bytes, asked of the library once."""
-    return update_pages_workspace_bytes(B)
-
-
 def update_pages(block_table, held, seq_lens, free_pages, free_count, *, page_size: int = PAGE, cu=None, slots=None,
-                 workspace=None, err_word=None, stream=None):
+                 err_word=None, stream=None):
     """Block tables, free pages and slots brought up to date from the sequences' lengths, on the GPU.
 
     Sequence b needs ceil(seq_lens[b] / page_size) pages. Where it holds more (held [B] int32), the pages past
@@ -755,8 +737,7 @@ def update_pages(block_table, held, seq_lens, free_pages, free_count, *, page_si
     The order is that of the sequences and of their pages; pages given back are the first to be taken, and a
     call with the lengths of before undoes a call. A sequence is served whole or not at all: from the first one
     that the free pages do not suffice for, sequences that miss pages keep what they have, their slots
-    become -1, and err_word tells MLA_ERR_NO_PAGES. A workspace is taken for more than 1024 sequences or 4096
-    slots only (one is allocated when none is given). Returns slots.
+    become -1, and err_word tells MLA_ERR_NO_PAGES. Returns slots.
     """
     import torch
     dev, i32 = block_table.get_device(), torch.int32
@@ -787,13 +768,9 @@ def update_pages(block_table, held, seq_lens, free_pages, free_count, *, page_si
         at_cu, at_slots = cu.data_ptr(), slots.data_ptr()
     if err_word is not None and (err_word.dtype is not i32 or err_word.numel() < 1 or err_word.get_device() != dev):
         raise ValueError("err_word: an int32 tensor beside the block table")
-    at_workspace = room = 0
-    if workspace is not None or B > PAGES_SMALL_BATCH or n_rows > PAGES_SMALL_ROWS:
-        workspace, room = _room(workspace, 0 if workspace is not None else _pages_bytes(B), block_table, stream)
-        at_workspace = workspace.data_ptr()
     _call("mla_update_pages", lib().mla_update_pages, dev, stream, block_table.data_ptr(), held.data_ptr(),
           seq_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), at_cu, at_slots, B, n_rows, num_pages,
-          page_size, max_pages, at_workspace, room, _address(err_word))
+          page_size, max_pages, _address(err_word))
     return slots
 
 

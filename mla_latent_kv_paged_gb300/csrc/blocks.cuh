@@ -78,7 +78,6 @@ struct Pages {
   int64_t* slots;         // [n_rows] or null
   int B, n_rows, num_pages, page_shift, max_pages;  // page_shift: log2 of the tokens of a page
 };
-size_t update_pages_workspace_bytes(int B);
-cudaError_t launch_update_pages(const Pages& p, void* workspace, int32_t* err_word, cudaStream_t s);
+cudaError_t launch_update_pages(const Pages& p, int32_t* err_word, cudaStream_t s);
 
 }  // namespace mla

@@ -521,29 +521,20 @@ mla_status mla_write_kv(const uint16_t* rows, uint8_t* cache8, uint8_t* entries,
                                        max_pages_per_seq, err_word, (cudaStream_t)stream));
 }
 
-size_t mla_update_pages_workspace_bytes(int B) {
-  return B < 1 || B > MLA_MAX_BATCH ? 0 : update_pages_workspace_bytes(B);
-}
-
 mla_status mla_update_pages(int32_t* block_table, int32_t* held, const int32_t* seq_lens, int32_t* free_pages,
                             int32_t* free_count, const int32_t* cu, int64_t* slots, int B, int n_rows, int num_pages,
-                            int page_size, int max_pages_per_seq, void* workspace, size_t workspace_bytes,
-                            int32_t* err_word, void* stream) {
+                            int page_size, int max_pages_per_seq, int32_t* err_word, void* stream) {
   if (!block_table || !held || !seq_lens || !free_pages || !free_count) return MLA_ERR_INVALID_ARG;
   if (!aligned16(block_table) || !aligned16(held) || !aligned16(seq_lens) || !aligned16(free_pages) ||
-      !aligned16(free_count) || !aligned16(cu) || !aligned16(slots) || !aligned16(workspace))
+      !aligned16(free_count) || !aligned16(cu) || !aligned16(slots))
     return MLA_ERR_INVALID_ARG;
   if ((cu == nullptr) != (slots == nullptr)) return MLA_ERR_INVALID_ARG;
   if (B < 1 || num_pages < 1 || max_pages_per_seq < 1 || n_rows < (slots ? 1 : 0)) return MLA_ERR_INVALID_ARG;
   if (!chunk_counts_ok(B, n_rows) || !page_size_ok(page_size)) return MLA_ERR_UNSUPPORTED_SHAPE;
   if (!token_counts_ok(num_pages, page_size, max_pages_per_seq)) return MLA_ERR_UNSUPPORTED_SHAPE;
-  if (!(B <= MLA_PAGES_SMALL_BATCH && n_rows <= MLA_PAGES_SMALL_ROWS)) {
-    if (!workspace) return MLA_ERR_INVALID_ARG;
-    if (workspace_bytes < update_pages_workspace_bytes(B)) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  }
   Pages p = {block_table, held, seq_lens, free_pages, free_count, cu, slots, B, slots ? n_rows : 0, num_pages,
              page_size == 64 ? 6 : 7, max_pages_per_seq};
-  return launch_status(launch_update_pages(p, workspace, err_word, (cudaStream_t)stream));
+  return launch_status(launch_update_pages(p, err_word, (cudaStream_t)stream));
 }
 
 size_t mla_append_chunk_workspace_bytes(int T, int d_model) {

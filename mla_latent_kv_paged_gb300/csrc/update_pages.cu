@@ -16,13 +16,13 @@
 // counts and scans (three running sums over the sequences), then the pages are dealt out
 // to groups of eight lanes (without slots: to lanes), a page with the slots in it to a group; no two
 // groups touch one entry: a page that goes from one sequence to another in the same call is
-// read and cleared by the group that takes it. While the slots are few the scanning
-// block does that work itself (one launch); else a grid does, after it.
-// Measured (calls back to back in a graph): 32 sequences 4.0 us, about a launch; 2048 sequences, prompts of up to
-// 4096 tokens started in an eighth of them, 9.8 us, 4.4 of it the scanning block. In that: a
-// sequence stored by one instruction, and warp totals added by one reduction each (five shuffles: 0.4 us more).
-// One cluster of 8 or 16 CTAs that scan each for itself and deal together (no workspace): 23 and 16 us.
-// Grids of 152 x 512 and 608 x 256 took the same, 152 x 1024 2.4 us more. The one block without slots, all
+// read and cleared by the group that takes it. While the slots are few one block does
+// it all (one launch); else every block of a grid scans for itself, in its shared memory, and deals out its part,
+// and a last block updates `held` and the count, which the grid's blocks have to read as they were.
+// Measured: 32 sequences 3.9 us a call in a graph, about a launch; 2048 sequences, prompts of up to 4096 tokens
+// started in an eighth of them, 11.6 us, and 11.6 a call from Python. One scan handed to the grid through a workspace:
+// 9.8 in a graph but 15 from Python, which has to allocate it. One cluster of 8 or 16 CTAs: 23 and 16. Warp totals
+// added by one reduction each save 0.4 us over five shuffles. The one block without slots, all
 // pages taken or given back: 2048 pages 4.3 us, 8192 7.4, 65536 47 (a page to eight lanes, one read after another: 9.5,
 // 28, 239).
 #include "blocks.cuh"
@@ -34,9 +34,9 @@ namespace {
 constexpr int kThreads = 1024;
 static_assert(MLA_MAX_BATCH == 4 * kThreads, "one, two or four sequences a thread");
 constexpr int kLanesOfAPage = 8;  // with slots to fill
-constexpr int kGridThreads = 256;
-// One launch up to these sizes, without a workspace.
-constexpr int kSmallRows = MLA_PAGES_SMALL_ROWS, kSmallBatch = MLA_PAGES_SMALL_BATCH;
+constexpr int kGridBlocks = 152;
+// One launch up to these sizes.
+constexpr int kSmallRows = 4096, kSmallBatch = 1024;
 static_assert(kSmallBatch <= kThreads, "a sequence a thread");
 
 struct alignas(32) Sequence {  // one read of what a page's group needs
@@ -49,41 +49,20 @@ struct alignas(32) Sequence {  // one read of what a page's group needs
   int32_t refused;
   int32_t taken;   // pages taken by those before
 };
-// In one access: field by field, the stores of 2048 sequences (32 lanes to as many sectors each) cost the scanning
-// block 6 us, and as two of 16 bytes 1 us.
 __device__ __forceinline__ void put(Sequence* to, const Sequence& s) {
-  const uint32_t w[8] = {(uint32_t)s.page0, (uint32_t)s.held, (uint32_t)s.need,    (uint32_t)s.row0,
-                         (uint32_t)s.pos0,  (uint32_t)s.end,  (uint32_t)s.refused, (uint32_t)s.taken};
-  sm100::st_global_32(to, w);
+  reinterpret_cast<int4*>(to)[0] = make_int4(s.page0, s.held, s.need, s.row0);
+  reinterpret_cast<int4*>(to)[1] = make_int4(s.pos0, s.end, s.refused, s.taken);
 }
 __device__ __forceinline__ Sequence get(const Sequence* from) {
   const int4 a = reinterpret_cast<const int4*>(from)[0], b = reinterpret_cast<const int4*>(from)[1];
   return Sequence{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
-struct Work {
+struct Work {  // in shared memory
   int32_t* give;   // [B] pages given back by the sequences before
   int32_t* unit;   // [B] pages worked on for those before
   Sequence* seq;   // [B]
   int32_t* total;  // [4] free pages before, given back, taken, units
 };
-size_t work_layout(void* base, int B, Work* w) {
-  size_t off = 0;
-  auto take = [&](size_t bytes) {
-    const size_t o = off;
-    off = align256(off + bytes);
-    return o;
-  };
-  const size_t og = take((size_t)B * 4), ou = take((size_t)B * 4);
-  const size_t os = take((size_t)B * sizeof(Sequence)), on = take(16);
-  if (base && w) {
-    char* c = workspace_base(base);
-    w->give = reinterpret_cast<int32_t*>(c + og);
-    w->unit = reinterpret_cast<int32_t*>(c + ou);
-    w->seq = reinterpret_cast<Sequence*>(c + os);
-    w->total = reinterpret_cast<int32_t*>(c + on);
-  }
-  return off + 256;
-}
 
 // the last i in [0, n) with sum[i] <= x (sum[0] = 0 <= x)
 __device__ __forceinline__ int last_at(const int32_t* sum, int n, int x) {
@@ -96,7 +75,7 @@ __device__ __forceinline__ int last_at(const int32_t* sum, int n, int x) {
 }
 
 // The pages, each by one group of lanes; then the pages given back and not taken, each
-// by a thread; then the rows behind the last sequence. w's give and unit lie in shared memory.
+// by a thread; then the rows behind the last sequence.
 template <int kLanes>
 __device__ __forceinline__ void deal_pages(const Pages& p, const Work& w, int thread, int threads, int32_t* err_word) {
   const int F = w.total[0], R = w.total[1], K = w.total[2], units = w.total[3];
@@ -187,16 +166,22 @@ __device__ __forceinline__ void block_scan(int (&v)[kN], int (&all)[kN], int (*s
   }
 }
 
-// kPer: sequences a thread. kAll: this block also deals out the pages (kPer is 1).
-template <int kPer, bool kAll>
+// Every block counts and scans all sequences for itself. kAlone: one block does everything; kDeal: a grid
+// that deals out the pages and leaves `held` and the count as its other blocks still have to read them; kState:
+// one block, after that grid, that updates these two.
+enum Way { kAlone, kDeal, kState };
+// kPer: sequences a thread
+template <int kPer, Way kWay>
 __global__ void __launch_bounds__(kThreads)
-update_pages_scan(Pages p, Work w, int32_t* err_word) {
+update_pages_kernel(Pages p, int32_t* err_word) {
   __shared__ int sums[32][2], unit_sums[32][1];
   __shared__ int served;  // pages taken in all
-  static_assert(!kAll || kPer == 1, "shared memory");
-  __shared__ int32_t give[kAll ? kThreads : 1], unit[kAll ? kThreads : 1], total[4];
-  __shared__ Sequence seq[kAll ? kThreads : 1];
-  if (kAll) w = Work{give, unit, seq, total};
+  __shared__ int32_t total[4];
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kMost = kPer * kThreads;
+  const Work w = {reinterpret_cast<int32_t*>(smem + kMost * sizeof(Sequence)),
+                  reinterpret_cast<int32_t*>(smem + kMost * (sizeof(Sequence) + 4)), reinterpret_cast<Sequence*>(smem),
+                  total};
   sm100::grid_dependency_wait();
   sm100::grid_launch_dependents();
   const int tid = threadIdx.x, b0 = tid * kPer;
@@ -264,7 +249,7 @@ update_pages_scan(Pages p, Work w, int32_t* err_word) {
     if (broken) s[i].refused = 1;
     if (s[i].refused) {
       s[i].need = held;
-    } else if (s[i].need != held) {
+    } else if (s[i].need != held && kWay != kDeal) {
       p.held[b0 + i] = s[i].need;
     }
     const int n = s[i].end - s[i].pos0;
@@ -279,6 +264,8 @@ update_pages_scan(Pages p, Work w, int32_t* err_word) {
   }
   if (most > 0) atomicMax(&served, most);
   block_scan<1>(units, all_units, unit_sums);
+  if (kWay != kDeal && tid == 0 && R != served) *p.free_count = F + R - served;
+  if (kWay == kState) return;
   int u = units[0];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -286,8 +273,7 @@ update_pages_scan(Pages p, Work w, int32_t* err_word) {
     if (b < p.B) {
       w.give[b] = gives[i];
       w.unit[b] = u;
-      if (kAll) w.seq[b] = s[i];  // (in shared memory)
-      else put(w.seq + b, s[i]);
+      put(w.seq + b, s[i]);
     }
     u = plus(u, count[i]);
   }
@@ -296,50 +282,36 @@ update_pages_scan(Pages p, Work w, int32_t* err_word) {
     w.total[1] = R;
     w.total[2] = served;
     w.total[3] = all_units[0];
-    if (R != served) *p.free_count = F + R - served;
   }
-  if (short_of) report_error(err_word, MLA_ERR_NO_PAGES);
-  else if (bad) report_error(err_word, MLA_ERR_BOUNDS);
-  if (kAll) {
-    __syncthreads();
-    if (p.slots) deal_pages<kLanesOfAPage>(p, w, tid, kThreads, err_word);
-    else deal_pages<1>(p, w, tid, kThreads, err_word);
-  }
-}
-
-__global__ void __launch_bounds__(kGridThreads)
-update_pages_deal(Pages p, Work w, int32_t* err_word) {
-  extern __shared__ int32_t prefix[];
-  int32_t *give = prefix, *unit = prefix + p.B;  // every search is in these
-  sm100::grid_dependency_wait();
-  sm100::grid_launch_dependents();
-  for (int b = threadIdx.x; b < p.B; b += kGridThreads) {
-    give[b] = w.give[b];
-    unit[b] = w.unit[b];
+  if (blockIdx.x == 0) {
+    if (short_of) report_error(err_word, MLA_ERR_NO_PAGES);
+    else if (bad) report_error(err_word, MLA_ERR_BOUNDS);
   }
   __syncthreads();
-  w.give = give;
-  w.unit = unit;
-  const int thread = blockIdx.x * kGridThreads + threadIdx.x, threads = gridDim.x * kGridThreads;
+  const int thread = blockIdx.x * kThreads + tid, threads = gridDim.x * kThreads;
   if (p.slots) deal_pages<kLanesOfAPage>(p, w, thread, threads, err_word);
   else deal_pages<1>(p, w, thread, threads, err_word);
 }
 
+template <int kPer>
+cudaError_t deal_and_update(const Pages& p, int32_t* err_word, cudaStream_t s) {
+  constexpr size_t kSmem = (size_t)kPer * kThreads * (sizeof(Sequence) + 8);
+  cudaError_t e = smem_limit<update_pages_kernel<kPer, kDeal>>(kSmem);
+  if (e == cudaSuccess)
+    e = launch_pdl(update_pages_kernel<kPer, kDeal>, dim3(kGridBlocks), dim3(kThreads), kSmem, s, p, err_word);
+  if (e == cudaSuccess) e = launch_pdl(update_pages_kernel<kPer, kState>, dim3(1), dim3(kThreads), 0, s, p, err_word);
+  return e;
+}
+
 }  // namespace
 
-size_t update_pages_workspace_bytes(int B) { return work_layout(nullptr, B, nullptr); }
-
-cudaError_t launch_update_pages(const Pages& p, void* workspace, int32_t* err_word, cudaStream_t s) {
-  Work w = {};
-  work_layout(workspace, p.B, &w);
+cudaError_t launch_update_pages(const Pages& p, int32_t* err_word, cudaStream_t s) {
   if (p.n_rows <= kSmallRows && p.B <= kSmallBatch)
-    return launch_pdl(update_pages_scan<1, true>, dim3(1), dim3(kThreads), 0, s, p, w, err_word);
-  const auto scan = p.B <= kThreads       ? update_pages_scan<1, false>
-                    : p.B <= 2 * kThreads ? update_pages_scan<2, false>
-                                          : update_pages_scan<4, false>;
-  cudaError_t e = launch_pdl(scan, dim3(1), dim3(kThreads), 0, s, p, w, err_word);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(update_pages_deal, dim3(2 * 152), dim3(kGridThreads), 8 * (size_t)p.B, s, p, w, err_word);
+    return launch_pdl(update_pages_kernel<1, kAlone>, dim3(1), dim3(kThreads), kThreads * (sizeof(Sequence) + 8), s, p,
+                      err_word);
+  return (p.B <= kThreads       ? deal_and_update<1>
+          : p.B <= 2 * kThreads ? deal_and_update<2>
+                                : deal_and_update<4>)(p, err_word, s);
 }
 
 }  // namespace mla

@@ -112,21 +112,16 @@ def test_attend_chunk_blocks_refusals(lib):
 
 
 def test_update_pages_refusals(lib):
-    ws = lib.mla_update_pages_workspace_bytes(3)
-    assert ws > 0 and lib.mla_update_pages_workspace_bytes(0) == 0 and lib.mla_update_pages_workspace_bytes(4097) == 0
-
     def call(**kw):
-        a = dict(bt=P, held=P, sl=P, free=P, count=P, cu=P, slots=P, B=3, n=9, pages=8, page=64, maxp=4, ws=P, wsb=ws)
+        a = dict(bt=P, held=P, sl=P, free=P, count=P, cu=P, slots=P, B=3, n=9, pages=8, page=64, maxp=4)
         a.update(kw)
         return lib.mla_update_pages(*a.values(), None, None)
 
     refusals(call, ("bt", "held", "sl", "free", "count", "cu", "slots"))
-    assert call(ws=P + 4) == 1 and call(ws=None, n=4097) == 1  # (up to 1024 sequences and 4096 rows it may be null)
     assert call(B=0) == 1 and call(n=0) == 1 and call(n=-1) == 1 and call(pages=0) == 1 and call(maxp=0) == 1
     assert call(cu=None, slots=None, n=-1) == 1
     assert call(B=4097) == 2 and call(n=(1 << 20) + 1) == 2 and call(page=32) == 2
     assert call(maxp=(1 << 24) + 1) == 2 and call(pages=1 << 26) == 2
-    assert call(wsb=ws - 1, n=4097) == 3 and call(B=1025, ws=None) == 1 and call(B=1025) == 3
 
 
 def test_python_refusals():
@@ -149,8 +144,6 @@ def test_python_refusals():
         mla.write_kv(t(4, 576, dtype=torch.bfloat16), cache, i(2, 4), i(2), i(3), fp8_scales=t(8, 2, 8))
     with pytest.raises(ValueError, match="CUDA device"):
         mla.update_pages(i(2, 4), i(2), i(2), i(8), i(1))
-    with pytest.raises(mla.MlaError, match="INVALID_ARG"):
-        mla.update_pages_workspace_bytes(0)
 
 
 def test_reference_codes_are_torchs():

@@ -690,13 +690,11 @@ def test_a_captured_serving_step(mla, err):
     lens, cu = torch.full((B,), 60, dtype=i32, device="cuda"), torch.arange(B + 1, dtype=i32, device="cuda")
     rows = torch.zeros(B, 576, dtype=torch.bfloat16, device="cuda")
     slots = torch.zeros(B, dtype=torch.int64, device="cuda")
-    ws = torch.empty(mla.update_pages_workspace_bytes(B), dtype=torch.uint8, device="cuda")
     g = mla.default_splits(1)
     bufs = dict(workspace=torch.empty(mla.workspace_bytes(B, 1, H, g), dtype=torch.uint8, device="cuda"))
 
     def step():
-        mla.update_pages(table, held, lens, free, count, page_size=page, cu=cu, slots=slots, workspace=ws,
-                         err_word=err)
+        mla.update_pages(table, held, lens, free, count, page_size=page, cu=cu, slots=slots, err_word=err)
         mla.write_kv(rows, codes, table, lens, cu, fp8_scales=entries, err_word=err)
         return mla.decode_step(c.q_nope, c.q_rope, c.w_uk, c.w_uv, codes, table, lens, n_q=1, num_splits=g, bufs=bufs,
                                fp8_scales=entries, err_word=err)

@@ -214,10 +214,9 @@ def test_replayed_with_other_lengths(mla, err):
     s = State(5, 4, 17, 64)
     lens, cu = s.i([0] * 5), s.i([0] * 6)
     slots = torch.zeros(300, dtype=torch.int64, device="cuda")
-    ws = torch.empty(mla.update_pages_workspace_bytes(5), dtype=torch.uint8, device="cuda")
 
     def call():
-        mla.update_pages(s.table, s.held, lens, s.free, s.count, cu=cu, slots=slots, workspace=ws, err_word=err)
+        mla.update_pages(s.table, s.held, lens, s.free, s.count, cu=cu, slots=slots, err_word=err)
 
     call()
     torch.cuda.synchronize()
@@ -263,6 +262,5 @@ def test_python_checks(mla):
         mla.update_pages(**good, cu=s.i([0, 1, 2]))
     with pytest.raises(ValueError, match="slots"):
         mla.update_pages(**good, cu=s.i([0, 1, 2]), slots=s.i([0, 0]))
-    with pytest.raises(mla.MlaError, match="WORKSPACE"):
-        mla.update_pages(**good, cu=s.i([0, 1, 2]), slots=torch.zeros(4097, dtype=torch.int64, device="cuda"),
-                         workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(mla.MlaError, match="INVALID_ARG"):
+        mla.update_pages(**good, cu=s.i([0, 1, 2]), slots=torch.zeros(0, dtype=torch.int64, device="cuda"))
