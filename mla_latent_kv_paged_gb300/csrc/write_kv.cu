@@ -15,7 +15,7 @@
 // tile has a CTA without a plan on the device before (the CTAs left over end at once).
 //
 // Measured: 42026 rows of 24 prompt pieces 14.5 us (72.7 MB, 5.0 TB/s: the reads that come before a row's,
-// of cu, length and page, are as long as the row's own, and two thirds of the issue slots are taken), one row for
+// of cu, length and page, are as long as the row's own, and over half of the issue slots are taken), one row for
 // each of 128 sequences 4.0 us, a launch and five dependent reads. With magnitudes looked over two by two first and
 // what is not finite only where there is some, and the products two by two in bf16 (exact: powers): 16.3 and
 // 4.8 before. With 256 threads 15.2 and 4.9, held to 48 registers (ten CTAs an SM) 14.0 and 4.3; before that step
