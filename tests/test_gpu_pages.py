@@ -208,12 +208,13 @@ def test_page_ids_outside_the_pool_are_reported(mla, err):
     assert (slots[:64] == -1).all() and slots[64:].tolist() == [s.free[3].item() * 64 + k for k in range(6)]
 
 
-def test_replayed_with_other_lengths(mla, err):
+@pytest.mark.parametrize("n_rows", [300, 5000])  # one launch, two launches
+def test_replayed_with_other_lengths(mla, err, n_rows):
     """One captured call serves every step: lengths, cu and the arrays change in place."""
     import torch
     s = State(5, 4, 17, 64)
     lens, cu = s.i([0] * 5), s.i([0] * 6)
-    slots = torch.zeros(300, dtype=torch.int64, device="cuda")
+    slots = torch.zeros(n_rows, dtype=torch.int64, device="cuda")
 
     def call():
         mla.update_pages(s.table, s.held, lens, s.free, s.count, cu=cu, slots=slots, err_word=err)
@@ -227,7 +228,7 @@ def test_replayed_with_other_lengths(mla, err):
         lens.copy_(s.i(L))
         cu.copy_(s.i(cum(n)))
         graph.replay()
-        want = s.want.update(L, n, 300)
+        want = s.want.update(L, n, n_rows)
         torch.cuda.synchronize()
         s.check()
         assert slots.tolist() == want and int(err.item()) == 0
