@@ -246,15 +246,11 @@ size_t mla_decode_workspace_bytes(int B, int n_q, int H, int num_splits);
  *   workspace   >= mla_decode_workspace_bytes(B, n_q, H, num_splits) bytes
  *   err_word    device int32 or NULL (see the conventions above).
  * Ordering: the split plan is computed while the kernel enqueued just before
- * the call is still finishing (in the step, mla_absorb_q): seq_lens is read
- * and the plan arrays of workspace are written in that time, so that kernel
- * must neither write seq_lens nor use workspace (for example an mla_combine
- * of an earlier call on the same workspace). With programmatic dependent
- * launch that kernel may itself have started before the kernels ahead of it
- * finished, so none of those may still use workspace either: a step that ends
- * with mla_out_proj (or mla_out_comb) lets the next kernel start only once the
- * whole step has finished, so consecutive such steps may share one workspace;
- * after other sequences of calls, alternate two workspaces. q_abs, cache and block_table
+ * the call is still finishing (in the step, mla_absorb_q): seq_lens is read in
+ * that time, so that kernel must not write seq_lens (no kernel of this library
+ * does but mla_copy16, after which the next kernel waits). workspace is written
+ * only once every kernel enqueued before has finished: it may be the workspace of
+ * earlier calls, or memory that they read. q_abs, cache and block_table
  * are read after the kernel before has finished. */
 mla_status mla_decode_paged(const uint16_t* q_abs, const uint16_t* cache,
                             const int32_t* block_table, const int32_t* seq_lens,
@@ -266,7 +262,7 @@ mla_status mla_decode_paged(const uint16_t* q_abs, const uint16_t* cache,
 /* mla_decode_plan + mla_decode_paged_planned — mla_decode_paged in two calls,
  * so that the split plan can be computed earlier in the step: enqueue
  * mla_decode_plan before mla_absorb_q (it then runs beside the kernel before
- * it, under the same ordering rule for seq_lens and workspace), and
+ * it, under the same ordering rule for seq_lens), and
  * mla_decode_paged_planned where mla_decode_paged would go. The planned call
  * launches only the decode kernel and reads the plan that mla_decode_plan
  * wrote into workspace for the same B, n_q, H, max_pages_per_seq and

@@ -142,7 +142,7 @@ cudaError_t smem_limit(size_t bytes) {
 
 // ---------------------------------------------------------------- launchers
 // overlap: start beside the kernel enqueued before (programmatic dependent
-// launch); it then reads seq_lens and writes the plan while that kernel runs.
+// launch); it then reads seq_lens while that kernel runs, and writes the plan after it.
 // page_size: 64 or 128 tokens (1 or 2 tiles per block-table entry)
 inline bool page_size_ok(int page_size) { return page_size == kTile || page_size == 2 * kTile; }
 // sizes in tokens that stay in int32 (positions, and rows of the cache)

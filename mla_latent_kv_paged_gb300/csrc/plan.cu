@@ -13,6 +13,11 @@
 // One block of 256 threads. Integer work only; the output is a pure function
 // of (seq_lens, n_q, max_pages * page_size, G), so repeated calls give
 // identical plans.
+//
+// The plan of a decode (not that of a chunk's rows) is computed while the kernels enqueued before
+// it still run, and only seq_lens is read then. What is written goes to shared memory first and to
+// the workspace after those kernels have finished: the workspace may be memory that they use, be it
+// an earlier step's plan or an array that its owner has given back to an allocator meanwhile.
 #include "chunk.cuh"
 #include "mla_internal.cuh"
 #include "sm100.cuh"
@@ -23,6 +28,9 @@ namespace {
 constexpr int kPlanThreads = 256;  // barriers of a smaller block are cheaper; the work is light
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kSwitchPages = 3;
+// Shared memory for the plan on its way to the workspace: 4 KB at 32 sequences, 86 KB at 4096 with
+// the default splits. A plan that does not fit (some 6000 splits and more) waits and writes in place.
+constexpr size_t kStageMost = 192 * 1024;
 
 // Exclusive scan of v[0..n) in place (shared memory), returns the total.
 // Every thread of the block must call it.
@@ -61,6 +69,41 @@ __device__ int block_exclusive_scan(int* v, int n, int* warp_sums) {
   }
   __syncthreads();
   return total;
+}
+
+// The plan in shared memory, as it will lie in the workspace: the arrays from hdr up to the partials at
+// `base`, the ranges' descriptions behind them.
+struct Stage {
+  uint32_t arrays, descs;  // 16-byte words
+};
+__host__ __device__ inline Stage stage_of(int B, int G) {
+  Plan p;
+  plan_layout(reinterpret_cast<void*>(256), B, 1, 1, G, &p);
+  return {(uint32_t)((reinterpret_cast<uintptr_t>(p.lse_part) - 256) / 16), (uint32_t)G + 1};
+}
+__host__ __device__ inline size_t stage_bytes(Stage s) { return (size_t)16 * (s.arrays + s.descs); }
+__device__ __forceinline__ Plan staged_plan(uint8_t* base, Stage s, int B, int G) {
+  Plan p;
+  plan_layout(base, B, 1, 1, G, &p);
+  p.range_desc = reinterpret_cast<int4*>(base) + s.arrays;
+  return p;
+}
+// The plan stored once the kernels before have finished. The same loop copies it onto itself first, so that
+// its code is there when the wait ends (0.9 us a step without that, 0.5 with it).
+__device__ __forceinline__ void store_plan(const Plan& from, const Plan& to, Stage s, int tid, int threads) {
+  const int4* src = reinterpret_cast<const int4*>(from.hdr);
+  int4 *arrays = reinterpret_cast<int4*>(from.hdr), *descs = arrays + s.arrays;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 4
+    for (uint32_t i = tid; i < s.arrays + s.descs; i += threads)
+      (i < s.arrays ? arrays + i : descs + (i - s.arrays))[0] = src[i];
+    if (pass == 0) {
+      sm100::grid_dependency_wait();
+      arrays = reinterpret_cast<int4*>(to.hdr);
+      descs = to.range_desc;
+    }
+  }
 }
 
 // a / b for a >= 0, b > 0: a 32-bit division when both fit (always at serving
@@ -116,10 +159,12 @@ __device__ __forceinline__ int row_length(const int32_t* seq_lens, const RowArgs
 template <bool kRows>
 __global__ void __launch_bounds__(kPlanThreads, 1)
 plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table, int B,
-            int n_q, int max_tokens, int num_pages, int G, Plan plan, RowArgs rows, int32_t* err_word) {
-  extern __shared__ int smem_i[];
-  int* s_pstart = smem_i;            // [B+1] exclusive page prefix
-  int* s_istart = smem_i + (B + 1);  // [B+1] exclusive piece prefix
+            int n_q, int max_tokens, int num_pages, int G, Plan out, RowArgs rows, int32_t* err_word, Stage stage) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const bool staged = !kRows && stage.descs;
+  const Plan plan = staged ? staged_plan(smem, stage, B, G) : out;  // where it is written at first
+  int* s_pstart = reinterpret_cast<int*>(smem + stage_bytes(stage));  // [B+1] exclusive page prefix
+  int* s_istart = s_pstart + (B + 1);                                 // [B+1] exclusive piece prefix
   __shared__ int warp_sums[32];
   __shared__ int s_items;
   const int tid = threadIdx.x;
@@ -134,19 +179,16 @@ plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bl
       copy_weights(rows, (blockIdx.x - 1) * kPlanThreads + tid, (gridDim.x - 1) * kPlanThreads, err_word);
       return;
     }
+  } else if (!staged) {
+    sm100::grid_dependency_wait();
   }
+  bool bad = false;
 
   // 1. clamp context lengths (to the block table's max_pages * page_size tokens), count tiles
   for (int b = tid; b < B; b += kPlanThreads) {
     int L = kRows ? row_length(seq_lens, rows, b, B, max_tokens, err_word) : seq_lens[b];
-    if (L < n_q) {
-      report_error(err_word, MLA_ERR_BOUNDS);
-      L = n_q;
-    }
-    if (L > max_tokens) {
-      report_error(err_word, MLA_ERR_BOUNDS);
-      L = max_tokens;
-    }
+    bad |= L < n_q || L > max_tokens;
+    L = min(max(L, n_q), max_tokens);
     plan.seq_len_eff[b] = L;
     s_pstart[b] = (L + kTile - 1) / kTile;
   }
@@ -247,10 +289,14 @@ plan_kernel(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bl
   }
 
   // Page ids are checked by the decode kernel when it reads them. The plan
-  // does not read anything the previous kernel wrote, so it runs beside it;
-  // it waits for that kernel only before finishing, so a kernel that waits
-  // for the plan also sees everything written before it.
-  sm100::grid_dependency_wait();
+  // does not read anything the previous kernel wrote, so it runs beside it
+  // and waits for that kernel before it writes to global memory; a kernel that
+  // waits for the plan also sees everything written before it.
+  if (staged) {
+    __syncthreads();
+    store_plan(plan, out, stage, tid, kPlanThreads);
+  }
+  if (bad) report_error(err_word, MLA_ERR_BOUNDS);
 }
 
 // The same plan for at most 32 sequences by one warp: lane b holds sequence b,
@@ -271,8 +317,11 @@ __device__ __forceinline__ int warp_exclusive_scan(int v, int lane, int* total) 
 
 template <bool kRows>
 __global__ void __launch_bounds__(kRows ? kPlanThreads : 32, 1)
-plan_small_kernel(const int32_t* __restrict__ seq_lens, int B, int n_q, int max_tokens, int G, Plan plan,
-                  RowArgs rows, int32_t* err_word) {
+plan_small_kernel(const int32_t* __restrict__ seq_lens, int B, int n_q, int max_tokens, int G, Plan out,
+                  RowArgs rows, int32_t* err_word, Stage stage) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const bool staged = !kRows && stage.descs;
+  const Plan plan = staged ? staged_plan(smem, stage, B, G) : out;  // where it is written at first
   const int lane = threadIdx.x;
   sm100::grid_launch_dependents();
   if (kRows) {
@@ -283,19 +332,16 @@ plan_small_kernel(const int32_t* __restrict__ seq_lens, int B, int n_q, int max_
       copy_weights(rows, thread, gridDim.x * kPlanThreads - 32, err_word);
       return;
     }
+  } else if (!staged) {
+    sm100::grid_dependency_wait();
   }
+  bool bad = false;
   const bool live = lane < B;
   int n_b = 0;  // tiles of sequence `lane`
   if (live) {
     int L = kRows ? row_length(seq_lens, rows, lane, B, max_tokens, err_word) : seq_lens[lane];
-    if (L < n_q) {
-      report_error(err_word, MLA_ERR_BOUNDS);
-      L = n_q;
-    }
-    if (L > max_tokens) {
-      report_error(err_word, MLA_ERR_BOUNDS);
-      L = max_tokens;
-    }
+    bad = L < n_q || L > max_tokens;
+    L = min(max(L, n_q), max_tokens);
     plan.seq_len_eff[lane] = L;
     n_b = (L + kTile - 1) / kTile;
   }
@@ -349,7 +395,11 @@ plan_small_kernel(const int32_t* __restrict__ seq_lens, int B, int n_q, int max_
     plan.range_item[p] = items;
     plan.range_desc[p] = make_int4(items, -1, 0, 0);
   }
-  sm100::grid_dependency_wait();
+  if (staged) {
+    __syncwarp();
+    store_plan(plan, out, stage, lane, 32);
+  }
+  if (bad) report_error(err_word, MLA_ERR_BOUNDS);
 }
 
 }  // namespace
@@ -358,25 +408,24 @@ cudaError_t launch_plan(const int32_t* seq_lens, const int32_t* block_table, int
                         int max_pages, int page_size, int num_pages, int G, const Plan& plan, int32_t* err_word,
                         cudaStream_t s, bool overlap) {
   const int max_tokens = max_pages * page_size;
+  const size_t prefixes = B <= 32 ? 0 : (size_t)2 * (B + 1) * sizeof(int);
+  Stage stage = stage_of(B, G);
+  if (!overlap || stage_bytes(stage) + prefixes > kStageMost) stage = Stage{0, 0};  // it waits and writes in place
+  const size_t smem = prefixes + stage_bytes(stage);
+  cudaError_t e = B <= 32 ? smem_limit<plan_small_kernel<false>>(kStageMost) : smem_limit<plan_kernel<false>>(kStageMost);
+  if (e != cudaSuccess) return e;
   if (B <= 32) {
     if (overlap)
-      return launch_pdl(plan_small_kernel<false>, dim3(1), dim3(32), 0, s, seq_lens, B, n_q, max_tokens, G, plan,
-                        RowArgs{}, err_word);
-    plan_small_kernel<false><<<1, 32, 0, s>>>(seq_lens, B, n_q, max_tokens, G, plan, RowArgs{}, err_word);
+      return launch_pdl(plan_small_kernel<false>, dim3(1), dim3(32), smem, s, seq_lens, B, n_q, max_tokens, G, plan,
+                        RowArgs{}, err_word, stage);
+    plan_small_kernel<false><<<1, 32, smem, s>>>(seq_lens, B, n_q, max_tokens, G, plan, RowArgs{}, err_word, stage);
     return cudaGetLastError();
-  }
-  const size_t smem = (size_t)2 * (B + 1) * sizeof(int);
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e != cudaSuccess) return e;
   }
   if (overlap)
     return launch_pdl(plan_kernel<false>, dim3(1), dim3(kPlanThreads), smem, s, seq_lens, block_table, B, n_q,
-                      max_tokens, num_pages, G, plan, RowArgs{}, err_word);
-  // after the previous kernel has finished (its grid dependency wait then returns at once)
+                      max_tokens, num_pages, G, plan, RowArgs{}, err_word, stage);
   plan_kernel<false><<<1, kPlanThreads, smem, s>>>(seq_lens, block_table, B, n_q, max_tokens, num_pages, G, plan,
-                                                   RowArgs{}, err_word);
+                                                   RowArgs{}, err_word, stage);
   return cudaGetLastError();
 }
 
@@ -396,10 +445,10 @@ cudaError_t launch_rows_plan(const int32_t* seq_lens, const int32_t* cu, int seq
   const int want = (rows.n8 + 4 * kPlanThreads - 1) / (4 * kPlanThreads), blocks = 1 + (want < 304 ? want : 304);
   if (T <= 32)
     return launch_pdl(plan_small_kernel<true>, dim3(blocks), dim3(kPlanThreads), 0, s, seq_lens, T, 1, max_tokens, G,
-                      plan, rows, err_word);
+                      plan, rows, err_word, Stage{0, 0});
   const size_t smem = (size_t)2 * (T + 1) * sizeof(int);  // T <= MLA_MAX_BATCH: 32 KB
   return launch_pdl(plan_kernel<true>, dim3(blocks), dim3(kPlanThreads), smem, s, seq_lens, (const int32_t*)nullptr, T,
-                    1, max_tokens, num_pages, G, plan, rows, err_word);
+                    1, max_tokens, num_pages, G, plan, rows, err_word, Stage{0, 0});
 }
 
 }  // namespace mla

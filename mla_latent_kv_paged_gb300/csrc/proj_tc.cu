@@ -108,10 +108,8 @@ proj_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
   const uint32_t tmem = *tmem_slot;
   // everything above overlaps the previous kernel; its outputs are read below
   grid_dependency_wait();
-  // out_proj: the next kernel (the next step's split plan, which writes the
-  // plan part of the workspace before its own dependency wait) starts only now,
-  // when every kernel before this one has finished: none of them still reads
-  // the workspace, so consecutive steps may share one
+  // out_proj: the next kernel (the next step's split plan) starts only now, when
+  // every kernel before this one has finished, and is computed beside this one
   if (!kAbsorb) grid_launch_dependents();
   // rows at and past *rows_live are computed at most as part of a tile, never
   // written; the first tile always runs, since its loads are under way
