@@ -1,0 +1,113 @@
+"""The decode and the absorbed attention on a block-scaled cache where their fp16 operands end: values below fp16's
+normal range and above it."""
+import pytest
+
+from tests import chunk_reference as ref
+from tests.test_gpu_blocks import Blocks, attend, bits, check_decode, decode
+
+pytestmark = pytest.mark.gpu
+
+RANGE = 7
+
+
+@pytest.fixture(scope="module")
+def mla():
+    import mla_latent_kv_paged_gb300 as m
+    m.build()
+    return m
+
+
+@pytest.fixture()
+def err():
+    import torch
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def e4m3(codes):
+    import torch
+    return codes.view(torch.float8_e4m3fn).double()
+
+
+@pytest.mark.parametrize("block", [16, 64])
+def test_values_below_fp16_are_rounded_once(mla, err, block):
+    """One attended token a sequence, of powers from 2^-16 down: u is the value rounded once to fp16 (2^-24's
+    multiples there, ties to even), and that to bf16."""
+    import torch
+    powers = list(range(-36, -15))
+    B, dev = len(powers), "cuda"
+    g = torch.Generator(device=dev).manual_seed(block)
+    codes = torch.randint(0, 255, (B, 64, 576), dtype=torch.uint8, generator=g, device=dev)
+    codes[(codes & 0x7F) == 0x7F] = 0x09
+    codes[:, 0, :508] = torch.arange(254, dtype=torch.uint8, device=dev).repeat(2)  # all but 0x7F, 0xFE and 0xFF
+    codes[:, 0, 127] = codes[:, 0, 381] = 0x7E
+    entries = torch.zeros(B, 64 // block, 8, dtype=torch.uint8, device=dev)
+    entries[:, :, :5] = torch.tensor([127 + p for p in powers], dtype=torch.uint8, device=dev)[:, None, None]
+    q = torch.randn(B, 3, 576, generator=g, device=dev).to(torch.float16)
+    ws, splits = mla.decode_paged_fp8(q, codes, entries, torch.arange(B, dtype=torch.int32, device=dev)[:, None],
+                                      torch.ones(B, dtype=torch.int32, device=dev), n_q=1, err_word=err)
+    u, _ = mla.combine(ws, B=B, n_q=1, H=3, num_splits=splits)
+    torch.cuda.synchronize()
+    v = e4m3(codes[:, 0, :512]) * torch.exp2(torch.tensor(powers, dtype=torch.float64, device=dev))[:, None]
+    want = (v * 2.0 ** 24).round() * 2.0 ** -24  # (half to even)
+    want = torch.where(v.abs() < 2.0 ** -14, want, v.to(torch.float16).double()).to(torch.bfloat16)
+    assert int(err.item()) == 0 and (u.float() == want.float()[:, None]).all()
+    # (at 2^-25 the codes above 1, 0x39 .. 0x7E and 0xB9 .. 0xFD, are not zero: 139 of them, twice)
+    assert (want[0] == 0).all() and (want[powers.index(-25), :508] != 0).sum() >= 2 * 139
+
+
+def test_absorbed_attention_reports_values_outside_fp16(mla, err):
+    """A value of the context of 65520 or more is reported, one behind it is not; the expanded form, which takes
+    rows in bf16, has its own limits (the keys and values that it makes of them)."""
+    import torch
+    for at, entry, want in ((60, 127 + 8, RANGE), (60, 127 + 7, 0), (75, 127 + 20, 0)):
+        c = Blocks([5], [70], H=16, block=16, seed=8)
+        pool = c.rows(0)[at].item() if at < 70 else c.host_table[0][1] * 64 + at - 64
+        rows = slice(pool // 16 * 16, pool // 16 * 16 + 16)
+        c.codes.view(-1, 576)[rows, 256:384] = 0
+        c.codes.view(-1, 576)[pool, 300] = 0x7E
+        c.entries.view(-1, 8)[pool // 16, 2] = entry
+        c.q_nope.zero_()  # (scores of ordinary size)
+        c.w_uv.mul_(2.0 ** -6)
+        err.zero_()
+        attend(mla, c, c.codes, c.entries, "absorbed", err)
+        torch.cuda.synchronize()
+        assert int(err.item()) == want, (at, entry)
+
+
+def test_small_values_in_every_reader(mla, err):
+    """Latents of about 2^-20. Read back and the expanded attention take them as they are; the decode and the
+    absorbed attention hold values, partials and (the attention) u to 2^-25, whatever their size, and so does the
+    decode of a bf16 cache with its partials."""
+    import torch
+    c = Blocks([40, 3], [200, 130], H=8, block=16, seed=8, powers=(-20, -20), spread=0.0)
+    c.codes, c.entries = c.codes.clone(), c.entries.clone()
+    assert c.cache.nan_to_num().abs().max() < 2.0 ** -17
+    back = mla.read_kv(c.codes, c.table, c.seq_lens, c.cu, n_rows=43, fp8_scales=c.entries, err_word=err)
+    for b, n in enumerate(c.new):
+        rows = back[sum(c.new[:b]):sum(c.new[:b]) + n]
+        assert torch.equal(rows, c.cache.view(-1, 576)[c.rows(b, 0, n)])
+    got = {form: attend(mla, c, c.codes, c.entries, form, err)[0].double() for form in ("expanded", "absorbed")}
+    torch.cuda.synchronize()
+    want, _, bounds = ref.attend(c)
+    held = c.w_uv.double().abs().sum(-1)  # each latent of u off by 2^-25: [H, 128]
+    keys = torch.expm1(torch.tensor(2 * ref.SCALE * 576 * 6 * ref.TINY_F16)).item() * want.abs().max()
+    assert ((got["expanded"] - want).abs() <= bounds["expanded"] + keys).all()
+    assert ((got["absorbed"] - want).abs() <= bounds["absorbed"] + 4 * ref.TINY_F16 * held + keys).all()
+    # a step on either cache
+    last = [sum(c.new[:b + 1]) - 1 for b in range(2)]
+    c.q_nope, c.q_rope = c.q_nope[last].contiguous(), c.q_rope[last].contiguous()
+    blocks = decode(mla, c, c.codes, c.entries, 1, err)
+    plain = mla.decode_step(c.q_nope, c.q_rope, c.w_uk, c.w_uv, c.cache, c.table, c.seq_lens, n_q=1, err_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check_decode(c, blocks, 1)
+    for b in range(2):
+        x = c.values(b)
+        z = (torch.einsum("hd,hdc->hc", c.q_nope[b].double(), c.w_uk.double()) @ x[:, :512].t()
+             + c.q_rope[b].double() @ x[:, 512:].t()) * ref.SCALE
+        u = torch.softmax(z, -1) @ x[:, :512]
+        # (weights of nearly equal tokens; the query in bf16 or fp16 moves scores of 2^-17 by nothing)
+        near = 2.0 ** -7 * x[:, :512].abs().amax(0)
+        for r, parts in ((blocks, 2), (plain, 1)):
+            assert ((r["u"][b].double() - u).abs() <= near + parts * ref.TINY_F16).all()
+    assert bits(blocks["u"]).shape == bits(plain["u"]).shape
