@@ -107,7 +107,13 @@ static_assert(2 * kQBoxBytes + kQrBoxBytes <= kOpBytes, "an operand slot holds h
 
 constexpr uint32_t kTmO = 0, kTmS = 256, kTmP = 320, kTmQr = 368, kTmQ = 384, kTmCols = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: P values stay <= 256
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: weights stay <= 2^8 of the reference
+// P holds weights times 2^7 (at most 2^15 then, of fp16's 65504), so that one becomes zero below 2^-32 of the
+// reference only, and not below 2^-25, where 131072 light tokens together are 2^-8 of a heavy one. (Of 131072 tokens
+// of 2^-25.5 in one range, values of the heavy one zero: u off by all of itself before, by 0.6% now. The fp32 sums
+// of the value MMAs cut each addend at 2^-24 of the sum, n 2^-24 of n tokens, whatever the type of the weights: a
+// value that all tokens share is off by up to 0.3% in that case, before and now.)
+constexpr float kWeightShift = 7.0f;
 
 #if MLA_DEBUG_CHECKS
 // Test builds only: the counters of decode_tc.cu, for this kernel, and its switch.
@@ -157,8 +163,9 @@ __device__ __forceinline__ uint32_t power_f16x2(uint32_t p) {
 // 16 codes times 2^(p - 127), as fp16 pairs, by: power_f16x2(p). Exact but below fp16's normal range (2^-14),
 // where a value is rounded once to 2^-24's multiples: codes are multiples of 2^-9, so products with 2^-15 and
 // more are exact, and of a power below the rest comes last, in a product that rounds (its factor underflows
-// where every value is less than 2^-30, a zero either way). fp16 holds no power above 2^15, which stands for
-// values that it does not hold either. Returns whether one of the values became infinite.
+// where every value is less than 2^-30, a zero either way): steps on such blocks take 1 to 4% longer. fp16 holds
+// no power above 2^15, which stands for values that it does not hold either. Returns whether one of the
+// values became infinite.
 __device__ __forceinline__ bool widen16(const uint32_t (&v)[4], uint32_t by, uint32_t p, uint32_t (&o)[8]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -843,9 +850,12 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
           const uint32_t pfr = r_pf + 8u * pb;
           (void)MLA_SMEM_OK(sbase + kOffP + pb * kPPeerBytes + (uint32_t)row * 64, 64);
           (void)MLA_TMEM_OK(kTmP + 16 * pb, 16);
-          // (the sum of the weights before their rounding to fp16: off by less than 2^-12 of itself)
+          // (the sum of the weights before their rounding to fp16. A rounded weight is off by 2^-11 of itself at
+          // most, and below 2^-21 of the reference by 2^-32 of that, which is at most the sum: of n tokens the
+          // sum of the rounded ones is off by 2^-11 + n 2^-32 of itself. Summed after their rounding, the
+          // same cases were off as much in u, up to 0.3% more in lse, and steps took 0.5 to 1% longer.)
           uint64_t sum = pair(0.f, 0.f);
-          const uint64_t off = pair(-mref, -mref);
+          const uint64_t off = pair(kWeightShift - mref, kWeightShift - mref);
           uint32_t pw[16];
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
@@ -903,7 +913,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
             if (rank == 0 && row < H)
               // a chunk's row keeps a sum that is not a number, so that the merge passes it on
               plan.lse_part[orow] =
-                  l_tot > 0.f ? (m_new + log2f(l_tot)) * kLn2 : (kRows && l_tot != l_tot ? l_tot : -INFINITY);
+                  l_tot > 0.f ? (m_new + log2f(l_tot * 0x1p-7f)) * kLn2 : (kRows && l_tot != l_tot ? l_tot : -INFINITY);
           }
         }
         if (ntiles >= 2) ++lg_n;

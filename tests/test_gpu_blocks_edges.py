@@ -1,5 +1,6 @@
-"""The decode and the absorbed attention on a block-scaled cache where their fp16 operands end: values below fp16's
-normal range and above it."""
+"""The decode and the absorbed attention on a block-scaled cache where their fp16 operands end: weights far below
+the largest, values below fp16's normal range and above it."""
+import numpy as np
 import pytest
 
 from tests import chunk_reference as ref
@@ -26,6 +27,57 @@ def err():
 def e4m3(codes):
     import torch
     return codes.view(torch.float8_e4m3fn).double()
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+def test_many_light_tokens_beside_a_heavy_one(mla, err, splits):
+    """One token of score 0 and 131072 behind it of 2^-d each: together they hold up to an eighth of the sum, and a
+    sink keeps neither more nor less than its share. All values are of one sign.
+
+    A weight is held in fp16, 2^7 times its size, so off by 2^-11 of itself or by 2^-25 / 2^7 at most; ex2 and the
+    scores (whose sums here are single products) by 2^-15. The L products of a value are added in fp32, each addend
+    cut below 2^-24 of the sum: L 2^-24 of the absolute sum, which is a tight bound where the heavy token's value
+    is zero (columns 128 to 191) and a loose one elsewhere. The partial is rounded to fp16, the merged u to bf16. The
+    sum of the weights grows by one tile's in every second of the L / 64 tiles, each time rounded by 2^-24."""
+    import torch
+    d = [20.0, 24.5, 25.5, 27.25, 30.0, 31.5, 33.0, 60.0]
+    H, L, dev = len(d), 131073, "cuda"
+    # page 0: light tokens, page 1: the heavy one and light ones behind it, page 2: a light one
+    g = torch.Generator(device=dev).manual_seed(1)
+    codes = torch.randint(0x30, 0x40, (3, 64, 576), dtype=torch.uint8, generator=g, device=dev)  # 0.5 .. 1.875
+    codes[..., :64] = 0x38          # 1 in every token
+    codes[..., 64:128] = 0x40       # 2 in the light tokens, 1 in the heavy one
+    codes[1, 0, 64:128] = 0x38
+    codes[..., 128:192] = 0x38      # 1 in the light tokens, 0 in the heavy one
+    codes[1, 0, 128:192] = 0
+    codes[..., 512:] = 0
+    codes[..., 575] = 0xB8          # the key: -1 in the light tokens
+    codes[1, 0, 575] = 0
+    entries = torch.full((3, 2, 8), 127, dtype=torch.uint8, device=dev)
+    table = torch.zeros(1, -(-L // 64), dtype=torch.int32, device=dev)
+    table[0, 0], table[0, -1] = 1, 2
+    q = torch.zeros(1, H, 576, dtype=torch.float16, device=dev)
+    q[0, :, 575] = torch.tensor(d, device=dev)
+    lens = torch.tensor([L], dtype=torch.int32, device=dev)
+    scale = float(np.log(2.0))
+    ws, g = mla.decode_paged_fp8(q, codes, entries, table, lens, n_q=1, num_splits=splits, softmax_scale=scale,
+                                 err_word=err)
+    u, lse = mla.combine(ws, B=1, n_q=1, H=H, num_splits=g)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    rows = e4m3(codes).view(-1, 576)
+    at = (table[0].long()[:, None] * 64 + torch.arange(64, device=dev)).view(-1)[:L]
+    lat = rows[at, :512]
+    w = torch.exp2(q[0, :, 575].double()[:, None] * rows[at, 575][None])
+    total = w.sum(-1, keepdim=True)
+    want = w @ lat / total
+    # splits: a range without the heavy token has a reference of its own, 2^-d
+    held = torch.full_like(w, 2.0 ** -32)
+    bound = (w @ lat * (ref.U_F16 + 2.0 ** -15 + L * ref.U_F32) + held @ lat) / total
+    bound += 1.01 * (ref.U_F16 + ref.U_BF16) * want
+    assert ((u[0].double() - want).abs() <= bound).all()
+    assert ((lse[0].double() - total[:, 0].log()).abs()
+            <= 2.0 ** -15 + L / 128 * ref.U_F32 + 2.0 ** -20 * total[:, 0].log().abs()).all()
 
 
 @pytest.mark.parametrize("block", [16, 64])
