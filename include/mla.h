@@ -321,7 +321,7 @@ mla_status mla_decode_paged_planned_fp8(const uint16_t* q_abs, const uint8_t* ca
  *   lse = ln sum_k exp(lse_k),  u = sum_k exp(lse_k - lse) * o_k
  * (the flash-decoding merge; Huny's Dev Blog section 4 table names
  * FlashDecoding as the decode technique). A partial with lse_k = -inf has
- * weight 0.
+ * weight 0, and makes u and lse NaN where it holds NaN (a context with a NaN in it).
  *   workspace  as filled by mla_decode_paged with the same B, n_q, H, num_splits
  *   u          [B][n_q][H][512] bf16 output (round-to-nearest-even)
  *   lse        [B][n_q][H] float output (natural log), may be NULL; device

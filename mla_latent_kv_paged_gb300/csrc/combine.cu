@@ -71,7 +71,8 @@ combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __res
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = fmaxf(m, l[i]);
     }
-    if (m != -INFINITY) {
+    // (a decode's partial whose sum is not a number has lse -inf and NaN columns: its weight, 0, makes the row NaN)
+    if (!kRows || m != -INFINITY) {
       for (int kb = k0; kb < k1; kb += kKB) {
         float w[kKB];
         if (kb > k0) {  // later batches: their own loads
@@ -102,7 +103,7 @@ combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __res
           }
         }
       }
-    } else if (kRows) {  // no finite partial: NaN if one of them is
+    } else {  // no finite partial: NaN if one of them is
       for (int k = k0; k < k1; ++k) {
         const float l = lse_of(k);
         if (l != l) wsum = l;
@@ -126,7 +127,9 @@ combine_kernel(Plan plan, int n_q, int H, uint16_t* __restrict__ u, float* __res
     *reinterpret_cast<uint4*>(u + ((size_t)bj * H + row) * kDC + blockIdx.y * kCols + 8 * q) = o;
   }
   if (lse_out && blockIdx.y == 0 && part == 0 && h < H && (!kRows || bj < *rows_live))
-    lse_out[(size_t)bj * H + h] = wsum > 0.f ? m + logf(wsum) : (!kRows || wsum == 0.f ? -INFINITY : wsum);
+    lse_out[(size_t)bj * H + h] = !kRows && acc[0] != acc[0] ? acc[0]
+                                  : wsum > 0.f               ? m + logf(wsum)
+                                                             : (!kRows || wsum == 0.f ? -INFINITY : wsum);
 }
 
 }  // namespace

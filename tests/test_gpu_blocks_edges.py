@@ -1,5 +1,5 @@
 """The decode and the absorbed attention on a block-scaled cache where their fp16 operands end: weights far below
-the largest, values below fp16's normal range and above it."""
+the largest, values below fp16's normal range and above it, contexts that hold a NaN."""
 import numpy as np
 import pytest
 
@@ -105,6 +105,25 @@ def test_values_below_fp16_are_rounded_once(mla, err, block):
     assert int(err.item()) == 0 and (u.float() == want.float()[:, None]).all()
     # (at 2^-25 the codes above 1, 0x39 .. 0x7E and 0xB9 .. 0xFD, are not zero: 139 of them, twice)
     assert (want[0] == 0).all() and (want[powers.index(-25), :508] != 0).sum() >= 2 * 139
+
+
+@pytest.mark.parametrize("col", [77, 570])
+@pytest.mark.parametrize("kind", ["blocks", "bf16"])
+def test_a_nan_in_contexts_of_every_length(mla, err, kind, col):
+    """A latent or a positional NaN gives NaN to all of its sequence's results, whether one CTA pair has the whole
+    context or several share it, and to no other sequence's."""
+    import torch
+    c = Blocks([1] * 6, [1, 40, 64, 100, 1000, 70], H=16, block=32, seed=8)
+    for b in range(5):
+        row = c.rows(b)[c.lens[b] // 2]
+        c.codes.view(-1, 576)[row, col] = 0xFF
+        c.cache.view(-1, 576)[row, col] = float("nan")
+    got = decode(mla, c, *((c.codes, c.entries) if kind == "blocks" else (c.cache, None)), 1, err)
+    torch.cuda.synchronize()
+    for k in ("u", "lse", "out"):
+        assert torch.isnan(got[k][:5].float()).all() and torch.isfinite(got[k][5].float()).all(), k
+    if kind == "blocks":
+        check_decode(c, got, 1, skip=range(5))
 
 
 def test_absorbed_attention_reports_values_outside_fp16(mla, err):
