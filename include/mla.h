@@ -622,7 +622,7 @@ mla_status mla_attend_chunk_blocks(const uint16_t* q_nope, const uint16_t* q_rop
  * exactly. Entries of free_pages past the new count are left as they were. Results do not depend on timing.
  * A sequence is served whole or not at all: the first one whose missing pages pass what the stack and
  * the pages given back hold, and every one behind it that misses pages, keeps what it has, its slots
- * become -1 and MLA_ERR_NO_PAGES is reported (give pages back and call again).
+ * become -1 and MLA_ERR_NO_PAGES is reported (give pages back and call again), unless MLA_ERR_BOUNDS is.
  *   block_table [B][max_pages_per_seq], held [B], free_pages [num_pages], free_count [1] int32: updated
  *   seq_lens [B] int32; cu [B + 1] int32 and slots [n_rows] int64, both or neither (n_rows 0):
  *               sequence b's new tokens have rows cu[b] .. cu[b+1] - 1; slots of rows at and past
@@ -630,7 +630,8 @@ mla_status mla_attend_chunk_blocks(const uint16_t* q_nope, const uint16_t* q_rop
  * A sequence with a length outside [n_b, max_pages_per_seq * page_size], held outside
  * [0, max_pages_per_seq] or rows outside the array is left as it is, its slots become -1; pages outside
  * the pool that are met are moved all the same, their slots become -1; and if there are more pages on the
- * stack and given back than num_pages (one is there twice) nothing is moved: MLA_ERR_BOUNDS. Every
+ * stack and given back than num_pages (one is there twice) nothing is moved: MLA_ERR_BOUNDS. (Where cu falls, a
+ * row that two sequences' ranges name gets the slot of either, or -1.) Every
  * input is read after the kernel before has finished. 1 <= B <= MLA_MAX_BATCH, n_rows <= 2^20. */
 mla_status mla_update_pages(int32_t* block_table, int32_t* held, const int32_t* seq_lens, int32_t* free_pages,
                             int32_t* free_count, const int32_t* cu, int64_t* slots, int B, int n_rows, int num_pages,

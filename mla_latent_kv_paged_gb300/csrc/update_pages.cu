@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kThreads)
 update_pages_kernel(Pages p, int32_t* err_word) {
   __shared__ int sums[32][2], unit_sums[32][1];
   __shared__ int served;  // pages taken in all
+  __shared__ int refused;  // some sequence is short of pages
   __shared__ int32_t total[4];
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kMost = kPer * kThreads;
@@ -186,7 +187,7 @@ update_pages_kernel(Pages p, int32_t* err_word) {
   sm100::grid_launch_dependents();
   const int tid = threadIdx.x, b0 = tid * kPer;
   const int shift = p.page_shift, round = (1 << shift) - 1, max_tokens = p.max_pages << shift;
-  if (tid == 0) served = 0;
+  if (tid == 0) served = refused = 0;
   int F = *p.free_count;
   bool bad = false;
   Sequence s[kPer];
@@ -229,7 +230,6 @@ update_pages_kernel(Pages p, int32_t* err_word) {
   bad |= broken;
   const int R = broken ? 0 : all[0], room = broken ? 0 : F + R;
   int units[1] = {0}, all_units[1];
-  bool short_of = false;
   int gives[kPer], count[kPer], most = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -241,7 +241,7 @@ update_pages_kernel(Pages p, int32_t* err_word) {
     if (more > 0 && !broken) {
       if (k > room) {
         s[i].refused = 1;
-        short_of = true;
+        refused = 1;
       } else {
         most = k;
       }
@@ -265,7 +265,18 @@ update_pages_kernel(Pages p, int32_t* err_word) {
   if (most > 0) atomicMax(&served, most);
   block_scan<1>(units, all_units, unit_sums);
   if (kWay != kDeal && tid == 0 && R != served) *p.free_count = F + R - served;
-  if (kWay == kState) return;
+  // MLA_ERR_BOUNDS is told before MLA_ERR_NO_PAGES, whichever thread or block finds it: the latter by the last
+  // block to run, once all of its threads have told the former.
+  if (kWay != kDeal && bad) report_error(err_word, MLA_ERR_BOUNDS);
+  auto tell_refused = [&]() {
+    if (kWay == kDeal || !refused) return;
+    __syncthreads();
+    if (tid == 0) report_error(err_word, MLA_ERR_NO_PAGES);
+  };
+  if (kWay == kState) {
+    tell_refused();
+    return;
+  }
   int u = units[0];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -283,14 +294,11 @@ update_pages_kernel(Pages p, int32_t* err_word) {
     w.total[2] = served;
     w.total[3] = all_units[0];
   }
-  if (blockIdx.x == 0) {
-    if (short_of) report_error(err_word, MLA_ERR_NO_PAGES);
-    else if (bad) report_error(err_word, MLA_ERR_BOUNDS);
-  }
   __syncthreads();
   const int thread = blockIdx.x * kThreads + tid, threads = gridDim.x * kThreads;
   if (p.slots) deal_pages<kLanesOfAPage>(p, w, thread, threads, err_word);
   else deal_pages<1>(p, w, thread, threads, err_word);
+  tell_refused();
 }
 
 template <int kPer>
