@@ -450,6 +450,9 @@ def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, 
     float16). Returns (workspace, num_splits) for ``combine``."""
     import torch
     block = _block_tokens(cache8, scales)
+    if block:
+        return _decode_paged_blocks(q_abs, cache8, scales, block, block_table, seq_lens, n_q, num_splits, softmax_scale,
+                                    workspace, err_word, stream, planned)
     B, max_pages = block_table.shape
     H = q_abs.shape[-2]
     num_pages, page_size = cache8.shape[0], cache8.shape[1]
@@ -458,26 +461,10 @@ def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, 
     if workspace is None:
         workspace = torch.empty(workspace_bytes(B, n_q, H, num_splits), dtype=torch.uint8, device=q_abs.device)
     assert cache8.dtype == torch.uint8 and cache8.is_contiguous()
-    assert block or (scales.dtype == torch.float32 and scales.is_contiguous())
+    assert scales.dtype == torch.float32 and scales.is_contiguous()
     assert block_table.dtype == torch.int32 and block_table.is_contiguous()
     nb = workspace.numel() * workspace.element_size()
-    if block:
-        dev, f16 = cache8.get_device(), q_abs.dtype is torch.float16
-        _tensor("q_abs", q_abs, torch.float16 if f16 else torch.bfloat16, tuple(q_abs.shape[:-2]) + (H, D_ROW), dev)
-        if q_abs.numel() != B * n_q * H * D_ROW:
-            raise ValueError(f"q_abs: shape {tuple(q_abs.shape)}, expected {B} x {n_q} rows of {H} heads")
-        _tensor("block_table", block_table, torch.int32, (B, max_pages), dev)
-        if not planned:
-            _tensor("seq_lens", seq_lens, torch.int32, (B,), dev)
-        head = (q_abs.data_ptr(), int(f16), cache8.data_ptr(), scales.data_ptr(), block, block_table.data_ptr())
-        rest = (B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale), num_splits, workspace.data_ptr(), nb,
-                _address(err_word))
-        if planned:
-            _call("mla_decode_paged_planned_blocks", lib().mla_decode_paged_planned_blocks, dev, stream, *head, *rest)
-        else:
-            _call("mla_decode_paged_blocks", lib().mla_decode_paged_blocks, dev, stream, *head, seq_lens.data_ptr(),
-                  *rest)
-    elif planned:
+    if planned:
         st = lib().mla_decode_paged_planned_fp8(_ptr(_bits(q_abs)), _ptr(cache8), _ptr(scales), _ptr(block_table),
                                                 B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale),
                                                 num_splits, _ptr(workspace), nb, _ptr(err_word), _stream(stream))
@@ -489,6 +476,41 @@ def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, 
                                         float(softmax_scale), num_splits, _ptr(workspace), nb, _ptr(err_word),
                                         _stream(stream))
         _check(st, "mla_decode_paged_fp8")
+    return workspace, num_splits
+
+
+def _decode_paged_blocks(q_abs, cache8, scales, block, block_table, seq_lens, n_q, num_splits, softmax_scale, workspace,
+                         err_word, stream, planned):
+    """decode_paged_fp8 on a block-scaled cache."""
+    import torch
+    num_pages, page_size, _ = _dims("cache8", cache8, 3)
+    dev = cache8.get_device()
+    _tensor("cache8", cache8, torch.uint8, (num_pages, page_size, D_ROW), dev)
+    if dev < 0:
+        raise ValueError(f"cache8: on {cache8.device}, a CUDA device is needed")
+    B, max_pages = _dims("block_table", block_table, 2)
+    _tensor("block_table", block_table, torch.int32, (B, max_pages), dev)
+    if q_abs.dim() < 2:
+        raise ValueError(f"q_abs: shape {tuple(q_abs.shape)}, expected {B} x {n_q} rows of heads")
+    H, f16 = q_abs.shape[-2], q_abs.dtype is torch.float16
+    _tensor("q_abs", q_abs, torch.float16 if f16 else torch.bfloat16, tuple(q_abs.shape[:-2]) + (H, D_ROW), dev)
+    if q_abs.numel() != B * n_q * H * D_ROW:
+        raise ValueError(f"q_abs: shape {tuple(q_abs.shape)}, expected {B} x {n_q} rows of {H} heads")
+    if err_word is not None and (err_word.dtype is not torch.int32 or err_word.numel() < 1
+                                 or err_word.get_device() != dev):
+        raise ValueError("err_word: an int32 tensor beside the cache")
+    if num_splits is None:
+        num_splits = _splits_on(dev, n_q)
+    workspace, room = _room(workspace, 0 if workspace is not None else _step_bytes(B, n_q, H, num_splits), cache8,
+                            stream)
+    head = (q_abs.data_ptr(), int(f16), cache8.data_ptr(), scales.data_ptr(), block, block_table.data_ptr())
+    rest = (B, n_q, H, num_pages, page_size, max_pages, float(softmax_scale), num_splits, workspace.data_ptr(), room,
+            _address(err_word))
+    if planned:
+        _call("mla_decode_paged_planned_blocks", lib().mla_decode_paged_planned_blocks, dev, stream, *head, *rest)
+    else:
+        _tensor("seq_lens", seq_lens, torch.int32, (B,), dev)
+        _call("mla_decode_paged_blocks", lib().mla_decode_paged_blocks, dev, stream, *head, seq_lens.data_ptr(), *rest)
     return workspace, num_splits
 
 

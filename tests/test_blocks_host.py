@@ -194,3 +194,16 @@ def test_reference_pages_go_back_and_forth():
     assert (p.table, p.held, p.free) == start
     # page 1 comes back and is the first to be taken, then 4 and 6: place 3 is page 6
     assert p.update([64, 64 * 4, 64 * 4], [0, 1, 1], 2) == [6 * 64 + 63, -1] and p.refused == [2]
+
+
+@pytest.mark.parametrize("what,match", [
+    (dict(cache8=(4, 64, 512)), "cache8: shape"), (dict(cache8=(4, 64, 640)), "cache8: shape"),
+    (dict(cache8=(4, 64, 576)), "a CUDA device is needed"),
+])
+def test_decode_refuses_caches_of_another_width(what, match):
+    """A row of another width would be read past the cache's end."""
+    import torch
+    z = lambda shape, dtype: torch.zeros(shape, dtype=dtype)  # noqa: E731
+    with pytest.raises(ValueError, match=match):
+        mla.decode_paged_fp8(z((2, 16, 576), torch.float16), z(what["cache8"], torch.uint8), z((4, 2, 8), torch.uint8),
+                             z((2, 2), torch.int32), z((2,), torch.int32), n_q=1, num_splits=4)

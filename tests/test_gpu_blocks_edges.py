@@ -182,3 +182,29 @@ def test_small_values_in_every_reader(mla, err):
         for r, parts in ((blocks, 2), (plain, 1)):
             assert ((r["u"][b].double() - u).abs() <= near + parts * ref.TINY_F16).all()
     assert bits(blocks["u"]).shape == bits(plain["u"]).shape
+
+
+def test_decode_paged_refusals(mla, err):
+    """decode_paged_fp8 with block scales checks what it passes on, as the calls beside it do."""
+    import torch
+    c = Blocks([1, 1], [70, 100], H=16, seed=8)
+    q = mla.absorb_q(c.q_nope, c.q_rope, c.w_uk)
+    good = dict(q_abs=q, cache8=c.codes, scales=c.entries, block_table=c.table, seq_lens=c.seq_lens, n_q=1,
+                err_word=err)
+    ws = torch.zeros(2 * mla.workspace_bytes(2, 1, 16, mla.default_splits(1)), dtype=torch.uint8, device="cuda")
+    for name, bad in (("cache8", c.codes[..., :512].contiguous()), ("q_abs", q[..., :512].contiguous()),
+                      ("q_abs", q.float()), ("q_abs", q[0, 0]), ("q_abs", q[:1].contiguous()),
+                      ("block_table", c.table.long()), ("block_table", c.table[0]), ("seq_lens", c.seq_lens[:1]),
+                      ("seq_lens", c.seq_lens.cpu()), ("err_word", err.long()), ("err_word", err.cpu()),
+                      ("workspace", ws[::2]), ("workspace", ws.cpu()), ("scales", c.entries[:, :, :7].contiguous())):
+        with pytest.raises(ValueError):
+            mla.decode_paged_fp8(**{**good, name: bad})
+    with pytest.raises(mla.MlaError, match="WORKSPACE_TOO_SMALL"):
+        mla.decode_paged_fp8(**good, workspace=ws[:1024])
+    side = torch.cuda.Stream()
+    want = mla.combine(mla.decode_paged_fp8(**good)[0], B=2, n_q=1, H=16, num_splits=mla.default_splits(1))
+    torch.cuda.synchronize()
+    ws, g = mla.decode_paged_fp8(**good, stream=side)
+    got = mla.combine(ws, B=2, n_q=1, H=16, num_splits=g, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(bits(x), bits(y)) for x, y in zip(got, want)) and int(err.item()) == 0
