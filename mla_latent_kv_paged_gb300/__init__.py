@@ -1027,9 +1027,9 @@ class CapturedStep:
     """A whole decode step (decode_plan -> absorb_q -> decode_paged -> combine ->
     out_proj) captured once in a CUDA graph, for serving loops with fixed shapes.
 
-    The step owns its query, workspace and output buffers; it keeps pointers to
-    the caller's weights, cache, block_table and seq_lens, so changing their
-    contents in place between calls (appending tokens, new pages) is seen by
+    The step owns its query, workspace and output buffers; it reads (and keeps alive)
+    the caller's weights, cache, scales, block_table, seq_lens and err_word, so changing
+    their contents in place between calls (appending tokens, new pages) is seen by
     the next replay: the split plan is derived on the device from seq_lens
     every time. Shapes (batch, max pages per sequence, heads, n_q) and
     num_splits are fixed at construction. An FP8 cache (uint8 codes) is given with
@@ -1068,6 +1068,8 @@ class CapturedStep:
                          out=torch.empty((T, H, D_V), dtype=bf, device=dev))
         self.q_nope.zero_()
         self.q_rope.zero_()
+        # the graphs hold addresses only: without these a caller's last reference would free what they read
+        self._inputs = (w_uk, w_uv, cache, block_table, seq_lens, fp8_scales, err_word)
         args = (self.q_nope, self.q_rope, w_uk, w_uv, cache, block_table, seq_lens)
         kw = dict(n_q=n_q, num_splits=g, softmax_scale=softmax_scale, bufs=self.bufs, err_word=err_word,
                   fp8_scales=fp8_scales)
