@@ -155,17 +155,17 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-constexpr uint32_t kLeastF16 = 127 - 15, kMostF16 = 127 + 15, kSafeF16 = 127 + 7;  // 448 * 2^7 < 65504
+constexpr uint32_t kLeastF16 = 127 - 24, kMostF16 = 127 + 15, kSafeF16 = 127 + 7;  // 448 * 2^7 < 65504
+constexpr uint32_t kExactF16 = 127 - 15;  // codes are multiples of 2^-9: products with 2^-15 and more are exact
 __device__ __forceinline__ uint32_t power_f16x2(uint32_t p) {
-  const float step = step_of(min(max(p, kLeastF16), kMostF16));
+  const float step = step_of(min(p < kLeastF16 ? kExactF16 : p, kMostF16));
   return cvt_f16x2(step, step);
 }
 // 16 codes times 2^(p - 127), as fp16 pairs, by: power_f16x2(p). Exact but below fp16's normal range (2^-14),
-// where a value is rounded once to 2^-24's multiples: codes are multiples of 2^-9, so products with 2^-15 and
-// more are exact, and of a power below the rest comes last, in a product that rounds (its factor underflows
-// where every value is less than 2^-30, a zero either way): steps on such blocks take 1 to 4% longer. fp16 holds
-// no power above 2^15, which stands for values that it does not hold either. Returns whether one of the
-// values became infinite.
+// where a value is rounded once to 2^-24's multiples. fp16 holds the powers 2^-24 .. 2^15. One below takes two
+// products, the first of them, with 2^-15, exact (the other factor underflows where every value is less than 2^-30,
+// a zero either way); one above stands for values that fp16 does not hold. Returns whether one of the values
+// became infinite.
 __device__ __forceinline__ bool widen16(const uint32_t (&v)[4], uint32_t by, uint32_t p, uint32_t (&o)[8]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -176,7 +176,7 @@ __device__ __forceinline__ bool widen16(const uint32_t (&v)[4], uint32_t by, uin
   bool beyond = false;
   if (__builtin_expect(p < kLeastF16 || p > kSafeF16, 0)) {
     // what is left of the power (at most 2^15 of it: every value but zero then is infinite)
-    const float rest = step_of(p < kLeastF16 ? p + 15 : p > kMostF16 ? min(p - 15, kMostF16) : 127);
+    const float rest = step_of(p < kLeastF16 ? p + 127 - kExactF16 : p > kMostF16 ? min(p - 15, kMostF16) : 127);
     const uint32_t more = cvt_f16x2(rest, rest);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
