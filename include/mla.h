@@ -42,8 +42,8 @@
  *     mla_out_proj and mla_append_kv load their weights (w_uk, w_uv, w_dkr)
  *     in that time, so weights must not be written by the kernel enqueued
  *     just before the call. Every other input is read after that kernel has
- *     finished, except seq_lens and the workspace of mla_decode_paged (see
- *     its ordering rule).
+ *     finished, except seq_lens of mla_decode_paged (see its ordering rule),
+ *     and nothing is written before.
  *   - Errors that only the device can see (a context length out of range, a
  *     page id outside [0, num_pages), a wait that timed out) are written as
  *     the first nonzero mla_status into *err_word (a device int32 the caller
@@ -558,9 +558,13 @@ mla_status mla_attend_chunk(const uint16_t* q_nope, const uint16_t* q_rope, cons
  * mla_attend_chunk_blocks — their counterparts without the suffix on such a cache, with the same
  * ordering rules, workspaces and errors. Reading back and the expanded form of the attention give bit for
  * bit what they give on a bf16 cache that holds the values. The decode and the absorbed form take fp16
- * operands, as on the per-column cache: values, absorbed query and weights are rounded to fp16 (exact from 2^-14
- * on, below it their resolution is 2^-25), and a value of the context or of a query that fp16 does not
- * hold (65520 and more) is reported as MLA_ERR_RANGE. q_f16: q_abs holds fp16 and not bf16.
+ * operands, as on the per-column cache: values and absorbed query are rounded to fp16 (exact from 2^-14
+ * on, below it their resolution is 2^-25), weights, times 2^7, too, and a value of the context or of a query that
+ * fp16 does not hold (65520 and more) is reported as MLA_ERR_RANGE. Values too small are not reported: a group whose
+ * values are all below 2^-25 counts as zeros. Reading back and the expanded form have neither limit, so where a
+ * cache holds such values MLA_CHUNK_AUTO, which goes by sizes alone, is no choice: name the expanded form. (On
+ * any cache the partials of a decode, and u of the absorbed form, are fp16 too, with that resolution.)
+ * q_f16: q_abs holds fp16 and not bf16.
  *
  * mla_decode_step_blocks — a whole decode step on such a cache in one call: mla_decode_plan, mla_absorb_q
  * with its result rounded once, to fp16, mla_decode_paged_planned_blocks, mla_combine and mla_out_proj.

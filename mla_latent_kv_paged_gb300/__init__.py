@@ -23,7 +23,9 @@ An 8-bit cache (uint8 e4m3 codes [num_pages, page_size, 576]) comes with ``fp8_s
 forms: [576] float32, one fixed scale per column; or [num_pages, page_size / block, 8] uint8, block
 scales: for each block of 16, 32 or 64 tokens of a page the powers (plus 127) of two of its five groups of
 columns (four of 128 latent columns, the 64 positional ones), in bytes 0..4. The calls that write
-such a cache (write_kv, append_chunk) find and write the powers; start with a tensor of zeros.
+such a cache (write_kv, append_chunk) find and write the powers; start with a tensor of zeros. Powers go down to
+2^-110, but the decode and the absorbed form of attend_chunk take values as fp16: to 2^-25 at best, unreported,
+and below 65520 (MLA_ERR_RANGE). read_kv and the expanded form have neither limit.
 """
 from __future__ import annotations
 
@@ -447,7 +449,7 @@ def decode_paged_fp8(q_abs, cache8, scales, block_table, seq_lens, *, n_q: int, 
                      planned: bool = False):
     """decode_paged on an FP8 cache: cache8 [num_pages, page_size, 576] uint8 e4m3 codes, scales [576]
     float32 per column, or block scales [num_pages, page_size / block, 8] uint8 (q_abs then may be
-    float16). Returns (workspace, num_splits) for ``combine``."""
+    float16; values are taken as fp16, to 2^-25 at best). Returns (workspace, num_splits) for ``combine``."""
     import torch
     block = _block_tokens(cache8, scales)
     if block:
@@ -844,7 +846,8 @@ def attend_chunk(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, cu, *
     form, one for the whole call: "expanded" (keys and values of every head expanded first),
     "absorbed" (each token decoded over the latents; on a bf16 cache the absorbed query and
     the weights are rounded to bf16, as in decode_step) or "auto" (by T / B, H and
-    max_tokens / B: few new tokens on a context are absorbed).
+    max_tokens / B: few new tokens on a context are absorbed; not by the values, so name "expanded"
+    where a block-scaled cache holds values that fp16 does not).
     lse [T, H] float32, when given, receives the log-sum-exp of the scores. Rows at and
     past cu[B] of out and lse are left as they were.
     """
@@ -915,7 +918,8 @@ def decode_step(q_nope, q_rope, w_uk, w_uv, cache, block_table, seq_lens, *, n_q
     ``cache`` is the bf16 cache, or the FP8 cache (uint8 e4m3 codes of the same
     shape, from ``quantize_fp8``) together with its column scales ``fp8_scales``
     [576] float32, or a block-scaled one (from ``write_kv``) with its block scales
-    (uint8), which the decode then reads through decode_paged_fp8.
+    (uint8), which the decode then reads through decode_paged_fp8, values as fp16 (to 2^-25
+    at best).
     ``bufs`` may hold preallocated q_abs, workspace, u, lse, out tensors; steps
     enqueued back to back may share one workspace (the step's up-projection lets
     the next step's plan start only once the step has finished).

@@ -36,9 +36,8 @@ __device__ __forceinline__ uint32_t power_of(uint32_t top_bits) {
   const int e = (int)(top_bits >> 23) - 8 + ((top_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return (uint32_t)max(e, kLeastPower);
 }
-// 2^(b - 127) and 2^(127 - b) of a power's byte, fp32 (b in [1, 253])
+// 2^(b - 127) of a power's byte, fp32 (b in [1, 254])
 __device__ __forceinline__ float step_of(uint32_t b) { return __uint_as_float(b << 23); }
-__device__ __forceinline__ float inverse_step_of(uint32_t b) { return __uint_as_float((254u - b) << 23); }
 
 // Rows of a chunk (rows [T][576] bf16; chunk.cuh) quantised into their pages.
 cudaError_t launch_write_kv(const uint16_t* rows, uint8_t* cache, const BlockScales& scales, const int32_t* block_table,

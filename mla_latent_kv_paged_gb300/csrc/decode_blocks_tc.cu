@@ -16,17 +16,18 @@
 // It is a kernel of its own because a change to the other's code, even one that its template
 // folds away, costs it up to 2%.
 //
-// What bounds it: a tile's chain of work, as there (2300 cycles a tile at long contexts), and the wideners'
+// What bounds it: a tile's chain of work, as there (2400 cycles a tile at long contexts), and the wideners'
 // share of the issue slots and of shared memory. More room does not help: five operand slots in place of
 // four (with the positional columns in a ring of two, and P in two buffers) took the same time.
 // 32 sequences of 4096 tokens, 128 heads (this kernel alone with cold caches / decode step, us): 8-bit with
-// column scales 60 / 75; here 45 / 57; bf16 44 / 56. Four sequences of 131072 (step): 166; 132; 122.
-// Steps on the way (step of 32 x 4096): widened by the score readers 102; by four warps of their
-// own, to bf16 73 (83 instructions for 16 codes), to fp16 72; by eight 63; with the roles' code made
+// column scales 60 / 71; here 44 / 56; bf16 41 / 55. Four sequences of 131072: here 133 / 159; steps of the other two
+// 213 and 147. (Steps: twelve in one graph, on three sets of inputs in turn.)
+// Steps on the way (32 x 4096, a graph a step, some us of which are the gaps between them): widened by the score
+// readers 102; by four warps of their own, to bf16 73 (83 instructions for 16 codes), to fp16 72; by eight 63; with the roles' code made
 // short (packed fp32 pairs, maxima of three, waits of few instructions, loops left rolled) and the next
 // codes read ahead 60: five roles share the SM's instruction caches, and every unrolled loop was
 // slower; with registers dealt by need 58.5; by twelve, three chunks each, all read before the wait for the
-// operand slot, 57 (and the long contexts from 139 to 132).
+// operand slot, 57.
 // Measured and not taken: tiles prefetched into L2 (65), codes as 256-byte rows (60), the entries read ahead
 // (60 to 63), score MMAs started on the first half of a widened tile (60), weights taken with an older reference
 // while the maxima travel (58). A slot of codes is given back
@@ -853,7 +854,7 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
           // (the sum of the weights before their rounding to fp16. A rounded weight is off by 2^-11 of itself at
           // most, and below 2^-21 of the reference by 2^-32 of that, which is at most the sum: of n tokens the
           // sum of the rounded ones is off by 2^-11 + n 2^-32 of itself. Summed after their rounding, the
-          // same cases were off as much in u, up to 0.3% more in lse, and steps took 0.5 to 1% longer.)
+          // same cases were off as much in u, up to 0.3% more in lse, and steps took 1 to 2% longer.)
           uint64_t sum = pair(0.f, 0.f);
           const uint64_t off = pair(kWeightShift - mref, kWeightShift - mref);
           uint32_t pw[16];

@@ -22,7 +22,8 @@ def test_captured_step_outlives_its_callers_references(mla, kind, host_io):
     import torch
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     c = Blocks([1, 1], [700, 300], H=16, block=32, seed=8)
-    given = [t.clone() for t in (c.w_uk, c.w_uv, c.cache if kind == "bf16" else c.codes, c.table, c.seq_lens, c.entries)]
+    cache = c.cache if kind == "bf16" else c.codes
+    given = [t.clone() for t in (c.w_uk, c.w_uv, cache, c.table, c.seq_lens, c.entries)]
     sizes = [(t.shape, t.dtype) for t in given]
     step = mla.CapturedStep(*given[:5], n_q=1, fp8_scales=None if kind == "bf16" else given[5], err_word=err,
                             host_io=host_io)
