@@ -238,7 +238,8 @@ size_t mla_decode_workspace_bytes(int B, int n_q, int H, int num_splits);
  * d_k = d_nope + d_r, so softmax_scale is normally 1/sqrt(192)). The value
  * sum uses only the first 512 columns of each row. Unused block-table
  * entries are never read; slack rows past L in a sequence's last page may
- * hold any bits (NaN included) and never reach the result.
+ * hold any bits (NaN included) and never reach the result, nor does the second
+ * new token reach the first query's.
  *   q_abs       [B][n_q][H][576] bf16 (from mla_absorb_q)
  *   cache       [num_pages][page_size][576] bf16
  *   block_table [B][max_pages_per_seq] int32 physical page ids

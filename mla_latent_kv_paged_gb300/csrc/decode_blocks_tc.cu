@@ -20,8 +20,8 @@
 // share of the issue slots and of shared memory. More room does not help: five operand slots in place of
 // four (with the positional columns in a ring of two, and P in two buffers) took the same time.
 // 32 sequences of 4096 tokens, 128 heads (this kernel alone with cold caches / decode step, us): 8-bit with
-// column scales 60 / 71; here 44 / 56; bf16 41 / 55. Four sequences of 131072: here 133 / 159; steps of the other two
-// 213 and 147. (Steps: twelve in one graph, on three sets of inputs in turn.)
+// column scales 60 / 72; here 44 / 56; bf16 41 / 55. Four sequences of 131072: here 133 / 159; steps of the other two
+// 215 and 148. (Steps: twelve in one graph, on three sets of inputs in turn.)
 // Steps on the way (32 x 4096, a graph a step, some us of which are the gaps between them): widened by the score
 // readers 102; by four warps of their own, to bf16 73 (83 instructions for 16 codes), to fp16 72; by eight 63; with the roles' code made
 // short (packed fp32 pairs, maxima of three, waits of few instructions, loops left rolled) and the next
@@ -774,9 +774,9 @@ decode_blocks_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_con
           // order and this group waited for page g-5 at page g-2.)
           const int pb = g % kPBufs;
           if (g >= kPBufs && !wait(bar(PVD0 + pb), ((g / kPBufs) & 1) ^ 1)) { ok = false; break; }
-          const int rows_valid = L - (pg0 + i) * kTile;
+          const int rows_valid = n_att - (pg0 + i) * kTile;
           if (rows_valid < kTile) {
-            // slack rows past the context may hold any bits: zero this CTA's latent
+            // rows past what the query sees may hold any bits: zero this CTA's latent
             // half so 0-weight x NaN cannot reach O. The score MMAs have read the
             // stage (SF); the value MMAs read it after this group's P-ready arrive.
             const int stage = (g + kQSlots * (li + 1)) % kOpSlots;  // operand slot of page g

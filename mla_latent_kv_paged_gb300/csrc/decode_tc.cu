@@ -803,9 +803,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap map_c, const __grid_constan
           // order and this group waited for page g-5 at page g-2.)
           const int pb = g % kPBufs;
           if (g >= kPBufs && !wait_phase(bar(PVD0 + pb), ((g / kPBufs) & 1) ^ 1, abort_flag, err_word)) { ok = false; break; }
-          const int rows_valid = L - (pg0 + i) * kTile;
+          const int rows_valid = nv + 32 * (int)rank;  // of the tile's rows
           if (rows_valid < kTile) {
-            // slack rows past the context may hold any bits: zero this CTA's latent
+            // rows past what the query sees may hold any bits: zero this CTA's latent
             // half so 0-weight x NaN cannot reach O. The score MMAs have read the
             // stage (SF); the value MMAs read it after this group's P-ready arrive.
             const int stage = (g + kQSlots * (li + 1)) % kStages;  // ring slot of page g

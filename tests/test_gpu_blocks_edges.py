@@ -208,3 +208,25 @@ def test_decode_paged_refusals(mla, err):
     got = mla.combine(ws, B=2, n_q=1, H=16, num_splits=g, stream=side)
     torch.cuda.synchronize()
     assert all(torch.equal(bits(x), bits(y)) for x, y in zip(got, want)) and int(err.item()) == 0
+
+
+@pytest.mark.parametrize("kind", ["blocks", "bf16", "columns"])
+def test_a_nan_in_the_last_draft_reaches_only_the_query_that_sees_it(mla, err, kind):
+    """Two new tokens, the second with a NaN: the first one's results are, bit for bit, those without it, wherever
+    the second lies in its tile."""
+    import torch
+    lens = [65, 64, 129, 200, 2, 1000, 128]
+    c = Blocks([2] * len(lens), lens, H=16, block=16, seed=8)
+    scales = torch.ones(576, device="cuda")
+    cache = {"blocks": c.codes, "bf16": c.cache, "columns": c.codes}[kind]
+    kw = {"blocks": c.entries, "bf16": None, "columns": scales}[kind]
+    want = {k: v.clone() for k, v in decode(mla, c, cache, kw, 2, err).items() if k in ("u", "lse", "out")}
+    rows = torch.stack([c.rows(b)[-1] for b in range(len(lens))])
+    for col in (70, 300, 570):
+        cache.view(-1, 576)[rows, col] = float("nan") if kind == "bf16" else 0x7F
+    got = decode(mla, c, cache, kw, 2, err)
+    torch.cuda.synchronize()
+    for k in ("u", "lse", "out"):
+        assert torch.equal(bits(got[k][::2]), bits(want[k][::2])), k
+        assert torch.isfinite(want[k].float()).all() and torch.isnan(got[k][1::2].float()).all(), k
+    assert int(err.item()) == 0
